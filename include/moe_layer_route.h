@@ -491,6 +491,150 @@ MOE_API int moe_down_fp8(const void* hq, const float* sh, const void* Wd_q, cons
                          int64_t T, int32_t H, int32_t E, int32_t k, int32_t I, float* o,
                          int32_t path, void* stream);
 
+/*
+ * Residual addition and RMS norm in front of the block -- xserv "Phase 19:
+ * gpt-oss-20b MoE support", section 2 (the block reads the normalised hidden
+ * state) and section 5 (FP8 activations with dynamic scales).
+ *
+ * moe_add_rmsnorm -- one row of H values per token:
+ *   r   = bf16(x + residual), the float32 sum rounded once (r = x without a
+ *         residual)
+ *   inv = float32(1 / sqrt(sum_h r[h]^2 / H + eps)), the sum and the root in
+ *         float64
+ *   y   = bf16((r * inv) * gamma), each product rounded to float32
+ *
+ *   x, residual  bf16 [T][H]   in; residual NULL: r = x
+ *   gamma        bf16 [H]      in
+ *   eps          finite and above 0
+ *   residual_out bf16 [T][H]   out: r (NULL exactly when residual is NULL)
+ *   y            bf16 [T][H]   out
+ * All pointers 16-byte aligned, H % 8 == 0 in [8, 16384], T below 2^31.
+ * residual_out and y may each be the very buffer of x or residual (in place);
+ * any other overlap with an output is refused.  A row with a NaN or an
+ * infinity gives NaN where the formula does.
+ */
+MOE_API int moe_add_rmsnorm(const void* x, const void* residual, const void* gamma, int64_t T, int32_t H, float eps,
+                            void* residual_out, void* y, void* stream);
+
+/*
+ * moe_add_rmsnorm_fp8 -- moe_add_rmsnorm that also quantises the normalised
+ * rows for the FP8 experts, in the format of moe_quantize_rows_fp8, from the
+ * float32 values (r * inv) * gamma rather than from y: one rounding, not two.
+ *   y       as above, or NULL to leave it out
+ *   codes   uint8 [T][H]   out
+ *   scales  float [T]      out (4-byte aligned)
+ * H % 16 == 0.
+ */
+MOE_API int moe_add_rmsnorm_fp8(const void* x, const void* residual, const void* gamma, int64_t T, int32_t H, float eps,
+                                void* residual_out, void* y, void* codes, float* scales, void* stream);
+
+/*
+ * moe_forward_norm_fp8 -- moe_add_rmsnorm_fp8 and the FP8 block on its result
+ * in one call: the router reads the bf16 rows, gate_up their codes (no
+ * quantisation launch and no second read of the rows).
+ *   x, residual, gamma, eps, residual_out   as in moe_add_rmsnorm
+ *   the router, weights, y, topk outputs and path as in moe_forward_fp8_ex
+ *   (y: the block's output, written last; it must not overlap residual_out)
+ *   workspace   at least moe_workspace_bytes_norm_fp8(...) bytes
+ */
+MOE_API size_t moe_workspace_bytes_norm_fp8(int64_t T, int32_t H, int32_t E, int32_t k, int32_t I);
+MOE_API int moe_forward_norm_fp8(const void* x, const void* residual, const void* gamma, float eps,
+                                 const void* Wr, const void* br,
+                                 const void* Wgu_q, const float* Wgu_s, const void* bgu,
+                                 const void* Wd_q, const float* Wd_s, const void* bd,
+                                 int64_t T, int32_t H, int32_t E, int32_t k, int32_t I,
+                                 void* residual_out, void* y, int32_t* topk_ids_out, float* topk_w_out,
+                                 void* workspace, size_t workspace_bytes, int32_t path, void* stream);
+
+/*
+ * 4-bit integer expert weights with group scales (W4A16) -- xserv "Phase 19:
+ * gpt-oss-20b MoE support", section 5 (4-bit expert weights, bf16
+ * activations); the uniform codes that integer-quantised checkpoints hold,
+ * beside the E2M1 codes of MXFP4.
+ *
+ * A weight is (q - z) * s: q in 0..15; s a bf16 scale and z a zero point in
+ * 0..15 for each group of G consecutive values of K in a column (G = 32, 64 or
+ * 128; the last group of a column may be shorter).  Without zero points z = 8.
+ * The products take the integers exactly and apply s to float32 sums over a
+ * group, so no weight is rounded.
+ *
+ * For a weight with contraction dimension K and N columns (gate_up: K = H,
+ * N = 2I; down: K = I, N = H):
+ *   codes   uint8 [E][ceil(N/64)][K/32][1024], tiles of 64 columns x 32 values
+ *           of K: 64 lanes x four little-endian 32-bit words; word j of lane
+ *           16 g + c holds column 64 nt + 4 c + j and K = 32 kt + 8 g + i for
+ *           i = 0..7, value i at bit (3 + 4 (i / 2) + 16 (i % 2)) mod 32, low
+ *           bit first (a field may wrap round the word's end).  Columns past N
+ *           hold anything.
+ *   scales  bf16 [E][ceil(K/G)][N], 16-byte aligned
+ *   zeros   uint8 [E][ceil(K/G)][N], 8-byte aligned, or NULL; values above 15
+ *           count as they are
+ * Requires K % 32 == 0 (the forwards: H % 32 == 0 and I % 32 == 0); codes
+ * 16-byte aligned.
+ */
+
+/*
+ * moe_quantize_int4 -- bf16 weights W [E][K][N] (x.W form, finite) to that
+ * format, rounding to nearest: without zeros s = bf16(max|v| / 7) and
+ * q = clamp(rint(v / s), -8, 7) + 8; with zeros, lo = min(v, 0) and
+ * hi = max(v, 0) over the group, s = bf16(hi / 15 - lo / 15),
+ * z = clamp(rint(-lo / s), 0, 15), q = clamp(rint(v / s) + z, 0, 15).  float32
+ * operations, halves to even; a group whose s is 0 stores q = z (z = 0 with
+ * zeros).  K % 32 == 0, N % 8 == 0.
+ *
+ * moe_pack_int4 -- codes that a checkpoint holds K-contiguous, uint8
+ * [E][N][K/2] (the low nibble the even value), to the tile order above.
+ */
+MOE_API int moe_quantize_int4(const void* W, int32_t E, int32_t K, int32_t N, int32_t G, void* codes, void* scales,
+                              void* zeros, void* stream);
+MOE_API int moe_pack_int4(const void* codes_kn, int32_t E, int32_t K, int32_t N, void* codes, void* stream);
+
+/* moe_forward_int4, moe_forward_int4_ex -- moe_forward with these weights
+ * (Wgu_z, Wd_z: zero points or NULL, each on its own); every other argument,
+ * the workspace (moe_workspace_bytes) and the result's definition as in
+ * moe_forward_mxfp4(_ex). */
+MOE_API int moe_forward_int4(const void* x, const void* Wr, const void* br,
+                             const void* Wgu_q, const void* Wgu_s, const void* Wgu_z, const void* bgu,
+                             const void* Wd_q, const void* Wd_s, const void* Wd_z, const void* bd,
+                             int64_t T, int32_t H, int32_t E, int32_t k, int32_t I, int32_t G,
+                             void* y, int32_t* topk_ids_out, float* topk_w_out,
+                             void* workspace, size_t workspace_bytes, void* stream);
+MOE_API int moe_forward_int4_ex(const void* x, const void* Wr, const void* br,
+                                const void* Wgu_q, const void* Wgu_s, const void* Wgu_z, const void* bgu,
+                                const void* Wd_q, const void* Wd_s, const void* Wd_z, const void* bd,
+                                int64_t T, int32_t H, int32_t E, int32_t k, int32_t I, int32_t G,
+                                void* y, int32_t* topk_ids_out, float* topk_w_out,
+                                void* workspace, size_t workspace_bytes, int32_t path, void* stream);
+
+/* moe_forward_padded_int4, moe_forward_ep_int4 -- as moe_forward_padded and
+ * moe_forward_ep, with these weights (the rank's n_local experts in the latter). */
+MOE_API int moe_forward_padded_int4(const void* x, const void* Wr, const void* br,
+                                    const void* Wgu_q, const void* Wgu_s, const void* Wgu_z, const void* bgu,
+                                    const void* Wd_q, const void* Wd_s, const void* Wd_z, const void* bd,
+                                    int64_t T, int32_t H, int32_t E, int32_t k, int32_t I, int32_t G,
+                                    const int32_t* n_valid, void* y, int32_t* topk_ids_out, float* topk_w_out,
+                                    int32_t* expert_counts_out, void* workspace, size_t workspace_bytes,
+                                    int32_t path, void* stream);
+MOE_API int moe_forward_ep_int4(const void* x, const void* Wr, const void* br,
+                                const void* Wgu_q_local, const void* Wgu_s_local, const void* Wgu_z_local,
+                                const void* bgu_local,
+                                const void* Wd_q_local, const void* Wd_s_local, const void* Wd_z_local,
+                                const void* bd_local,
+                                int64_t T, int32_t H, int32_t E, int32_t k, int32_t I, int32_t G,
+                                int32_t e_begin, int32_t n_local, float* y_partial,
+                                int32_t* topk_ids_out, float* topk_w_out,
+                                void* workspace, size_t workspace_bytes, int32_t path, void* stream);
+
+/* Stage calls of moe_forward_int4: moe_gate_up and moe_down with these weights. */
+MOE_API int moe_gate_up_int4(const void* x, const void* Wgu_q, const void* Wgu_s, const void* Wgu_z, const void* bgu,
+                             const int32_t* cnt, const int32_t* off, const int32_t* rows,
+                             int64_t T, int32_t H, int32_t E, int32_t k, int32_t I, int32_t G, void* h,
+                             int32_t path, void* stream);
+MOE_API int moe_down_int4(const void* h, const void* Wd_q, const void* Wd_s, const void* Wd_z, const void* bd,
+                          const int32_t* cnt, const int32_t* off,
+                          int64_t T, int32_t H, int32_t E, int32_t k, int32_t I, int32_t G, float* o,
+                          int32_t path, void* stream);
+
 /* ---------------------------------------------------------------------------
  * Measurement probes.  They are not part of the block: they measure what a
  * plain hand-written kernel gets from the matrix cores and from HBM on this

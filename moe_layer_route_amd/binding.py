@@ -8,6 +8,7 @@ fallback implementation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -30,7 +31,10 @@ EXPORTS = ("moe_abi_version", "moe_status_str", "moe_last_error", "moe_workspace
            "moe_forward_fp8", "moe_forward_fp8_ex", "moe_gate_up_fp8", "moe_down_fp8", "moe_forward_padded",
            "moe_probe_mfma_bf16", "moe_probe_read", "moe_forward_padded_mxfp4", "moe_forward_padded_fp8",
            "moe_forward_ep_mxfp4", "moe_forward_ep_fp8", "moe_probe_mfma_dot_bf16",
-           "moe_forward_noalloc")
+           "moe_forward_noalloc",
+           "moe_add_rmsnorm", "moe_add_rmsnorm_fp8", "moe_workspace_bytes_norm_fp8", "moe_forward_norm_fp8",
+           "moe_quantize_int4", "moe_pack_int4", "moe_forward_int4", "moe_forward_int4_ex", "moe_gate_up_int4",
+           "moe_down_int4", "moe_forward_padded_int4", "moe_forward_ep_int4")
 
 
 class MoEError(RuntimeError):
@@ -40,6 +44,7 @@ class MoEError(RuntimeError):
 _lib = None
 
 _vp, _i64, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+_f32 = ctypes.c_float
 _SIGS = {
     "moe_abi_version": (ctypes.c_int, []),
     "moe_status_str": (ctypes.c_char_p, [ctypes.c_int]),
@@ -81,6 +86,19 @@ _SIGS = {
     "moe_probe_read": (ctypes.c_int, [_vp, _sz, _i32, _vp, _vp]),
     "moe_probe_mfma_dot_bf16": (ctypes.c_int, [_vp, _vp, _i32, _i32, _vp, _vp]),
     "moe_forward_noalloc": (ctypes.c_int, [_vp] * 7 + [_i64, _i32, _i32, _i32, _i32] + [_vp] * 4),
+    "moe_add_rmsnorm": (ctypes.c_int, [_vp] * 3 + [_i64, _i32, _f32] + [_vp] * 3),
+    "moe_add_rmsnorm_fp8": (ctypes.c_int, [_vp] * 3 + [_i64, _i32, _f32] + [_vp] * 5),
+    "moe_workspace_bytes_norm_fp8": (_sz, [_i64, _i32, _i32, _i32, _i32]),
+    "moe_forward_norm_fp8": (ctypes.c_int, [_vp] * 3 + [_f32] + [_vp] * 8 + [_i64, _i32, _i32, _i32, _i32] + [_vp] * 5
+                             + [_sz, _i32, _vp]),
+    "moe_quantize_int4": (ctypes.c_int, [_vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp]),
+    "moe_pack_int4": (ctypes.c_int, [_vp, _i32, _i32, _i32, _vp, _vp]),
+    "moe_forward_int4": (ctypes.c_int, [_vp] * 11 + [_i64] + [_i32] * 5 + [_vp] * 4 + [_sz, _vp]),
+    "moe_forward_int4_ex": (ctypes.c_int, [_vp] * 11 + [_i64] + [_i32] * 5 + [_vp] * 4 + [_sz, _i32, _vp]),
+    "moe_forward_padded_int4": (ctypes.c_int, [_vp] * 11 + [_i64] + [_i32] * 5 + [_vp] * 6 + [_sz, _i32, _vp]),
+    "moe_forward_ep_int4": (ctypes.c_int, [_vp] * 11 + [_i64] + [_i32] * 7 + [_vp] * 4 + [_sz, _i32, _vp]),
+    "moe_gate_up_int4": (ctypes.c_int, [_vp] * 8 + [_i64] + [_i32] * 5 + [_vp, _i32, _vp]),
+    "moe_down_int4": (ctypes.c_int, [_vp] * 7 + [_i64] + [_i32] * 5 + [_vp, _i32, _vp]),
 }
 
 
@@ -125,6 +143,36 @@ def _dev(*ts):
                 raise MoEError("tensors must be on the GPU")
             if not t.is_contiguous():
                 raise MoEError("tensors must be contiguous")
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(t, stream):
+    """Where a call runs: t's device, and stream (a torch stream or a raw handle; default: that device's current
+    stream).  Within it both are current, so that what the call allocates belongs to the stream that uses it."""
+    if stream is None:
+        return _HERE if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), t.device) if int(stream) else torch.cuda.default_stream(t.device)
+    if stream.device != t.device:
+        raise MoEError(f"stream is on {stream.device}, the tensors on {t.device}")
+    return torch.cuda.stream(stream)
+
+
+def _at(t):
+    """_ptr, with an address that is never read for a tensor without elements (a call for no tokens is valid)."""
+    if t is None:
+        return None
+    return ctypes.c_void_p(t.data_ptr() if t.numel() else 4096)
+
+
+def _dev_as(first, *ts):
+    """_dev, and every tensor on the device of the first."""
+    _dev(first, *ts)
+    for t in ts:
+        if t is not None and t.device != first.device:
+            raise MoEError(f"tensors are on {first.device} and on {t.device}")
 
 
 # ---------------------------------------------------------------------------
@@ -300,7 +348,10 @@ def moe_forward_noalloc(x, Wr, br, Wgu, bgu, Wd, bd, k: int = 4, y=None, topk_id
     _dev(y, topk_ids, topk_w)
     _check(library().moe_forward_noalloc(_ptr(x), _ptr(Wr), _ptr(br), _ptr(Wgu), _ptr(bgu), _ptr(Wd), _ptr(bd),
                                          T, H, E, k, I, _ptr(y), _ptr(topk_ids), _ptr(topk_w), _stream(stream)),
-           "moe_forward_noalloc")
+           "moe_forward_noalloc",
+           "moe_add_rmsnorm", "moe_add_rmsnorm_fp8", "moe_workspace_bytes_norm_fp8", "moe_forward_norm_fp8",
+           "moe_quantize_int4", "moe_pack_int4", "moe_forward_int4", "moe_forward_int4_ex", "moe_gate_up_int4",
+           "moe_down_int4", "moe_forward_padded_int4", "moe_forward_ep_int4")
     return y
 
 
@@ -730,6 +781,262 @@ def moe_forward_ep_fp8(x, Wr, br, Wgu_q_local, Wgu_s_local, bgu_local, Wd_q_loca
                                       path_code(path), _stream(stream))
     _check(st, "moe_forward_ep_fp8")
     return y_partial
+
+
+# ---------------------------------------------------------------------------
+# residual addition and RMS norm in front of the block
+# ---------------------------------------------------------------------------
+def _norm_args(x, gamma, residual, residual_out, y, y_name="y"):
+    """x, residual, residual_out, y [T][H] and gamma [H], bf16; residual_out only beside a residual."""
+    _dims(x, "x", 2)
+    T, H = x.shape
+    for t, name, shape in ((x, "x", (T, H)), (gamma, "gamma", (H,)), (residual, "residual", (T, H)),
+                           (residual_out, "residual_out", (T, H)), (y, y_name, (T, H))):
+        _req(t, name, shape, torch.bfloat16)
+    if residual is None and residual_out is not None:
+        raise MoEError("residual_out: given without a residual")
+    return T, H
+
+
+def moe_add_rmsnorm(x, gamma, residual=None, eps: float = 1e-5, y=None, residual_out=None, stream=None):
+    """r = bf16(x + residual) and y = RMS norm of r times gamma; returns (y, r).
+
+    Without a residual r is x itself.  y and residual_out may be the buffer of x or residual (in place)."""
+    T, H = _norm_args(x, gamma, residual, residual_out, y)
+    _dev_as(x, gamma, residual, residual_out, y)
+    with _on(x, stream):
+        if y is None:
+            y = torch.empty_like(x)
+        if residual is not None and residual_out is None:
+            residual_out = torch.empty_like(x)
+        _check(library().moe_add_rmsnorm(_at(x), _at(residual), _at(gamma), T, H, eps, _at(residual_out), _at(y),
+                                         _stream(None)), "moe_add_rmsnorm")
+    return y, x if residual is None else residual_out
+
+
+def moe_add_rmsnorm_fp8(x, gamma, residual=None, eps: float = 1e-5, y=None, residual_out=None, codes=None, scales=None,
+                        stream=None):
+    """moe_add_rmsnorm that also quantises the normalised rows for the FP8 experts; returns (y, codes, scales, r):
+    codes uint8 [T][H] and scales float32 [T] in moe_quantize_rows_fp8's format, from the unrounded values."""
+    T, H = _norm_args(x, gamma, residual, residual_out, y)
+    _req(codes, "codes", (T, H), torch.uint8)
+    _req(scales, "scales", (T,), torch.float32)
+    _dev_as(x, gamma, residual, residual_out, y, codes, scales)
+    with _on(x, stream):
+        if y is None:
+            y = torch.empty_like(x)
+        if residual is not None and residual_out is None:
+            residual_out = torch.empty_like(x)
+        if codes is None:
+            codes = torch.empty((T, H), dtype=torch.uint8, device=x.device)
+        if scales is None:
+            scales = torch.empty((T,), dtype=torch.float32, device=x.device)
+        _check(library().moe_add_rmsnorm_fp8(_at(x), _at(residual), _at(gamma), T, H, eps, _at(residual_out),
+                                             _at(y), _at(codes), _at(scales), _stream(None)), "moe_add_rmsnorm_fp8")
+    return y, codes, scales, x if residual is None else residual_out
+
+
+def workspace_bytes_norm_fp8(T: int, H: int, E: int, k: int, I: int) -> int:
+    return int(library().moe_workspace_bytes_norm_fp8(T, H, E, k, I))
+
+
+def alloc_workspace_norm_fp8(T: int, H: int, E: int, k: int, I: int, device=None) -> torch.Tensor:
+    n = workspace_bytes_norm_fp8(T, H, E, k, I)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device or "cuda")
+
+
+def moe_forward_norm_fp8(x, gamma, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, k: int = 4, residual=None,
+                         eps: float = 1e-5, y=None, residual_out=None, workspace=None, topk_ids=None, topk_w=None,
+                         path="auto", stream=None):
+    """moe_add_rmsnorm_fp8 and the FP8 block on its rows, in one call; returns (y, r)."""
+    T, H = _norm_args(x, gamma, residual, residual_out, y)
+    _, _, E = _route_args(x, Wr, br, k, topk_ids, topk_w)
+    I = _fp8_experts(Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, E, H)
+    _dev_as(x, gamma, residual, residual_out, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, y, workspace, topk_ids, topk_w)
+    with _on(x, stream):
+        if y is None:
+            y = torch.empty_like(x)
+        if residual is not None and residual_out is None:
+            residual_out = torch.empty_like(x)
+        if workspace is None:
+            workspace = alloc_workspace_norm_fp8(T, H, E, k, I, x.device)
+        st = library().moe_forward_norm_fp8(_at(x), _at(residual), _at(gamma), eps, _at(Wr), _at(br), _at(Wgu_q),
+                                            _at(Wgu_s), _at(bgu), _at(Wd_q), _at(Wd_s), _at(bd), T, H, E, k, I,
+                                            _at(residual_out), _at(y), _at(topk_ids), _at(topk_w), _at(workspace),
+                                            workspace.numel() * workspace.element_size(), path_code(path),
+                                            _stream(None))
+        _check(st, "moe_forward_norm_fp8")
+    return y, x if residual is None else residual_out
+
+
+# ---------------------------------------------------------------------------
+# 4-bit integer expert weights: codes uint8 [E][ceil(N/64)][K/32][1024] in tile
+# order, scales bf16 and zero points uint8 (or None: 8) [E][ceil(K/G)][N]
+# (gate_up: K = H, N = 2I; down: K = I, N = H); G = 32, 64 or 128 follows from
+# the scales' shape
+# ---------------------------------------------------------------------------
+_GROUPS = (32, 64, 128)
+
+
+def _int4_group(*pairs):
+    """The group size with ceil(K / G) scales for every (K, scales) pair (several fit only where they mean the same)."""
+    for G in _GROUPS:
+        if all(-(-K // G) == n for K, n in pairs):
+            return G
+    raise MoEError("scales: no group size of " + ", ".join(map(str, _GROUPS)) + " gives "
+                   + " and ".join(f"{n} scales for K={K}" for K, n in pairs))
+
+
+def _int4_shape(n, K, N):
+    return n, -(-N // 64), K // 32, 1024
+
+
+def _int4_matrix(q, s, z, bias, names, n, K, N):
+    _req(q, names + "_q", _int4_shape(n, K, N), torch.uint8)
+    _req(s, names + "_s", (n, s.shape[1], N), torch.bfloat16)
+    _req(z, names + "_z", tuple(s.shape), torch.uint8)
+    _req(bias, "b" + names[1:], (n, N), bf16=True)
+
+
+def _int4_experts(Wgu_q, Wgu_s, Wgu_z, bgu, Wd_q, Wd_s, Wd_z, bd, n, H):
+    """Codes, scales, zero points and biases of n experts; returns (I, G)."""
+    _dims(Wgu_s, "Wgu_s", 3)
+    _dims(Wd_s, "Wd_s", 3)
+    I = Wgu_s.shape[2] // 2
+    if H % 32 or I % 32:
+        raise MoEError(f"int4 weights need H and I divisible by 32, got H={H}, I={I}")
+    _int4_matrix(Wgu_q, Wgu_s, Wgu_z, bgu, "Wgu", n, H, 2 * I)
+    _int4_matrix(Wd_q, Wd_s, Wd_z, bd, "Wd", n, I, H)
+    return I, _int4_group((H, Wgu_s.shape[1]), (I, Wd_s.shape[1]))
+
+
+def moe_quantize_int4(W, G: int = 64, zeros: bool = False, stream=None):
+    """bf16 weights [E][K][N] (x.W form) -> (codes, scales, zero points or None), groups of G values of K."""
+    _dims(W, "W", 3)
+    E, K, N = W.shape
+    _req(W, "W", (E, K, N), torch.bfloat16)
+    if G not in _GROUPS:
+        raise MoEError(f"G: expected one of {_GROUPS}, got {G}")
+    _dev(W)
+    with _on(W, stream):
+        q = torch.empty(_int4_shape(E, K, N), dtype=torch.uint8, device=W.device)
+        s = torch.empty((E, -(-K // G), N), dtype=torch.bfloat16, device=W.device)
+        z = torch.empty((E, -(-K // G), N), dtype=torch.uint8, device=W.device) if zeros else None
+        _check(library().moe_quantize_int4(_at(W), E, K, N, G, _at(q), _at(s), _at(z), _stream(None)),
+               "moe_quantize_int4")
+    return q, s, z
+
+
+def moe_pack_int4(codes, stream=None):
+    """K-contiguous codes uint8 [E][N][K/2] (low nibble the even value) -> the tile order of the int4 calls."""
+    _dims(codes, "codes", 3)
+    E, N, K = codes.shape[0], codes.shape[1], 2 * codes.shape[2]
+    _req(codes, "codes", (E, N, K // 2), torch.uint8)
+    _dev(codes)
+    with _on(codes, stream):
+        q = torch.empty(_int4_shape(E, K, N), dtype=torch.uint8, device=codes.device)
+        _check(library().moe_pack_int4(_at(codes), E, K, N, _at(q), _stream(None)), "moe_pack_int4")
+    return q
+
+
+def _forward_int4(name, x, Wr, br, Wgu_q, Wgu_s, Wgu_z, bgu, Wd_q, Wd_s, Wd_z, bd, k, n, y, y_dtype, workspace, topk_ids,
+                  topk_w, path, stream, before=(), between=(), more=()):
+    """The int4 forwards: `before` y come further sizes or inputs, `between` the outputs and the workspace further
+    outputs; `more` are the tensors among them, for the device check."""
+    T, H, E = _route_args(x, Wr, br, k, topk_ids, topk_w)
+    I, G = _int4_experts(Wgu_q, Wgu_s, Wgu_z, bgu, Wd_q, Wd_s, Wd_z, bd, E if n is None else n, H)
+    _req(y, "y" if y_dtype == torch.bfloat16 else "y_partial", (T, H), y_dtype)
+    _dev_as(x, Wr, br, Wgu_q, Wgu_s, Wgu_z, bgu, Wd_q, Wd_s, Wd_z, bd, y, workspace, topk_ids, topk_w, *more)
+    with _on(x, stream):
+        if y is None:
+            y = torch.empty((T, H), dtype=y_dtype, device=x.device)
+        if workspace is None:
+            workspace = alloc_workspace(T, H, E, k, I, x.device)
+        st = getattr(library(), name)(_at(x), _at(Wr), _at(br), _at(Wgu_q), _at(Wgu_s), _at(Wgu_z), _at(bgu),
+                                      _at(Wd_q), _at(Wd_s), _at(Wd_z), _at(bd), T, H, E, k, I, G, *before, _at(y),
+                                      _at(topk_ids), _at(topk_w), *between, _at(workspace),
+                                      workspace.numel() * workspace.element_size(), path_code(path), _stream(None))
+        _check(st, name.removesuffix("_ex"))
+    return y
+
+
+def moe_forward_int4(x, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, k: int = 4, Wgu_z=None, Wd_z=None, y=None,
+                     workspace=None, topk_ids=None, topk_w=None, path="auto", stream=None):
+    """moe_forward with 4-bit integer expert weights; returns y (bf16 [T,H])."""
+    return _forward_int4("moe_forward_int4_ex", x, Wr, br, Wgu_q, Wgu_s, Wgu_z, bgu, Wd_q, Wd_s, Wd_z, bd, k, None, y,
+                         torch.bfloat16, workspace, topk_ids, topk_w, path, stream)
+
+
+def moe_forward_padded_int4(x, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, k: int = 4, Wgu_z=None, Wd_z=None,
+                            n_valid=None, y=None, workspace=None, topk_ids=None, topk_w=None, expert_counts=None,
+                            path="auto", stream=None):
+    """moe_forward_padded with 4-bit integer expert weights; returns y (bf16 [T,H])."""
+    _dims(Wr, "Wr", 2)
+    _padded_args(n_valid, expert_counts, Wr.shape[0])
+    return _forward_int4("moe_forward_padded_int4", x, Wr, br, Wgu_q, Wgu_s, Wgu_z, bgu, Wd_q, Wd_s, Wd_z, bd, k, None,
+                         y, torch.bfloat16, workspace, topk_ids, topk_w, path, stream, before=(_at(n_valid),),
+                         between=(_at(expert_counts),), more=(n_valid, expert_counts))
+
+
+def moe_forward_ep_int4(x, Wr, br, Wgu_q_local, Wgu_s_local, bgu_local, Wd_q_local, Wd_s_local, bd_local, e_begin: int,
+                        k: int = 4, Wgu_z_local=None, Wd_z_local=None, y_partial=None, workspace=None, topk_ids=None,
+                        topk_w=None, path="auto", stream=None):
+    """moe_forward_ep with 4-bit integer expert weights (the rank's n_local = Wgu_q_local.shape[0] experts from
+    e_begin); returns y_partial (float32 [T,H])."""
+    _dims(Wr, "Wr", 2)
+    _dims(Wgu_q_local, "Wgu_q_local", 4)
+    n_local = Wgu_q_local.shape[0]
+    _local_experts(e_begin, n_local, Wr.shape[0])
+    return _forward_int4("moe_forward_ep_int4", x, Wr, br, Wgu_q_local, Wgu_s_local, Wgu_z_local, bgu_local, Wd_q_local,
+                         Wd_s_local, Wd_z_local, bd_local, k, n_local, y_partial, torch.float32, workspace, topk_ids,
+                         topk_w, path, stream, before=(e_begin, n_local))
+
+
+def _permutation(cnt, off, rows, E, S):
+    _req(cnt, "cnt", (E,), torch.int32)
+    _req(off, "off", (E + 1,), torch.int32)
+    if rows is not None:
+        _req_rows(rows, "rows", S, None, torch.int32)
+
+
+def moe_gate_up_int4(x, Wgu_q, Wgu_s, bgu, cnt, off, rows, k: int, Wgu_z=None, h=None, path="auto", stream=None):
+    """int4 gate_up + bias + GLU; returns h (bf16 [T*k, I], permuted order)."""
+    _dims(x, "x", 2)
+    _dims(Wgu_s, "Wgu_s", 3)
+    T, H = x.shape
+    E, I = Wgu_s.shape[0], Wgu_s.shape[2] // 2
+    _req(x, "x", (T, H), bf16=True)
+    _int4_matrix(Wgu_q, Wgu_s, Wgu_z, bgu, "Wgu", E, H, 2 * I)
+    G = _int4_group((H, Wgu_s.shape[1]))
+    _permutation(cnt, off, rows, E, T * k)
+    _req_rows(h, "h", T * k, I, torch.bfloat16)
+    _dev_as(x, Wgu_q, Wgu_s, Wgu_z, bgu, cnt, off, rows, h)
+    with _on(x, stream):
+        if h is None:
+            h = torch.empty((max(T * k, 1), I), dtype=torch.bfloat16, device=x.device)
+        _check(library().moe_gate_up_int4(_at(x), _at(Wgu_q), _at(Wgu_s), _at(Wgu_z), _at(bgu), _at(cnt), _at(off),
+                                          _at(rows), T, H, E, k, I, G, _at(h), path_code(path), _stream(None)),
+               "moe_gate_up_int4")
+    return h[:T * k]
+
+
+def moe_down_int4(h, Wd_q, Wd_s, bd, cnt, off, T: int, k: int, Wd_z=None, o=None, path="auto", stream=None):
+    """int4 down + bias; returns o (float32 [T*k, H], permuted order)."""
+    _dims(h, "h", 2)
+    _dims(Wd_s, "Wd_s", 3)
+    E, H, I = Wd_s.shape[0], Wd_s.shape[2], h.shape[1]
+    _int4_matrix(Wd_q, Wd_s, Wd_z, bd, "Wd", E, I, H)
+    G = _int4_group((I, Wd_s.shape[1]))
+    _permutation(cnt, off, None, E, T * k)
+    _req_rows(h, "h", T * k, I, torch.bfloat16)
+    _req_rows(o, "o", T * k, H, torch.float32)
+    _dev_as(h, Wd_q, Wd_s, Wd_z, bd, cnt, off, o)
+    with _on(h, stream):
+        if o is None:
+            o = torch.empty((max(T * k, 1), H), dtype=torch.float32, device=h.device)
+        _check(library().moe_down_int4(_at(h), _at(Wd_q), _at(Wd_s), _at(Wd_z), _at(bd), _at(cnt), _at(off), T, H,
+                                       E, k, I, G, _at(o), path_code(path), _stream(None)), "moe_down_int4")
+    return o[:T * k]
 
 
 # ---------------------------------------------------------------------------

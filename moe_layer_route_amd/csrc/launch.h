@@ -84,6 +84,23 @@ hipError_t launch_gemv_fp8_down(const void* hq, const float* sh, const void* Wq,
                                 const int32_t* cnt, const int32_t* off, int64_t T, int H, int E, int k, int I,
                                 float* o, hipStream_t stream);
 
+// 4-bit integer expert weights with group scales: codes in tile order, scales
+// bf16 and zero points uint8 (nullable: 8) of [E][ceil(K/G)][N] (K % 32 == 0)
+hipError_t launch_int4_quantize(const void* W, int E, int K, int N, int G, void* codes, void* scales, void* zeros,
+                                hipStream_t stream);
+hipError_t launch_int4_pack(const void* src, int E, int K, int N, void* codes, hipStream_t stream);
+hipError_t launch_int4_gate_up(const void* x, const void* Wq, const void* Ws, const void* Wz, const void* bgu,
+                               const int32_t* cnt, const int32_t* off, const int32_t* rows, int H, int E, int k, int I,
+                               int G, void* h, hipStream_t stream);
+hipError_t launch_int4_down(const void* h, const void* Wq, const void* Ws, const void* Wz, const void* bd,
+                            const int32_t* cnt, const int32_t* off, int H, int E, int I, int G, float* o,
+                            hipStream_t stream);
+
+// Residual addition and RMS norm (residual and residual_out both or neither;
+// codes and scales both or neither; y may be null with codes)
+hipError_t launch_add_rmsnorm(const void* x, const void* residual, const void* gamma, int64_t T, int H, float eps,
+                              void* residual_out, void* y, void* codes, float* scales, hipStream_t stream);
+
 // measurement probes (probe.hip)
 hipError_t launch_probe_mfma(int iters, int workgroups, float* out, hipStream_t stream);
 hipError_t launch_probe_read(const void* buf, size_t bytes, int workgroups, uint32_t* out, hipStream_t stream);

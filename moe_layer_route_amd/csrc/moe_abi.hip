@@ -640,6 +640,221 @@ int moe_down_mxfp4(const void* h, const void* Wd_q, const void* Wd_s, const void
 }
 
 // ---------------------------------------------------------------------------
+// 4-bit integer expert weights with group scales
+// ---------------------------------------------------------------------------
+static int check_int4_group(const char* fn, int32_t G) {
+  if (G != 32 && G != 64 && G != 128)
+    return fail(MOE_ERR_INVALID_ARG, "%s: G=%d must be 32, 64 or 128 (values of K per scale)", fn, G);
+  return MOE_OK;
+}
+
+// the contraction dimensions: H of gate_up, I of down, both of the forward
+static int check_int4_dims(const char* fn, const char* name, int32_t K, int32_t G) {
+  if (K % 32 != 0) return fail(MOE_ERR_INVALID_ARG, "%s: %s=%d must be a multiple of 32 (int4 tiles)", fn, name, K);
+  return check_int4_group(fn, G);
+}
+
+static int check_int4_matrix(const char* fn, int32_t E, int32_t K, int32_t N) {
+  if (E < 1 || E > MOE_MAX_E) return fail(MOE_ERR_INVALID_ARG, "%s: E=%d outside [1, %d]", fn, E, MOE_MAX_E);
+  if (K < 32 || K > MOE_MAX_DIM || K % 32 != 0)
+    return fail(MOE_ERR_INVALID_ARG, "%s: K=%d must be a multiple of 32 in [32, %d]", fn, K, MOE_MAX_DIM);
+  if (N < 8 || N > 2 * MOE_MAX_DIM || N % 8 != 0)
+    return fail(MOE_ERR_INVALID_ARG, "%s: N=%d must be a multiple of 8 in [8, %d]", fn, N, 2 * MOE_MAX_DIM);
+  return MOE_OK;
+}
+
+int moe_quantize_int4(const void* W, int32_t E, int32_t K, int32_t N, int32_t G, void* codes, void* scales,
+                      void* zeros, void* stream) {
+  const char* fn = "moe_quantize_int4";
+  if (int st = check_int4_matrix(fn, E, K, N)) return st;
+  if (int st = check_int4_group(fn, G)) return st;
+  CHECK_PTR(W, 2);
+  CHECK_PTR(codes, 16);
+  CHECK_PTR(scales, 2);
+  if (int st = hip_status(fn, moe::launch_int4_quantize(W, E, K, N, G, codes, scales, zeros, (hipStream_t)stream)))
+    return st;
+  return ok();
+}
+
+int moe_pack_int4(const void* codes_kn, int32_t E, int32_t K, int32_t N, void* codes, void* stream) {
+  const char* fn = "moe_pack_int4";
+  if (int st = check_int4_matrix(fn, E, K, N)) return st;
+  CHECK_PTR(codes_kn, 4);
+  CHECK_PTR(codes, 16);
+  if (codes_kn == codes) return fail(MOE_ERR_INVALID_ARG, "%s: codes must not be codes_kn (no packing in place)", fn);
+  if (int st = hip_status(fn, moe::launch_int4_pack(codes_kn, E, K, N, codes, (hipStream_t)stream))) return st;
+  return ok();
+}
+
+static int run_gate_up_int4(const char* fn, const void* x, const void* Wq, const void* Ws, const void* Wz,
+                            const void* bgu, const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T,
+                            int32_t H, int32_t E, int32_t k, int32_t I, int32_t G, void* h, int32_t path,
+                            hipStream_t s) {
+  path = choose_path(path, T, E, k);
+  return hip_status(fn, moe::launch_int4_gate_up(x, Wq, Ws, Wz, bgu, cnt, off, rows, H, E, k, I, G, h, s));
+}
+
+static int run_down_int4(const char* fn, const void* h, const void* Wq, const void* Ws, const void* Wz, const void* bd,
+                         const int32_t* cnt, const int32_t* off, int64_t T, int32_t H, int32_t E, int32_t k, int32_t I,
+                         int32_t G, float* o, int32_t path, hipStream_t s) {
+  path = choose_path(path, T, E, k);
+  return hip_status(fn, moe::launch_int4_down(h, Wq, Ws, Wz, bd, cnt, off, H, E, I, G, o, s));
+}
+
+// The int4 forward; n_valid (device, optional) marks the rows from *n_valid on
+// as padding, expert_counts_out (optional) receives the per-expert loads.
+static int forward_int4(const char* fn, const void* x, const void* Wr, const void* br, const void* Wgu_q,
+                        const void* Wgu_s, const void* Wgu_z, const void* bgu, const void* Wd_q, const void* Wd_s,
+                        const void* Wd_z, const void* bd, int64_t T, int32_t H, int32_t E, int32_t k, int32_t I,
+                        int32_t G, int32_t e_begin, int32_t n_local, const int32_t* n_valid, void* y, bool partial,
+                        int32_t* topk_ids_out, float* topk_w_out, int32_t* expert_counts_out, void* workspace,
+                        size_t workspace_bytes, int32_t path, void* stream) {
+  if (int st = check_dims(fn, T, H, E, k, I)) return st;
+  if (n_local < 1 || e_begin < 0 || e_begin > E - n_local)
+    return fail(MOE_ERR_INVALID_ARG, "%s: local experts [%d, %d + %d) outside [0, E=%d)", fn, e_begin, e_begin,
+                n_local, E);
+  if (int st = check_int4_dims(fn, "H", H, G)) return st;
+  if (int st = check_int4_dims(fn, "I", I, G)) return st;
+  CHECK_PTR(x, 16);
+  CHECK_PTR(Wr, 16);
+  CHECK_PTR(br, 2);
+  CHECK_PTR(Wgu_q, 16);
+  CHECK_PTR(Wgu_s, 16);
+  CHECK_PTR(bgu, 4);
+  CHECK_PTR(Wd_q, 16);
+  CHECK_PTR(Wd_s, 16);
+  CHECK_PTR(bd, 4);
+  CHECK_PTR(y, 16);
+  if (Wgu_z && !aligned(Wgu_z, 8)) return fail(MOE_ERR_INVALID_ARG, "%s: Wgu_z is not 8-byte aligned", fn);
+  if (Wd_z && !aligned(Wd_z, 8)) return fail(MOE_ERR_INVALID_ARG, "%s: Wd_z is not 8-byte aligned", fn);
+  if (topk_ids_out && !aligned(topk_ids_out, 4))
+    return fail(MOE_ERR_INVALID_ARG, "%s: topk_ids_out is not 4-byte aligned", fn);
+  if (topk_w_out && !aligned(topk_w_out, 4))
+    return fail(MOE_ERR_INVALID_ARG, "%s: topk_w_out is not 4-byte aligned", fn);
+  if (n_valid && !aligned(n_valid, 4)) return fail(MOE_ERR_INVALID_ARG, "%s: n_valid is not 4-byte aligned", fn);
+  if (expert_counts_out && !aligned(expert_counts_out, 4))
+    return fail(MOE_ERR_INVALID_ARG, "%s: expert_counts_out is not 4-byte aligned", fn);
+  if (path < MOE_PATH_AUTO || path > MOE_PATH_GEMM)
+    return fail(MOE_ERR_INVALID_ARG, "%s: unknown path %d", fn, path);
+  if (T == 0) return ok();
+  const Layout L = layout(T, H, E, k, I);
+  if (workspace == nullptr || workspace_bytes < L.total)
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace of %zu bytes given, %zu needed", fn,
+                workspace ? workspace_bytes : (size_t)0, L.total);
+  if (!aligned(workspace, 256))
+    return fail(MOE_ERR_INVALID_ARG, "%s: workspace is not 256-byte aligned", fn);
+
+  char* ws = static_cast<char*>(workspace);
+  int32_t* ids = topk_ids_out ? topk_ids_out : reinterpret_cast<int32_t*>(ws + L.ids);
+  float* w = topk_w_out ? topk_w_out : reinterpret_cast<float*>(ws + L.w);
+  int32_t* cnt = expert_counts_out ? expert_counts_out : reinterpret_cast<int32_t*>(ws + L.cnt);
+  int32_t* off = reinterpret_cast<int32_t*>(ws + L.off);
+  int32_t* rows = reinterpret_cast<int32_t*>(ws + L.rows);
+  int32_t* pos = reinterpret_cast<int32_t*>(ws + L.pos);
+  void* h = ws + L.h;
+  float* o = reinterpret_cast<float*>(ws + L.o);
+  hipStream_t s = (hipStream_t)stream;
+  // the expert path follows the whole layer's load per expert, T*k/E
+  path = choose_path(path, T, E, k);
+
+  if (int st = hip_status(fn, moe::launch_route(x, Wr, br, T, H, E, k, ids, w, MOE_ROUTE_AUTO, s))) return st;
+  if (n_valid)
+    if (int st = hip_status(fn, moe::launch_mask_padding(ids, w, T, k, n_valid, s))) return st;
+  if (int st = hip_status(fn, moe::launch_permute(ids, T, n_local, k, cnt, off, rows, pos, s, e_begin))) return st;
+  if (int st = run_gate_up_int4(fn, x, Wgu_q, Wgu_s, Wgu_z, bgu, cnt, off, rows, T, H, n_local, k, I, G, h, path, s))
+    return st;
+  if (int st = run_down_int4(fn, h, Wd_q, Wd_s, Wd_z, bd, cnt, off, T, H, n_local, k, I, G, o, path, s)) return st;
+  if (int st = hip_status(fn, moe::launch_combine(o, pos, w, T, H, k, y, s, partial))) return st;
+  return ok();
+}
+
+int moe_forward_int4_ex(const void* x, const void* Wr, const void* br, const void* Wgu_q, const void* Wgu_s,
+                        const void* Wgu_z, const void* bgu, const void* Wd_q, const void* Wd_s, const void* Wd_z,
+                        const void* bd, int64_t T, int32_t H, int32_t E, int32_t k, int32_t I, int32_t G, void* y,
+                        int32_t* topk_ids_out, float* topk_w_out, void* workspace, size_t workspace_bytes,
+                        int32_t path, void* stream) {
+  return forward_int4("moe_forward_int4", x, Wr, br, Wgu_q, Wgu_s, Wgu_z, bgu, Wd_q, Wd_s, Wd_z, bd, T, H, E, k, I, G,
+                      0, E, nullptr, y, false, topk_ids_out, topk_w_out, nullptr, workspace, workspace_bytes, path,
+                      stream);
+}
+
+int moe_forward_int4(const void* x, const void* Wr, const void* br, const void* Wgu_q, const void* Wgu_s,
+                     const void* Wgu_z, const void* bgu, const void* Wd_q, const void* Wd_s, const void* Wd_z,
+                     const void* bd, int64_t T, int32_t H, int32_t E, int32_t k, int32_t I, int32_t G, void* y,
+                     int32_t* topk_ids_out, float* topk_w_out, void* workspace, size_t workspace_bytes, void* stream) {
+  return moe_forward_int4_ex(x, Wr, br, Wgu_q, Wgu_s, Wgu_z, bgu, Wd_q, Wd_s, Wd_z, bd, T, H, E, k, I, G, y,
+                             topk_ids_out, topk_w_out, workspace, workspace_bytes, MOE_PATH_AUTO, stream);
+}
+
+int moe_forward_padded_int4(const void* x, const void* Wr, const void* br, const void* Wgu_q, const void* Wgu_s,
+                            const void* Wgu_z, const void* bgu, const void* Wd_q, const void* Wd_s, const void* Wd_z,
+                            const void* bd, int64_t T, int32_t H, int32_t E, int32_t k, int32_t I, int32_t G,
+                            const int32_t* n_valid, void* y, int32_t* topk_ids_out, float* topk_w_out,
+                            int32_t* expert_counts_out, void* workspace, size_t workspace_bytes, int32_t path,
+                            void* stream) {
+  return forward_int4("moe_forward_padded_int4", x, Wr, br, Wgu_q, Wgu_s, Wgu_z, bgu, Wd_q, Wd_s, Wd_z, bd, T, H, E, k,
+                      I, G, 0, E, n_valid, y, false, topk_ids_out, topk_w_out, expert_counts_out, workspace,
+                      workspace_bytes, path, stream);
+}
+
+int moe_forward_ep_int4(const void* x, const void* Wr, const void* br, const void* Wgu_q_local,
+                        const void* Wgu_s_local, const void* Wgu_z_local, const void* bgu_local,
+                        const void* Wd_q_local, const void* Wd_s_local, const void* Wd_z_local, const void* bd_local,
+                        int64_t T, int32_t H, int32_t E, int32_t k, int32_t I, int32_t G, int32_t e_begin,
+                        int32_t n_local, float* y_partial, int32_t* topk_ids_out, float* topk_w_out, void* workspace,
+                        size_t workspace_bytes, int32_t path, void* stream) {
+  return forward_int4("moe_forward_ep_int4", x, Wr, br, Wgu_q_local, Wgu_s_local, Wgu_z_local, bgu_local, Wd_q_local,
+                      Wd_s_local, Wd_z_local, bd_local, T, H, E, k, I, G, e_begin, n_local, nullptr, y_partial, true,
+                      topk_ids_out, topk_w_out, nullptr, workspace, workspace_bytes, path, stream);
+}
+
+int moe_gate_up_int4(const void* x, const void* Wgu_q, const void* Wgu_s, const void* Wgu_z, const void* bgu,
+                     const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T, int32_t H, int32_t E,
+                     int32_t k, int32_t I, int32_t G, void* h, int32_t path, void* stream) {
+  const char* fn = "moe_gate_up_int4";
+  if (int st = check_dims(fn, T, H, E, k, I)) return st;
+  if (int st = check_int4_dims(fn, "H", H, G)) return st;
+  CHECK_PTR(x, 16);
+  CHECK_PTR(Wgu_q, 16);
+  CHECK_PTR(Wgu_s, 16);
+  if (Wgu_z && !aligned(Wgu_z, 8)) return fail(MOE_ERR_INVALID_ARG, "%s: Wgu_z is not 8-byte aligned", fn);
+  CHECK_PTR(bgu, 4);
+  CHECK_PTR(cnt, 4);
+  CHECK_PTR(off, 4);
+  CHECK_PTR(rows, 4);
+  CHECK_PTR(h, 16);
+  if (path < MOE_PATH_AUTO || path > MOE_PATH_GEMM)
+    return fail(MOE_ERR_INVALID_ARG, "%s: unknown path %d", fn, path);
+  if (T == 0) return ok();
+  if (int st = run_gate_up_int4(fn, x, Wgu_q, Wgu_s, Wgu_z, bgu, cnt, off, rows, T, H, E, k, I, G, h, path,
+                                (hipStream_t)stream))
+    return st;
+  return ok();
+}
+
+int moe_down_int4(const void* h, const void* Wd_q, const void* Wd_s, const void* Wd_z, const void* bd,
+                  const int32_t* cnt, const int32_t* off, int64_t T, int32_t H, int32_t E, int32_t k, int32_t I,
+                  int32_t G, float* o, int32_t path, void* stream) {
+  const char* fn = "moe_down_int4";
+  if (int st = check_dims(fn, T, H, E, k, I)) return st;
+  if (int st = check_int4_dims(fn, "I", I, G)) return st;
+  CHECK_PTR(h, 16);
+  CHECK_PTR(Wd_q, 16);
+  CHECK_PTR(Wd_s, 16);
+  if (Wd_z && !aligned(Wd_z, 8)) return fail(MOE_ERR_INVALID_ARG, "%s: Wd_z is not 8-byte aligned", fn);
+  CHECK_PTR(bd, 4);
+  CHECK_PTR(cnt, 4);
+  CHECK_PTR(off, 4);
+  CHECK_PTR(o, 16);
+  if (path < MOE_PATH_AUTO || path > MOE_PATH_GEMM)
+    return fail(MOE_ERR_INVALID_ARG, "%s: unknown path %d", fn, path);
+  if (T == 0) return ok();
+  if (int st = run_down_int4(fn, h, Wd_q, Wd_s, Wd_z, bd, cnt, off, T, H, E, k, I, G, o, path, (hipStream_t)stream))
+    return st;
+  return ok();
+}
+
+// ---------------------------------------------------------------------------
 // FP8 W8A8
 // ---------------------------------------------------------------------------
 static int check_fp8_dims(const char* fn, int32_t H, int32_t I) {
@@ -665,6 +880,9 @@ static Fp8Layout fp8_layout(int64_t T, int32_t H, int32_t E, int32_t k, int32_t 
   F.total = cur;
   return F;
 }
+
+// the normalised bf16 rows, behind the FP8 layout
+static size_t norm_bytes(int64_t T, int32_t H) { return ((size_t)T * H * 2 + 255) & ~(size_t)255; }
 
 size_t moe_workspace_bytes_fp8(int64_t T, int32_t H, int32_t E, int32_t k, int32_t I) {
   if (check_dims("moe_workspace_bytes_fp8", T, H, E, k, I) != MOE_OK) return 0;
@@ -720,14 +938,23 @@ static int run_down_fp8(const char* fn, const void* hq, const float* sh, const v
   return fail(MOE_ERR_INVALID_ARG, "%s: unknown path %d", fn, path);
 }
 
+// The residual addition and norm that moe_forward_norm_fp8 puts ahead of the
+// block: x is then the rows before the norm.
+struct NormIn {
+  const void *residual, *gamma;
+  float eps;
+  void* residual_out;
+};
+
 // The FP8 forward; n_valid (device, optional) marks the rows from *n_valid on
-// as padding, expert_counts_out (optional) receives the per-expert loads.
+// as padding, expert_counts_out (optional) receives the per-expert loads; norm
+// (optional) runs first and hands the block its rows and their codes.
 static int forward_fp8(const char* fn, const void* x, const void* Wr, const void* br, const void* Wgu_q,
                        const float* Wgu_s, const void* bgu, const void* Wd_q, const float* Wd_s, const void* bd,
                        int64_t T, int32_t H, int32_t E, int32_t k, int32_t I, int32_t e_begin, int32_t n_local,
                          const int32_t* n_valid, void* y, bool partial,
                        int32_t* topk_ids_out, float* topk_w_out, int32_t* expert_counts_out, void* workspace,
-                       size_t workspace_bytes, int32_t path, void* stream) {
+                       size_t workspace_bytes, int32_t path, void* stream, const NormIn* norm = nullptr) {
   if (int st = check_dims(fn, T, H, E, k, I)) return st;
   if (n_local < 1 || e_begin < 0 || e_begin > E - n_local)
     return fail(MOE_ERR_INVALID_ARG, "%s: local experts [%d, %d + %d) outside [0, E=%d)", fn, e_begin, e_begin,
@@ -754,9 +981,10 @@ static int forward_fp8(const char* fn, const void* x, const void* Wr, const void
     return fail(MOE_ERR_INVALID_ARG, "%s: unknown path %d", fn, path);
   if (T == 0) return ok();
   const Fp8Layout F = fp8_layout(T, H, E, k, I);
-  if (workspace == nullptr || workspace_bytes < F.total)
+  const size_t need = F.total + (norm ? norm_bytes(T, H) : 0);
+  if (workspace == nullptr || workspace_bytes < need)
     return fail(MOE_ERR_WORKSPACE, "%s: workspace of %zu bytes given, %zu needed", fn,
-                workspace ? workspace_bytes : (size_t)0, F.total);
+                workspace ? workspace_bytes : (size_t)0, need);
   if (!aligned(workspace, 256))
     return fail(MOE_ERR_INVALID_ARG, "%s: workspace is not 256-byte aligned", fn);
 
@@ -779,11 +1007,19 @@ static int forward_fp8(const char* fn, const void* x, const void* Wr, const void
   path = choose_path(path, T, E, k);
   const int64_t S = T * k;
 
+  if (norm) {
+    void* xn = ws + F.total;
+    if (int st = hip_status(fn, moe::launch_add_rmsnorm(x, norm->residual, norm->gamma, T, H, norm->eps,
+                                                        norm->residual_out, xn, xq, sx, s)))
+      return st;
+    x = xn;
+  }
   if (int st = hip_status(fn, moe::launch_route(x, Wr, br, T, H, E, k, ids, w, MOE_ROUTE_AUTO, s))) return st;
   if (n_valid)
     if (int st = hip_status(fn, moe::launch_mask_padding(ids, w, T, k, n_valid, s))) return st;
   if (int st = hip_status(fn, moe::launch_permute(ids, T, n_local, k, cnt, off, rows, pos, s, e_begin))) return st;
-  if (int st = hip_status(fn, moe::launch_fp8_quantize_rows(x, T, H, xq, sx, s))) return st;
+  if (!norm)
+    if (int st = hip_status(fn, moe::launch_fp8_quantize_rows(x, T, H, xq, sx, s))) return st;
   if (int st = run_gate_up_fp8(fn, xq, sx, Wgu_q, Wgu_s, bgu, cnt, off, rows, T, H, n_local, k, I, h, path, s)) return st;
   // only the rows of h the permutation filled (off[n_local] of them; fewer
   // than T*k with padding rows or on an expert-parallel rank)
@@ -873,6 +1109,100 @@ int moe_down_fp8(const void* hq, const float* sh, const void* Wd_q, const float*
   if (int st = run_down_fp8(fn, hq, sh, Wd_q, Wd_s, bd, cnt, off, T, H, E, k, I, o, path, (hipStream_t)stream))
     return st;
   return ok();
+}
+
+// ---------------------------------------------------------------------------
+// Residual addition and RMS norm
+// ---------------------------------------------------------------------------
+static bool disjoint(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x + an <= y || y + bn <= x;
+}
+
+// Sizes, pointers and overlaps of the norm (x, residual, gamma in;
+// residual_out, y, codes, scales out; the optional ones null).
+static int check_norm(const char* fn, const void* x, const void* residual, const void* gamma, int64_t T, int32_t H,
+                      float eps, const void* residual_out, const void* y, const void* codes, const void* scales) {
+  if (T < 0 || T >= (int64_t)1 << 31)
+    return fail(MOE_ERR_INVALID_ARG, "%s: T=%lld outside [0, 2^31)", fn, (long long)T);
+  const int step = codes ? 16 : 8;
+  if (H < step || H > MOE_MAX_DIM || H % step != 0)
+    return fail(MOE_ERR_INVALID_ARG, "%s: H=%d must be a multiple of %d in [%d, %d]", fn, H, step, step, MOE_MAX_DIM);
+  if (!(eps > 0.0f) || eps > 3.4e38f) return fail(MOE_ERR_INVALID_ARG, "%s: eps=%g must be finite and above 0", fn, eps);
+  CHECK_PTR(x, 16);
+  CHECK_PTR(gamma, 16);
+  if ((residual == nullptr) != (residual_out == nullptr))
+    return fail(MOE_ERR_INVALID_ARG, "%s: residual and residual_out are both given or both NULL", fn);
+  if (residual) CHECK_PTR(residual, 16);
+  if (residual_out) CHECK_PTR(residual_out, 16);
+  const size_t rows = (size_t)T * H * 2;
+  const struct { const char* name; const void* p; size_t n; bool in_place; } outs[] = {
+      {"residual_out", residual_out, rows, true}, {"y", y, rows, true},
+      {"codes", codes, (size_t)T * H, false}, {"scales", scales, (size_t)T * 4, false}};
+  const struct { const char* name; const void* p; size_t n; } ins[] = {
+      {"x", x, rows}, {"residual", residual, rows}, {"gamma", gamma, (size_t)H * 2}};
+  for (int i = 0; i < 4; ++i) {
+    if (!outs[i].p) continue;
+    for (int j = 0; j < 3; ++j)
+      if (ins[j].p && !disjoint(outs[i].p, outs[i].n, ins[j].p, ins[j].n) &&
+          !(outs[i].in_place && j < 2 && outs[i].p == ins[j].p))
+        return fail(MOE_ERR_INVALID_ARG, "%s: %s overlaps %s", fn, outs[i].name, ins[j].name);
+    for (int j = 0; j < i; ++j)
+      if (outs[j].p && !disjoint(outs[i].p, outs[i].n, outs[j].p, outs[j].n))
+        return fail(MOE_ERR_INVALID_ARG, "%s: %s overlaps %s", fn, outs[i].name, outs[j].name);
+  }
+  return MOE_OK;
+}
+
+int moe_add_rmsnorm(const void* x, const void* residual, const void* gamma, int64_t T, int32_t H, float eps,
+                    void* residual_out, void* y, void* stream) {
+  const char* fn = "moe_add_rmsnorm";
+  CHECK_PTR(y, 16);
+  if (int st = check_norm(fn, x, residual, gamma, T, H, eps, residual_out, y, nullptr, nullptr)) return st;
+  if (T == 0) return ok();
+  if (int st = hip_status(fn, moe::launch_add_rmsnorm(x, residual, gamma, T, H, eps, residual_out, y, nullptr, nullptr,
+                                                      (hipStream_t)stream)))
+    return st;
+  return ok();
+}
+
+int moe_add_rmsnorm_fp8(const void* x, const void* residual, const void* gamma, int64_t T, int32_t H, float eps,
+                        void* residual_out, void* y, void* codes, float* scales, void* stream) {
+  const char* fn = "moe_add_rmsnorm_fp8";
+  if (y) CHECK_PTR(y, 16);
+  CHECK_PTR(codes, 16);
+  CHECK_PTR(scales, 4);
+  if (int st = check_norm(fn, x, residual, gamma, T, H, eps, residual_out, y, codes, scales)) return st;
+  if (T == 0) return ok();
+  if (int st = hip_status(fn, moe::launch_add_rmsnorm(x, residual, gamma, T, H, eps, residual_out, y, codes, scales,
+                                                      (hipStream_t)stream)))
+    return st;
+  return ok();
+}
+
+size_t moe_workspace_bytes_norm_fp8(int64_t T, int32_t H, int32_t E, int32_t k, int32_t I) {
+  if (check_dims("moe_workspace_bytes_norm_fp8", T, H, E, k, I) != MOE_OK) return 0;
+  if (T == 0) return 0;
+  return fp8_layout(T, H, E, k, I).total + norm_bytes(T, H);
+}
+
+int moe_forward_norm_fp8(const void* x, const void* residual, const void* gamma, float eps, const void* Wr,
+                         const void* br, const void* Wgu_q, const float* Wgu_s, const void* bgu, const void* Wd_q,
+                         const float* Wd_s, const void* bd, int64_t T, int32_t H, int32_t E, int32_t k, int32_t I,
+                         void* residual_out, void* y, int32_t* topk_ids_out, float* topk_w_out, void* workspace,
+                         size_t workspace_bytes, int32_t path, void* stream) {
+  const char* fn = "moe_forward_norm_fp8";
+  if (int st = check_dims(fn, T, H, E, k, I)) return st;
+  CHECK_PTR(y, 16);
+  if (int st = check_norm(fn, x, residual, gamma, T, H, eps, residual_out, nullptr, nullptr, nullptr)) return st;
+  // y is written by the last launch: it may be the buffer of x or residual,
+  // which only the first one reads, but would destroy residual_out
+  const size_t rows = (size_t)T * H * 2;
+  if (residual_out && !disjoint(y, rows, residual_out, rows))
+    return fail(MOE_ERR_INVALID_ARG, "%s: y overlaps residual_out", fn);
+  const NormIn norm{residual, gamma, eps, residual_out};
+  return forward_fp8(fn, x, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, T, H, E, k, I, 0, E, nullptr, y, false,
+                     topk_ids_out, topk_w_out, nullptr, workspace, workspace_bytes, path, stream, &norm);
 }
 
 // ---------------------------------------------------------------------------

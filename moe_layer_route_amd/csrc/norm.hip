@@ -1,0 +1,175 @@
+// Residual addition and RMS norm ahead of the block, with the normalised rows
+// in bf16 (the router's and the bf16/4-bit experts' input) and, for the FP8
+// experts, as E4M3 codes with one scale per row.
+//
+// xserv "Phase 19: gpt-oss-20b MoE support", section 2 (the block runs on the
+// normalised hidden state) and section 5 (FP8 activations with dynamic
+// scales).  Per row t of H values:
+//   r = bf16(x + residual)            (r = x without a residual)
+//   inv = float32(1 / sqrt(sum_h r[h]^2 / H + eps)), the sum in float64: the
+//         squares of bf16 values are exact there, so the result does not
+//         depend on how a row is split over lanes, beyond the last bit of a
+//         float64 sum
+//   v = (r * inv) * gamma             (float32, each product rounded)
+//   y = bf16(v)
+//   s = max|v| / 448, code = E4M3(v * (448 / max|v|)): from the float32 values,
+//         not from y, so a code carries one rounding and not two.
+//
+// It is a stream: x and residual are read once, r, y and the codes written
+// once, the row stays in registers between the two reductions.
+#include "device_common.h"
+#include "launch.h"
+
+namespace moe {
+namespace {
+
+constexpr float kE4m3Max = 448.0f;
+
+// E4M3 code of v, nearest with ties to even, saturated at 448, NaN -> 0x7F:
+// with e = max(exponent, -6), q = rint(|v| * 2^(3-e)) counts quanta of
+// 2^(e-3), and the code is (e + 6) * 8 + q (q = 16 carries into the next
+// binade).  Rows whose scale is not an ordinary number take this path.
+__device__ __forceinline__ uint32_t e4m3_any(float v) {
+  const uint32_t sign = (__float_as_uint(v) >> 24) & 0x80u;
+  const float a = fminf(fabsf(v), kE4m3Max);
+  const int e = max((int)(__float_as_uint(a) >> 23) - 127, -6);
+  const uint32_t q = (uint32_t)__builtin_rintf(__builtin_amdgcn_ldexpf(a, 3 - e));
+  const uint32_t code = sign | (uint32_t)((e + 6) * 8 + (int)q);
+  return v != v ? 0x7Fu : code;
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) v += __shfl_xor(v, d, kWave);
+  return v;
+}
+
+__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, d, kWave));
+  return v;
+}
+
+constexpr int kNormMaxWaves = 16;
+
+// One row per workgroup; thread i holds the 16-byte pieces i, i + blockDim,
+// ... (P of them).  x, residual, residual_out and y carry no __restrict__: an
+// output may be the very buffer of an input, and a thread reads all its
+// pieces before it writes any.
+template <int P, bool RES, bool FP8>
+__global__ __launch_bounds__(P <= 2 ? 1024 : (P <= 4 ? 512 : 256)) void add_rmsnorm_kernel(
+    const bf16_t* x, const bf16_t* residual, const bf16_t* __restrict__ gamma, int H, double eps, bf16_t* residual_out,
+    bf16_t* y, uint8_t* __restrict__ codes, float* __restrict__ scales) {
+  __shared__ double s_sum[kNormMaxWaves];
+  __shared__ uint32_t s_max[kNormMaxWaves];
+  const int np = H / 8;
+  const int tid = threadIdx.x, nt = blockDim.x;
+  const int wave = tid / kWave, lane = tid & (kWave - 1), waves = nt / kWave;
+  const size_t base = (size_t)blockIdx.x * (size_t)H;
+  const u32x4_t zero = u32x4_t{0u, 0u, 0u, 0u};
+
+  u32x4_t r[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int i = tid + p * nt;
+    r[p] = i < np ? *reinterpret_cast<const u32x4_t*>(x + base + 8 * (size_t)i) : zero;
+  }
+  if (RES) {
+    u32x4_t a[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int i = tid + p * nt;
+      a[p] = i < np ? *reinterpret_cast<const u32x4_t*>(residual + base + 8 * (size_t)i) : zero;
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        r[p][q] = pack_bf16x2(bf16lo(r[p][q]) + bf16lo(a[p][q]), bf16hi(r[p][q]) + bf16hi(a[p][q]));
+  }
+  double ss = 0.0;
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const double lo = bf16lo(r[p][q]), hi = bf16hi(r[p][q]);
+      ss = __builtin_fma(lo, lo, ss);
+      ss = __builtin_fma(hi, hi, ss);
+    }
+  ss = wave_sum(ss);
+  if (waves > 1) {
+    if (lane == 0) s_sum[wave] = ss;
+    __syncthreads();
+    ss = 0.0;
+    for (int w = 0; w < waves; ++w) ss += s_sum[w];
+  }
+  const float inv = (float)(1.0 / sqrt(ss / (double)H + eps));
+
+  float v[P][8];
+  uint32_t m = 0;
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int i = tid + p * nt;
+    const u32x4_t g = i < np ? *reinterpret_cast<const u32x4_t*>(gamma + 8 * (size_t)i) : zero;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v[p][2 * q] = (bf16lo(r[p][q]) * inv) * bf16lo(g[q]);
+      v[p][2 * q + 1] = (bf16hi(r[p][q]) * inv) * bf16hi(g[q]);
+    }
+    if (i < np) {
+      if (RES) *reinterpret_cast<u32x4_t*>(residual_out + base + 8 * (size_t)i) = r[p];
+      if (!FP8 || y != nullptr)
+        *reinterpret_cast<u32x4_t*>(y + base + 8 * (size_t)i) =
+            u32x4_t{pack_bf16x2(v[p][0], v[p][1]), pack_bf16x2(v[p][2], v[p][3]), pack_bf16x2(v[p][4], v[p][5]),
+                    pack_bf16x2(v[p][6], v[p][7])};
+      // the maximum on the bit patterns: a NaN compares above every number
+      if (FP8)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) m = max(m, __float_as_uint(v[p][q]) & 0x7FFFFFFFu);
+    }
+  }
+  if (!FP8) return;
+  m = wave_umax(m);
+  if (waves > 1) {
+    if (lane == 0) s_max[wave] = m;
+    __syncthreads();
+    m = 0;
+    for (int w = 0; w < waves; ++w) m = max(m, s_max[w]);
+  }
+  const float amax = __uint_as_float(m);
+  const float s = m == 0 ? 1.0f : __fdiv_rn(amax, kE4m3Max);
+  const float up = m == 0 ? 1.0f : __fdiv_rn(kE4m3Max, amax);
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int i = tid + p * nt;
+    uint32_t c[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) c[q] = e4m3_any(v[p][q] * up);
+    if (i < np)
+      *reinterpret_cast<u32x2_t*>(codes + base + 8 * (size_t)i) =
+          u32x2_t{c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24};
+  }
+  if (tid == 0) scales[blockIdx.x] = s;
+}
+
+template <int P>
+hipError_t launch_p(const void* x, const void* residual, const void* gamma, int64_t T, int H, float eps,
+                    void* residual_out, void* y, void* codes, float* scales, hipStream_t stream) {
+  const int np = H / 8;
+  const int waves = (np + kWave * P - 1) / (kWave * P);
+  auto kern = residual ? (codes ? add_rmsnorm_kernel<P, true, true> : add_rmsnorm_kernel<P, true, false>)
+                       : (codes ? add_rmsnorm_kernel<P, false, true> : add_rmsnorm_kernel<P, false, false>);
+  hipLaunchKernelGGL(kern, dim3((unsigned)T), dim3(waves * kWave), 0, stream, (const bf16_t*)x, (const bf16_t*)residual,
+                     (const bf16_t*)gamma, H, (double)eps, (bf16_t*)residual_out, (bf16_t*)y, (uint8_t*)codes, scales);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// H <= 16384 is 2048 pieces: P = 2 needs at most 16 waves a row.
+hipError_t launch_add_rmsnorm(const void* x, const void* residual, const void* gamma, int64_t T, int H, float eps,
+                              void* residual_out, void* y, void* codes, float* scales, hipStream_t stream) {
+  return launch_p<2>(x, residual, gamma, T, H, eps, residual_out, y, codes, scales, stream);
+}
+
+}  // namespace moe

@@ -416,14 +416,15 @@ def fp8_down(hb, Wd_q_e, s_d_e, bd_e64):
 
 
 def moe_forward_fp8(x, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, k: int, tokens=None, keep=False,
-                    experts=None):
+                    experts=None, rows=None):
     """The forward with FP8 W8A8 experts: gate_up codes [E][2I][H] with scales
     [E], down codes [E][H][I] with scales [E].  x rows are quantised per token
     (F4), h rows per (token, slot) after rounding to bf16 (F5).  Returns what
-    moe_forward returns, plus (keep) the h codes and scales per slot."""
+    moe_forward returns, plus (keep) the h codes and scales per slot.  rows:
+    the x codes and scales, where they are not those of x (N3)."""
     sel = slice(None) if tokens is None else np.asarray(tokens)
     ids, w, lg = route(x[sel], Wr, br, k)
-    xq, sx = fp8_quantize_rows(widen(x[sel]))
+    xq, sx = fp8_quantize_rows(widen(x[sel])) if rows is None else rows
     T = xq.shape[0]
     E, I2, Hout = Wr.shape[0], Wgu_q.shape[1], Wd_q.shape[1]
     y = np.zeros((T, Hout))
@@ -448,6 +449,104 @@ def moe_forward_fp8(x, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, k: int, tokens
     out = {"y": y, "ids": ids, "w": w, "logits": lg, "sx": sx}
     if keep:
         out.update(u=u_all, h=h_all, o=o_all, hq=hq_all, sh=sh_all, xq=xq)
+    return out
+
+
+# --------------------------------------------------------------------------
+# Residual addition and RMS norm ahead of the block (section 2: the block runs
+# on the normalised hidden state), and the FP8 codes of its rows.
+#   N1  the new residual stream is bf16(x + residual), the float32 sum rounded;
+#   N2  1 / rms is rounded to float32, its products with r and gamma are
+#       rounded to float32 one by one; y is their bf16 rounding;
+#   N3  FP8 codes and scales come from those float32 values (F2, F4).
+# --------------------------------------------------------------------------
+def add_rmsnorm(x, residual, gamma, eps: float):
+    """bf16 bits x, residual (or None) [T][H], gamma [H] -> (y, r, v): y and r as
+    float64 values of bf16, v the float32 values before y's rounding."""
+    r = widen(x)
+    if residual is not None:
+        r = bf16_round((r.astype(np.float32) + widen(residual).astype(np.float32)).astype(np.float64))
+    with np.errstate(invalid="ignore", over="ignore"):
+        inv = (1.0 / np.sqrt((r * r).mean(axis=1, keepdims=True) + float(np.float32(eps)))).astype(np.float32)
+        v = (r.astype(np.float32) * inv) * widen(gamma).astype(np.float32)
+    return bf16_round(v.astype(np.float64)), r, v
+
+
+# --------------------------------------------------------------------------
+# 4-bit integer weights with group scales (section 5: 4-bit expert weights).
+#   I1  a weight is (q - z) * s, q in 0..15, s bf16 and z (8 without zero
+#       points) per group of G values of K in a column, the last group shorter;
+#   I2  stored order: tiles of 64 columns x 32 values of K, in 256 words of 32
+#       bits; word 4 (16 g + c) + j holds column 4 c + j, K = 8 g .. 8 g + 7,
+#       value i at bit (3 + 4 (i // 2) + 16 (i % 2)) mod 32 (wrapping round);
+#   I3  quantiser: round to nearest even in float32, s = bf16(max|v| / 7), or
+#       bf16(hi / 15 - lo / 15) and z = rint(-lo / s) with zero points.
+# --------------------------------------------------------------------------
+def int4_pack(q: np.ndarray) -> np.ndarray:
+    """q uint8 [E][K][N] -> tiles uint8 [E][ceil(N/64)][K/32][1024] (columns past N hold 0)."""
+    E, K, N = q.shape
+    nt = -(-N // 64)
+    out = np.zeros((E, nt, K // 32, 256), np.uint32)
+    for n in range(N):
+        c, j = (n % 64) // 4, n % 4
+        for g in range(4):
+            w = np.zeros((E, K // 32), np.uint64)
+            for i in range(8):
+                at = (3 + 4 * (i // 2) + 16 * (i % 2)) % 32
+                w |= q[:, 8 * g + i::32, n].astype(np.uint64) << np.uint64(at)
+            out[:, n // 64, :, 4 * (16 * g + c) + j] = ((w | (w >> np.uint64(32))) & np.uint64(0xFFFFFFFF)).astype(np.uint32)
+    return out.view(np.uint8).reshape(E, nt, K // 32, 1024)
+
+
+def int4_dequantize(q, s, z, G: int) -> np.ndarray:
+    """Plain codes q [K][N], scales s (bf16 bits) and zero points z (or None) [ceil(K/G)][N] -> float64 [K][N]."""
+    group = np.arange(q.shape[0]) // G
+    zero = 8.0 if z is None else z.astype(np.float64)[group]
+    return (q.astype(np.float64) - zero) * widen(s)[group]
+
+
+def int4_quantize(W, G: int, zeros: bool):
+    """bf16 bits W [E][K][N] -> (q uint8 [E][K][N], s bf16 bits, z uint8 or None [E][ceil(K/G)][N])."""
+    w = widen(W).astype(np.float32)
+    E, K, N = w.shape
+    ng = -(-K // G)
+    q = np.zeros((E, K, N), np.uint8)
+    s = np.zeros((E, ng, N), np.uint16)
+    z = np.zeros((E, ng, N), np.uint8) if zeros else None
+    f = np.float32
+    for b in range(ng):
+        v = w[:, b * G:(b + 1) * G]
+        lo, hi = np.minimum(v.min(axis=1), f(0)), np.abs(np.maximum(v.max(axis=1), f(0)))
+        want = hi / f(15) - lo / f(15) if zeros else np.maximum(hi, np.abs(lo)) / f(7)
+        sv = bf16_round(want.astype(np.float64)).astype(np.float32)
+        s[:, b] = (sv.view(np.uint32) >> 16).astype(np.uint16)
+        safe = np.where(sv == 0, f(1), sv)
+        zv = np.where(sv == 0, f(0), np.clip(np.rint(-lo / safe), 0, 15)) if zeros else np.full_like(sv, 8)
+        if zeros:
+            z[:, b] = zv.astype(np.uint8)
+        qv = np.clip(np.rint(v / safe[:, None]) + zv[:, None], 0, 15)
+        q[:, b * G:(b + 1) * G] = np.where(sv[:, None] == 0, zv[:, None], qv).astype(np.uint8)
+    return q, s, z
+
+
+def moe_forward_int4(x, Wr, br, gu, bgu, down, bd, k: int, G: int, tokens=None, keep=False, experts=None):
+    """The forward with int4 expert weights: gu and down are (plain codes
+    [E][K][N], scales, zero points or None); the weights are dequantised
+    exactly and the rest is moe_forward."""
+    def weights(e):
+        def one(m):
+            return int4_dequantize(m[0][e], m[1][e], None if m[2] is None else m[2][e], G)
+        return one(gu), widen(bgu[e]), one(down), widen(bd[e])
+    return _forward(x, Wr, br, weights, gu[0].shape[2], down[0].shape[2], k, tokens, keep, experts)
+
+
+def moe_forward_norm_fp8(x, residual, gamma, eps, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, k: int):
+    """add_rmsnorm and the FP8 forward on its rows: the router reads y, the
+    experts the codes of the unrounded rows (N3)."""
+    y, r, v = add_rmsnorm(x, residual, gamma, eps)
+    bits = (y.astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
+    out = moe_forward_fp8(bits, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, k, rows=fp8_quantize_rows(v))
+    out["residual"] = r
     return out
 
 

@@ -1,0 +1,360 @@
+"""Expert products with 4-bit integer weights and group scales against the
+float64 oracle (needs an MI355X).  Every call goes through the C ABI.
+
+Tolerance of a product (before bias and GLU), derived: the integers, zero
+points and bf16 activations are exact operands, so the errors are float32
+accumulation, in two places.
+ - Inside a group of G values, sums whose terms are at most
+   |a| (16 + q) + |a| (16 + z) in total (the operands are 16 + q, and
+   (16 + z) times the sum of a is taken off).  One v_mfma_f32_16x16x32 step
+   accumulates within 128 / 90 u of the sum of its terms' magnitudes (the
+   bound the MFMA router rests on, which tests/test_gpu_router_bound.py
+   measures), u = 2^-24; a group is at most 4 steps and as many for the sum
+   of a, and its parts meet in at most 4 more operations: 16 u.
+ - Over groups: at most ceil(K/G) + 8 float32 operations on partial sums that
+   the sum of |a w| bounds, each off by u.
+A GLU with gate <= 7 and |up + 1| <= 8 has slopes of at most 8.8 in gate (1.1,
+the largest slope of g sigmoid(1.702 g), times 8) and 7 in up; the hardware
+exponential and reciprocal are within 2^-20 of h; h is rounded to bf16, half a
+step of which is 2^-8 of the value.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from moe_layer_route_amd import binding, datagen as d  # noqa: E402
+import oracle.moe_oracle as orc  # noqa: E402
+from checks import assert_nan_rows, assert_routing, assert_y_close, bf16_bits, dev, host_f64  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+PATHS = ["gemv", "gemm"]
+
+
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def _up(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda() if a.dtype != np.uint16 else dev(a)
+
+
+def _matrix(E, K, N, G, zeros, seed):
+    """Plain codes [E][K][N], scales (bf16 bits) and zero points; a few groups with scale 0 and codes at the ends."""
+    rng = np.random.default_rng([seed, E, K, N, G])
+    ng = -(-K // G)
+    q = rng.integers(0, 16, (E, K, N), dtype=np.uint8)
+    q[:, :, 0], q[:, :, 1] = 15, 0
+    s = d.f32_to_bf16_bits((0.02 / 4.6 * 2.0 ** rng.uniform(-1, 1, (E, ng, N))).astype(np.float32))
+    s[:, -1, 2] = 0
+    z = rng.integers(0, 16, (E, ng, N), dtype=np.uint8) if zeros else None
+    return q, s, z
+
+
+def _gpu(m):
+    q, s, z = m
+    return torch.from_numpy(orc.int4_pack(q)).cuda(), dev(s), None if z is None else torch.from_numpy(z).cuda()
+
+
+def _bound(a, m, e, G):
+    """Error bound of a @ W[e] as derived above, and the exact product."""
+    q, s, z = m
+    W = orc.int4_dequantize(q[e], s[e], None if z is None else z[e], G)
+    group = np.arange(q.shape[1]) // G
+    big = (32.0 + q[e] + (8.0 if z is None else z[e].astype(np.float64)[group])) * np.abs(orc.widen(s[e]))[group]
+    return a @ W, 16 * U * (np.abs(a) @ big) + (len(s[e]) + 8) * U * (np.abs(a) @ np.abs(W))
+
+
+def _assert_within(got, want, tol, what):
+    bad = np.argwhere(~(np.abs(got - want) <= tol))
+    assert bad.size == 0, (f"{what}: {len(bad)} of {got.size} off, first {bad[0].tolist()}: {got[tuple(bad[0])]} for "
+                           f"{want[tuple(bad[0])]} +- {tol[tuple(bad[0])]}")
+
+
+def _routing(T, E, k, seed, live=None):
+    """ids [T][k], all different in a row, among the first `live` experts."""
+    rng = np.random.default_rng([seed, T, E])
+    return np.stack([rng.permutation(live or E)[:k] for _ in range(T)]).astype(np.int32)
+
+
+# T, E, k, K (H or I), columns (2I or H), live experts
+STAGES = [
+    (1, 4, 1, 32, 16, None),       # one token, one tile of K, a quarter of a tile of columns
+    (3, 8, 2, 96, 80, None),       # three tiles of K: a ragged group of 64, a lone one of 128
+    (16, 2, 1, 160, 64, None),     # about eight rows an expert
+    (17, 1, 1, 288, 128, None),    # 17 rows: one past a 16-row operand
+    (33, 3, 2, 2880, 72, 2),       # full K, 33 rows: a third chunk; an expert without rows
+    (100, 4, 2, 352, 208, None),   # 50 rows an expert
+    (70, 2, 2, 64, 2880, None),    # full width, 70 rows
+    (300, 1, 1, 128, 96, None),    # 300 rows of one expert
+    (40, 40, 8, 224, 136, 30),     # many experts, k = 8
+    (129, 5, 4, 1440, 144, None),  # 103 rows an expert, K = 11.25 groups of 128
+]
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("G", [32, 64, 128])
+@pytest.mark.parametrize("T,E,k,K,N,live", STAGES)
+def test_down(T, E, k, K, N, live, G, zeros, path):
+    _need_gpu()
+    m = _matrix(E, K, N, G, zeros, 1)
+    q, s, z = _gpu(m)
+    bd = d.normal_bf16((E, N), 0.5, 2, 1, E, N)
+    ids = _routing(T, E, k, 3, live)
+    cnt, off, rows, pos = binding.moe_permute(torch.from_numpy(ids).cuda(), E)
+    h = d.normal_bf16((T * k, K), 3.0, 4, 1, T, K)
+    o = torch.full((T * k, N), float("nan"), device="cuda")
+    binding.moe_down_int4(dev(h), q, s, dev(bd), cnt, off, T, k, Wd_z=z, o=o, path=path)
+    got, off = host_f64(o), off.cpu().numpy()
+    for e in range(E):
+        a = orc.widen(h[off[e]:off[e + 1]])
+        want, tol = _bound(a, m, e, G)
+        b = orc.widen(bd[e])
+        _assert_within(got[off[e]:off[e + 1]], want + b, tol + U * np.abs(want + b), f"expert {e}")
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("G", [32, 64, 128])
+@pytest.mark.parametrize("T,E,k,K,N,live", STAGES)
+def test_gate_up(T, E, k, K, N, live, G, zeros, path):
+    _need_gpu()
+    N = -(-N // 16) * 16                                              # I % 8 == 0
+    m = _matrix(E, K, N, G, zeros, 5)
+    q, s, z = _gpu(m)
+    bgu = d.normal_bf16((E, N), 0.5, 6, 1, E, N)
+    ids = _routing(T, E, k, 7, live)
+    cnt, off, rows, pos = binding.moe_permute(torch.from_numpy(ids).cuda(), E)
+    x = d.normal_bf16((T, K), 60.0 / np.sqrt(K) / 0.3, 8, 1, T, K)   # some gates and ups reach the clamps
+    h = torch.full((T * k, N // 2), float("nan"), dtype=torch.bfloat16, device="cuda")
+    binding.moe_gate_up_int4(dev(x), q, s, dev(bgu), cnt, off, rows, k, Wgu_z=z, h=h, path=path)
+    got, off, rows = host_f64(h), off.cpu().numpy(), rows.cpu().numpy()
+    for e in range(E):
+        a = orc.widen(x[rows[off[e]:off[e + 1]] // k])
+        u, tol = _bound(a, m, e, G)
+        u = u + orc.widen(bgu[e])
+        tol = tol + U * np.abs(u)
+        want = orc.clamped_glu(u)
+        _assert_within(got[off[e]:off[e + 1]], want,
+                       (8.8 * tol[:, 0::2] + 7 * tol[:, 1::2]) * (1 + 2.0 ** -8) + np.abs(want) * (2.0 ** -8 + 2.0 ** -20)
+                       + 2.0 ** -134, f"expert {e}")
+
+
+def _block(T, E, H, I, k, G, zeros, seed=0, router_bias="normal"):
+    cfg = d.small_config(T=T, E=E, H=H, I=I, k=k, x_scale=d.scale_for_hidden(H), router_bias=router_bias)
+    x = d.make_activations(cfg, seed)
+    Wr, br = d.make_router(cfg, seed)
+    gu, down = _matrix(E, H, 2 * I, G, zeros, seed + 1), _matrix(E, I, H, G, zeros, seed + 2)
+    bgu, bd = d.normal_bf16((E, 2 * I), 0.01, seed, 5, E, I), d.normal_bf16((E, H), 0.01, seed, 7, E, H)
+    return x, Wr, br, gu, bgu, down, bd
+
+
+def _gpu_args(b):
+    x, Wr, br, gu, bgu, down, bd = b
+    gq, gs, gz = _gpu(gu)
+    dq, ds, dz = _gpu(down)
+    return (dev(x), dev(Wr), dev(br), gq, gs, dev(bgu), dq, ds, dev(bd)), {"Wgu_z": gz, "Wd_z": dz}
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("T,E,H,I,k,G,zeros", [
+    (1, 4, 32, 32, 1, 32, False), (5, 8, 64, 96, 2, 64, True), (33, 8, 96, 64, 4, 128, False),
+    (200, 16, 256, 160, 4, 32, True), (17, 8, 2880, 2880, 4, 128, True), (300, 4, 160, 608, 4, 64, False),
+    (60, 256, 128, 96, 8, 64, True), (257, 4, 1440, 2880, 2, 32, False)])
+def test_forward(T, E, H, I, k, G, zeros, path):
+    _need_gpu()
+    b = _block(T, E, H, I, k, G, zeros, seed=T)
+    args, z = _gpu_args(b)
+    ids = torch.empty((T, k), dtype=torch.int32, device="cuda")
+    w = torch.empty((T, k), dtype=torch.float32, device="cuda")
+    y = binding.moe_forward_int4(*args, k=k, topk_ids=ids, topk_w=w, path=path, **z)
+    ref = orc.moe_forward_int4(*b, k=k, G=G)
+    assert_routing(ids.cpu().numpy(), w.cpu().numpy(), ref["ids"], ref["w"], ref["logits"], k)
+    assert_y_close(host_f64(y), ref["y"], f"y T{T} E{E}")
+
+
+@pytest.mark.parametrize("E,K,N,G", [(2, 96, 40, 64), (1, 2880, 72, 128), (3, 32, 8, 32), (1, 160, 200, 32), (2, 128, 64, 64)])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_quantizer_matches_oracle(E, K, N, G, zeros):
+    """Codes, scales and zero points bit for bit; columns of zeros, of one sign, of exact halves, tiny and huge."""
+    _need_gpu()
+    W = d.normal_bf16((E, K, N), 0.02, 9, 1, K, N)
+    W[:, :, 0] = 0
+    W[:, :, 1] &= 0x7FFF
+    W[:, :, 2] |= 0x8000
+    W[:, :, 3] = d.f32_to_bf16_bits((np.arange(K) % 15 * 0.5 - 3.5).astype(np.float32))
+    W[:, :, 4] = np.arange(K) % 100                                   # subnormals
+    W[:, :, 5] = d.f32_to_bf16_bits(np.where(np.arange(K) % 2, 3e38, -3e38).astype(np.float32))
+    q, s, z = binding.moe_quantize_int4(dev(W), G=G, zeros=zeros)
+    q_ref, s_ref, z_ref = orc.int4_quantize(W, G, zeros)
+    assert (bf16_bits(s) == s_ref).all(), np.argwhere(bf16_bits(s) != s_ref)[:5].tolist()
+    assert (z is None) == (z_ref is None) and (z is None or (z.cpu().numpy() == z_ref).all())
+    want = orc.int4_pack(q_ref)
+    assert (q.cpu().numpy() == want).all(), np.argwhere(q.cpu().numpy() != want)[:5].tolist()
+
+
+@pytest.mark.parametrize("E,K,N", [(2, 96, 40), (1, 32, 64), (3, 224, 136)])
+def test_pack_matches_oracle(E, K, N):
+    _need_gpu()
+    q = np.random.default_rng(10).integers(0, 16, (E, K, N), dtype=np.uint8)
+    kn = np.swapaxes(q, 1, 2)
+    got = binding.moe_pack_int4(torch.from_numpy(np.ascontiguousarray(kn[:, :, 0::2] | (kn[:, :, 1::2] << 4))).cuda())
+    assert (got.cpu().numpy() == orc.int4_pack(q)).all()
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_columns_past_the_width_are_ignored(path):
+    """Whatever the codes of a tile's columns past N hold, the results are the same bits."""
+    _need_gpu()
+    T, E, H, I, k, G = 40, 4, 96, 64, 2, 64
+    b = _block(T, E, H, I, k, G, True, seed=11)
+    args, z = _gpu_args(b)
+    ref = binding.moe_forward_int4(*args, k=k, path=path, **z)
+    dq = args[6].clone()                                               # down: N = 96, the second tile half used
+    v = dq.view(E, 2, I // 32, 64, 4, 4)
+    v[:, 1].view(E, I // 32, 4, 16, 16)[:, :, :, 8:] = 0xFF            # lanes c = 8..15 of the last tile: columns 96..127
+    y = binding.moe_forward_int4(*args[:6], dq, *args[7:], k=k, path=path, **z)
+    assert torch.equal(ref, y)
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_nan_stays_in_its_rows(path):
+    """A token with NaN or infinite values spoils its own rows alone: every other row keeps its bits."""
+    _need_gpu()
+    T, E, H, I, k, G = 50, 4, 160, 96, 2, 64
+    b = _block(T, E, H, I, k, G, False, seed=12)
+    ids = _routing(T, E, k, 13)
+    args, z = _gpu_args(b)
+    cnt, off, rows, pos = binding.moe_permute(torch.from_numpy(ids).cuda(), E)
+    x = args[0].clone()
+    h0 = binding.moe_gate_up_int4(x, args[3], args[4], args[5], cnt, off, rows, k, path=path)
+    x[7, 3], x[31, 150], x[49, 0] = float("nan"), float("inf"), float("-inf")
+    h1 = binding.moe_gate_up_int4(x, args[3], args[4], args[5], cnt, off, rows, k, path=path)
+    tok = rows.cpu().numpy() // k
+    clean = ~np.isin(tok, (7, 31, 49))
+    assert (bf16_bits(h0)[clean] == bf16_bits(h1)[clean]).all()
+    assert np.isnan(host_f64(h1)[tok == 7]).all()
+    o0 = binding.moe_down_int4(h0, args[6], args[7], args[8], cnt, off, T, k, path=path)
+    o1 = binding.moe_down_int4(h1, args[6], args[7], args[8], cnt, off, T, k, path=path)
+    assert torch.equal(o0[torch.from_numpy(clean).cuda()], o1[torch.from_numpy(clean).cuda()])
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_nan_scale(path):
+    """A NaN scale makes its column NaN, for its expert's rows alone."""
+    _need_gpu()
+    T, E, H, I, k, G = 30, 4, 96, 64, 2, 32
+    x, Wr, br, gu, bgu, down, bd = _block(T, E, H, I, k, G, False, seed=14)
+    down[1][2, 1, 17] = 0x7FC0
+    b = (x, Wr, br, gu, bgu, down, bd)
+    args, z = _gpu_args(b)
+    y = binding.moe_forward_int4(*args, k=k, path=path, **z)
+    ref = orc.moe_forward_int4(*b, k=k, G=G)
+    got, want = np.isnan(host_f64(y)), np.isnan(ref["y"])
+    assert want.any() and not want.all() and (got == want).all()
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("n", [0, 1, 37, 64, 90])
+def test_padded(n, path):
+    _need_gpu()
+    T, E, H, I, k, G = 64, 8, 96, 64, 2, 32
+    b = _block(T, E, H, I, k, G, True, seed=15)
+    args, z = _gpu_args(b)
+    counts = torch.full((E,), -1, dtype=torch.int32, device="cuda")
+    ids = torch.empty((T, k), dtype=torch.int32, device="cuda")
+    y = binding.moe_forward_padded_int4(*args, k=k, n_valid=torch.tensor([n], dtype=torch.int32, device="cuda"),
+                                        expert_counts=counts, topk_ids=ids, path=path, **z)
+    m = min(n, T)
+    assert (host_f64(y)[m:] == 0).all() and (ids[m:] == -1).all()
+    if m:
+        ref = orc.moe_forward_int4(b[0][:m], *b[1:], k=k, G=G)
+        assert_y_close(host_f64(y)[:m], ref["y"])
+        assert (counts.cpu().numpy() == orc.expert_loads(ref["ids"], E)).all()
+    else:
+        assert (counts == 0).all()
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_expert_parallel_ranks_sum_to_the_whole(path):
+    _need_gpu()
+    T, E, H, I, k, G = 70, 8, 96, 64, 4, 64
+    b = _block(T, E, H, I, k, G, True, seed=16)
+    (x, Wr, br, gq, gs, bgu, dq, ds, bd), z = _gpu_args(b)
+    total = torch.zeros((T, H), device="cuda")
+    for lo, n in ((0, 3), (3, 1), (4, 4)):
+        c = slice(lo, lo + n)
+        part = binding.moe_forward_ep_int4(x, Wr, br, gq[c], gs[c], bgu[c], dq[c], ds[c], bd[c], e_begin=lo, k=k,
+                                           Wgu_z_local=z["Wgu_z"][c], Wd_z_local=z["Wd_z"][c], path=path)
+        ref = orc.moe_forward_int4(*b, k=k, G=G, experts=(lo, lo + n))
+        assert_y_close(host_f64(part), ref["y"], f"experts {lo}..{lo + n - 1}")
+        total += part
+    assert_y_close(host_f64(total), orc.moe_forward_int4(*b, k=k, G=G)["y"])
+
+
+def test_norm_then_int4_block():
+    """A decode step as served: norm with the residual's addition, then the block on its rows."""
+    _need_gpu()
+    T, E, H, I, k, G = 9, 8, 288, 160, 4, 64
+    b = _block(T, E, H, I, k, G, False, seed=17)
+    args, z = _gpu_args(b)
+    res = d.normal_bf16((T, H), 2.0, 18, 3, T, H)
+    gamma = d.f32_to_bf16_bits(np.full(H, 3.0, np.float32))
+    n, r = binding.moe_add_rmsnorm(args[0], dev(gamma), dev(res))
+    y = binding.moe_forward_int4(n, *args[1:], k=k, **z)
+    n_ref, _, _ = orc.add_rmsnorm(b[0], res, gamma, 1e-5)
+    bits = (n_ref.astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
+    assert_y_close(host_f64(y), orc.moe_forward_int4(bits, *b[1:], k=k, G=G)["y"])
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_graph_replays(path):
+    """Two captured forwards that share a workspace and a stream, replayed in turn with eager calls between."""
+    _need_gpu()
+    T, E, H, I, k, G = 96, 8, 256, 160, 4, 64
+    args, z = _gpu_args(_block(T, E, H, I, k, G, True, seed=19))
+    x2 = args[0].flip(0).contiguous()
+    ws = binding.alloc_workspace(T, H, E, k, I)
+    ys = [torch.empty((T, H), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    want = [binding.moe_forward_int4(x, *args[1:], k=k, path=path, **z) for x in (args[0], x2)]
+    torch.cuda.synchronize()
+    graphs = []
+    for x, y in zip((args[0], x2), ys):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            binding.moe_forward_int4(x, *args[1:], k=k, y=y, workspace=ws, path=path, **z)
+        graphs.append(g)
+    for i in range(3):
+        for y in ys:
+            y.fill_(-1.0)
+        ws.fill_(0xAB if i % 2 else 0x11)
+        eager = binding.moe_forward_int4(x2, *args[1:], k=k, path=path, **z)
+        torch.cuda.synchronize()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(eager, want[1])
+        assert all(torch.equal(y, w) for y, w in zip(ys, want)), i
+
+
+def test_other_stream_with_its_own_workspace():
+    _need_gpu()
+    T, E, H, I, k, G = 96, 8, 256, 160, 4, 64
+    args, z = _gpu_args(_block(T, E, H, I, k, G, False, seed=20))
+    want = binding.moe_forward_int4(*args, k=k, **z)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = [binding.moe_forward_int4(*args, k=k, stream=s, **z) for _ in range(3)]
+    s.synchronize()
+    assert all(torch.equal(want, y) for y in got)
+
+
+def test_no_tokens():
+    _need_gpu()
+    args, z = _gpu_args(_block(4, 4, 64, 32, 2, 32, False, seed=21))
+    assert binding.moe_forward_int4(args[0][:0], *args[1:], k=2, **z).shape == (0, 64)
