@@ -38,10 +38,6 @@ __device__ __forceinline__ uint32_t int4_store_order(uint32_t w) {
   }
   return o;
 }
-__device__ __forceinline__ uint32_t int4_value(uint32_t w, int i) {
-  const int at = int4_bit(i);
-  return (at ? (w >> at) | (w << (32 - at)) : w) & 15u;
-}
 
 // ---------------------------------------------------------------------------
 // Quantiser: one thread per (column, group).  Symmetric: s = bf16(max|v| / 7),
@@ -115,63 +111,228 @@ __global__ __launch_bounds__(kQThreads) void int4_pack_kernel(const uint8_t* __r
 }
 
 // ---------------------------------------------------------------------------
-// Expert products: one wave per (expert, 64 columns), a lane per column, four
-// token rows at a time.  Group sums of (q - z) * a in float32, scaled once per
-// group.
+// Weight streaming: a workgroup owns one expert and one strip of 64 columns;
+// its four waves split K and stream their part of the strip, a contiguous
+// kilobyte a tile, four tiles (a quad, 128 values of K) at a time and one quad
+// ahead.  16 MG token rows per pass over the strip.
+//   Operands of v_mfma_f32_16x16x32_bf16: A = 16 token rows, lane (row c,
+//   group g) holding K = 32 kt + 8 g .. + 7; B = word j of the tile, i.e. MFMA
+//   column c of call j is column 4 c + j of the strip, so the four columns of
+//   a lane are two (gate, up) pairs.
+//   A word gives 16 + q exactly (seven integer instructions for eight codes).
+//   The 16 and the zero point come off through the accumulator: a group's sum
+//   starts at -(16 + z) sum(a), where sum(a) is one more MFMA with a constant
+//   operand (-24 without zero points, 1 with them).  The group's sum times its
+//   scale is added to the accumulators in float32.
 // ---------------------------------------------------------------------------
-template <bool GATE_UP>
-__global__ __launch_bounds__(kWave) void int4_kernel(const bf16_t* __restrict__ A, const uint32_t* __restrict__ Wq,
-                                                     const uint16_t* __restrict__ Ws, const uint8_t* __restrict__ Wz,
-                                                     const bf16_t* __restrict__ bias, const int32_t* __restrict__ cnt,
-                                                     const int32_t* __restrict__ off, const int32_t* __restrict__ rows,
-                                                     int K, int N, int G, int kslots, void* __restrict__ out) {
+constexpr int kWaves = 4;
+
+// codes of one word -> the bf16 operand 16 + q
+__device__ __forceinline__ u32x4_t int4_operand(uint32_t w) {
+  const uint32_t m = 0x00780078u, o = 0x41804180u;
+  return u32x4_t{(w & m) | o, ((w >> 4) & m) | o, ((w >> 8) & m) | o,
+                 (__builtin_amdgcn_alignbit(w, w, 12) & m) | o};
+}
+
+// A quad's loads: tiles, token rows, and the lane's four columns' scales and
+// zero points of its 4 / GS groups.
+template <int MG, int NGQ>
+struct Quad {
+  u32x4_t w[4];
+  u32x4_t a[MG][4];
+  u32x2_t s[NGQ];
+  uint32_t z[NGQ];
+};
+
+template <bool GATE_UP, int MG, int GS, bool ZERO>
+__global__ __launch_bounds__(kWaves * kWave, MG == 1 ? 3 : 2) void int4_stream_kernel(
+    const bf16_t* __restrict__ A, const uint8_t* __restrict__ Wq, const uint16_t* __restrict__ Ws,
+    const uint8_t* __restrict__ Wz, const bf16_t* __restrict__ bias, const int32_t* __restrict__ cnt,
+    const int32_t* __restrict__ off, const int32_t* __restrict__ rows, int K, int N, int kslots,
+    void* __restrict__ out) {
+  constexpr int NGQ = 4 / GS;
+  __shared__ float red[kWaves][4][4][kWave];   // [wave][call j][element v][lane]
+
   const int e = blockIdx.y, M = cnt[e];
-  if (M == 0) return;
+  if (M == 0) return;   // block-uniform
   const int row0 = off[e];
-  const int lane = threadIdx.x, c = lane / 4, j = lane % 4;
-  const int n = blockIdx.x * kTileN + lane;
-  const int nc = min(n, N - 1);
-  const int ng = (K + G - 1) / G, nkt = K / kTileK;
-  const uint32_t* wp = Wq + ((size_t)e * gridDim.x + blockIdx.x) * (size_t)nkt * (kTileBytes / 4) + c * 4 + j;
-  for (int r0 = 0; r0 < M; r0 += 4) {
-    const bf16_t* ap[4];
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int g = lane >> 4, c = lane & 15;
+  const int nkt = K / kTileK, nq = (nkt + 3) / 4, ng = (nkt + GS - 1) / GS;
+  // N % 8 == 0: a lane's four columns are all in range or all out
+  const int ncol = blockIdx.x * kTileN + 4 * c;
+  const bool col_ok = ncol < N;
+  const uint32_t s_col = (uint32_t)min(ncol, N - 4);
+  const uint8_t* wp = Wq + ((size_t)e * gridDim.x + blockIdx.x) * (size_t)nkt * kTileBytes;
+  const uint16_t* sp = Ws + (size_t)e * ng * N;
+  const uint8_t* zp = ZERO ? Wz + (size_t)e * ng * N : nullptr;
+  const int q_begin = nq * wave / kWaves, q_end = nq * (wave + 1) / kWaves;
+  const u32x4_t flat = ZERO ? u32x4_t{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}
+                            : u32x4_t{0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u};
+
+  for (int r0 = 0; r0 < M; r0 += 16 * MG) {
+    const int nch = min(MG, (M - r0 + 15) / 16);   // block-uniform
+    const bf16_t* ap[MG];
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const int r = row0 + min(r0 + m, M - 1);
-      ap[m] = A + (size_t)(GATE_UP ? rows[r] / kslots : r) * K;
+    for (int m = 0; m < MG; ++m) {
+      const int r = row0 + min(r0 + 16 * m + c, M - 1);   // rows past M repeat the last one
+      ap[m] = A + (size_t)(GATE_UP ? rows[r] / kslots : r) * (size_t)K + 8 * g;
     }
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int b = 0; b < ng; ++b) {
-      const size_t at = ((size_t)e * ng + b) * N + nc;
-      const float s = bf16_to_f32(Ws[at]);
-      const float z = Wz ? (float)Wz[at] : 8.0f;
-      float part[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int k = b * G; k < min(K, (b + 1) * G); k += 8) {
-        const uint32_t w = wp[(size_t)(k / kTileK) * (kTileBytes / 4) + (k % kTileK) * 8];
+    f32x4_t acc[MG][4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float q = (float)int4_value(w, i) - z;
+    for (int m = 0; m < MG; ++m)
 #pragma unroll
-          for (int m = 0; m < 4; ++m) part[m] = __builtin_fmaf(bf16_to_f32(ap[m][k + i]), q, part[m]);
-        }
+      for (int j = 0; j < 4; ++j) acc[m][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+    auto load = [&](int q, Quad<MG, NGQ>& b) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int kt = min(4 * q + t, nkt - 1);
+        b.w[t] = ldg16_stream(wp + (size_t)kt * kTileBytes + 16 * lane);
       }
 #pragma unroll
-      for (int m = 0; m < 4; ++m) acc[m] = __builtin_fmaf(part[m], s, acc[m]);
-    }
-    const float bb = bf16_to_f32(bias[(size_t)e * N + nc]);
+      for (int i = 0; i < NGQ; ++i) {
+        const size_t at = (size_t)min(NGQ * q + i, ng - 1) * N + s_col;
+        b.s[i] = *reinterpret_cast<const u32x2_t*>(sp + at);
+        if (ZERO) b.z[i] = *reinterpret_cast<const uint32_t*>(zp + at);
+      }
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const float v = acc[m] + bb;
-      const float other = __shfl_xor(v, 1, kWave);
-      if (r0 + m < M && n < N) {
-        const size_t r = (size_t)(row0 + r0 + m);
-        if (!GATE_UP)
-          reinterpret_cast<float*>(out)[r * N + n] = v;
-        else if (lane % 2 == 0)
-          reinterpret_cast<uint16_t*>(out)[r * (N / 2) + n / 2] = (uint16_t)f32_to_bf16(clamped_glu(v, other));
+      for (int m = 0; m < MG; ++m)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) b.a[m][t] = ld16(ap[m] + 32 * min(4 * q + t, nkt - 1));
+    };
+    auto compute = [&](int q, Quad<MG, NGQ>& b) {
+      if (4 * q + 4 > nkt) {   // the last quad may be short: nothing from its missing tiles
+#pragma unroll
+        for (int t = 1; t < 4; ++t)
+          if (4 * q + t >= nkt)
+#pragma unroll
+            for (int m = 0; m < MG; ++m) b.a[m][t] = u32x4_t{0u, 0u, 0u, 0u};
+      }
+#pragma unroll
+      for (int i = 0; i < NGQ; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
+        float s[4], z[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[j] = j & 1 ? bf16hi(b.s[i][j >> 1]) : bf16lo(b.s[i][j >> 1]);
+          if (ZERO) z[j] = -16.0f - (float)((b.z[i] >> (8 * j)) & 0xFFu);
+        }
+        f32x4_t part[MG][4];
+#pragma unroll
+        for (int m = 0; m < MG; ++m) {
+          f32x4_t sum = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int t = GS * i; t < GS * i + GS; ++t) sum = mfma16x16x32(b.a[m][t], flat, sum);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) part[m][j][v] = ZERO ? z[j] * sum[v] : sum[v];
+        }
+#pragma unroll
+        for (int t = GS * i; t < GS * i + GS; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const u32x4_t bw = int4_operand(b.w[t][j]);
+            part[0][j] = mfma16x16x32(b.a[0][t], bw, part[0][j]);
+            if (MG > 1 && nch > 1) {
+#pragma unroll
+              for (int m = 1; m < MG; ++m) part[m][j] = mfma16x16x32(b.a[m][t], bw, part[m][j]);
+            }
+          }
+#pragma unroll
+        for (int m = 0; m < MG; ++m)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) acc[m][j][v] = __builtin_fmaf(s[j], part[m][j][v], acc[m][j][v]);
+      }
+    };
+
+    if (q_begin < q_end) {
+      Quad<MG, NGQ> b0, b1;
+      int q = q_begin;
+      load(q, b0);
+      for (; q + 2 < q_end; q += 2) {
+        load(q + 1, b1);
+        compute(q, b0);
+        load(q + 2, b0);
+        compute(q + 1, b1);
+      }
+      if (q + 1 < q_end) {
+        load(q + 1, b1);
+        compute(q, b0);
+        compute(q + 1, b1);
+      } else {
+        compute(q, b0);
+      }
+    }
+
+    // Sum the K partials (wave 0, 1, 2, 3); wave w finishes element v = w (row
+    // 4 g + w of each chunk) of the lane's four columns.
+    float bb[4];
+    {
+      const uint32_t* bp = reinterpret_cast<const uint32_t*>(bias + (size_t)e * N + s_col);   // 4-byte aligned
+      const uint32_t b01 = bp[0], b23 = bp[1];
+      bb[0] = bf16lo(b01), bb[1] = bf16hi(b01), bb[2] = bf16lo(b23), bb[3] = bf16hi(b23);
+    }
+#pragma unroll
+    for (int m = 0; m < MG; ++m) {
+      if (m < nch) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) red[wave][j][v][lane] = acc[m][j][v];
+        __syncthreads();
+        float sum[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float t = 0.f;
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) t += red[w][j][wave][lane];
+          sum[j] = t + bb[j];
+        }
+        const int r = r0 + 16 * m + 4 * g + wave;
+        if (r < M && col_ok) {
+          const size_t orow = (size_t)(row0 + r);
+          if (GATE_UP)
+            *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(out) + orow * (N / 2) + ncol / 2) =
+                pack_bf16x2(clamped_glu(sum[0], sum[1]), clamped_glu(sum[2], sum[3]));
+          else
+            *reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(out) + orow * N + ncol) =
+                f32x4_t{sum[0], sum[1], sum[2], sum[3]};
+        }
+        __syncthreads();
       }
     }
   }
+}
+
+template <bool GATE_UP, int MG, int GS>
+hipError_t launch_stream(const void* A, const void* Wq, const void* Ws, const void* Wz, const void* bias,
+                         const int32_t* cnt, const int32_t* off, const int32_t* rows, int K, int N, int E, int k,
+                         void* out, hipStream_t stream) {
+  dim3 grid((unsigned)((N + kTileN - 1) / kTileN), (unsigned)E);
+  auto kern = Wz ? int4_stream_kernel<GATE_UP, MG, GS, true> : int4_stream_kernel<GATE_UP, MG, GS, false>;
+  hipLaunchKernelGGL(kern, grid, dim3(kWaves * kWave), 0, stream, (const bf16_t*)A, (const uint8_t*)Wq,
+                     (const uint16_t*)Ws, (const uint8_t*)Wz, (const bf16_t*)bias, cnt, off, rows, K, N, k, out);
+  return hipGetLastError();
+}
+
+// Mean rows per expert up to which one 16-row chunk a pass is enough.
+constexpr int64_t kOneChunkMeanRows = 10;
+
+template <bool GATE_UP>
+hipError_t launch_int4(const void* A, const void* Wq, const void* Ws, const void* Wz, const void* bias,
+                       const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T, int K, int N, int E, int k,
+                       int G, void* out, hipStream_t stream) {
+  const bool one = T * k <= kOneChunkMeanRows * E;
+  auto pick = [&](auto one_c, auto two_c) { return one ? one_c : two_c; };
+  auto launch = G == 32   ? pick(launch_stream<GATE_UP, 1, 1>, launch_stream<GATE_UP, 2, 1>)
+                : G == 64 ? pick(launch_stream<GATE_UP, 1, 2>, launch_stream<GATE_UP, 2, 2>)
+                          : pick(launch_stream<GATE_UP, 1, 4>, launch_stream<GATE_UP, 2, 4>);
+  return launch(A, Wq, Ws, Wz, bias, cnt, off, rows, K, N, E, k, out, stream);
 }
 
 }  // namespace
@@ -192,21 +353,15 @@ hipError_t launch_int4_pack(const void* src, int E, int K, int N, void* codes, h
 }
 
 hipError_t launch_int4_gate_up(const void* x, const void* Wq, const void* Ws, const void* Wz, const void* bgu,
-                               const int32_t* cnt, const int32_t* off, const int32_t* rows, int H, int E, int k, int I,
-                               int G, void* h, hipStream_t stream) {
-  dim3 grid((unsigned)((2 * I + kTileN - 1) / kTileN), (unsigned)E);
-  hipLaunchKernelGGL(int4_kernel<true>, grid, dim3(kWave), 0, stream, (const bf16_t*)x, (const uint32_t*)Wq,
-                     (const uint16_t*)Ws, (const uint8_t*)Wz, (const bf16_t*)bgu, cnt, off, rows, H, 2 * I, G, k, h);
-  return hipGetLastError();
+                               const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T, int H, int E,
+                               int k, int I, int G, void* h, hipStream_t stream) {
+  return launch_int4<true>(x, Wq, Ws, Wz, bgu, cnt, off, rows, T, H, 2 * I, E, k, G, h, stream);
 }
 
 hipError_t launch_int4_down(const void* h, const void* Wq, const void* Ws, const void* Wz, const void* bd,
-                            const int32_t* cnt, const int32_t* off, int H, int E, int I, int G, float* o,
+                            const int32_t* cnt, const int32_t* off, int64_t T, int H, int E, int k, int I, int G, float* o,
                             hipStream_t stream) {
-  dim3 grid((unsigned)((H + kTileN - 1) / kTileN), (unsigned)E);
-  hipLaunchKernelGGL(int4_kernel<false>, grid, dim3(kWave), 0, stream, (const bf16_t*)h, (const uint32_t*)Wq,
-                     (const uint16_t*)Ws, (const uint8_t*)Wz, (const bf16_t*)bd, cnt, off, nullptr, I, H, G, 1, o);
-  return hipGetLastError();
+  return launch_int4<false>(h, Wq, Ws, Wz, bd, cnt, off, nullptr, T, I, H, E, k, G, o, stream);
 }
 
 }  // namespace moe

@@ -90,10 +90,10 @@ hipError_t launch_int4_quantize(const void* W, int E, int K, int N, int G, void*
                                 hipStream_t stream);
 hipError_t launch_int4_pack(const void* src, int E, int K, int N, void* codes, hipStream_t stream);
 hipError_t launch_int4_gate_up(const void* x, const void* Wq, const void* Ws, const void* Wz, const void* bgu,
-                               const int32_t* cnt, const int32_t* off, const int32_t* rows, int H, int E, int k, int I,
-                               int G, void* h, hipStream_t stream);
+                               const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T, int H, int E,
+                               int k, int I, int G, void* h, hipStream_t stream);
 hipError_t launch_int4_down(const void* h, const void* Wq, const void* Ws, const void* Wz, const void* bd,
-                            const int32_t* cnt, const int32_t* off, int H, int E, int I, int G, float* o,
+                            const int32_t* cnt, const int32_t* off, int64_t T, int H, int E, int k, int I, int G, float* o,
                             hipStream_t stream);
 
 // Residual addition and RMS norm (residual and residual_out both or neither;
