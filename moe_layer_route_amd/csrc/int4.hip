@@ -17,12 +17,11 @@
 //          pair (16 + q[2p], 16 + q[2p + 1]).  Columns past N hold anything.
 //   scales bf16 [E][ceil(K/G)][N], zeros uint8 of the same shape.
 #include "device_common.h"
+#include "int4_device.h"
 #include "launch.h"
 
 namespace moe {
 namespace {
-
-constexpr int kTileN = 64, kTileK = 32, kTileBytes = 1024;
 
 // bit of value i in its word
 __device__ __forceinline__ int int4_bit(int i) { return (3 + 4 * (i >> 1) + 16 * (i & 1)) & 31; }
@@ -127,13 +126,6 @@ __global__ __launch_bounds__(kQThreads) void int4_pack_kernel(const uint8_t* __r
 // ---------------------------------------------------------------------------
 constexpr int kWaves = 4;
 
-// codes of one word -> the bf16 operand 16 + q
-__device__ __forceinline__ u32x4_t int4_operand(uint32_t w) {
-  const uint32_t m = 0x00780078u, o = 0x41804180u;
-  return u32x4_t{(w & m) | o, ((w >> 4) & m) | o, ((w >> 8) & m) | o,
-                 (__builtin_amdgcn_alignbit(w, w, 12) & m) | o};
-}
-
 // A quad's loads: tiles, token rows, and the lane's four columns' scales and
 // zero points of its 4 / GS groups.
 template <int MG, int NGQ>
@@ -149,7 +141,7 @@ __global__ __launch_bounds__(kWaves * kWave, MG == 1 ? 3 : 2) void int4_stream_k
     const bf16_t* __restrict__ A, const uint8_t* __restrict__ Wq, const uint16_t* __restrict__ Ws,
     const uint8_t* __restrict__ Wz, const bf16_t* __restrict__ bias, const int32_t* __restrict__ cnt,
     const int32_t* __restrict__ off, const int32_t* __restrict__ rows, int K, int N, int kslots,
-    void* __restrict__ out) {
+    int64_t a_rows, void* __restrict__ out) {
   constexpr int NGQ = 4 / GS;
   __shared__ float red[kWaves][4][4][kWave];   // [wave][call j][element v][lane]
 
@@ -164,20 +156,21 @@ __global__ __launch_bounds__(kWaves * kWave, MG == 1 ? 3 : 2) void int4_stream_k
   const int ncol = blockIdx.x * kTileN + 4 * c;
   const bool col_ok = ncol < N;
   const uint32_t s_col = (uint32_t)min(ncol, N - 4);
-  const uint8_t* wp = Wq + ((size_t)e * gridDim.x + blockIdx.x) * (size_t)nkt * kTileBytes;
-  const uint16_t* sp = Ws + (size_t)e * ng * N;
-  const uint8_t* zp = ZERO ? Wz + (size_t)e * ng * N : nullptr;
+  const rsrc_t w_rs = make_rsrc(Wq + ((size_t)e * gridDim.x + blockIdx.x) * (size_t)nkt * kTileBytes, nkt * kTileBytes);
+  const rsrc_t s_rs = make_rsrc(Ws + (size_t)e * ng * N, (uint32_t)ng * N * 2);
+  const rsrc_t z_rs = make_rsrc(ZERO ? Wz + (size_t)e * ng * N : Wq, ZERO ? (uint32_t)ng * N : 0u);
+  const rsrc_t a_rs = make_rsrc(GATE_UP ? A : A + (size_t)row0 * K, (uint32_t)((size_t)(GATE_UP ? a_rows : M) * K * 2));
   const int q_begin = nq * wave / kWaves, q_end = nq * (wave + 1) / kWaves;
   const u32x4_t flat = ZERO ? u32x4_t{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}
                             : u32x4_t{0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u};
 
   for (int r0 = 0; r0 < M; r0 += 16 * MG) {
     const int nch = min(MG, (M - r0 + 15) / 16);   // block-uniform
-    const bf16_t* ap[MG];
+    uint32_t a_off[MG];
 #pragma unroll
     for (int m = 0; m < MG; ++m) {
-      const int r = row0 + min(r0 + 16 * m + c, M - 1);   // rows past M repeat the last one
-      ap[m] = A + (size_t)(GATE_UP ? rows[r] / kslots : r) * (size_t)K + 8 * g;
+      const int r = min(r0 + 16 * m + c, M - 1);   // rows past M repeat the last one
+      a_off[m] = ((uint32_t)(GATE_UP ? rows[row0 + r] / kslots : r) * (uint32_t)K + 8u * g) * 2u;
     }
     f32x4_t acc[MG][4];
 #pragma unroll
@@ -188,19 +181,18 @@ __global__ __launch_bounds__(kWaves * kWave, MG == 1 ? 3 : 2) void int4_stream_k
     auto load = [&](int q, Quad<MG, NGQ>& b) {
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const int kt = min(4 * q + t, nkt - 1);
-        b.w[t] = ldg16_stream(wp + (size_t)kt * kTileBytes + 16 * lane);
+        b.w[t] = buf_ld16<2>(w_rs, 16u * lane, (uint32_t)min(4 * q + t, nkt - 1) * kTileBytes);   // read once
       }
 #pragma unroll
       for (int i = 0; i < NGQ; ++i) {
-        const size_t at = (size_t)min(NGQ * q + i, ng - 1) * N + s_col;
-        b.s[i] = *reinterpret_cast<const u32x2_t*>(sp + at);
-        if (ZERO) b.z[i] = *reinterpret_cast<const uint32_t*>(zp + at);
+        const uint32_t at = (uint32_t)min(NGQ * q + i, ng - 1) * N;
+        b.s[i] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(s_rs, (int)(2u * s_col), (int)(2u * at), 0));
+        if (ZERO) b.z[i] = __builtin_amdgcn_raw_buffer_load_b32(z_rs, (int)s_col, (int)at, 0);
       }
 #pragma unroll
       for (int m = 0; m < MG; ++m)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) b.a[m][t] = ld16(ap[m] + 32 * min(4 * q + t, nkt - 1));
+        for (int t = 0; t < 4; ++t) b.a[m][t] = buf_ld16(a_rs, a_off[m], 64u * (uint32_t)min(4 * q + t, nkt - 1));
     };
     auto compute = [&](int q, Quad<MG, NGQ>& b) {
       if (4 * q + 4 > nkt) {   // the last quad may be short: nothing from its missing tiles
@@ -212,6 +204,8 @@ __global__ __launch_bounds__(kWaves * kWave, MG == 1 ? 3 : 2) void int4_stream_k
       }
 #pragma unroll
       for (int i = 0; i < NGQ; ++i) {
+        // one group after the other (below, its sums are added at once): the
+        // compiler would otherwise keep every group's partial sums to the end
         __builtin_amdgcn_sched_barrier(0);
         float s[4], z[4];
 #pragma unroll
@@ -247,6 +241,10 @@ __global__ __launch_bounds__(kWaves * kWave, MG == 1 ? 3 : 2) void int4_stream_k
           for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int v = 0; v < 4; ++v) acc[m][j][v] = __builtin_fmaf(s[j], part[m][j][v], acc[m][j][v]);
+#pragma unroll
+        for (int m = 0; m < MG; ++m)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(acc[m][j]));
       }
     };
 
@@ -311,12 +309,12 @@ __global__ __launch_bounds__(kWaves * kWave, MG == 1 ? 3 : 2) void int4_stream_k
 
 template <bool GATE_UP, int MG, int GS>
 hipError_t launch_stream(const void* A, const void* Wq, const void* Ws, const void* Wz, const void* bias,
-                         const int32_t* cnt, const int32_t* off, const int32_t* rows, int K, int N, int E, int k,
-                         void* out, hipStream_t stream) {
+                         const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T, int K, int N, int E,
+                         int k, void* out, hipStream_t stream) {
   dim3 grid((unsigned)((N + kTileN - 1) / kTileN), (unsigned)E);
   auto kern = Wz ? int4_stream_kernel<GATE_UP, MG, GS, true> : int4_stream_kernel<GATE_UP, MG, GS, false>;
   hipLaunchKernelGGL(kern, grid, dim3(kWaves * kWave), 0, stream, (const bf16_t*)A, (const uint8_t*)Wq,
-                     (const uint16_t*)Ws, (const uint8_t*)Wz, (const bf16_t*)bias, cnt, off, rows, K, N, k, out);
+                     (const uint16_t*)Ws, (const uint8_t*)Wz, (const bf16_t*)bias, cnt, off, rows, K, N, k, T, out);
   return hipGetLastError();
 }
 
@@ -327,12 +325,14 @@ template <bool GATE_UP>
 hipError_t launch_int4(const void* A, const void* Wq, const void* Ws, const void* Wz, const void* bias,
                        const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T, int K, int N, int E, int k,
                        int G, void* out, hipStream_t stream) {
+  // 32-bit offsets into the token rows (of one expert, for down)
+  if ((GATE_UP ? T : T * k) * K * 2 >= (int64_t)1 << 32) return hipErrorNotSupported;
   const bool one = T * k <= kOneChunkMeanRows * E;
   auto pick = [&](auto one_c, auto two_c) { return one ? one_c : two_c; };
   auto launch = G == 32   ? pick(launch_stream<GATE_UP, 1, 1>, launch_stream<GATE_UP, 2, 1>)
                 : G == 64 ? pick(launch_stream<GATE_UP, 1, 2>, launch_stream<GATE_UP, 2, 2>)
                           : pick(launch_stream<GATE_UP, 1, 4>, launch_stream<GATE_UP, 2, 4>);
-  return launch(A, Wq, Ws, Wz, bias, cnt, off, rows, K, N, E, k, out, stream);
+  return launch(A, Wq, Ws, Wz, bias, cnt, off, rows, T, K, N, E, k, out, stream);
 }
 
 }  // namespace

@@ -95,6 +95,13 @@ hipError_t launch_int4_gate_up(const void* x, const void* Wq, const void* Ws, co
 hipError_t launch_int4_down(const void* h, const void* Wq, const void* Ws, const void* Wz, const void* bd,
                             const int32_t* cnt, const int32_t* off, int64_t T, int H, int E, int k, int I, int G, float* o,
                             hipStream_t stream);
+// the LDS-tiled grouped GEMMs (int4_gemm.hip)
+hipError_t launch_gemm_int4_gate_up(const void* x, const void* Wq, const void* Ws, const void* Wz, const void* bgu,
+                               const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T, int H, int E,
+                               int k, int I, int G, void* h, hipStream_t stream);
+hipError_t launch_gemm_int4_down(const void* h, const void* Wq, const void* Ws, const void* Wz, const void* bd,
+                            const int32_t* cnt, const int32_t* off, int64_t T, int H, int E, int k, int I, int G, float* o,
+                            hipStream_t stream);
 
 // Residual addition and RMS norm (residual and residual_out both or neither;
 // codes and scales both or neither; y may be null with codes)

@@ -691,6 +691,8 @@ static int run_gate_up_int4(const char* fn, const void* x, const void* Wq, const
                             int32_t H, int32_t E, int32_t k, int32_t I, int32_t G, void* h, int32_t path,
                             hipStream_t s) {
   path = choose_path(path, T, E, k);
+  if (path == MOE_PATH_GEMM)
+    return hip_status(fn, moe::launch_gemm_int4_gate_up(x, Wq, Ws, Wz, bgu, cnt, off, rows, T, H, E, k, I, G, h, s));
   return hip_status(fn, moe::launch_int4_gate_up(x, Wq, Ws, Wz, bgu, cnt, off, rows, T, H, E, k, I, G, h, s));
 }
 
@@ -698,6 +700,8 @@ static int run_down_int4(const char* fn, const void* h, const void* Wq, const vo
                          const int32_t* cnt, const int32_t* off, int64_t T, int32_t H, int32_t E, int32_t k, int32_t I,
                          int32_t G, float* o, int32_t path, hipStream_t s) {
   path = choose_path(path, T, E, k);
+  if (path == MOE_PATH_GEMM)
+    return hip_status(fn, moe::launch_gemm_int4_down(h, Wq, Ws, Wz, bd, cnt, off, T, H, E, k, I, G, o, s));
   return hip_status(fn, moe::launch_int4_down(h, Wq, Ws, Wz, bd, cnt, off, T, H, E, k, I, G, o, s));
 }
 
