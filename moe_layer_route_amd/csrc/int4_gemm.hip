@@ -18,6 +18,8 @@
 #include "int4_device.h"
 #include "launch.h"
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
@@ -29,13 +31,21 @@ constexpr int kXcds = 8;
 constexpr int kMBlock = 8;   // M tiles per block of the tile order
 constexpr uint32_t kOutOfRange = 0xFFFFFFF0u;
 
+template <int GU>
+struct Ring {
+  u32x4_t rows[kRing][GU][kChunks][kWave];      // fragments of the token rows, in lane order
+  u32x4_t w[kGemmWaves][kRing][GU][kWave];      // each wave's tiles
+  uint32_t s[kGemmWaves][kRing][kWave];         // scales of its 64 columns, twice
+  uint32_t z[kGemmWaves][kRing][kWave];         // zero points, four times
+};
+
 template <bool GATE_UP, int GU, bool ZERO>
 __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
     const bf16_t* __restrict__ A, const uint8_t* __restrict__ Wq, const uint16_t* __restrict__ Ws,
     const uint8_t* __restrict__ Wz, const bf16_t* __restrict__ bias, const int32_t* __restrict__ cnt,
     const int32_t* __restrict__ off, const int32_t* __restrict__ rows, int K, int N, int E, int kslots, int64_t a_rows,
     int n_tiles, int units_per_group, void* __restrict__ out) {
-  __shared__ __align__(16) u32x4_t lds[kRing][GU][kChunks][kWave];
+  __shared__ __align__(16) Ring<GU> ring;
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   int e, m0, nt;
@@ -49,40 +59,37 @@ __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
   const int strip = nt * kGemmWaves + wave;
   const bool live = strip < strips;   // wave-uniform; a wave past the last strip only loads rows
   const int ncol = strip * kTileN + 4 * c;
-  const uint32_t s_col = (uint32_t)min(ncol, N - 4);
+  const int wstrip = min(strip, strips - 1);
 
-  const rsrc_t w_rs = make_rsrc(Wq + ((size_t)e * strips + min(strip, strips - 1)) * (size_t)nkt * kTileBytes,
-                                (uint32_t)nkt * kTileBytes);
-  const rsrc_t s_rs = make_rsrc(Ws + (size_t)e * ng * N, (uint32_t)ng * N * 2);
-  const rsrc_t z_rs = make_rsrc(ZERO ? Wz + (size_t)e * ng * N : Wq, ZERO ? (uint32_t)ng * N : 0u);
+  const u32x4_t w_rs = rsrc_words(Wq + ((size_t)e * strips + wstrip) * (size_t)nkt * kTileBytes, (uint32_t)nkt * kTileBytes);
+  const u32x4_t s_rs = rsrc_words(Ws + (size_t)e * ng * N, (uint32_t)ng * N * 2);
+  const u32x4_t z_rs = rsrc_words(ZERO ? Wz + (size_t)e * ng * N : Wq, ZERO ? (uint32_t)ng * N : 0u);
   const u32x4_t a_rs = rsrc_words(GATE_UP ? A : A + (size_t)row0 * K, (uint32_t)((size_t)(GATE_UP ? a_rows : M) * K * 2));
 
-  // wave w brings in chunk w's fragments: lane (row c, group g)
+  // wave w brings in chunk w's fragments: lane (row c, group g); rows past M
+  // repeat the last one, columns past N the last ones
   const int r = min(m0 + 16 * wave + c, M - 1);
   const uint32_t a_off = ((uint32_t)(GATE_UP ? rows[row0 + r] / kslots : r) * (uint32_t)K + 8u * g) * 2u;
-  const uint32_t lds0 = (uint32_t)(uintptr_t)&lds[0][0][0][0];
-  auto load_rows = [&](int u) {
-    if (wave < nch) {
+  const uint32_t s_off = 2u * (uint32_t)min(wstrip * kTileN + 2 * (lane & 31), N - 2);
+  const uint32_t z_off = (uint32_t)min(wstrip * kTileN + 4 * c, N - 4);
+  const uint32_t rows_at = (uint32_t)(uintptr_t)&ring.rows[0][0][wave][0];
+  const uint32_t w_at = (uint32_t)(uintptr_t)&ring.w[wave][0][0][0];
+  const uint32_t s_at = (uint32_t)(uintptr_t)&ring.s[wave][0][0], z_at = (uint32_t)(uintptr_t)&ring.z[wave][0][0];
+  // Every wave issues the same loads for every unit, past the end too (where
+  // nothing is read): the waits count on it.
+  constexpr int kLoads = 2 * GU + 1 + (ZERO ? 1 : 0);
+  auto load = [&](int u) __attribute__((always_inline)) {
+    const int slot = u % kRing;
 #pragma unroll
-      for (int t = 0; t < GU; ++t) {
-        const int kt = GU * u + t;
-        dma16(a_rs, kt < nkt ? a_off : kOutOfRange, kt < nkt ? 64u * (uint32_t)kt : 0u,
-              lds0 + (uint32_t)((((u % kRing) * GU + t) * kChunks + wave) * kWave) * 16u);
-      }
+    for (int t = 0; t < GU; ++t) {
+      const int kt = GU * u + t;
+      const bool in = kt < nkt;
+      dma16(a_rs, in ? a_off : kOutOfRange, in ? 64u * (uint32_t)kt : 0u, rows_at + (uint32_t)((slot * GU + t) * kChunks * kWave) * 16u);
+      dma16(w_rs, in ? 16u * (uint32_t)lane : kOutOfRange, in ? (uint32_t)kt * kTileBytes : 0u, w_at + (uint32_t)((slot * GU + t) * kWave) * 16u);
     }
-  };
-  struct Unit {
-    u32x4_t w[GU];
-    u32x2_t s;
-    uint32_t z;
-  };
-  auto load_weights = [&](int u, Unit& b) {
-    const int uu = min(u, nu - 1);
-#pragma unroll
-    for (int t = 0; t < GU; ++t) b.w[t] = buf_ld16(w_rs, 16u * lane, (uint32_t)min(GU * uu + t, nkt - 1) * kTileBytes);
-    const uint32_t at = (uint32_t)(uu / units_per_group) * N;
-    b.s = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(s_rs, (int)(2u * s_col), (int)(2u * at), 0));
-    if (ZERO) b.z = __builtin_amdgcn_raw_buffer_load_b32(z_rs, (int)s_col, (int)at, 0);
+    const uint32_t at = (uint32_t)(min(u, nu - 1) / units_per_group) * N;
+    dma4(s_rs, s_off, 2u * at, s_at + (uint32_t)(slot * kWave) * 4u);
+    if (ZERO) dma4(z_rs, z_off, at, z_at + (uint32_t)(slot * kWave) * 4u);
   };
   const u32x4_t flat = ZERO ? u32x4_t{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}
                             : u32x4_t{0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u};
@@ -92,68 +99,98 @@ __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[m][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  auto compute = [&](int u, const Unit& b) {
-    float s[4], z[4];
-    u32x4_t bw[GU][4];
+  // The chunk's operands from LDS, and the sum over its rows in every column.
+  auto chunk_in = [&](int u, int m, u32x4_t (&a)[GU], f32x4_t& sum) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < GU; ++t) a[t] = ring.rows[u % kRing][t][m][lane];
+    sum = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int t = 0; t < GU; ++t) sum = mfma16x16x32(a[t], flat, sum);
+  };
+  auto chunk_mul = [&](const u32x4_t (&a)[GU], const f32x4_t& sum, const u32x4_t (&bw)[GU][4], const float (&z)[4],
+                       f32x4_t (&part)[4]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) part[j][v] = ZERO ? z[j] * sum[v] : sum[v];
+#pragma unroll
+    for (int t = 0; t < GU; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) part[j] = mfma16x16x32(a[t], bw[t][j], part[j]);
+  };
+  auto chunk_add = [&](f32x4_t (&sums)[4], const f32x4_t (&part)[4], const float (&s)[4]) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      s[j] = j & 1 ? bf16hi(b.s[j >> 1]) : bf16lo(b.s[j >> 1]);
-      if (ZERO) z[j] = -16.0f - (float)((b.z >> (8 * j)) & 0xFFu);
 #pragma unroll
-      for (int t = 0; t < GU; ++t) bw[t][j] = int4_operand(b.w[t][j]);
+      for (int v = 0; v < 4; ++v) sums[j][v] = __builtin_fmaf(s[j], part[j][v], sums[j][v]);
+      asm volatile("" : "+v"(sums[j]));   // here, not at the end: the parts would fill the registers
     }
+  };
+  auto compute = [&](auto full, int u) __attribute__((always_inline)) {
+    const int slot = u % kRing;
+    float s[4], z[4];
+    u32x4_t bw[GU][4];
+    u32x4_t w[GU];
 #pragma unroll
-    for (int m = 0; m < kChunks; ++m) {
-      if (m < nch) {
-        u32x4_t a[GU];
+    for (int t = 0; t < GU; ++t) w[t] = ring.w[wave][slot][t][lane];
+    const u32x2_t sw = *reinterpret_cast<const u32x2_t*>(&ring.s[wave][slot][2 * c]);
+    const uint32_t zw = ZERO ? ring.z[wave][slot][c] : 0u;
 #pragma unroll
-        for (int t = 0; t < GU; ++t) a[t] = lds[u % kRing][t][m][lane];
-        f32x4_t sum = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < 4; ++j) {
+      s[j] = j & 1 ? bf16hi(sw[j >> 1]) : bf16lo(sw[j >> 1]);
+      if (ZERO) z[j] = -16.0f - (float)((zw >> (8 * j)) & 0xFFu);
 #pragma unroll
-        for (int t = 0; t < GU; ++t) sum = mfma16x16x32(a[t], flat, sum);
-        f32x4_t part[4];
+      for (int t = 0; t < GU; ++t) bw[t][j] = int4_operand(w[t][j]);
+    }
+    if (decltype(full)::value) {
+      // Full tiles, without branches: a chunk is read ahead of the previous
+      // one's products, and added behind the next one's.
+      u32x4_t a[2][GU];
+      f32x4_t sum[2], part[2][4];
+      chunk_in(u, 0, a[0], sum[0]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+      for (int m = 0; m < kChunks; ++m) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (m + 1 < kChunks) chunk_in(u, m + 1, a[(m + 1) & 1], sum[(m + 1) & 1]);
+        chunk_mul(a[m & 1], sum[m & 1], bw, z, part[m & 1]);
+        if (m > 0) chunk_add(acc[m - 1], part[(m - 1) & 1], s);
+      }
+      chunk_add(acc[kChunks - 1], part[(kChunks - 1) & 1], s);
+    } else {
 #pragma unroll
-          for (int v = 0; v < 4; ++v) part[j][v] = ZERO ? z[j] * sum[v] : sum[v];
-#pragma unroll
-        for (int t = 0; t < GU; ++t)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) part[j] = mfma16x16x32(a[t], bw[t][j], part[j]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-#pragma unroll
-          for (int v = 0; v < 4; ++v) acc[m][j][v] = __builtin_fmaf(s[j], part[j][v], acc[m][j][v]);
-          asm volatile("" : "+v"(acc[m][j]));
+      for (int m = 0; m < kChunks; ++m) {
+        if (m < nch) {
+          u32x4_t a[GU];
+          f32x4_t sum, part[4];
+          chunk_in(u, m, a, sum);
+          chunk_mul(a, sum, bw, z, part);
+          chunk_add(acc[m], part, s);
         }
       }
     }
   };
 
-  Unit b0, b1;
-  load_rows(0);
-  if (nu > 1) load_rows(1);
-  if (nu > 2) load_rows(2);
-  load_weights(0, b0);
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  load(0);
+  load(1);
+  load(2);
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kLoads) : "memory");
   __syncthreads();
-  // Unit u: rows of u + 3 and weights of u + 1 are asked for; the rows of u + 1
-  // (asked for in unit u - 2) have arrived when the unit ends.
-  auto step = [&](int u, Unit& now, Unit& next) {
-    if (u + 3 < nu) load_rows(u + 3);
-    load_weights(u + 1, next);
-    if (live) compute(u, now);
-    // at most this unit's own loads may still be on their way
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(0) : "memory");
-    __syncthreads();
+  // Loads retire in order: with those of two units still under way, the wave's
+  // part of unit u + 1 is in LDS.
+  auto run = [&](auto full) __attribute__((always_inline)) {
+    for (int u = 0; u < nu; ++u) {
+      load(u + 3);   // into the slot that unit u - 1 was read from
+      if (live) compute(full, u);
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kLoads) : "memory");
+      __syncthreads();
+    }
   };
-  int u = 0;
-  for (; u + 2 <= nu; u += 2) {
-    step(u, b0, b1);
-    step(u + 1, b1, b0);
-  }
-  if (u < nu) step(u, b0, b1);
-  if (!live || ncol >= N) return;   // no barrier follows
+  if (nch == kChunks)
+    run(std::true_type{});
+  else
+    run(std::false_type{});
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no load may reach this LDS after the workgroup's end
+  if (!live || ncol >= N) return;                    // no barrier follows
 
   float bb[4];
   {
