@@ -164,6 +164,7 @@ __global__ __launch_bounds__(kWaves * kWave, MG == 1 ? 3 : 2) void int4_stream_k
   const u32x4_t flat = ZERO ? u32x4_t{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}
                             : u32x4_t{0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u};
 
+  const Int4Masks masks;
   for (int r0 = 0; r0 < M; r0 += 16 * MG) {
     const int nch = min(MG, (M - r0 + 15) / 16);   // block-uniform
     uint32_t a_off[MG];
@@ -228,7 +229,7 @@ __global__ __launch_bounds__(kWaves * kWave, MG == 1 ? 3 : 2) void int4_stream_k
         for (int t = GS * i; t < GS * i + GS; ++t)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const u32x4_t bw = int4_operand(b.w[t][j]);
+            const u32x4_t bw = int4_operand(b.w[t][j], masks);
             part[0][j] = mfma16x16x32(b.a[0][t], bw, part[0][j]);
             if (MG > 1 && nch > 1) {
 #pragma unroll

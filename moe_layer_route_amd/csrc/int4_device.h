@@ -17,11 +17,20 @@ __device__ __forceinline__ u32x4_t buf_ld16(rsrc_t r, uint32_t lane_off, uint32_
   return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)lane_off, (int)wave_off, AUX));
 }
 
+// The masks of int4_operand in registers (v_and_or_b32 takes no literal; left
+// to itself the compiler makes two instructions with one literal each).
+struct Int4Masks {
+  uint32_t field, base;
+  __device__ __forceinline__ Int4Masks() {
+    asm("v_mov_b32 %0, 0x00780078" : "=v"(field));
+    asm("s_mov_b32 %0, 0x41804180" : "=s"(base));
+  }
+};
+
 // codes of one word -> the bf16 operand 16 + q
-__device__ __forceinline__ u32x4_t int4_operand(uint32_t w) {
-  const uint32_t m = 0x00780078u, o = 0x41804180u;
-  return u32x4_t{(w & m) | o, ((w >> 4) & m) | o, ((w >> 8) & m) | o,
-                 (__builtin_amdgcn_alignbit(w, w, 12) & m) | o};
+__device__ __forceinline__ u32x4_t int4_operand(uint32_t w, const Int4Masks& m) {
+  return u32x4_t{(w & m.field) | m.base, ((w >> 4) & m.field) | m.base, ((w >> 8) & m.field) | m.base,
+                 (__builtin_amdgcn_alignbit(w, w, 12) & m.field) | m.base};
 }
 
 }  // namespace moe

@@ -99,10 +99,25 @@ __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[m][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  // The chunk's operands from LDS, and the sum over its rows in every column.
-  auto chunk_in = [&](int u, int m, u32x4_t (&a)[GU], f32x4_t& sum) __attribute__((always_inline)) {
+  // A unit's codes, scales and zero points of this lane.
+  struct Words {
+    u32x4_t w[GU];
+    u32x2_t s;
+    uint32_t z;
+  };
+  auto words = [&](int u, Words& b) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < GU; ++t) b.w[t] = ring.w[wave][u % kRing][t][lane];
+    b.s = *reinterpret_cast<const u32x2_t*>(&ring.s[wave][u % kRing][2 * c]);
+    if (ZERO) b.z = ring.z[wave][u % kRing][c];
+  };
+  // The chunk's operands from LDS.
+  auto chunk_in = [&](int u, int m, u32x4_t (&a)[GU]) __attribute__((always_inline)) {
 #pragma unroll
     for (int t = 0; t < GU; ++t) a[t] = ring.rows[u % kRing][t][m][lane];
+  };
+  // The sums over its rows, the same in every column.
+  auto chunk_sum = [&](const u32x4_t (&a)[GU], f32x4_t& sum) __attribute__((always_inline)) {
     sum = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int t = 0; t < GU; ++t) sum = mfma16x16x32(a[t], flat, sum);
@@ -126,33 +141,33 @@ __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
       asm volatile("" : "+v"(sums[j]));   // here, not at the end: the parts would fill the registers
     }
   };
-  auto compute = [&](auto full, int u) __attribute__((always_inline)) {
-    const int slot = u % kRing;
+  const Int4Masks masks;
+  auto compute = [&](auto full, int u, const Words& b) __attribute__((always_inline)) {
     float s[4], z[4];
     u32x4_t bw[GU][4];
-    u32x4_t w[GU];
 #pragma unroll
-    for (int t = 0; t < GU; ++t) w[t] = ring.w[wave][slot][t][lane];
-    const u32x2_t sw = *reinterpret_cast<const u32x2_t*>(&ring.s[wave][slot][2 * c]);
-    const uint32_t zw = ZERO ? ring.z[wave][slot][c] : 0u;
+    for (int t = 0; t < GU; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) bw[t][j] = int4_operand(b.w[t][j], masks);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      s[j] = j & 1 ? bf16hi(sw[j >> 1]) : bf16lo(sw[j >> 1]);
-      if (ZERO) z[j] = -16.0f - (float)((zw >> (8 * j)) & 0xFFu);
-#pragma unroll
-      for (int t = 0; t < GU; ++t) bw[t][j] = int4_operand(w[t][j]);
+      s[j] = j & 1 ? bf16hi(b.s[j >> 1]) : bf16lo(b.s[j >> 1]);
+      if (ZERO) z[j] = -16.0f - (float)((b.z >> (8 * j)) & 0xFFu);
     }
     if (decltype(full)::value) {
-      // Full tiles, without branches: a chunk is read ahead of the previous
-      // one's products, and added behind the next one's.
-      u32x4_t a[2][GU];
+      // Full tiles, without branches: a chunk is read two ahead of its
+      // products, summed one ahead, and added behind the next one's.
+      u32x4_t a[3][GU];
       f32x4_t sum[2], part[2][4];
-      chunk_in(u, 0, a[0], sum[0]);
+      chunk_in(u, 0, a[0]);
+      chunk_in(u, 1, a[1]);
+      chunk_sum(a[0], sum[0]);
 #pragma unroll
       for (int m = 0; m < kChunks; ++m) {
         __builtin_amdgcn_sched_barrier(0);
-        if (m + 1 < kChunks) chunk_in(u, m + 1, a[(m + 1) & 1], sum[(m + 1) & 1]);
-        chunk_mul(a[m & 1], sum[m & 1], bw, z, part[m & 1]);
+        if (m + 2 < kChunks) chunk_in(u, m + 2, a[(m + 2) % 3]);
+        chunk_mul(a[m % 3], sum[m & 1], bw, z, part[m & 1]);
+        if (m + 1 < kChunks) chunk_sum(a[(m + 1) % 3], sum[(m + 1) & 1]);
         if (m > 0) chunk_add(acc[m - 1], part[(m - 1) & 1], s);
       }
       chunk_add(acc[kChunks - 1], part[(kChunks - 1) & 1], s);
@@ -162,7 +177,8 @@ __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
         if (m < nch) {
           u32x4_t a[GU];
           f32x4_t sum, part[4];
-          chunk_in(u, m, a, sum);
+          chunk_in(u, m, a);
+          chunk_sum(a, sum);
           chunk_mul(a, sum, bw, z, part);
           chunk_add(acc[m], part, s);
         }
@@ -173,16 +189,21 @@ __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
   load(0);
   load(1);
   load(2);
+  Words b;
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kLoads) : "memory");
-  __syncthreads();
+  words(0, b);
+  asm volatile("s_barrier" ::: "memory");
   // Loads retire in order: with those of two units still under way, the wave's
-  // part of unit u + 1 is in LDS.
+  // part of unit u + 1 is in LDS.  Its own weights it may read at once, the
+  // other waves' rows behind the barrier.  At the barrier every read of unit
+  // u's rows has returned (the products used it).
   auto run = [&](auto full) __attribute__((always_inline)) {
     for (int u = 0; u < nu; ++u) {
       load(u + 3);   // into the slot that unit u - 1 was read from
-      if (live) compute(full, u);
+      if (live) compute(full, u, b);
       asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kLoads) : "memory");
-      __syncthreads();
+      words(u + 1, b);
+      asm volatile("s_barrier" ::: "memory");
     }
   };
   if (nch == kChunks)
