@@ -37,6 +37,7 @@ struct Ring {
   u32x4_t w[kGemmWaves][kRing][GU][kWave];      // each wave's tiles
   uint32_t s[kGemmWaves][kRing][kWave];         // scales of its 64 columns, twice
   uint32_t z[kGemmWaves][kRing][kWave];         // zero points, four times
+  float sum[2][kChunks][16];                    // of each row's values over a unit, times `flat`
 };
 
 template <bool GATE_UP, int GU, bool ZERO>
@@ -116,11 +117,19 @@ __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
 #pragma unroll
     for (int t = 0; t < GU; ++t) a[t] = ring.rows[u % kRing][t][m][lane];
   };
-  // The sums over its rows, the same in every column.
-  auto chunk_sum = [&](const u32x4_t (&a)[GU], f32x4_t& sum) __attribute__((always_inline)) {
-    sum = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  // Unit u's sums over the rows of this wave's own chunk (whose fragments the
+  // wave itself brought in), for all waves behind the next barrier: one more
+  // product with a constant operand, the same in every column.
+  auto sum_rows = [&](int u) __attribute__((always_inline)) {
+    u32x4_t a[GU];
+    chunk_in(u, wave, a);
+    f32x4_t sum = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int t = 0; t < GU; ++t) sum = mfma16x16x32(a[t], flat, sum);
+    if (c == 0) *reinterpret_cast<f32x4_t*>(&ring.sum[u & 1][wave][4 * g]) = sum;
+  };
+  auto sum_in = [&](int u, int m) __attribute__((always_inline)) {
+    return *reinterpret_cast<const f32x4_t*>(&ring.sum[u & 1][m][4 * g]);
   };
   auto chunk_mul = [&](const u32x4_t (&a)[GU], const f32x4_t& sum, const u32x4_t (&bw)[GU][4], const float (&z)[4],
                        f32x4_t (&part)[4]) __attribute__((always_inline)) {
@@ -142,6 +151,12 @@ __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
     }
   };
   const Int4Masks masks;
+  // What a wave prepares of the next unit: loads retire in order, so with those
+  // of two units still under way its own part of unit u is in LDS.
+  auto next = [&](int u) __attribute__((always_inline)) {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kLoads) : "memory");
+    sum_rows(u);
+  };
   auto compute = [&](auto full, int u, const Words& b) __attribute__((always_inline)) {
     float s[4], z[4];
     u32x4_t bw[GU][4];
@@ -156,18 +171,23 @@ __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
     }
     if (decltype(full)::value) {
       // Full tiles, without branches: a chunk is read two ahead of its
-      // products, summed one ahead, and added behind the next one's.
+      // products and added behind the next one's.
       u32x4_t a[3][GU];
-      f32x4_t sum[2], part[2][4];
-      chunk_in(u, 0, a[0]);
-      chunk_in(u, 1, a[1]);
-      chunk_sum(a[0], sum[0]);
+      f32x4_t sum[3], part[2][4];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        chunk_in(u, m, a[m]);
+        sum[m] = sum_in(u, m);
+      }
 #pragma unroll
       for (int m = 0; m < kChunks; ++m) {
         __builtin_amdgcn_sched_barrier(0);
-        if (m + 2 < kChunks) chunk_in(u, m + 2, a[(m + 2) % 3]);
-        chunk_mul(a[m % 3], sum[m & 1], bw, z, part[m & 1]);
-        if (m + 1 < kChunks) chunk_sum(a[(m + 1) % 3], sum[(m + 1) & 1]);
+        if (m + 2 < kChunks) {
+          chunk_in(u, m + 2, a[(m + 2) % 3]);
+          sum[(m + 2) % 3] = sum_in(u, m + 2);
+        }
+        chunk_mul(a[m % 3], sum[m % 3], bw, z, part[m & 1]);
+        if (m == kChunks / 2) next(u + 1);
         if (m > 0) chunk_add(acc[m - 1], part[(m - 1) & 1], s);
       }
       chunk_add(acc[kChunks - 1], part[(kChunks - 1) & 1], s);
@@ -176,13 +196,13 @@ __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
       for (int m = 0; m < kChunks; ++m) {
         if (m < nch) {
           u32x4_t a[GU];
-          f32x4_t sum, part[4];
+          f32x4_t part[4];
           chunk_in(u, m, a);
-          chunk_sum(a, sum);
-          chunk_mul(a, sum, bw, z, part);
+          chunk_mul(a, sum_in(u, m), bw, z, part);
           chunk_add(acc[m], part, s);
         }
       }
+      next(u + 1);
     }
   };
 
@@ -190,20 +210,20 @@ __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
   load(1);
   load(2);
   Words b;
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kLoads) : "memory");
+  next(0);
   words(0, b);
-  asm volatile("s_barrier" ::: "memory");
-  // Loads retire in order: with those of two units still under way, the wave's
-  // part of unit u + 1 is in LDS.  Its own weights it may read at once, the
-  // other waves' rows behind the barrier.  At the barrier every read of unit
-  // u's rows has returned (the products used it).
+  __syncthreads();
+  // The wave's own weights it may read at once, the other waves' rows and sums
+  // behind the barrier, where every read of this unit's has returned too.
   auto run = [&](auto full) __attribute__((always_inline)) {
     for (int u = 0; u < nu; ++u) {
       load(u + 3);   // into the slot that unit u - 1 was read from
-      if (live) compute(full, u, b);
-      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kLoads) : "memory");
+      if (live)
+        compute(full, u, b);
+      else
+        next(u + 1);
       words(u + 1, b);
-      asm volatile("s_barrier" ::: "memory");
+      __syncthreads();
     }
   };
   if (nch == kChunks)
