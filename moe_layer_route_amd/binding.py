@@ -160,19 +160,32 @@ def _on(t, stream):
     return torch.cuda.stream(stream)
 
 
+# torch's own generated code reads the raw handle this way; building a stream object for it takes 2 us longer
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _here(t):
+    """Raw handle of the current stream of t's device."""
+    index = t.get_device()
+    return _raw_stream(index) if _raw_stream else torch.cuda.current_stream(index).cuda_stream
+
+
 def _at(t):
-    """_ptr, with an address that is never read for a tensor without elements (a call for no tokens is valid)."""
-    if t is None:
-        return None
-    return ctypes.c_void_p(t.data_ptr() if t.numel() else 4096)
+    """A tensor's address; one that is never read where it has no elements (a call for no tokens is valid)."""
+    return None if t is None else t.data_ptr() or 4096
 
 
 def _dev_as(first, *ts):
-    """_dev, and every tensor on the device of the first."""
-    _dev(first, *ts)
+    """Every tensor is contiguous and on the device of the first, a GPU."""
+    index = first.get_device()
+    ok = index >= 0 and first.is_contiguous()
     for t in ts:
-        if t is not None and t.device != first.device:
-            raise MoEError(f"tensors are on {first.device} and on {t.device}")
+        if t is not None and (t.get_device() != index or not t.is_contiguous()):
+            ok = False
+    if not ok:
+        _dev(first, *ts)
+        raise MoEError("tensors are on several devices: "
+                       + ", ".join(sorted({str(t.device) for t in (first, *ts) if t is not None})))
 
 
 # ---------------------------------------------------------------------------
@@ -786,13 +799,16 @@ def moe_forward_ep_fp8(x, Wr, br, Wgu_q_local, Wgu_s_local, bgu_local, Wd_q_loca
 # ---------------------------------------------------------------------------
 # residual addition and RMS norm in front of the block
 # ---------------------------------------------------------------------------
-def _norm_args(x, gamma, residual, residual_out, y, y_name="y"):
+def _norm_args(x, gamma, residual, residual_out, y):
     """x, residual, residual_out, y [T][H] and gamma [H], bf16; residual_out only beside a residual."""
     _dims(x, "x", 2)
-    T, H = x.shape
-    for t, name, shape in ((x, "x", (T, H)), (gamma, "gamma", (H,)), (residual, "residual", (T, H)),
-                           (residual_out, "residual_out", (T, H)), (y, y_name, (T, H))):
-        _req(t, name, shape, torch.bfloat16)
+    T, H = shape = x.shape
+    bf16 = torch.bfloat16
+    for t in (x, residual, residual_out, y):
+        if t is not None and (t.shape != shape or t.dtype != bf16):
+            for u, name in ((x, "x"), (residual, "residual"), (residual_out, "residual_out"), (y, "y")):
+                _req(u, name, (T, H), bf16)
+    _req(gamma, "gamma", (H,), bf16)
     if residual is None and residual_out is not None:
         raise MoEError("residual_out: given without a residual")
     return T, H
@@ -810,7 +826,7 @@ def moe_add_rmsnorm(x, gamma, residual=None, eps: float = 1e-5, y=None, residual
         if residual is not None and residual_out is None:
             residual_out = torch.empty_like(x)
         _check(library().moe_add_rmsnorm(_at(x), _at(residual), _at(gamma), T, H, eps, _at(residual_out), _at(y),
-                                         _stream(None)), "moe_add_rmsnorm")
+                                         _here(x)), "moe_add_rmsnorm")
     return y, x if residual is None else residual_out
 
 
@@ -832,7 +848,7 @@ def moe_add_rmsnorm_fp8(x, gamma, residual=None, eps: float = 1e-5, y=None, resi
         if scales is None:
             scales = torch.empty((T,), dtype=torch.float32, device=x.device)
         _check(library().moe_add_rmsnorm_fp8(_at(x), _at(residual), _at(gamma), T, H, eps, _at(residual_out),
-                                             _at(y), _at(codes), _at(scales), _stream(None)), "moe_add_rmsnorm_fp8")
+                                             _at(y), _at(codes), _at(scales), _here(x)), "moe_add_rmsnorm_fp8")
     return y, codes, scales, x if residual is None else residual_out
 
 
@@ -864,7 +880,7 @@ def moe_forward_norm_fp8(x, gamma, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, k:
                                             _at(Wgu_s), _at(bgu), _at(Wd_q), _at(Wd_s), _at(bd), T, H, E, k, I,
                                             _at(residual_out), _at(y), _at(topk_ids), _at(topk_w), _at(workspace),
                                             workspace.numel() * workspace.element_size(), path_code(path),
-                                            _stream(None))
+                                            _here(x))
         _check(st, "moe_forward_norm_fp8")
     return y, x if residual is None else residual_out
 
@@ -922,7 +938,7 @@ def moe_quantize_int4(W, G: int = 64, zeros: bool = False, stream=None):
         q = torch.empty(_int4_shape(E, K, N), dtype=torch.uint8, device=W.device)
         s = torch.empty((E, -(-K // G), N), dtype=torch.bfloat16, device=W.device)
         z = torch.empty((E, -(-K // G), N), dtype=torch.uint8, device=W.device) if zeros else None
-        _check(library().moe_quantize_int4(_at(W), E, K, N, G, _at(q), _at(s), _at(z), _stream(None)),
+        _check(library().moe_quantize_int4(_at(W), E, K, N, G, _at(q), _at(s), _at(z), _here(W)),
                "moe_quantize_int4")
     return q, s, z
 
@@ -935,7 +951,7 @@ def moe_pack_int4(codes, stream=None):
     _dev(codes)
     with _on(codes, stream):
         q = torch.empty(_int4_shape(E, K, N), dtype=torch.uint8, device=codes.device)
-        _check(library().moe_pack_int4(_at(codes), E, K, N, _at(q), _stream(None)), "moe_pack_int4")
+        _check(library().moe_pack_int4(_at(codes), E, K, N, _at(q), _here(codes)), "moe_pack_int4")
     return q
 
 
@@ -955,7 +971,7 @@ def _forward_int4(name, x, Wr, br, Wgu_q, Wgu_s, Wgu_z, bgu, Wd_q, Wd_s, Wd_z, b
         st = getattr(library(), name)(_at(x), _at(Wr), _at(br), _at(Wgu_q), _at(Wgu_s), _at(Wgu_z), _at(bgu),
                                       _at(Wd_q), _at(Wd_s), _at(Wd_z), _at(bd), T, H, E, k, I, G, *before, _at(y),
                                       _at(topk_ids), _at(topk_w), *between, _at(workspace),
-                                      workspace.numel() * workspace.element_size(), path_code(path), _stream(None))
+                                      workspace.numel() * workspace.element_size(), path_code(path), _here(x))
         _check(st, name.removesuffix("_ex"))
     return y
 
@@ -1015,7 +1031,7 @@ def moe_gate_up_int4(x, Wgu_q, Wgu_s, bgu, cnt, off, rows, k: int, Wgu_z=None, h
         if h is None:
             h = torch.empty((max(T * k, 1), I), dtype=torch.bfloat16, device=x.device)
         _check(library().moe_gate_up_int4(_at(x), _at(Wgu_q), _at(Wgu_s), _at(Wgu_z), _at(bgu), _at(cnt), _at(off),
-                                          _at(rows), T, H, E, k, I, G, _at(h), path_code(path), _stream(None)),
+                                          _at(rows), T, H, E, k, I, G, _at(h), path_code(path), _here(x)),
                "moe_gate_up_int4")
     return h[:T * k]
 
@@ -1035,7 +1051,7 @@ def moe_down_int4(h, Wd_q, Wd_s, bd, cnt, off, T: int, k: int, Wd_z=None, o=None
         if o is None:
             o = torch.empty((max(T * k, 1), H), dtype=torch.float32, device=h.device)
         _check(library().moe_down_int4(_at(h), _at(Wd_q), _at(Wd_s), _at(Wd_z), _at(bd), _at(cnt), _at(off), T, H,
-                                       E, k, I, G, _at(o), path_code(path), _stream(None)), "moe_down_int4")
+                                       E, k, I, G, _at(o), path_code(path), _here(h)), "moe_down_int4")
     return o[:T * k]
 
 
