@@ -111,7 +111,7 @@ __global__ __launch_bounds__(kQThreads) void int4_pack_kernel(const uint8_t* __r
 
 // ---------------------------------------------------------------------------
 // Weight streaming: a workgroup owns one expert and one strip of 64 columns;
-// its four waves split K and stream their part of the strip, a contiguous
+// its WAVES waves split K and stream their part of the strip, a contiguous
 // kilobyte a tile, four tiles (a quad, 128 values of K) at a time and one quad
 // ahead.  16 MG token rows per pass over the strip.
 //   Operands of v_mfma_f32_16x16x32_bf16: A = 16 token rows, lane (row c,
@@ -124,7 +124,7 @@ __global__ __launch_bounds__(kQThreads) void int4_pack_kernel(const uint8_t* __r
 //   operand (-24 without zero points, 1 with them).  The group's sum times its
 //   scale is added to the accumulators in float32.
 // ---------------------------------------------------------------------------
-constexpr int kWaves = 4;
+constexpr int kCus = 256;
 
 // A quad's loads: tiles, token rows, and the lane's four columns' scales and
 // zero points of its 4 / GS groups.
@@ -136,20 +136,52 @@ struct Quad {
   uint32_t z[NGQ];
 };
 
-template <bool GATE_UP, int MG, int GS, bool ZERO>
-__global__ __launch_bounds__(kWaves * kWave, MG == 1 ? 3 : 2) void int4_stream_kernel(
+// The n-th expert that has rows (in order; E <= 256): its index, row count and
+// first row.  Every lane gets the same; false if there are fewer.
+__device__ __forceinline__ bool nth_live_expert(const int32_t* __restrict__ cnt, const int32_t* __restrict__ off, int E,
+                                                int n, int lane, int& e, int& M, int& row0) {
+  int c[4], o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int at = kWave * i + lane;
+    c[i] = at < E ? cnt[at] : 0;
+    o[i] = at < E ? off[at] : 0;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t live = __ballot(c[i] > 0);
+    const int here = __popcll(live);
+    if (n < here) {
+      const int rank = __popcll(live & ((1ull << lane) - 1));
+      const int src = __ffsll((unsigned long long)__ballot(c[i] > 0 && rank == n)) - 1;
+      e = kWave * i + src;
+      M = __builtin_amdgcn_readlane(c[i], src);
+      row0 = __builtin_amdgcn_readlane(o[i], src);
+      return true;
+    }
+    n -= here;
+  }
+  return false;
+}
+
+template <bool GATE_UP, int MG, int GS, bool ZERO, int WAVES>
+__global__ __launch_bounds__(WAVES * kWave, WAVES == 4 && MG == 1 ? 3 : 2) void int4_stream_kernel(
     const bf16_t* __restrict__ A, const uint8_t* __restrict__ Wq, const uint16_t* __restrict__ Ws,
     const uint8_t* __restrict__ Wz, const bf16_t* __restrict__ bias, const int32_t* __restrict__ cnt,
-    const int32_t* __restrict__ off, const int32_t* __restrict__ rows, int K, int N, int kslots,
+    const int32_t* __restrict__ off, const int32_t* __restrict__ rows, int K, int N, int E, int kslots,
     int64_t a_rows, void* __restrict__ out) {
   constexpr int NGQ = 4 / GS;
-  __shared__ float red[kWaves][4][4][kWave];   // [wave][call j][element v][lane]
+  __shared__ float red[WAVES][4][4][kWave];   // [wave][call j][element v][lane]
 
-  const int e = blockIdx.y, M = cnt[e];
-  if (M == 0) return;   // block-uniform
-  const int row0 = off[e];
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  int e = blockIdx.y, M, row0;
+  if ((int)gridDim.y == E) {
+    M = cnt[e], row0 = off[e];
+    if (M == 0) return;   // block-uniform
+  } else if (!nth_live_expert(cnt, off, E, blockIdx.y, lane, e, M, row0)) {
+    return;               // block-uniform
+  }
   const int g = lane >> 4, c = lane & 15;
   const int nkt = K / kTileK, nq = (nkt + 3) / 4, ng = (nkt + GS - 1) / GS;
   // N % 8 == 0: a lane's four columns are all in range or all out
@@ -160,18 +192,20 @@ __global__ __launch_bounds__(kWaves * kWave, MG == 1 ? 3 : 2) void int4_stream_k
   const rsrc_t s_rs = make_rsrc(Ws + (size_t)e * ng * N, (uint32_t)ng * N * 2);
   const rsrc_t z_rs = make_rsrc(ZERO ? Wz + (size_t)e * ng * N : Wq, ZERO ? (uint32_t)ng * N : 0u);
   const rsrc_t a_rs = make_rsrc(GATE_UP ? A : A + (size_t)row0 * K, (uint32_t)((size_t)(GATE_UP ? a_rows : M) * K * 2));
-  const int q_begin = nq * wave / kWaves, q_end = nq * (wave + 1) / kWaves;
+  const uint32_t* bp = reinterpret_cast<const uint32_t*>(bias + (size_t)e * N + s_col);   // 4-byte aligned
+  const uint32_t b01 = bp[0], b23 = bp[1];
+  const int q_begin = nq * wave / WAVES, q_end = nq * (wave + 1) / WAVES;
   const u32x4_t flat = ZERO ? u32x4_t{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}
                             : u32x4_t{0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u};
-
   const Int4Masks masks;
+
   for (int r0 = 0; r0 < M; r0 += 16 * MG) {
     const int nch = min(MG, (M - r0 + 15) / 16);   // block-uniform
-    uint32_t a_off[MG];
+    int slot[MG];
 #pragma unroll
     for (int m = 0; m < MG; ++m) {
       const int r = min(r0 + 16 * m + c, M - 1);   // rows past M repeat the last one
-      a_off[m] = ((uint32_t)(GATE_UP ? rows[row0 + r] / kslots : r) * (uint32_t)K + 8u * g) * 2u;
+      slot[m] = GATE_UP ? rows[row0 + r] : r;
     }
     f32x4_t acc[MG][4];
 #pragma unroll
@@ -179,23 +213,29 @@ __global__ __launch_bounds__(kWaves * kWave, MG == 1 ? 3 : 2) void int4_stream_k
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[m][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-    auto load = [&](int q, Quad<MG, NGQ>& b) {
+    auto load_w = [&](int q, Quad<MG, NGQ>& b) __attribute__((always_inline)) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int t = 0; t < 4; ++t)
         b.w[t] = buf_ld16<2>(w_rs, 16u * lane, (uint32_t)min(4 * q + t, nkt - 1) * kTileBytes);   // read once
-      }
 #pragma unroll
       for (int i = 0; i < NGQ; ++i) {
         const uint32_t at = (uint32_t)min(NGQ * q + i, ng - 1) * N;
         b.s[i] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(s_rs, (int)(2u * s_col), (int)(2u * at), 0));
         if (ZERO) b.z[i] = __builtin_amdgcn_raw_buffer_load_b32(z_rs, (int)s_col, (int)at, 0);
       }
+    };
+    uint32_t a_off[MG];
+    auto load_a = [&](int q, Quad<MG, NGQ>& b) __attribute__((always_inline)) {
 #pragma unroll
       for (int m = 0; m < MG; ++m)
 #pragma unroll
         for (int t = 0; t < 4; ++t) b.a[m][t] = buf_ld16(a_rs, a_off[m], 64u * (uint32_t)min(4 * q + t, nkt - 1));
     };
-    auto compute = [&](int q, Quad<MG, NGQ>& b) {
+    auto load = [&](int q, Quad<MG, NGQ>& b) __attribute__((always_inline)) {
+      load_w(q, b);
+      load_a(q, b);
+    };
+    auto compute = [&](int q, Quad<MG, NGQ>& b) __attribute__((always_inline)) {
       if (4 * q + 4 > nkt) {   // the last quad may be short: nothing from its missing tiles
 #pragma unroll
         for (int t = 1; t < 4; ++t)
@@ -250,32 +290,31 @@ __global__ __launch_bounds__(kWaves * kWave, MG == 1 ? 3 : 2) void int4_stream_k
     };
 
     if (q_begin < q_end) {
+      // The first two quads' weights are under way while the rows' slots arrive.
       Quad<MG, NGQ> b0, b1;
       int q = q_begin;
-      load(q, b0);
-      for (; q + 2 < q_end; q += 2) {
-        load(q + 1, b1);
+      load_w(q, b0);
+      load_w(min(q + 1, q_end - 1), b1);
+#pragma unroll
+      for (int m = 0; m < MG; ++m)
+        a_off[m] = ((uint32_t)(GATE_UP ? slot[m] / kslots : slot[m]) * (uint32_t)K + 8u * g) * 2u;
+      load_a(q, b0);
+      load_a(min(q + 1, q_end - 1), b1);
+      for (; q + 4 <= q_end; q += 2) {
         compute(q, b0);
         load(q + 2, b0);
         compute(q + 1, b1);
+        load(q + 3, b1);
       }
-      if (q + 1 < q_end) {
-        load(q + 1, b1);
-        compute(q, b0);
-        compute(q + 1, b1);
-      } else {
-        compute(q, b0);
-      }
+      compute(q, b0);   // one to three quads are left
+      if (q + 2 < q_end) load(q + 2, b0);
+      if (q + 1 < q_end) compute(q + 1, b1);
+      if (q + 2 < q_end) compute(q + 2, b0);
     }
 
-    // Sum the K partials (wave 0, 1, 2, 3); wave w finishes element v = w (row
-    // 4 g + w of each chunk) of the lane's four columns.
-    float bb[4];
-    {
-      const uint32_t* bp = reinterpret_cast<const uint32_t*>(bias + (size_t)e * N + s_col);   // 4-byte aligned
-      const uint32_t b01 = bp[0], b23 = bp[1];
-      bb[0] = bf16lo(b01), bb[1] = bf16hi(b01), bb[2] = bf16lo(b23), bb[3] = bf16hi(b23);
-    }
+    // Sum the K partials in the waves' order; wave w < 4 finishes element v = w
+    // (row 4 g + w of each chunk) of the lane's four columns.
+    const float bb[4] = {bf16lo(b01), bf16hi(b01), bf16lo(b23), bf16hi(b23)};
 #pragma unroll
     for (int m = 0; m < MG; ++m) {
       if (m < nch) {
@@ -284,16 +323,16 @@ __global__ __launch_bounds__(kWaves * kWave, MG == 1 ? 3 : 2) void int4_stream_k
 #pragma unroll
           for (int v = 0; v < 4; ++v) red[wave][j][v][lane] = acc[m][j][v];
         __syncthreads();
-        float sum[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float t = 0.f;
-#pragma unroll
-          for (int w = 0; w < kWaves; ++w) t += red[w][j][wave][lane];
-          sum[j] = t + bb[j];
-        }
         const int r = r0 + 16 * m + 4 * g + wave;
-        if (r < M && col_ok) {
+        if (wave < 4 && r < M && col_ok) {
+          float sum[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float t = 0.f;
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) t += red[w][j][wave & 3][lane];
+            sum[j] = t + bb[j];
+          }
           const size_t orow = (size_t)(row0 + r);
           if (GATE_UP)
             *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(out) + orow * (N / 2) + ncol / 2) =
@@ -308,18 +347,29 @@ __global__ __launch_bounds__(kWaves * kWave, MG == 1 ? 3 : 2) void int4_stream_k
   }
 }
 
-template <bool GATE_UP, int MG, int GS>
+template <bool GATE_UP, int MG, int GS, int WAVES>
 hipError_t launch_stream(const void* A, const void* Wq, const void* Ws, const void* Wz, const void* bias,
                          const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T, int K, int N, int E,
-                         int k, void* out, hipStream_t stream) {
-  dim3 grid((unsigned)((N + kTileN - 1) / kTileN), (unsigned)E);
-  auto kern = Wz ? int4_stream_kernel<GATE_UP, MG, GS, true> : int4_stream_kernel<GATE_UP, MG, GS, false>;
-  hipLaunchKernelGGL(kern, grid, dim3(kWaves * kWave), 0, stream, (const bf16_t*)A, (const uint8_t*)Wq,
-                     (const uint16_t*)Ws, (const uint8_t*)Wz, (const bf16_t*)bias, cnt, off, rows, K, N, k, T, out);
+                         int k, int experts, void* out, hipStream_t stream) {
+  dim3 grid((unsigned)((N + kTileN - 1) / kTileN), (unsigned)experts);
+  auto kern = Wz ? int4_stream_kernel<GATE_UP, MG, GS, true, WAVES> : int4_stream_kernel<GATE_UP, MG, GS, false, WAVES>;
+  hipLaunchKernelGGL(kern, grid, dim3(WAVES * kWave), 0, stream, (const bf16_t*)A, (const uint8_t*)Wq,
+                     (const uint16_t*)Ws, (const uint8_t*)Wz, (const bf16_t*)bias, cnt, off, rows, K, N, E, k, T, out);
   return hipGetLastError();
 }
 
-// Mean rows per expert up to which one 16-row chunk a pass is enough.
+template <bool GATE_UP, int MG, int WAVES>
+hipError_t launch_group(int G, const void* A, const void* Wq, const void* Ws, const void* Wz, const void* bias,
+                        const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T, int K, int N, int E,
+                        int k, int experts, void* out, hipStream_t stream) {
+  auto launch = G == 32   ? launch_stream<GATE_UP, MG, 1, WAVES>
+                : G == 64 ? launch_stream<GATE_UP, MG, 2, WAVES>
+                          : launch_stream<GATE_UP, MG, 4, WAVES>;
+  return launch(A, Wq, Ws, Wz, bias, cnt, off, rows, T, K, N, E, k, experts, out, stream);
+}
+
+// Mean rows per expert up to which one 16-row chunk a pass is enough.  Where no
+// CU would get a second workgroup, eight waves halve each one's share of K.
 constexpr int64_t kOneChunkMeanRows = 10;
 
 template <bool GATE_UP>
@@ -328,12 +378,14 @@ hipError_t launch_int4(const void* A, const void* Wq, const void* Ws, const void
                        int G, void* out, hipStream_t stream) {
   // 32-bit offsets into the token rows (of one expert, for down)
   if ((GATE_UP ? T : T * k) * K * 2 >= (int64_t)1 << 32) return hipErrorNotSupported;
-  const bool one = T * k <= kOneChunkMeanRows * E;
-  auto pick = [&](auto one_c, auto two_c) { return one ? one_c : two_c; };
-  auto launch = G == 32   ? pick(launch_stream<GATE_UP, 1, 1>, launch_stream<GATE_UP, 2, 1>)
-                : G == 64 ? pick(launch_stream<GATE_UP, 1, 2>, launch_stream<GATE_UP, 2, 2>)
-                          : pick(launch_stream<GATE_UP, 1, 4>, launch_stream<GATE_UP, 2, 4>);
-  return launch(A, Wq, Ws, Wz, bias, cnt, off, rows, T, K, N, E, k, out, stream);
+  // No more experts than slots have rows: with fewer slots than experts the
+  // workgroups go to the ones that have.
+  const int experts = (int)(T * k < E ? T * k : E);
+  const int64_t workgroups = (int64_t)experts * ((N + kTileN - 1) / kTileN);
+  auto launch = T * k > kOneChunkMeanRows * E ? launch_group<GATE_UP, 2, 4>
+                : workgroups <= kCus          ? launch_group<GATE_UP, 1, 8>
+                                              : launch_group<GATE_UP, 1, 4>;
+  return launch(G, A, Wq, Ws, Wz, bias, cnt, off, rows, T, K, N, E, k, experts, out, stream);
 }
 
 }  // namespace
