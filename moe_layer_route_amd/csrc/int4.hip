@@ -20,6 +20,8 @@
 #include "int4_device.h"
 #include "launch.h"
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
@@ -118,6 +120,10 @@ __global__ __launch_bounds__(kQThreads) void int4_pack_kernel(const uint8_t* __r
 //   group g) holding K = 32 kt + 8 g .. + 7; B = word j of the tile, i.e. MFMA
 //   column c of call j is column 4 c + j of the strip, so the four columns of
 //   a lane are two (gate, up) pairs.
+//   NS strips share the token rows' loads: rows cost as many bytes of the
+//   path from L2 into a CU as the 64 columns they meet, and twice as many with
+//   two chunks (T = 192 of 32 experts, 24 rows each: 90 us with one strip, 74
+//   with two; with one chunk two strips gain nothing and halve the workgroups).
 //   A word gives 16 + q exactly (seven integer instructions for eight codes).
 //   The 16 and the zero point come off through the accumulator: a group's sum
 //   starts at -(16 + z) sum(a), where sum(a) is one more MFMA with a constant
@@ -125,16 +131,6 @@ __global__ __launch_bounds__(kQThreads) void int4_pack_kernel(const uint8_t* __r
 //   scale is added to the accumulators in float32.
 // ---------------------------------------------------------------------------
 constexpr int kCus = 256;
-
-// A quad's loads: tiles, token rows, and the lane's four columns' scales and
-// zero points of its 4 / GS groups.
-template <int MG, int NGQ>
-struct Quad {
-  u32x4_t w[4];
-  u32x4_t a[MG][4];
-  u32x2_t s[NGQ];
-  uint32_t z[NGQ];
-};
 
 // The n-th expert that has rows (in order; E <= 256): its index, row count and
 // first row.  Every lane gets the same; false if there are fewer.
@@ -164,8 +160,8 @@ __device__ __forceinline__ bool nth_live_expert(const int32_t* __restrict__ cnt,
   return false;
 }
 
-template <bool GATE_UP, int MG, int GS, bool ZERO, int WAVES>
-__global__ __launch_bounds__(WAVES * kWave, WAVES == 4 && MG == 1 ? 3 : 2) void int4_stream_kernel(
+template <bool GATE_UP, int MG, int GS, bool ZERO, int WAVES, int NS>
+__global__ __launch_bounds__(WAVES * kWave, WAVES == 8 || MG > 1 ? 2 : 3) void int4_stream_kernel(
     const bf16_t* __restrict__ A, const uint8_t* __restrict__ Wq, const uint16_t* __restrict__ Ws,
     const uint8_t* __restrict__ Wz, const bf16_t* __restrict__ bias, const int32_t* __restrict__ cnt,
     const int32_t* __restrict__ off, const int32_t* __restrict__ rows, int K, int N, int E, int kslots,
@@ -184,17 +180,25 @@ __global__ __launch_bounds__(WAVES * kWave, WAVES == 4 && MG == 1 ? 3 : 2) void 
   }
   const int g = lane >> 4, c = lane & 15;
   const int nkt = K / kTileK, nq = (nkt + 3) / 4, ng = (nkt + GS - 1) / GS;
-  // N % 8 == 0: a lane's four columns are all in range or all out
-  const int ncol = blockIdx.x * kTileN + 4 * c;
-  const bool col_ok = ncol < N;
-  const uint32_t s_col = (uint32_t)min(ncol, N - 4);
-  const rsrc_t w_rs = make_rsrc(Wq + ((size_t)e * gridDim.x + blockIdx.x) * (size_t)nkt * kTileBytes, nkt * kTileBytes);
-  const rsrc_t s_rs = make_rsrc(Ws + (size_t)e * ng * N, (uint32_t)ng * N * 2);
-  const rsrc_t z_rs = make_rsrc(ZERO ? Wz + (size_t)e * ng * N : Wq, ZERO ? (uint32_t)ng * N : 0u);
-  const rsrc_t a_rs = make_rsrc(GATE_UP ? A : A + (size_t)row0 * K, (uint32_t)((size_t)(GATE_UP ? a_rows : M) * K * 2));
-  const uint32_t* bp = reinterpret_cast<const uint32_t*>(bias + (size_t)e * N + s_col);   // 4-byte aligned
-  const uint32_t b01 = bp[0], b23 = bp[1];
+  // N % 8 == 0: a lane's four columns of a strip are all in range or all out
+  const int strips = (N + kTileN - 1) / kTileN;
+  int ncol[NS];
+  uint32_t s_col[NS];
+  const uint8_t* w_base[NS];
+  uint32_t b01[NS], b23[NS];
+#pragma unroll
+  for (int n = 0; n < NS; ++n) {
+    const int strip = blockIdx.x * NS + n;
+    ncol[n] = strip * kTileN + 4 * c;
+    s_col[n] = (uint32_t)min(ncol[n], N - 4);
+    w_base[n] = Wq + ((size_t)e * strips + min(strip, strips - 1)) * (size_t)nkt * kTileBytes;
+    const uint32_t* bp = reinterpret_cast<const uint32_t*>(bias + (size_t)e * N + s_col[n]);   // 4-byte aligned
+    b01[n] = bp[0], b23[n] = bp[1];
+  }
+  const bf16_t* a_base = GATE_UP ? A : A + (size_t)row0 * K;
+  const uint32_t a_bytes = (uint32_t)((size_t)(GATE_UP ? a_rows : M) * K * 2);
   const int q_begin = nq * wave / WAVES, q_end = nq * (wave + 1) / WAVES;
+  const int kt_end = min(nkt, 4 * q_end);
   const u32x4_t flat = ZERO ? u32x4_t{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}
                             : u32x4_t{0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u};
   const Int4Masks masks;
@@ -207,164 +211,183 @@ __global__ __launch_bounds__(WAVES * kWave, WAVES == 4 && MG == 1 ? 3 : 2) void 
       const int r = min(r0 + 16 * m + c, M - 1);   // rows past M repeat the last one
       slot[m] = GATE_UP ? rows[row0 + r] : r;
     }
-    f32x4_t acc[MG][4];
+    f32x4_t acc[NS][MG][4];
 #pragma unroll
-    for (int m = 0; m < MG; ++m)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[m][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-    auto load_w = [&](int q, Quad<MG, NGQ>& b) __attribute__((always_inline)) {
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-        b.w[t] = buf_ld16<2>(w_rs, 16u * lane, (uint32_t)min(4 * q + t, nkt - 1) * kTileBytes);   // read once
-#pragma unroll
-      for (int i = 0; i < NGQ; ++i) {
-        const uint32_t at = (uint32_t)min(NGQ * q + i, ng - 1) * N;
-        b.s[i] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(s_rs, (int)(2u * s_col), (int)(2u * at), 0));
-        if (ZERO) b.z[i] = __builtin_amdgcn_raw_buffer_load_b32(z_rs, (int)s_col, (int)at, 0);
-      }
-    };
-    uint32_t a_off[MG];
-    auto load_a = [&](int q, Quad<MG, NGQ>& b) __attribute__((always_inline)) {
+    for (int n = 0; n < NS; ++n)
 #pragma unroll
       for (int m = 0; m < MG; ++m)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) b.a[m][t] = buf_ld16(a_rs, a_off[m], 64u * (uint32_t)min(4 * q + t, nkt - 1));
+        for (int j = 0; j < 4; ++j) acc[n][m][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+    // Tile kt's codes and rows; one that is not there (past K, or past the wave's
+    // share) reads nothing and gives zeros.
+    u32x4_t w[NS][4], a[MG][4];
+    auto load_w = [&](int n, int t, int kt) __attribute__((always_inline)) {
+      w[n][t] = buf_ld16<2>(make_rsrc(w_base[n], kt < kt_end ? nkt * kTileBytes : 0), 16u * lane,
+                               (uint32_t)kt * kTileBytes);   // read once
     };
-    auto load = [&](int q, Quad<MG, NGQ>& b) __attribute__((always_inline)) {
-      load_w(q, b);
-      load_a(q, b);
+    uint32_t a_off[MG];
+    auto load_a = [&](int t, int kt) __attribute__((always_inline)) {
+      const rsrc_t a_rs = make_rsrc(a_base, kt < kt_end ? a_bytes : 0u);
+#pragma unroll
+      for (int m = 0; m < MG; ++m) a[m][t] = buf_ld16(a_rs, a_off[m], 64u * (uint32_t)kt);
     };
-    auto compute = [&](int q, Quad<MG, NGQ>& b) __attribute__((always_inline)) {
-      if (4 * q + 4 > nkt) {   // the last quad may be short: nothing from its missing tiles
-#pragma unroll
-        for (int t = 1; t < 4; ++t)
-          if (4 * q + t >= nkt)
-#pragma unroll
-            for (int m = 0; m < MG; ++m) b.a[m][t] = u32x4_t{0u, 0u, 0u, 0u};
-      }
+    u32x2_t s[NS][NGQ];
+    uint32_t z[NS][NGQ];
+    auto load_s = [&](int q) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < NGQ; ++i) {
-        // one group after the other (below, its sums are added at once): the
-        // compiler would otherwise keep every group's partial sums to the end
-        __builtin_amdgcn_sched_barrier(0);
-        float s[4], z[4];
+        // a group past K has the scale 0
+        const bool in = NGQ * q + i < ng;
+        const rsrc_t s_rs = make_rsrc(Ws + (size_t)e * ng * N, in ? (uint32_t)ng * N * 2 : 0u);
+        const uint32_t at = (uint32_t)(NGQ * q + i) * N;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s[j] = j & 1 ? bf16hi(b.s[i][j >> 1]) : bf16lo(b.s[i][j >> 1]);
-          if (ZERO) z[j] = -16.0f - (float)((b.z[i] >> (8 * j)) & 0xFFu);
+        for (int n = 0; n < NS; ++n) {
+          s[n][i] = __builtin_bit_cast(
+              u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(s_rs, (int)(2u * s_col[n]), (int)(2u * at), 0));
+          if (ZERO)
+            z[n][i] = __builtin_amdgcn_raw_buffer_load_b32(make_rsrc(Wz + (size_t)e * ng * N, in ? (uint32_t)ng * N : 0u),
+                                                           (int)s_col[n], (int)at, 0);
         }
-        f32x4_t part[MG][4];
+      }
+    };
+    // One quad's products; each tile's registers are refilled with the next
+    // quad's as soon as its last product has read them.
+    auto quad = [&](auto more, int q) __attribute__((always_inline)) {
+      constexpr bool kMore = decltype(more)::value;
+      u32x2_t sq[NS][NGQ];
+      uint32_t zq[NS][NGQ];
+#pragma unroll
+      for (int n = 0; n < NS; ++n)
+#pragma unroll
+        for (int i = 0; i < NGQ; ++i) {
+          sq[n][i] = s[n][i];
+          if (ZERO) zq[n][i] = z[n][i];
+        }
+      if (kMore) load_s(q + 1);
+#pragma unroll
+      for (int i = 0; i < NGQ; ++i) {
+        f32x4_t sum[MG];
 #pragma unroll
         for (int m = 0; m < MG; ++m) {
-          f32x4_t sum = f32x4_t{0.f, 0.f, 0.f, 0.f};
+          sum[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int t = GS * i; t < GS * i + GS; ++t) sum = mfma16x16x32(b.a[m][t], flat, sum);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) part[m][j][v] = ZERO ? z[j] * sum[v] : sum[v];
+          for (int t = GS * i; t < GS * i + GS; ++t) sum[m] = mfma16x16x32(a[m][t], flat, sum[m]);
         }
 #pragma unroll
-        for (int t = GS * i; t < GS * i + GS; ++t)
+        for (int n = 0; n < NS; ++n) {
+          // one group of one strip after the other (below, its sums are added
+          // at once): the compiler would otherwise keep all partial sums to the end
+          __builtin_amdgcn_sched_barrier(0);
+          float sf[4], zf[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const u32x4_t bw = int4_operand(b.w[t][j], masks);
-            part[0][j] = mfma16x16x32(b.a[0][t], bw, part[0][j]);
-            if (MG > 1 && nch > 1) {
+            sf[j] = j & 1 ? bf16hi(sq[n][i][j >> 1]) : bf16lo(sq[n][i][j >> 1]);
+            if (ZERO) zf[j] = -16.0f - (float)((zq[n][i] >> (8 * j)) & 0xFFu);
+          }
+          f32x4_t part[MG][4];
 #pragma unroll
-              for (int m = 1; m < MG; ++m) part[m][j] = mfma16x16x32(b.a[m][t], bw, part[m][j]);
+          for (int m = 0; m < MG; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int v = 0; v < 4; ++v) part[m][j][v] = ZERO ? zf[j] * sum[m][v] : sum[m][v];
+#pragma unroll
+          for (int t = GS * i; t < GS * i + GS; ++t) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const u32x4_t bw = int4_operand(w[n][t][j], masks);
+#pragma unroll
+              for (int m = 0; m < MG; ++m) part[m][j] = mfma16x16x32(a[m][t], bw, part[m][j]);
             }
+            if (kMore) load_w(n, t, 4 * q + 4 + t);
+            if (kMore && n == NS - 1) load_a(t, 4 * q + 4 + t);
           }
 #pragma unroll
-        for (int m = 0; m < MG; ++m)
+          for (int m = 0; m < MG; ++m)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 4; ++j) {
 #pragma unroll
-            for (int v = 0; v < 4; ++v) acc[m][j][v] = __builtin_fmaf(s[j], part[m][j][v], acc[m][j][v]);
-#pragma unroll
-        for (int m = 0; m < MG; ++m)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(acc[m][j]));
+              for (int v = 0; v < 4; ++v) acc[n][m][j][v] = __builtin_fmaf(sf[j], part[m][j][v], acc[n][m][j][v]);
+              asm volatile("" : "+v"(acc[n][m][j]));
+            }
+        }
       }
     };
 
     if (q_begin < q_end) {
-      // The first two quads' weights are under way while the rows' slots arrive.
-      Quad<MG, NGQ> b0, b1;
-      int q = q_begin;
-      load_w(q, b0);
-      load_w(min(q + 1, q_end - 1), b1);
+      // The weights are under way while the rows' slots arrive.
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int n = 0; n < NS; ++n) load_w(n, t, 4 * q_begin + t);
+      load_s(q_begin);
 #pragma unroll
       for (int m = 0; m < MG; ++m)
         a_off[m] = ((uint32_t)(GATE_UP ? slot[m] / kslots : slot[m]) * (uint32_t)K + 8u * g) * 2u;
-      load_a(q, b0);
-      load_a(min(q + 1, q_end - 1), b1);
-      for (; q + 4 <= q_end; q += 2) {
-        compute(q, b0);
-        load(q + 2, b0);
-        compute(q + 1, b1);
-        load(q + 3, b1);
-      }
-      compute(q, b0);   // one to three quads are left
-      if (q + 2 < q_end) load(q + 2, b0);
-      if (q + 1 < q_end) compute(q + 1, b1);
-      if (q + 2 < q_end) compute(q + 2, b0);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) load_a(t, 4 * q_begin + t);
+      int q = q_begin;
+      for (; q + 1 < q_end; ++q) quad(std::true_type{}, q);
+      quad(std::false_type{}, q);
     }
 
     // Sum the K partials in the waves' order; wave w < 4 finishes element v = w
     // (row 4 g + w of each chunk) of the lane's four columns.
-    const float bb[4] = {bf16lo(b01), bf16hi(b01), bf16lo(b23), bf16hi(b23)};
 #pragma unroll
     for (int m = 0; m < MG; ++m) {
+#pragma unroll
+     for (int n = 0; n < NS; ++n) {
       if (m < nch) {
+        const float bb[4] = {bf16lo(b01[n]), bf16hi(b01[n]), bf16lo(b23[n]), bf16hi(b23[n])};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int v = 0; v < 4; ++v) red[wave][j][v][lane] = acc[m][j][v];
+          for (int v = 0; v < 4; ++v) red[wave][j][v][lane] = acc[n][m][j][v];
         __syncthreads();
         const int r = r0 + 16 * m + 4 * g + wave;
-        if (wave < 4 && r < M && col_ok) {
+        if (wave < 4 && r < M && ncol[n] < N) {
           float sum[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             float t = 0.f;
 #pragma unroll
-            for (int w = 0; w < WAVES; ++w) t += red[w][j][wave & 3][lane];
+            for (int w2 = 0; w2 < WAVES; ++w2) t += red[w2][j][wave & 3][lane];
             sum[j] = t + bb[j];
           }
           const size_t orow = (size_t)(row0 + r);
           if (GATE_UP)
-            *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(out) + orow * (N / 2) + ncol / 2) =
+            *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(out) + orow * (N / 2) + ncol[n] / 2) =
                 pack_bf16x2(clamped_glu(sum[0], sum[1]), clamped_glu(sum[2], sum[3]));
           else
-            *reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(out) + orow * N + ncol) =
+            *reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(out) + orow * N + ncol[n]) =
                 f32x4_t{sum[0], sum[1], sum[2], sum[3]};
         }
         __syncthreads();
       }
+     }
     }
   }
 }
 
-template <bool GATE_UP, int MG, int GS, int WAVES>
+template <bool GATE_UP, int MG, int GS, int WAVES, int NS>
 hipError_t launch_stream(const void* A, const void* Wq, const void* Ws, const void* Wz, const void* bias,
                          const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T, int K, int N, int E,
                          int k, int experts, void* out, hipStream_t stream) {
-  dim3 grid((unsigned)((N + kTileN - 1) / kTileN), (unsigned)experts);
-  auto kern = Wz ? int4_stream_kernel<GATE_UP, MG, GS, true, WAVES> : int4_stream_kernel<GATE_UP, MG, GS, false, WAVES>;
+  dim3 grid((unsigned)(((N + kTileN - 1) / kTileN + NS - 1) / NS), (unsigned)experts);
+  auto kern = Wz ? int4_stream_kernel<GATE_UP, MG, GS, true, WAVES, NS> : int4_stream_kernel<GATE_UP, MG, GS, false, WAVES, NS>;
   hipLaunchKernelGGL(kern, grid, dim3(WAVES * kWave), 0, stream, (const bf16_t*)A, (const uint8_t*)Wq,
                      (const uint16_t*)Ws, (const uint8_t*)Wz, (const bf16_t*)bias, cnt, off, rows, K, N, E, k, T, out);
   return hipGetLastError();
 }
 
-template <bool GATE_UP, int MG, int WAVES>
+template <bool GATE_UP, int MG, int WAVES, int NS>
 hipError_t launch_group(int G, const void* A, const void* Wq, const void* Ws, const void* Wz, const void* bias,
                         const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T, int K, int N, int E,
                         int k, int experts, void* out, hipStream_t stream) {
-  auto launch = G == 32   ? launch_stream<GATE_UP, MG, 1, WAVES>
-                : G == 64 ? launch_stream<GATE_UP, MG, 2, WAVES>
-                          : launch_stream<GATE_UP, MG, 4, WAVES>;
+  auto launch = G == 32   ? launch_stream<GATE_UP, MG, 1, WAVES, NS>
+                : G == 64 ? launch_stream<GATE_UP, MG, 2, WAVES, NS>
+                          : launch_stream<GATE_UP, MG, 4, WAVES, NS>;
   return launch(A, Wq, Ws, Wz, bias, cnt, off, rows, T, K, N, E, k, experts, out, stream);
 }
 
@@ -382,9 +405,9 @@ hipError_t launch_int4(const void* A, const void* Wq, const void* Ws, const void
   // workgroups go to the ones that have.
   const int experts = (int)(T * k < E ? T * k : E);
   const int64_t workgroups = (int64_t)experts * ((N + kTileN - 1) / kTileN);
-  auto launch = T * k > kOneChunkMeanRows * E ? launch_group<GATE_UP, 2, 4>
-                : workgroups <= kCus          ? launch_group<GATE_UP, 1, 8>
-                                              : launch_group<GATE_UP, 1, 4>;
+  auto launch = T * k > kOneChunkMeanRows * E ? launch_group<GATE_UP, 2, 4, 2>
+                : workgroups <= kCus          ? launch_group<GATE_UP, 1, 8, 1>
+                                              : launch_group<GATE_UP, 1, 4, 1>;
   return launch(G, A, Wq, Ws, Wz, bias, cnt, off, rows, T, K, N, E, k, experts, out, stream);
 }
 
