@@ -25,6 +25,7 @@ namespace {
 
 constexpr int kGemmWaves = 8;
 constexpr int kBM = 128, kChunks = kBM / 16;
+static_assert(kChunks == kGemmWaves && kChunks == 8, "a wave brings in one chunk; run() below counts them");
 constexpr int kBN = kGemmWaves * kTileN;
 constexpr int kRing = 4;
 constexpr int kXcds = 8;
@@ -79,18 +80,28 @@ __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
   // Every wave issues the same loads for every unit, past the end too (where
   // nothing is read): the waits count on it.
   constexpr int kLoads = 2 * GU + 1 + (ZERO ? 1 : 0);
-  auto load = [&](int u) __attribute__((always_inline)) {
+  auto load = [&](int u, int i) __attribute__((always_inline)) {
     const int slot = u % kRing;
-#pragma unroll
-    for (int t = 0; t < GU; ++t) {
-      const int kt = GU * u + t;
+    if (i < 2 * GU) {
+      const int t = i >> 1, kt = GU * u + t;
       const bool in = kt < nkt;
-      dma16(a_rs, in ? a_off : kOutOfRange, in ? 64u * (uint32_t)kt : 0u, rows_at + (uint32_t)((slot * GU + t) * kChunks * kWave) * 16u);
-      dma16(w_rs, in ? 16u * (uint32_t)lane : kOutOfRange, in ? (uint32_t)kt * kTileBytes : 0u, w_at + (uint32_t)((slot * GU + t) * kWave) * 16u);
+      if ((i & 1) == 0)
+        dma16(a_rs, in ? a_off : kOutOfRange, in ? 64u * (uint32_t)kt : 0u,
+              rows_at + (uint32_t)((slot * GU + t) * kChunks * kWave) * 16u);
+      else
+        dma16(w_rs, in ? 16u * (uint32_t)lane : kOutOfRange, in ? (uint32_t)kt * kTileBytes : 0u,
+              w_at + (uint32_t)((slot * GU + t) * kWave) * 16u);
+    } else {
+      const uint32_t at = (uint32_t)(min(u, nu - 1) / units_per_group) * N;
+      if (i == 2 * GU)
+        dma4(s_rs, s_off, 2u * at, s_at + (uint32_t)(slot * kWave) * 4u);
+      else
+        dma4(z_rs, z_off, at, z_at + (uint32_t)(slot * kWave) * 4u);
     }
-    const uint32_t at = (uint32_t)(min(u, nu - 1) / units_per_group) * N;
-    dma4(s_rs, s_off, 2u * at, s_at + (uint32_t)(slot * kWave) * 4u);
-    if (ZERO) dma4(z_rs, z_off, at, z_at + (uint32_t)(slot * kWave) * 4u);
+  };
+  auto load_all = [&](int u) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) load(u, i);
   };
   const u32x4_t flat = ZERO ? u32x4_t{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}
                             : u32x4_t{0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u};
@@ -157,7 +168,7 @@ __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kLoads) : "memory");
     sum_rows(u);
   };
-  auto compute = [&](auto full, int u, const Words& b) __attribute__((always_inline)) {
+  auto compute = [&](auto count, int u, const Words& b) __attribute__((always_inline)) {
     float s[4], z[4];
     u32x4_t bw[GU][4];
 #pragma unroll
@@ -169,67 +180,66 @@ __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
       s[j] = j & 1 ? bf16hi(b.s[j >> 1]) : bf16lo(b.s[j >> 1]);
       if (ZERO) z[j] = -16.0f - (float)((b.z >> (8 * j)) & 0xFFu);
     }
-    if (decltype(full)::value) {
-      // Full tiles, without branches: a chunk is read two ahead of its
-      // products and added behind the next one's.
-      u32x4_t a[3][GU];
-      f32x4_t sum[3], part[2][4];
+    // Without branches: a chunk is read two ahead of its products and added
+    // behind the next one's.
+    constexpr int kCount = decltype(count)::value;
+    u32x4_t a[3][GU];
+    f32x4_t sum[3], part[2][4];
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        chunk_in(u, m, a[m]);
-        sum[m] = sum_in(u, m);
-      }
-#pragma unroll
-      for (int m = 0; m < kChunks; ++m) {
-        __builtin_amdgcn_sched_barrier(0);
-        if (m + 2 < kChunks) {
-          chunk_in(u, m + 2, a[(m + 2) % 3]);
-          sum[(m + 2) % 3] = sum_in(u, m + 2);
-        }
-        chunk_mul(a[m % 3], sum[m % 3], bw, z, part[m & 1]);
-        if (m == kChunks / 2) next(u + 1);
-        if (m > 0) chunk_add(acc[m - 1], part[(m - 1) & 1], s);
-      }
-      chunk_add(acc[kChunks - 1], part[(kChunks - 1) & 1], s);
-    } else {
-#pragma unroll
-      for (int m = 0; m < kChunks; ++m) {
-        if (m < nch) {
-          u32x4_t a[GU];
-          f32x4_t part[4];
-          chunk_in(u, m, a);
-          chunk_mul(a, sum_in(u, m), bw, z, part);
-          chunk_add(acc[m], part, s);
-        }
-      }
-      next(u + 1);
+    for (int m = 0; m < 2; ++m) {
+      chunk_in(u, m, a[m]);
+      sum[m] = sum_in(u, m);
     }
+#pragma unroll
+    for (int m = 0; m < kCount; ++m) {
+      __builtin_amdgcn_sched_barrier(0);
+      // The loads of unit u + 3 (into the slot that unit u - 1 was read from),
+      // spread over the chunks: a load that the CU's load path cannot take yet
+      // holds up its wave's products.
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        if (i * (kCount - 1) / kLoads == m) load(u + 3, i);
+      if (m + 2 < kCount) {
+        chunk_in(u, m + 2, a[(m + 2) % 3]);
+        sum[(m + 2) % 3] = sum_in(u, m + 2);
+      }
+      chunk_mul(a[m % 3], sum[m % 3], bw, z, part[m & 1]);
+      if (m == kCount - 1) next(u + 1);
+      if (m > 0) chunk_add(acc[m - 1], part[(m - 1) & 1], s);
+    }
+    chunk_add(acc[kCount - 1], part[(kCount - 1) & 1], s);
   };
 
-  load(0);
-  load(1);
-  load(2);
+  load_all(0);
+  load_all(1);
+  load_all(2);
   Words b;
   next(0);
   words(0, b);
   __syncthreads();
   // The wave's own weights it may read at once, the other waves' rows and sums
   // behind the barrier, where every read of this unit's has returned too.
-  auto run = [&](auto full) __attribute__((always_inline)) {
+  auto run = [&](auto count) __attribute__((always_inline)) {
     for (int u = 0; u < nu; ++u) {
-      load(u + 3);   // into the slot that unit u - 1 was read from
-      if (live)
-        compute(full, u, b);
-      else
+      if (live) {
+        compute(count, u, b);
+      } else {
+        load_all(u + 3);
         next(u + 1);
+      }
       words(u + 1, b);
       __syncthreads();
     }
   };
-  if (nch == kChunks)
-    run(std::true_type{});
+  // an even count of chunks: at most one is computed for nothing
+  if (nch > 6)
+    run(std::integral_constant<int, 8>{});
+  else if (nch > 4)
+    run(std::integral_constant<int, 6>{});
+  else if (nch > 2)
+    run(std::integral_constant<int, 4>{});
   else
-    run(std::false_type{});
+    run(std::integral_constant<int, 2>{});
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no load may reach this LDS after the workgroup's end
   if (!live || ncol >= N) return;                    // no barrier follows
 
