@@ -570,7 +570,8 @@ MOE_API int moe_forward_norm_fp8(const void* x, const void* residual, const void
  *   zeros   uint8 [E][ceil(K/G)][N], 8-byte aligned, or NULL; values above 15
  *           count as they are
  * Requires K % 32 == 0 (the forwards: H % 32 == 0 and I % 32 == 0); codes
- * 16-byte aligned.
+ * 16-byte aligned.  x and h below 4 GiB each (T*H*2 and T*k*I*2 bytes;
+ * MOE_ERR_UNSUPPORTED otherwise).
  */
 
 /*

@@ -642,6 +642,12 @@ int moe_down_mxfp4(const void* h, const void* Wd_q, const void* Wd_s, const void
 // ---------------------------------------------------------------------------
 // 4-bit integer expert weights with group scales
 // ---------------------------------------------------------------------------
+// The exact router takes one workgroup a token; past three a CU the MFMA router
+// is faster whatever E (T = 512, 1021, 2048 of 2880: exact 18.5, 34.9, 67.1 us,
+// MFMA 26.8, 26.8, 27.6 at E = 32; 47.6, 91.2, 173 against 54.9, 55.8, 55.5 at
+// E = 128).  Both make the same decision.
+static int route_method(int64_t T) { return T > 768 ? MOE_ROUTE_MFMA : MOE_ROUTE_EXACT; }
+
 static int check_int4_group(const char* fn, int32_t G) {
   if (G != 32 && G != 64 && G != 128)
     return fail(MOE_ERR_INVALID_ARG, "%s: G=%d must be 32, 64 or 128 (values of K per scale)", fn, G);
@@ -652,6 +658,15 @@ static int check_int4_group(const char* fn, int32_t G) {
 static int check_int4_dims(const char* fn, const char* name, int32_t K, int32_t G) {
   if (K % 32 != 0) return fail(MOE_ERR_INVALID_ARG, "%s: %s=%d must be a multiple of 32 (int4 tiles)", fn, name, K);
   return check_int4_group(fn, G);
+}
+
+// The kernels address the token rows with 32-bit byte offsets: x of T rows, or
+// the rows of h that one expert may have.
+static int check_int4_rows(const char* fn, const char* name, int64_t rows, int32_t K) {
+  if (rows * K * 2 >= (int64_t)1 << 32)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: %s of %lld rows of %d takes 4 GiB or more: split the batch", fn, name,
+                (long long)rows, K);
+  return MOE_OK;
 }
 
 static int check_int4_matrix(const char* fn, int32_t E, int32_t K, int32_t N) {
@@ -740,6 +755,8 @@ static int forward_int4(const char* fn, const void* x, const void* Wr, const voi
     return fail(MOE_ERR_INVALID_ARG, "%s: expert_counts_out is not 4-byte aligned", fn);
   if (path < MOE_PATH_AUTO || path > MOE_PATH_GEMM)
     return fail(MOE_ERR_INVALID_ARG, "%s: unknown path %d", fn, path);
+  if (int st = check_int4_rows(fn, "x", T, H)) return st;
+  if (int st = check_int4_rows(fn, "h", T * k, I)) return st;
   if (T == 0) return ok();
   const Layout L = layout(T, H, E, k, I);
   if (workspace == nullptr || workspace_bytes < L.total)
@@ -761,7 +778,7 @@ static int forward_int4(const char* fn, const void* x, const void* Wr, const voi
   // the expert path follows the whole layer's load per expert, T*k/E
   path = choose_path(path, T, E, k);
 
-  if (int st = hip_status(fn, moe::launch_route(x, Wr, br, T, H, E, k, ids, w, MOE_ROUTE_AUTO, s))) return st;
+  if (int st = hip_status(fn, moe::launch_route(x, Wr, br, T, H, E, k, ids, w, route_method(T), s))) return st;
   if (n_valid)
     if (int st = hip_status(fn, moe::launch_mask_padding(ids, w, T, k, n_valid, s))) return st;
   if (int st = hip_status(fn, moe::launch_permute(ids, T, n_local, k, cnt, off, rows, pos, s, e_begin))) return st;
@@ -829,6 +846,7 @@ int moe_gate_up_int4(const void* x, const void* Wgu_q, const void* Wgu_s, const 
   CHECK_PTR(h, 16);
   if (path < MOE_PATH_AUTO || path > MOE_PATH_GEMM)
     return fail(MOE_ERR_INVALID_ARG, "%s: unknown path %d", fn, path);
+  if (int st = check_int4_rows(fn, "x", T, H)) return st;
   if (T == 0) return ok();
   if (int st = run_gate_up_int4(fn, x, Wgu_q, Wgu_s, Wgu_z, bgu, cnt, off, rows, T, H, E, k, I, G, h, path,
                                 (hipStream_t)stream))
@@ -852,6 +870,7 @@ int moe_down_int4(const void* h, const void* Wd_q, const void* Wd_s, const void*
   CHECK_PTR(o, 16);
   if (path < MOE_PATH_AUTO || path > MOE_PATH_GEMM)
     return fail(MOE_ERR_INVALID_ARG, "%s: unknown path %d", fn, path);
+  if (int st = check_int4_rows(fn, "h", T * k, I)) return st;
   if (T == 0) return ok();
   if (int st = run_down_int4(fn, h, Wd_q, Wd_s, Wd_z, bd, cnt, off, T, H, E, k, I, G, o, path, (hipStream_t)stream))
     return st;
@@ -1011,14 +1030,16 @@ static int forward_fp8(const char* fn, const void* x, const void* Wr, const void
   path = choose_path(path, T, E, k);
   const int64_t S = T * k;
 
+  int method = MOE_ROUTE_AUTO;
   if (norm) {
+    method = route_method(T);
     void* xn = ws + F.total;
     if (int st = hip_status(fn, moe::launch_add_rmsnorm(x, norm->residual, norm->gamma, T, H, norm->eps,
                                                         norm->residual_out, xn, xq, sx, s)))
       return st;
     x = xn;
   }
-  if (int st = hip_status(fn, moe::launch_route(x, Wr, br, T, H, E, k, ids, w, MOE_ROUTE_AUTO, s))) return st;
+  if (int st = hip_status(fn, moe::launch_route(x, Wr, br, T, H, E, k, ids, w, method, s))) return st;
   if (n_valid)
     if (int st = hip_status(fn, moe::launch_mask_padding(ids, w, T, k, n_valid, s))) return st;
   if (int st = hip_status(fn, moe::launch_permute(ids, T, n_local, k, cnt, off, rows, pos, s, e_begin))) return st;

@@ -75,122 +75,131 @@ __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
 }
 
 constexpr int kNormMaxWaves = 16;
+constexpr int64_t kNormMaxGrid = (int64_t)1 << 21;
 
-// One row per workgroup; thread i holds the 16-byte pieces i, i + blockDim,
-// ... (P of them).  x, residual, residual_out and y carry no __restrict__: an
+// One row per workgroup at a time (the grid is cut at kNormMaxGrid rows: a
+// launch holds fewer than 2^32 threads); thread i holds the 16-byte pieces i,
+// i + blockDim, ... (P of them).  x, residual, residual_out and y carry no __restrict__: an
 // output may be the very buffer of an input, and a thread reads all its
 // pieces before it writes any.
 template <int P, bool RES, bool FP8>
 __global__ __launch_bounds__(kNormMaxWaves * kWave) void add_rmsnorm_kernel(
-    const bf16_t* x, const bf16_t* residual, const bf16_t* __restrict__ gamma, int H, double eps, bf16_t* residual_out,
+    const bf16_t* x, const bf16_t* residual, const bf16_t* __restrict__ gamma, int T, int H, double eps,
+    bf16_t* residual_out,
     bf16_t* y, uint8_t* __restrict__ codes, float* __restrict__ scales) {
-  __shared__ double s_sum[kNormMaxWaves];
-  __shared__ uint32_t s_max[kNormMaxWaves];
+  // two of each: a wave may begin the next row while another still reads
+  __shared__ double s_sum[2][kNormMaxWaves];
+  __shared__ uint32_t s_max[2][kNormMaxWaves];
   const int np = H / 8;
   const int tid = threadIdx.x, nt = blockDim.x;
   const int wave = tid / kWave, lane = tid & (kWave - 1), waves = nt / kWave;
-  const size_t base = (size_t)blockIdx.x * (size_t)H;
   const u32x4_t zero = u32x4_t{0u, 0u, 0u, 0u};
 
-  u32x4_t r[P];
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    const int i = tid + p * nt;
-    r[p] = i < np ? *reinterpret_cast<const u32x4_t*>(x + base + 8 * (size_t)i) : zero;
-  }
-  if (RES) {
-    u32x4_t a[P];
+  int parity = 1;
+  for (int64_t row = blockIdx.x; row < T; row += gridDim.x) {
+    parity ^= 1;
+    const size_t base = (size_t)row * (size_t)H;
+
+    u32x4_t r[P];
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int i = tid + p * nt;
-      a[p] = i < np ? *reinterpret_cast<const u32x4_t*>(residual + base + 8 * (size_t)i) : zero;
+      r[p] = i < np ? *reinterpret_cast<const u32x4_t*>(x + base + 8 * (size_t)i) : zero;
     }
+    if (RES) {
+      u32x4_t a[P];
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const int i = tid + p * nt;
+        a[p] = i < np ? *reinterpret_cast<const u32x4_t*>(residual + base + 8 * (size_t)i) : zero;
+      }
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          r[p][q] = pack_bf16x2(bf16lo(r[p][q]) + bf16lo(a[p][q]), bf16hi(r[p][q]) + bf16hi(a[p][q]));
+    }
+    u32x4_t gm[P];   // asked for ahead of the reduction, used behind it
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int i = tid + p * nt;
+      gm[p] = i < np ? *reinterpret_cast<const u32x4_t*>(gamma + 8 * (size_t)i) : zero;
+    }
+    double ss = 0.0;
 #pragma unroll
     for (int p = 0; p < P; ++p)
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        r[p][q] = pack_bf16x2(bf16lo(r[p][q]) + bf16lo(a[p][q]), bf16hi(r[p][q]) + bf16hi(a[p][q]));
-  }
-  u32x4_t gm[P];   // asked for ahead of the reduction, used behind it
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    const int i = tid + p * nt;
-    gm[p] = i < np ? *reinterpret_cast<const u32x4_t*>(gamma + 8 * (size_t)i) : zero;
-  }
-  double ss = 0.0;
-#pragma unroll
-  for (int p = 0; p < P; ++p)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const double lo = bf16lo(r[p][q]), hi = bf16hi(r[p][q]);
-      ss = __builtin_fma(lo, lo, ss);
-      ss = __builtin_fma(hi, hi, ss);
-    }
-  ss = wave_sum(ss);
-  if (waves > 1) {
-    if (lane == 0) s_sum[wave] = ss;
-    __syncthreads();
-    ss = 0.0;
-    for (int w = 0; w < waves; ++w) ss += s_sum[w];
-  }
-  const float inv = (float)(1.0 / sqrt(ss / (double)H + eps));
-
-  float v[P][8];
-  uint32_t m = 0;
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    const int i = tid + p * nt;
-    const u32x4_t g = gm[p];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      v[p][2 * q] = (bf16lo(r[p][q]) * inv) * bf16lo(g[q]);
-      v[p][2 * q + 1] = (bf16hi(r[p][q]) * inv) * bf16hi(g[q]);
-    }
-    if (i < np) {
-      if (RES) *reinterpret_cast<u32x4_t*>(residual_out + base + 8 * (size_t)i) = r[p];
-      if (!FP8 || y != nullptr)
-        *reinterpret_cast<u32x4_t*>(y + base + 8 * (size_t)i) =
-            u32x4_t{pack_bf16x2(v[p][0], v[p][1]), pack_bf16x2(v[p][2], v[p][3]), pack_bf16x2(v[p][4], v[p][5]),
-                    pack_bf16x2(v[p][6], v[p][7])};
-      // the maximum on the bit patterns: a NaN compares above every number
-      if (FP8)
-#pragma unroll
-        for (int q = 0; q < 8; ++q) m = max(m, __float_as_uint(v[p][q]) & 0x7FFFFFFFu);
-    }
-  }
-  if (!FP8) return;
-  m = wave_umax(m);
-  if (waves > 1) {
-    if (lane == 0) s_max[wave] = m;
-    __syncthreads();
-    m = 0;
-    for (int w = 0; w < waves; ++w) m = max(m, s_max[w]);
-  }
-  const float amax = __uint_as_float(m);
-  const float s = m == 0 ? 1.0f : __fdiv_rn(amax, kE4m3Max);
-  const float up = m == 0 ? 1.0f : __fdiv_rn(kE4m3Max, amax);
-  // From 2^-119 on 448 / amax is finite, and |v * up| rounds to 448 at most:
-  // the conversion instruction (nearest, ties to even) never overflows.
-  const bool ordinary = __builtin_amdgcn_readfirstlane(m) - 0x04000000u < 0x7F800000u - 0x04000000u;
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    const int i = tid + p * nt;
-    u32x2_t c;
-    if (ordinary) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[p][4 * h] * up, v[p][4 * h + 1] * up, 0, false);
-        c[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[p][4 * h + 2] * up, v[p][4 * h + 3] * up, w, true);
+      for (int q = 0; q < 4; ++q) {
+        const double lo = bf16lo(r[p][q]), hi = bf16hi(r[p][q]);
+        ss = __builtin_fma(lo, lo, ss);
+        ss = __builtin_fma(hi, hi, ss);
       }
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        c[h] = e4m3_any(v[p][4 * h] * up) | e4m3_any(v[p][4 * h + 1] * up) << 8 |
-               e4m3_any(v[p][4 * h + 2] * up) << 16 | e4m3_any(v[p][4 * h + 3] * up) << 24;
+    ss = wave_sum(ss);
+    if (waves > 1) {
+      if (lane == 0) s_sum[parity][wave] = ss;
+      __syncthreads();
+      ss = 0.0;
+      for (int w = 0; w < waves; ++w) ss += s_sum[parity][w];
     }
-    if (i < np) *reinterpret_cast<u32x2_t*>(codes + base + 8 * (size_t)i) = c;
+    const float inv = (float)(1.0 / sqrt(ss / (double)H + eps));
+
+    float v[P][8];
+    uint32_t m = 0;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int i = tid + p * nt;
+      const u32x4_t g = gm[p];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        v[p][2 * q] = (bf16lo(r[p][q]) * inv) * bf16lo(g[q]);
+        v[p][2 * q + 1] = (bf16hi(r[p][q]) * inv) * bf16hi(g[q]);
+      }
+      if (i < np) {
+        if (RES) *reinterpret_cast<u32x4_t*>(residual_out + base + 8 * (size_t)i) = r[p];
+        if (!FP8 || y != nullptr)
+          *reinterpret_cast<u32x4_t*>(y + base + 8 * (size_t)i) =
+              u32x4_t{pack_bf16x2(v[p][0], v[p][1]), pack_bf16x2(v[p][2], v[p][3]), pack_bf16x2(v[p][4], v[p][5]),
+                      pack_bf16x2(v[p][6], v[p][7])};
+        // the maximum on the bit patterns: a NaN compares above every number
+        if (FP8)
+#pragma unroll
+          for (int q = 0; q < 8; ++q) m = max(m, __float_as_uint(v[p][q]) & 0x7FFFFFFFu);
+      }
+    }
+    if (!FP8) continue;
+    m = wave_umax(m);
+    if (waves > 1) {
+      if (lane == 0) s_max[parity][wave] = m;
+      __syncthreads();
+      m = 0;
+      for (int w = 0; w < waves; ++w) m = max(m, s_max[parity][w]);
+    }
+    const float amax = __uint_as_float(m);
+    const float s = m == 0 ? 1.0f : __fdiv_rn(amax, kE4m3Max);
+    const float up = m == 0 ? 1.0f : __fdiv_rn(kE4m3Max, amax);
+    // From 2^-119 on 448 / amax is finite, and |v * up| rounds to 448 at most:
+    // the conversion instruction (nearest, ties to even) never overflows.
+    const bool ordinary = __builtin_amdgcn_readfirstlane(m) - 0x04000000u < 0x7F800000u - 0x04000000u;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int i = tid + p * nt;
+      u32x2_t c;
+      if (ordinary) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[p][4 * h] * up, v[p][4 * h + 1] * up, 0, false);
+          c[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[p][4 * h + 2] * up, v[p][4 * h + 3] * up, w, true);
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          c[h] = e4m3_any(v[p][4 * h] * up) | e4m3_any(v[p][4 * h + 1] * up) << 8 |
+                 e4m3_any(v[p][4 * h + 2] * up) << 16 | e4m3_any(v[p][4 * h + 3] * up) << 24;
+      }
+      if (i < np) *reinterpret_cast<u32x2_t*>(codes + base + 8 * (size_t)i) = c;
+    }
+    if (tid == 0) scales[row] = s;
   }
-  if (tid == 0) scales[blockIdx.x] = s;
 }
 
 template <int P>
@@ -200,8 +209,10 @@ hipError_t launch_p(const void* x, const void* residual, const void* gamma, int6
   const int waves = (np + kWave * P - 1) / (kWave * P);
   auto kern = residual ? (codes ? add_rmsnorm_kernel<P, true, true> : add_rmsnorm_kernel<P, true, false>)
                        : (codes ? add_rmsnorm_kernel<P, false, true> : add_rmsnorm_kernel<P, false, false>);
-  hipLaunchKernelGGL(kern, dim3((unsigned)T), dim3(waves * kWave), 0, stream, (const bf16_t*)x, (const bf16_t*)residual,
-                     (const bf16_t*)gamma, H, (double)eps, (bf16_t*)residual_out, (bf16_t*)y, (uint8_t*)codes, scales);
+  const int64_t grid = T < kNormMaxGrid ? T : kNormMaxGrid;
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(waves * kWave), 0, stream, (const bf16_t*)x,
+                     (const bf16_t*)residual, (const bf16_t*)gamma, (int)T, H, (double)eps,
+                     (bf16_t*)residual_out, (bf16_t*)y, (uint8_t*)codes, scales);
   return hipGetLastError();
 }
 

@@ -313,6 +313,29 @@ def test_norm_then_int4_block():
 
 
 @pytest.mark.parametrize("path", PATHS)
+def test_rows_past_two_gib(path):
+    """Token rows up to just below 4 GiB, gathered (gate_up) and in place (down): the last rows as in a small call."""
+    _need_gpu()
+    T, K, E, G = 524000, 4096, 2, 128
+    m = _matrix(E, K, 64, G, False, 22)
+    q, s, _ = _gpu(m)
+    bias = dev(d.normal_bf16((E, 64), 0.5, 23, 1, E, 64))
+    a = torch.zeros((T, K), dtype=torch.bfloat16, device="cuda")
+    tail = dev(d.normal_bf16((40, K), 1.0, 24, 1, 40, K))
+    a[-40:] = tail
+    ids = torch.zeros((T, 1), dtype=torch.int32, device="cuda")
+    ids[-17:] = 1                                                     # both experts have rows in the tail
+    cnt, off, rows, pos = binding.moe_permute(ids, E)
+    small = binding.moe_permute(ids[-40:].contiguous(), E)
+    h = binding.moe_gate_up_int4(a, q, s, bias, cnt, off, rows, 1, path=path)
+    want = binding.moe_gate_up_int4(tail, q, s, bias, small[0], small[1], small[2], 1, path=path)
+    assert torch.equal(h[pos[-40:].long()], want[small[3].long()])
+    o = binding.moe_down_int4(a, q, s, bias, cnt, off, T, 1, path=path)   # rows in permuted order already
+    want = binding.moe_down_int4(tail, q, s, bias, small[0], small[1], 40, 1, path=path)
+    assert torch.equal(o[-40:], want)
+
+
+@pytest.mark.parametrize("path", PATHS)
 def test_graph_replays(path):
     """Two captured forwards that share a workspace and a stream, replayed in turn with eager calls between."""
     _need_gpu()

@@ -177,6 +177,30 @@ def test_offsets_past_32_bits():
     assert torch.equal(y[-5:], y2) and torch.equal(codes[-5:], codes2) and torch.equal(scales[-5:], scales2)
 
 
+@pytest.mark.parametrize("H", [8, 1040])
+def test_more_rows_than_workgroups(H):
+    """2^21 rows and more: a workgroup takes several, one after the other."""
+    _need_gpu()
+    T = (1 << 21) + 5 if H == 8 else (1 << 22) + 3
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn((T, H), generator=g, device="cuda", dtype=torch.bfloat16)
+    gamma = dev(_gamma(H, 34))
+    n = H if H % 16 == 0 else None                                   # FP8 rows come in sixteens
+    y = torch.empty_like(x)
+    codes = torch.empty((T, H), dtype=torch.uint8, device="cuda") if n else None
+    scales = torch.empty((T,), device="cuda") if n else None
+    if n:
+        binding.moe_add_rmsnorm_fp8(x, gamma, y=y, codes=codes, scales=scales)
+    else:
+        binding.moe_add_rmsnorm(x, gamma, y=y)
+    for lo in (0, (1 << 21) - 4, T - 9):
+        part = binding.moe_add_rmsnorm_fp8(x[lo:lo + 9], gamma) if n else binding.moe_add_rmsnorm(x[lo:lo + 9], gamma)
+        m = len(part[0])
+        assert torch.equal(y[lo:lo + m], part[0]), lo
+        if n:
+            assert torch.equal(codes[lo:lo + m], part[1]) and torch.equal(scales[lo:lo + m], part[2]), lo
+
+
 def test_no_tokens():
     _need_gpu()
     x, gamma = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda"), dev(_gamma(64, 18))

@@ -110,6 +110,17 @@ def test_forward_int4_workspace_and_no_tokens(lib):
     assert _fwd4(lib, T=0, ws=None, ws_bytes=0) == OK
 
 
+def test_int4_rows_from_four_gib_on_are_refused(lib):
+    """Before anything is enqueued; one row less is taken (T = 0 stands in for it here)."""
+    UNSUPPORTED = 2
+    T = (1 << 32) // (2 * 2880) + 1
+    assert _fwd4(lib, T=T, H=2880, ws_bytes=1 << 60) == UNSUPPORTED and b"x of" in lib.moe_last_error()
+    assert _fwd4(lib, T=1 << 20, k=2, I=1024, H=32, ws_bytes=1 << 60) == UNSUPPORTED and b"h of" in lib.moe_last_error()
+    v = _p
+    assert lib.moe_gate_up_int4(v(0), v(1), v(2), None, *[v(i) for i in range(4, 8)], T, 2880, 8, 2, 64, 32, v(9), 0, None) == UNSUPPORTED
+    assert lib.moe_down_int4(v(0), v(1), v(2), None, *[v(i) for i in range(4, 7)], T, 64, 8, 1, 2880, 32, v(9), 0, None) == UNSUPPORTED
+
+
 def test_int4_stages_quantizer_and_packer_refuse(lib):
     v = _p
     gate_up = lambda **kw: lib.moe_gate_up_int4(*[v(i) for i in range(3)], kw.get("z"), *[v(i) for i in range(4, 8)],  # noqa: E731
