@@ -123,7 +123,7 @@ __global__ __launch_bounds__(kQThreads) void int4_pack_kernel(const uint8_t* __r
 //   NS strips share the token rows' loads: rows cost as many bytes of the
 //   path from L2 into a CU as the 64 columns they meet, and twice as many with
 //   two chunks (T = 192 of 32 experts, 24 rows each: 90 us with one strip, 74
-//   with two; with one chunk two strips gain nothing and halve the workgroups).
+//   with two).
 //   A word gives 16 + q exactly (seven integer instructions for eight codes).
 //   The 16 and the zero point come off through the accumulator: a group's sum
 //   starts at -(16 + z) sum(a), where sum(a) is one more MFMA with a constant
@@ -161,7 +161,7 @@ __device__ __forceinline__ bool nth_live_expert(const int32_t* __restrict__ cnt,
 }
 
 template <bool GATE_UP, int MG, int GS, bool ZERO, int WAVES, int NS>
-__global__ __launch_bounds__(WAVES * kWave, WAVES == 8 || MG > 1 ? 2 : 3) void int4_stream_kernel(
+__global__ __launch_bounds__(WAVES * kWave, WAVES == 8 || MG > 1 || NS > GS ? 2 : 3) void int4_stream_kernel(
     const bf16_t* __restrict__ A, const uint8_t* __restrict__ Wq, const uint16_t* __restrict__ Ws,
     const uint8_t* __restrict__ Wz, const bf16_t* __restrict__ bias, const int32_t* __restrict__ cnt,
     const int32_t* __restrict__ off, const int32_t* __restrict__ rows, int K, int N, int E, int kslots,
@@ -294,6 +294,7 @@ __global__ __launch_bounds__(WAVES * kWave, WAVES == 8 || MG > 1 ? 2 : 3) void i
               for (int v = 0; v < 4; ++v) part[m][j][v] = ZERO ? zf[j] * sum[m][v] : sum[m][v];
 #pragma unroll
           for (int t = GS * i; t < GS * i + GS; ++t) {
+            __builtin_amdgcn_sched_barrier(0);   // tile by tile, or the operands of all of them fill the registers
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const u32x4_t bw = int4_operand(w[n][t][j], masks);
@@ -391,9 +392,16 @@ hipError_t launch_group(int G, const void* A, const void* Wq, const void* Ws, co
   return launch(A, Wq, Ws, Wz, bias, cnt, off, rows, T, K, N, E, k, experts, out, stream);
 }
 
-// Mean rows per expert up to which one 16-row chunk a pass is enough.  Where no
-// CU would get a second workgroup, eight waves halve each one's share of K.
+// Mean rows per expert up to which one 16-row chunk a pass is enough, and from
+// which most experts have rows, so that two strips a wave still leave every CU
+// two workgroups where the grid has them.  (T = 8, 32, 64 of 32 experts, 2880
+// columns and more: gate_up with one strip 33.6, 47.0, 53.5 us, with two 36.6,
+// 46.5, 52.3; T = 256 of 128 experts: down 104 against 98.6 us.  64 rows of 32
+// experts of 1024 x 1536, 384 workgroups of two strips: 8.8 against 10.3 us.)
+// Where no CU would get a second workgroup, eight waves halve each one's share
+// of K.
 constexpr int64_t kOneChunkMeanRows = 10;
+constexpr int64_t kTwoStripsMeanRows = 4;
 
 template <bool GATE_UP>
 hipError_t launch_int4(const void* A, const void* Wq, const void* Ws, const void* Wz, const void* bias,
@@ -405,7 +413,9 @@ hipError_t launch_int4(const void* A, const void* Wq, const void* Ws, const void
   // workgroups go to the ones that have.
   const int experts = (int)(T * k < E ? T * k : E);
   const int64_t workgroups = (int64_t)experts * ((N + kTileN - 1) / kTileN);
-  auto launch = T * k > kOneChunkMeanRows * E ? launch_group<GATE_UP, 2, 4, 2>
+  const bool two = T * k >= kTwoStripsMeanRows * E && workgroups >= 4 * kCus;
+  auto launch = T * k > kOneChunkMeanRows * E ? (two ? launch_group<GATE_UP, 2, 4, 2> : launch_group<GATE_UP, 2, 4, 1>)
+                : two                         ? launch_group<GATE_UP, 1, 4, 2>
                 : workgroups <= kCus          ? launch_group<GATE_UP, 1, 8, 1>
                                               : launch_group<GATE_UP, 1, 4, 1>;
   return launch(G, A, Wq, Ws, Wz, bias, cnt, off, rows, T, K, N, E, k, experts, out, stream);
