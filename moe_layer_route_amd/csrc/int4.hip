@@ -129,6 +129,10 @@ __global__ __launch_bounds__(kQThreads) void int4_pack_kernel(const uint8_t* __r
 //   starts at -(16 + z) sum(a), where sum(a) is one more MFMA with a constant
 //   operand (-24 without zero points, 1 with them).  The group's sum times its
 //   scale is added to the accumulators in float32.
+// What binds is HBM: T = 64 of 32 experts, 2880 x 5760, G = 64 with zero points
+// 51.3 us, 5.7 TB/s of the 6.1 that a plain read of as much reaches; T = 256 of
+// 128 experts, 2880 x 2880, G = 128 95.3 us, 5.9 TB/s; T = 8 of 32 experts, G =
+// 32 33.1 us, 5.9 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kCus = 256;
 
