@@ -361,10 +361,7 @@ def moe_forward_noalloc(x, Wr, br, Wgu, bgu, Wd, bd, k: int = 4, y=None, topk_id
     _dev(y, topk_ids, topk_w)
     _check(library().moe_forward_noalloc(_ptr(x), _ptr(Wr), _ptr(br), _ptr(Wgu), _ptr(bgu), _ptr(Wd), _ptr(bd),
                                          T, H, E, k, I, _ptr(y), _ptr(topk_ids), _ptr(topk_w), _stream(stream)),
-           "moe_forward_noalloc",
-           "moe_add_rmsnorm", "moe_add_rmsnorm_fp8", "moe_workspace_bytes_norm_fp8", "moe_forward_norm_fp8",
-           "moe_quantize_int4", "moe_pack_int4", "moe_forward_int4", "moe_forward_int4_ex", "moe_gate_up_int4",
-           "moe_down_int4", "moe_forward_padded_int4", "moe_forward_ep_int4")
+           "moe_forward_noalloc")
     return y
 
 
