@@ -19,6 +19,8 @@
 #include "device_common.h"
 #include "int4_device.h"
 #include "launch.h"
+#include "route_key.h"
+#include "wave_reduce.h"
 
 #include <type_traits>
 
@@ -164,19 +166,131 @@ __device__ __forceinline__ bool nth_live_expert(const int32_t* __restrict__ cnt,
   return false;
 }
 
-template <bool GATE_UP, int MG, int GS, bool ZERO, int WAVES, int NS>
+// Where a workgroup's expert and rows come from:
+//   kGrouped  the permutation: expert blockIdx.y, or the n-th one that has rows;
+//   kSlots    one token slot each (blockIdx.y = k t + j), for few tokens: gate_up
+//             picks the slot's expert from the router's logits (every wave by
+//             itself, which costs it less than a launch), and one more column of
+//             workgroups writes the decision for the later launches; down reads
+//             it.  Two slots of one expert read its weights twice.
+enum Mode { kGrouped, kSlots };
+
+// The decision of a call in slots: logits in; ids, weights and the identity
+// permutation out (gate_up), ids in (down).
+struct Slots {
+  const double* logits;   // [T][E]
+  int32_t* ids;           // [T][k]
+  float* w;               // [T][k]
+  int32_t* pos;           // [T k]
+  int k;
+};
+
+// The picks of one token, best first (float32 logit descending, index
+// ascending), up to and with pick `last`; wl takes their float64 logits.
+__device__ __forceinline__ void pick_experts(const double* __restrict__ logits, int E, int last, int lane,
+                                             int (&sel)[MOE_MAX_K_DEV], double (&wl)[MOE_MAX_K_DEV]) {
+  constexpr int kPer = MOE_MAX_E_DEV / kWave;
+  double l[kPer];
+  uint64_t key[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = lane + kWave * i;
+    l[i] = e < E ? logits[e] : 0.0;
+    key[i] = e < E ? make_key((float)l[i], e) : 0;
+  }
+#pragma unroll
+  for (int j = 0; j < MOE_MAX_K_DEV; ++j) {
+    if (j > last) break;
+    uint64_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < kPer; ++i) best = key[i] > best ? key[i] : best;
+    sel[j] = key_expert(wave_max(best));
+    double mine = 0.0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (lane + kWave * i == sel[j]) {
+        key[i] = 0;
+        mine = l[i];
+      }
+    wl[j] = lane_f64(mine, __builtin_amdgcn_readfirstlane(sel[j] % kWave));
+  }
+}
+
+// Logits of few tokens: one workgroup per (expert, token), exact products,
+// float64 sums, as the exact router's.
+constexpr int kLogitThreads = 256;
+__global__ __launch_bounds__(kLogitThreads) void slot_logits_kernel(const bf16_t* __restrict__ x,
+                                                                    const bf16_t* __restrict__ Wr,
+                                                                    const bf16_t* __restrict__ br, int H, int E,
+                                                                    double* __restrict__ logits) {
+  __shared__ double part[kLogitThreads / kWave];
+  const int e = blockIdx.x, t = blockIdx.y;
+  const u32x4_t* xr = reinterpret_cast<const u32x4_t*>(x + (size_t)t * H);
+  const u32x4_t* wr = reinterpret_cast<const u32x4_t*>(Wr + (size_t)e * H);
+  double a0 = 0.0, a1 = 0.0;
+  for (int i = threadIdx.x; i < H / 8; i += kLogitThreads) {
+    const u32x4_t a = xr[i], b = wr[i];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      a0 = __builtin_fma((double)bf16lo(a[q]), (double)bf16lo(b[q]), a0);
+      a1 = __builtin_fma((double)bf16hi(a[q]), (double)bf16hi(b[q]), a1);
+    }
+  }
+  const double sum = wave_add(a0 + a1);
+  if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0)
+    logits[(size_t)t * E + e] = ((part[0] + part[1]) + (part[2] + part[3])) + (double)bf16_to_f32(br[e]);
+}
+
+template <bool GATE_UP, int MG, int GS, bool ZERO, int WAVES, int NS, Mode MODE>
 __global__ __launch_bounds__(WAVES * kWave, WAVES == 8 || MG > 1 || NS > GS ? 2 : 3) void int4_stream_kernel(
     const bf16_t* __restrict__ A, const uint8_t* __restrict__ Wq, const uint16_t* __restrict__ Ws,
     const uint8_t* __restrict__ Wz, const bf16_t* __restrict__ bias, const int32_t* __restrict__ cnt,
     const int32_t* __restrict__ off, const int32_t* __restrict__ rows, int K, int N, int E, int kslots,
-    int64_t a_rows, void* __restrict__ out) {
+    int64_t a_rows, void* __restrict__ out, Slots slots) {
   constexpr int NGQ = 4 / GS;
   __shared__ float red[WAVES][4][4][kWave];   // [wave][call j][element v][lane]
 
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int strips = (N + kTileN - 1) / kTileN;
   int e = blockIdx.y, M, row0;
-  if ((int)gridDim.y == E) {
+  if (MODE == kSlots) {
+    M = 1, row0 = blockIdx.y;
+    if (GATE_UP) {
+      const int t = (int)blockIdx.y / slots.k, j = (int)blockIdx.y % slots.k;
+      const bool decide = (int)blockIdx.x * NS >= strips;   // block-uniform: past the strips
+      if (decide && (j != 0 || wave != 0)) return;          // no barrier follows there
+      int sel[MOE_MAX_K_DEV];
+      double wl[MOE_MAX_K_DEV];
+      pick_experts(slots.logits + (size_t)t * E, E, decide ? slots.k - 1 : j, lane, sel, wl);
+      if (decide) {
+        // lane i < k takes pick i; softmax over the picks in float64, summed in order
+        int my = sel[0];
+        double myl = wl[0];
+#pragma unroll
+        for (int i = 1; i < MOE_MAX_K_DEV; ++i)
+          if (i < slots.k && lane == i) my = sel[i], myl = wl[i];
+        const double z = lane < slots.k ? exp(myl - wl[0]) : 0.0;
+        double sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < MOE_MAX_K_DEV; ++i) sum += lane_f64(z, i);
+        if (lane < slots.k) {
+          const int slot = t * slots.k + lane;
+          slots.ids[slot] = my;
+          slots.w[slot] = (float)(z / sum);
+          slots.pos[slot] = slot;
+        }
+        return;
+      }
+#pragma unroll
+      for (int i = 0; i < MOE_MAX_K_DEV; ++i)
+        if (i == j) e = __builtin_amdgcn_readfirstlane(sel[i]);
+    } else {
+      e = slots.ids[blockIdx.y];
+    }
+  } else if ((int)gridDim.y == E) {
     M = cnt[e], row0 = off[e];
     if (M == 0) return;   // block-uniform
   } else if (!nth_live_expert(cnt, off, E, blockIdx.y, lane, e, M, row0)) {
@@ -185,7 +299,6 @@ __global__ __launch_bounds__(WAVES * kWave, WAVES == 8 || MG > 1 || NS > GS ? 2 
   const int g = lane >> 4, c = lane & 15;
   const int nkt = K / kTileK, nq = (nkt + 3) / 4, ng = (nkt + GS - 1) / GS;
   // N % 8 == 0: a lane's four columns of a strip are all in range or all out
-  const int strips = (N + kTileN - 1) / kTileN;
   int ncol[NS];
   uint32_t s_col[NS];
   const uint8_t* w_base[NS];
@@ -213,7 +326,7 @@ __global__ __launch_bounds__(WAVES * kWave, WAVES == 8 || MG > 1 || NS > GS ? 2 
 #pragma unroll
     for (int m = 0; m < MG; ++m) {
       const int r = min(r0 + 16 * m + c, M - 1);   // rows past M repeat the last one
-      slot[m] = GATE_UP ? rows[row0 + r] : r;
+      slot[m] = !GATE_UP ? r : MODE == kSlots ? row0 : rows[row0 + r];
     }
     f32x4_t acc[NS][MG][4];
 #pragma unroll
@@ -375,25 +488,28 @@ __global__ __launch_bounds__(WAVES * kWave, WAVES == 8 || MG > 1 || NS > GS ? 2 
   }
 }
 
-template <bool GATE_UP, int MG, int GS, int WAVES, int NS>
+template <bool GATE_UP, int MG, int GS, int WAVES, int NS, Mode MODE>
 hipError_t launch_stream(const void* A, const void* Wq, const void* Ws, const void* Wz, const void* bias,
                          const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T, int K, int N, int E,
-                         int k, int experts, void* out, hipStream_t stream) {
-  dim3 grid((unsigned)(((N + kTileN - 1) / kTileN + NS - 1) / NS), (unsigned)experts);
-  auto kern = Wz ? int4_stream_kernel<GATE_UP, MG, GS, true, WAVES, NS> : int4_stream_kernel<GATE_UP, MG, GS, false, WAVES, NS>;
+                         int k, int experts, void* out, const Slots& slots, hipStream_t stream) {
+  const int columns = ((N + kTileN - 1) / kTileN + NS - 1) / NS;
+  dim3 grid((unsigned)(columns + (MODE == kSlots && GATE_UP ? 1 : 0)), (unsigned)experts);
+  auto kern = Wz ? int4_stream_kernel<GATE_UP, MG, GS, true, WAVES, NS, MODE>
+                 : int4_stream_kernel<GATE_UP, MG, GS, false, WAVES, NS, MODE>;
   hipLaunchKernelGGL(kern, grid, dim3(WAVES * kWave), 0, stream, (const bf16_t*)A, (const uint8_t*)Wq,
-                     (const uint16_t*)Ws, (const uint8_t*)Wz, (const bf16_t*)bias, cnt, off, rows, K, N, E, k, T, out);
+                     (const uint16_t*)Ws, (const uint8_t*)Wz, (const bf16_t*)bias, cnt, off, rows, K, N, E, k, T, out,
+                     slots);
   return hipGetLastError();
 }
 
-template <bool GATE_UP, int MG, int WAVES, int NS>
+template <bool GATE_UP, int MG, int WAVES, int NS, Mode MODE>
 hipError_t launch_group(int G, const void* A, const void* Wq, const void* Ws, const void* Wz, const void* bias,
                         const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T, int K, int N, int E,
-                        int k, int experts, void* out, hipStream_t stream) {
-  auto launch = G == 32   ? launch_stream<GATE_UP, MG, 1, WAVES, NS>
-                : G == 64 ? launch_stream<GATE_UP, MG, 2, WAVES, NS>
-                          : launch_stream<GATE_UP, MG, 4, WAVES, NS>;
-  return launch(A, Wq, Ws, Wz, bias, cnt, off, rows, T, K, N, E, k, experts, out, stream);
+                        int k, int experts, void* out, const Slots& slots, hipStream_t stream) {
+  auto launch = G == 32   ? launch_stream<GATE_UP, MG, 1, WAVES, NS, MODE>
+                : G == 64 ? launch_stream<GATE_UP, MG, 2, WAVES, NS, MODE>
+                          : launch_stream<GATE_UP, MG, 4, WAVES, NS, MODE>;
+  return launch(A, Wq, Ws, Wz, bias, cnt, off, rows, T, K, N, E, k, experts, out, slots, stream);
 }
 
 // Mean rows per expert up to which one 16-row chunk a pass is enough, and from
@@ -418,11 +534,22 @@ hipError_t launch_int4(const void* A, const void* Wq, const void* Ws, const void
   const int experts = (int)(T * k < E ? T * k : E);
   const int64_t workgroups = (int64_t)experts * ((N + kTileN - 1) / kTileN);
   const bool two = T * k >= kTwoStripsMeanRows * E && workgroups >= 4 * kCus;
-  auto launch = T * k > kOneChunkMeanRows * E ? (two ? launch_group<GATE_UP, 2, 4, 2> : launch_group<GATE_UP, 2, 4, 1>)
-                : two                         ? launch_group<GATE_UP, 1, 4, 2>
-                : workgroups <= kCus          ? launch_group<GATE_UP, 1, 8, 1>
-                                              : launch_group<GATE_UP, 1, 4, 1>;
-  return launch(G, A, Wq, Ws, Wz, bias, cnt, off, rows, T, K, N, E, k, experts, out, stream);
+  auto launch = T * k > kOneChunkMeanRows * E
+                    ? (two ? launch_group<GATE_UP, 2, 4, 2, kGrouped> : launch_group<GATE_UP, 2, 4, 1, kGrouped>)
+                : two                ? launch_group<GATE_UP, 1, 4, 2, kGrouped>
+                : workgroups <= kCus ? launch_group<GATE_UP, 1, 8, 1, kGrouped>
+                                     : launch_group<GATE_UP, 1, 4, 1, kGrouped>;
+  return launch(G, A, Wq, Ws, Wz, bias, cnt, off, rows, T, K, N, E, k, experts, out, Slots{}, stream);
+}
+
+// One workgroup column per token slot (the rows of h and o in slot order).
+template <bool GATE_UP>
+hipError_t launch_slots(const void* A, const void* Wq, const void* Ws, const void* Wz, const void* bias, int64_t T, int K,
+                        int N, int E, int G, void* out, const Slots& slots, hipStream_t stream) {
+  const int S = (int)T * slots.k;
+  const int64_t workgroups = (int64_t)S * ((N + kTileN - 1) / kTileN);
+  auto launch = workgroups <= kCus ? launch_group<GATE_UP, 1, 8, 1, kSlots> : launch_group<GATE_UP, 1, 4, 1, kSlots>;
+  return launch(G, A, Wq, Ws, Wz, bias, nullptr, nullptr, nullptr, GATE_UP ? T : S, K, N, E, slots.k, S, out, slots, stream);
 }
 
 }  // namespace
@@ -440,6 +567,20 @@ hipError_t launch_int4_pack(const void* src, int E, int K, int N, void* codes, h
   dim3 grid((unsigned)(K / kTileK), (unsigned)((N + kTileN - 1) / kTileN), (unsigned)E);
   hipLaunchKernelGGL(int4_pack_kernel, grid, dim3(kQThreads), 0, stream, (const uint8_t*)src, K, N, (uint32_t*)codes);
   return hipGetLastError();
+}
+
+hipError_t launch_int4_slots(const void* x, const void* Wr, const void* br, const void* Wgu_q, const void* Wgu_s,
+                             const void* Wgu_z, const void* bgu, const void* Wd_q, const void* Wd_s, const void* Wd_z,
+                             const void* bd, int64_t T, int H, int E, int k, int I, int G, double* logits, int32_t* ids,
+                             float* w, int32_t* pos, void* h, float* o, hipStream_t stream) {
+  hipLaunchKernelGGL(slot_logits_kernel, dim3((unsigned)E, (unsigned)T), dim3(kLogitThreads), 0, stream,
+                     (const bf16_t*)x, (const bf16_t*)Wr, (const bf16_t*)br, H, E, logits);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const Slots slots{logits, ids, w, pos, k};
+  e = launch_slots<true>(x, Wgu_q, Wgu_s, Wgu_z, bgu, T, H, 2 * I, E, G, h, slots, stream);
+  if (e != hipSuccess) return e;
+  return launch_slots<false>(h, Wd_q, Wd_s, Wd_z, bd, T, I, H, E, G, o, slots, stream);
 }
 
 hipError_t launch_int4_gate_up(const void* x, const void* Wq, const void* Ws, const void* Wz, const void* bgu,

@@ -95,6 +95,14 @@ hipError_t launch_int4_gate_up(const void* x, const void* Wq, const void* Ws, co
 hipError_t launch_int4_down(const void* h, const void* Wq, const void* Ws, const void* Wz, const void* bd,
                             const int32_t* cnt, const int32_t* off, int64_t T, int H, int E, int k, int I, int G, float* o,
                             hipStream_t stream);
+// Router, gate_up and down for few tokens, one workgroup column per token slot
+// (h, o in slot order; ids, w and the identity pos written for the combine):
+// the streaming kernels' results without a router and a permutation launch.
+// logits: scratch of T E doubles that is neither h nor pos.
+hipError_t launch_int4_slots(const void* x, const void* Wr, const void* br, const void* Wgu_q, const void* Wgu_s,
+                             const void* Wgu_z, const void* bgu, const void* Wd_q, const void* Wd_s, const void* Wd_z,
+                             const void* bd, int64_t T, int H, int E, int k, int I, int G, double* logits, int32_t* ids,
+                             float* w, int32_t* pos, void* h, float* o, hipStream_t stream);
 // the LDS-tiled grouped GEMMs (int4_gemm.hip)
 hipError_t launch_gemm_int4_gate_up(const void* x, const void* Wq, const void* Ws, const void* Wz, const void* bgu,
                                const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T, int H, int E,

@@ -662,8 +662,8 @@ static int check_int4_dims(const char* fn, const char* name, int32_t K, int32_t 
 
 // The kernels address the token rows with 32-bit byte offsets: x of T rows, or
 // the rows of h that one expert may have.
-static int check_int4_rows(const char* fn, const char* name, int64_t rows, int32_t K) {
-  if (rows * K * 2 >= (int64_t)1 << 32)
+static int check_rows(const char* fn, const char* name, int64_t rows, int32_t K) {
+  if (rows * K * 2 >= ((int64_t)1 << 32) - 64)   // (the router's bound is 64 bytes short of it)
     return fail(MOE_ERR_UNSUPPORTED, "%s: %s of %lld rows of %d takes 4 GiB or more: split the batch", fn, name,
                 (long long)rows, K);
   return MOE_OK;
@@ -755,8 +755,8 @@ static int forward_int4(const char* fn, const void* x, const void* Wr, const voi
     return fail(MOE_ERR_INVALID_ARG, "%s: expert_counts_out is not 4-byte aligned", fn);
   if (path < MOE_PATH_AUTO || path > MOE_PATH_GEMM)
     return fail(MOE_ERR_INVALID_ARG, "%s: unknown path %d", fn, path);
-  if (int st = check_int4_rows(fn, "x", T, H)) return st;
-  if (int st = check_int4_rows(fn, "h", T * k, I)) return st;
+  if (int st = check_rows(fn, "x", T, H)) return st;
+  if (int st = check_rows(fn, "h", T * k, I)) return st;
   if (T == 0) return ok();
   const Layout L = layout(T, H, E, k, I);
   if (workspace == nullptr || workspace_bytes < L.total)
@@ -778,6 +778,20 @@ static int forward_int4(const char* fn, const void* x, const void* Wr, const voi
   // the expert path follows the whole layer's load per expert, T*k/E
   path = choose_path(path, T, E, k);
 
+  // Few slots, one by one: no permutation, and the router without its own last
+  // launch.  At H=I=2880, k=4, G=64 and evenly chosen experts: E=32 T=1 21.6 us
+  // against 31.5 in groups, E=128 T=1 22.2 against 44.9, T=8 78 against 94.  At
+  // half as many slots as experts the weights read twice have used that up (E=128
+  // T=16 140 against 137), and uneven choices repeat more of them: a quarter.
+  // The logits sit where o will be (down writes it when they have been read).
+  if (path == MOE_PATH_GEMV && T * k * 4 <= E && !n_valid && !expert_counts_out && n_local == E &&
+      (size_t)T * E * sizeof(double) <= (size_t)T * k * H * 4) {
+    if (int st = hip_status(fn, moe::launch_int4_slots(x, Wr, br, Wgu_q, Wgu_s, Wgu_z, bgu, Wd_q, Wd_s, Wd_z, bd, T, H,
+                                                       E, k, I, G, reinterpret_cast<double*>(o), ids, w, pos, h, o, s)))
+      return st;
+    if (int st = hip_status(fn, moe::launch_combine(o, pos, w, T, H, k, y, s, partial))) return st;
+    return ok();
+  }
   if (int st = hip_status(fn, moe::launch_route(x, Wr, br, T, H, E, k, ids, w, route_method(T), s))) return st;
   if (n_valid)
     if (int st = hip_status(fn, moe::launch_mask_padding(ids, w, T, k, n_valid, s))) return st;
@@ -846,7 +860,7 @@ int moe_gate_up_int4(const void* x, const void* Wgu_q, const void* Wgu_s, const 
   CHECK_PTR(h, 16);
   if (path < MOE_PATH_AUTO || path > MOE_PATH_GEMM)
     return fail(MOE_ERR_INVALID_ARG, "%s: unknown path %d", fn, path);
-  if (int st = check_int4_rows(fn, "x", T, H)) return st;
+  if (int st = check_rows(fn, "x", T, H)) return st;
   if (T == 0) return ok();
   if (int st = run_gate_up_int4(fn, x, Wgu_q, Wgu_s, Wgu_z, bgu, cnt, off, rows, T, H, E, k, I, G, h, path,
                                 (hipStream_t)stream))
@@ -870,7 +884,7 @@ int moe_down_int4(const void* h, const void* Wd_q, const void* Wd_s, const void*
   CHECK_PTR(o, 16);
   if (path < MOE_PATH_AUTO || path > MOE_PATH_GEMM)
     return fail(MOE_ERR_INVALID_ARG, "%s: unknown path %d", fn, path);
-  if (int st = check_int4_rows(fn, "h", T * k, I)) return st;
+  if (int st = check_rows(fn, "h", T * k, I)) return st;
   if (T == 0) return ok();
   if (int st = run_down_int4(fn, h, Wd_q, Wd_s, Wd_z, bd, cnt, off, T, H, E, k, I, G, o, path, (hipStream_t)stream))
     return st;
@@ -1225,6 +1239,10 @@ int moe_forward_norm_fp8(const void* x, const void* residual, const void* gamma,
   const size_t rows = (size_t)T * H * 2;
   if (residual_out && !disjoint(y, rows, residual_out, rows))
     return fail(MOE_ERR_INVALID_ARG, "%s: y overlaps residual_out", fn);
+  // Rows that the router and the FP8 kernels address with 32 bits (the codes of a
+  // row have half its bytes), refused before anything is enqueued.
+  if (int st = check_rows(fn, "x", T, H)) return st;
+  if (int st = check_rows(fn, "h", T * k, I)) return st;
   const NormIn norm{residual, gamma, eps, residual_out};
   return forward_fp8(fn, x, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, T, H, E, k, I, 0, E, nullptr, y, false,
                      topk_ids_out, topk_w_out, nullptr, workspace, workspace_bytes, path, stream, &norm);

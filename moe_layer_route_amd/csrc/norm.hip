@@ -22,6 +22,7 @@
 // takes 2.6 us.
 #include "device_common.h"
 #include "launch.h"
+#include "wave_reduce.h"
 
 namespace moe {
 namespace {
@@ -39,39 +40,6 @@ __device__ __forceinline__ uint32_t e4m3_any(float v) {
   const uint32_t q = (uint32_t)__builtin_rintf(__builtin_amdgcn_ldexpf(a, 3 - e));
   const uint32_t code = sign | (uint32_t)((e + 6) * 8 + (int)q);
   return v != v ? 0x7Fu : code;
-}
-
-// Reductions over a wave by data-parallel moves: within quads, halves of rows
-// and rows of 16 lanes (every lane of a row ends with the row's result, equal
-// bits, since the operands of each step are symmetric), then the four rows.
-template <int CTRL>
-__device__ __forceinline__ uint32_t moved(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
-}
-constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;
-
-template <int CTRL>
-__device__ __forceinline__ double add_moved(double v) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  return v + __builtin_bit_cast(double, (uint64_t)moved<CTRL>((uint32_t)(b >> 32)) << 32 | moved<CTRL>((uint32_t)b));
-}
-__device__ __forceinline__ double lane_f64(double v, int lane) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-__device__ __forceinline__ double wave_sum(double v) {
-  v = add_moved<kMirror>(add_moved<kHalfMirror>(add_moved<kXor2>(add_moved<kXor1>(v))));
-  return (lane_f64(v, 0) + lane_f64(v, 16)) + (lane_f64(v, 32) + lane_f64(v, 48));
-}
-__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
-  v = max(v, moved<kXor1>(v));
-  v = max(v, moved<kXor2>(v));
-  v = max(v, moved<kHalfMirror>(v));
-  v = max(v, moved<kMirror>(v));
-  return max(max((uint32_t)__builtin_amdgcn_readlane((int)v, 0), (uint32_t)__builtin_amdgcn_readlane((int)v, 16)),
-             max((uint32_t)__builtin_amdgcn_readlane((int)v, 32), (uint32_t)__builtin_amdgcn_readlane((int)v, 48)));
 }
 
 constexpr int kNormMaxWaves = 16;
@@ -134,7 +102,7 @@ __global__ __launch_bounds__(kNormMaxWaves * kWave) void add_rmsnorm_kernel(
         ss = __builtin_fma(lo, lo, ss);
         ss = __builtin_fma(hi, hi, ss);
       }
-    ss = wave_sum(ss);
+    ss = wave_add(ss);
     if (waves > 1) {
       if (lane == 0) s_sum[parity][wave] = ss;
       __syncthreads();
@@ -167,7 +135,7 @@ __global__ __launch_bounds__(kNormMaxWaves * kWave) void add_rmsnorm_kernel(
       }
     }
     if (!FP8) continue;
-    m = wave_umax(m);
+    m = wave_max(m);
     if (waves > 1) {
       if (lane == 0) s_max[parity][wave] = m;
       __syncthreads();

@@ -34,6 +34,7 @@
 // latency, not arithmetic, sets the time.
 #include "device_common.h"
 #include "launch.h"
+#include "route_key.h"
 
 namespace moe {
 namespace {
@@ -56,17 +57,6 @@ __device__ __forceinline__ u32x4_t abs_bf16x8(u32x4_t v) {
   const uint32_t m = 0x7FFF7FFFu;
   return u32x4_t{v[0] & m, v[1] & m, v[2] & m, v[3] & m};
 }
-
-// Monotone map of float32 to uint32 (larger float -> larger key); -0 == +0.
-__device__ __forceinline__ uint32_t order_key(float v) {
-  uint32_t u = __float_as_uint(v);
-  if (u == 0x80000000u) u = 0u;
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ uint64_t make_key(float v, int e) {
-  return ((uint64_t)order_key(v) << 32) | (uint64_t)(0xFFFFu - (uint32_t)e);
-}
-__device__ __forceinline__ int key_expert(uint64_t k) { return (int)(0xFFFFu - (uint32_t)(k & 0xFFFFu)); }
 
 __device__ __forceinline__ double wave_sum_f64(double v) {
 #pragma unroll

@@ -178,6 +178,84 @@ def test_forward(T, E, H, I, k, G, zeros, path):
     assert_y_close(host_f64(y), ref["y"], f"y T{T} E{E}")
 
 
+# Up to a quarter as many slots as experts run one by one, more of them in groups; a padded batch without padding
+# always runs in groups.
+@pytest.mark.parametrize("T,E,H,I,k,G,zeros", [
+    (1, 4, 32, 32, 1, 32, True), (1, 32, 2880, 2880, 4, 32, False), (2, 32, 96, 160, 4, 64, True),
+    (3, 32, 96, 160, 4, 64, True), (4, 64, 1440, 96, 4, 128, False), (5, 128, 608, 2880, 3, 128, True),
+    (8, 256, 256, 64, 8, 32, True), (64, 256, 64, 96, 1, 64, False), (1, 256, 32, 32, 1, 32, False),
+    (1, 20, 32, 5760, 5, 64, True)])
+def test_few_slots(T, E, H, I, k, G, zeros):
+    """The decision is the groups' (weights within one float step of each other), and so are the rows."""
+    _need_gpu()
+    b = _block(T, E, H, I, k, G, zeros, seed=T + E)
+    args, z = _gpu_args(b)
+    out = []
+    for call in (binding.moe_forward_int4, binding.moe_forward_padded_int4):
+        ids = torch.full((T, k), -1, dtype=torch.int32, device="cuda")
+        w = torch.full((T, k), -1.0, dtype=torch.float32, device="cuda")
+        out.append((call(*args, k=k, topk_ids=ids, topk_w=w, **z), ids, w))
+    (y, ids, w), (y2, ids2, w2) = out
+    ref = orc.moe_forward_int4(*b, k=k, G=G)
+    assert_routing(ids.cpu().numpy(), w.cpu().numpy(), ref["ids"], ref["w"], ref["logits"], k)
+    assert_y_close(host_f64(y), ref["y"], f"y T{T} E{E}")
+    assert torch.equal(ids, ids2)
+    torch.testing.assert_close(w, w2, rtol=2 ** -23, atol=0)
+    if torch.equal(w, w2):
+        assert torch.equal(y, y2)
+    assert torch.equal(binding.moe_forward_int4(*args, k=k, **z), y)   # and with ids and weights in the workspace
+
+
+def test_few_slots_ties():
+    """Equal logits go to the lower index, -0 and 0 are equal, and NaN logits still pick k experts."""
+    _need_gpu()
+    T, E, H, I, k, G = 2, 64, 64, 64, 8, 64
+    b = list(_block(T, E, H, I, k, G, False, seed=3))
+    b[1][:] = b[1][0]
+    b[2][:] = 0
+    args, z = _gpu_args(tuple(b))
+    ids = torch.empty((T, k), dtype=torch.int32, device="cuda")
+    w = torch.empty((T, k), dtype=torch.float32, device="cuda")
+    binding.moe_forward_int4(*args, k=k, topk_ids=ids, topk_w=w, **z)
+    assert ids.tolist() == [list(range(k))] * T and (w == 1 / k).all()
+    x = args[0].clone()
+    x[0] = 0
+    x[1, 5] = float("nan")
+    args[1][:, 0] = -args[1][:, 0]
+    y = binding.moe_forward_int4(x, *args[1:], k=k, topk_ids=ids, topk_w=w, **z)
+    assert ids[0].tolist() == list(range(k)) and torch.isfinite(y[0]).all()
+    assert len(set(ids[1].tolist())) == k and 0 <= ids[1].min() and ids[1].max() < E and torch.isnan(y[1]).all()
+
+
+def test_few_slots_graph_replays():
+    """Two captured calls that share a workspace, replayed in turn with eager calls between."""
+    _need_gpu()
+    T, E, H, I, k, G = 2, 64, 256, 160, 4, 64
+    args, z = _gpu_args(_block(T, E, H, I, k, G, True, seed=23))
+    xs = (args[0], args[0].flip(0).contiguous())
+    ws = binding.alloc_workspace(T, H, E, k, I)
+    ys = [torch.empty((T, H), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    want = [binding.moe_forward_int4(x, *args[1:], k=k, **z) for x in xs]
+    torch.cuda.synchronize()
+    graphs = []
+    for x, y in zip(xs, ys):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            binding.moe_forward_int4(x, *args[1:], k=k, y=y, workspace=ws, **z)
+        graphs.append(g)
+    for i in range(3):
+        for y in ys:
+            y.fill_(-1.0)
+        ws.fill_(0xFF if i % 2 else 0x11)
+        eager = binding.moe_forward_int4(xs[1], *args[1:], k=k, **z)
+        torch.cuda.synchronize()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(eager, want[1])
+        assert all(torch.equal(y, w) for y, w in zip(ys, want)), i
+
+
 @pytest.mark.parametrize("E,K,N,G", [(2, 96, 40, 64), (1, 2880, 72, 128), (3, 32, 8, 32), (1, 160, 200, 32), (2, 128, 64, 64)])
 @pytest.mark.parametrize("zeros", [False, True])
 def test_quantizer_matches_oracle(E, K, N, G, zeros):

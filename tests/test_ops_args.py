@@ -85,6 +85,14 @@ def test_forward_norm_workspace(lib):
     assert lib.moe_workspace_bytes_norm_fp8(0, 64, 8, 2, 64) == 0 and lib.moe_workspace_bytes_norm_fp8(4, 64, 1, 2, 64) == 0
 
 
+def test_forward_norm_refuses_what_its_kernels_cannot_address(lib):
+    """Before the norm is enqueued."""
+    UNSUPPORTED = 2
+    assert _fwd_norm(lib, T=(1 << 31) // 64, r=_p(60), res=_p(50), y=_p(70), ws=_p(90), ws_bytes=1 << 60) == UNSUPPORTED
+    assert b"x of" in lib.moe_last_error()
+    assert _fwd_norm(lib, T=1 << 20, I=1024, ws_bytes=1 << 60) == UNSUPPORTED and b"h of" in lib.moe_last_error()
+
+
 def _fwd4(lib, T=8, H=64, E=8, k=2, I=64, G=32, ptr=None, z=(None, None), ws=_p(20), ws_bytes=1 << 30, path=0):
     p = [_p(i) for i in range(12)]
     for i, v in (ptr or {}).items():
