@@ -556,7 +556,9 @@ MOE_API int moe_forward_norm_fp8(const void* x, const void* residual, const void
  * 0..15 for each group of G consecutive values of K in a column (G = 32, 64 or
  * 128; the last group of a column may be shorter).  Without zero points z = 8.
  * The products take the integers exactly and apply s to float32 sums over a
- * group, so no weight is rounded.
+ * group, so no weight is rounded.  The sums are of a (16 + q) less (16 + z)
+ * times the sum of a: a row with a NaN, an infinity or values whose sum over a
+ * group, times 31, leaves float32 gives NaN in that row.
  *
  * For a weight with contraction dimension K and N columns (gate_up: K = H,
  * N = 2I; down: K = I, N = H):

@@ -10,7 +10,7 @@
 // rows.  K goes in units of GU tiles that never cross a group of the scales
 // (64 values, or 32 where the groups are of 32).  A unit's token rows come into
 // LDS by direct loads, fragment by fragment (a fragment is the 16-row operand
-// of one MFMA, a kilobyte), three units ahead in a ring of four, and so do the
+// of one MFMA, a kilobyte), two units ahead in a ring of four, and so do the
 // wave's own tiles of weights, their scales and zero points.  (Weights loaded
 // into registers: 873 against 774 us at the first size below.  The compiler
 // counts only the loads it makes itself, so its waits for them take in the
@@ -19,10 +19,11 @@
 // times the scale, in float32: no weight is rounded, for 128 more VALU
 // instructions a unit beside its 64 products.
 //
-// T = 4096 of 32 experts, 2880 x 5760 (gate_up), G = 64: 584 us, 931 TFLOP/s;
-// down 325 us, 837 TFLOP/s (a large library product reaches 1155 to 1300 here).
-// VALU and MFMA issue bind: without the row loads and the additions the loop
-// takes 0.7 of that, without LDS row reads on top 0.45.
+// T = 4096 of 32 experts, 2880 x 5760 (gate_up), G = 64: 570 us, 954 TFLOP/s;
+// down 324 us, 839 TFLOP/s (a large library product reaches 1155 to 1300 here);
+// T = 16384: 2113 us, 1029 TFLOP/s.  Vector issue binds (each SIMD issues a
+// product and an addition through one port: 48% of all cycles, while the matrix
+// pipes are busy for 44%, at the 1.96 GHz that the card holds under this load).
 #include "device_common.h"
 #include "int4_device.h"
 #include "launch.h"
@@ -38,7 +39,7 @@ static_assert(kChunks == kGemmWaves && kChunks == 8, "a wave brings in one chunk
 constexpr int kBN = kGemmWaves * kTileN;
 constexpr int kRing = 4;
 constexpr int kXcds = 8;
-constexpr int kMBlock = 8;   // M tiles per block of the tile order
+constexpr int kMBlock = 8;   // M tiles that take an N tile together
 constexpr uint32_t kOutOfRange = 0xFFFFFFF0u;
 
 template <int GU>
@@ -47,8 +48,74 @@ struct Ring {
   u32x4_t w[kGemmWaves][kRing][GU][kWave];      // each wave's tiles
   uint32_t s[kGemmWaves][kRing][kWave];         // scales of its 64 columns, twice
   uint32_t z[kGemmWaves][kRing][kWave];         // zero points, four times
-  float sum[2][kChunks][16];                    // of each row's values over a unit, times `flat`
+  float sum[4][kChunks][16];                    // of each row's values over a unit, times `flat`
 };
+
+// Which tile a workgroup takes.  An expert has ceil(M / kBM) M tiles x n_tiles N
+// tiles.  They come in three rounds, the long ones first, so that the last to
+// run are short (T = 1024: 128 rows an expert on average, and every second one
+// has a tile of a few rows: gate_up 244 us in one sequence, 195 in rounds):
+//   0  M tiles with more than kBM / 2 rows x the `wide` N tiles whose strips are
+//      all there: expert by expert, kMBlock M tiles taking each N tile in turn;
+//   1  an expert's shorter last M tile x those N tiles;
+//   2  every M tile x the N tile that is not `wide`.
+// A round's tiles are dealt to the XCDs (block b runs on XCD b % 8) in equal
+// consecutive parts, whose L2 serves the tiles that share rows or weights.
+// Every lane gets the same; false for a block past the last tile (the grid is an
+// upper bound).  Lane l counts experts 4 l .. 4 l + 3: E <= 256.
+__device__ __forceinline__ bool tile_of(const int32_t* __restrict__ cnt, int E, int n_tiles, int wide, int lane, int& e,
+                                        int& m0, int& nt) {
+  int longer[4], shorter[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int at = lane * 4 + i, M = at < E ? cnt[at] : 0, rest = M % kBM;
+    longer[i] = M / kBM + (rest > kBM / 2);
+    shorter[i] = rest > 0 && rest <= kBM / 2;
+  }
+  int xi = (int)blockIdx.x / kXcds;
+#pragma unroll 1
+  for (int round = 0; round < 3; ++round) {
+    const int cols = round < 2 ? wide : n_tiles - wide;
+    int tiles[4], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      tiles[i] = ((round != 1 ? longer[i] : 0) + (round != 0 ? shorter[i] : 0)) * cols;
+      sum += tiles[i];
+    }
+    const int incl = wave_incl_scan(sum, lane);
+    const int all = __builtin_amdgcn_readlane(incl, kWave - 1), share = (all + kXcds - 1) / kXcds;
+    if (xi >= share) {   // block-uniform
+      xi -= share;
+      continue;
+    }
+    const int at = (int)(blockIdx.x % kXcds) * share + xi;
+    if (at >= all) return false;
+    int fe = -1, fm = 0, fn = 0, start = incl - sum;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (at >= start && at < start + tiles[i]) {
+        const int t = at - start;
+        fe = lane * 4 + i;
+        if (round == 0) {
+          const int block = t / (kMBlock * wide), in_block = t - block * kMBlock * wide;
+          const int height = min(kMBlock, longer[i] - block * kMBlock);
+          fm = block * kMBlock + in_block % height, fn = in_block / height;
+        } else if (round == 1) {
+          fm = longer[i], fn = t;
+        } else {
+          fm = t, fn = wide;
+        }
+      }
+      start += tiles[i];
+    }
+    const int src = __ffsll((unsigned long long)__ballot(fe >= 0)) - 1;
+    e = __builtin_amdgcn_readlane(fe, src);
+    m0 = __builtin_amdgcn_readlane(fm, src) * kBM;
+    nt = __builtin_amdgcn_readlane(fn, src);
+    return true;
+  }
+  return false;
+}
 
 template <bool GATE_UP, int GU, bool ZERO>
 __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
@@ -60,7 +127,7 @@ __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   int e, m0, nt;
-  if (!grouped_gemm_tile(cnt, E, kBM, n_tiles, kMBlock, lane, e, m0, nt)) return;   // block-uniform
+  if (!tile_of(cnt, E, n_tiles, (N + kTileN - 1) / kTileN / kGemmWaves, lane, e, m0, nt)) return;   // block-uniform
   const int M = cnt[e], row0 = off[e];
   const int nch = min(kChunks, (M - m0 + 15) / 16);   // chunks with rows
   const int g = lane >> 4, c = lane & 15;
@@ -78,9 +145,12 @@ __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
   const u32x4_t a_rs = rsrc_words(GATE_UP ? A : A + (size_t)row0 * K, (uint32_t)((size_t)(GATE_UP ? a_rows : M) * K * 2));
 
   // wave w brings in chunk w's fragments: lane (row c, group g); rows past M
-  // repeat the last one, columns past N the last ones
+  // repeat the last one, a chunk without rows reads nothing (zeros), columns
+  // past N are the last ones
   const int r = min(m0 + 16 * wave + c, M - 1);
-  const uint32_t a_off = ((uint32_t)(GATE_UP ? rows[row0 + r] / kslots : r) * (uint32_t)K + 8u * g) * 2u;
+  const uint32_t a_off = m0 + 16 * wave >= M ? kOutOfRange
+                                             : ((uint32_t)(GATE_UP ? rows[row0 + r] / kslots : r) * (uint32_t)K +
+                                                8u * g) * 2u;
   const uint32_t s_off = 2u * (uint32_t)min(wstrip * kTileN + 2 * (lane & 31), N - 2);
   const uint32_t z_off = (uint32_t)min(wstrip * kTileN + 4 * c, N - 4);
   const uint32_t rows_at = (uint32_t)(uintptr_t)&ring.rows[0][0][wave][0];
@@ -146,10 +216,10 @@ __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
     f32x4_t sum = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int t = 0; t < GU; ++t) sum = mfma16x16x32(a[t], flat, sum);
-    if (c == 0) *reinterpret_cast<f32x4_t*>(&ring.sum[u & 1][wave][4 * g]) = sum;
+    if (c == 0) *reinterpret_cast<f32x4_t*>(&ring.sum[u & 3][wave][4 * g]) = sum;
   };
   auto sum_in = [&](int u, int m) __attribute__((always_inline)) {
-    return *reinterpret_cast<const f32x4_t*>(&ring.sum[u & 1][m][4 * g]);
+    return *reinterpret_cast<const f32x4_t*>(&ring.sum[u & 3][m][4 * g]);
   };
   auto chunk_mul = [&](const u32x4_t (&a)[GU], const f32x4_t& sum, const u32x4_t (&bw)[GU][4], const float (&z)[4],
                        f32x4_t (&part)[4]) __attribute__((always_inline)) {
@@ -172,12 +242,12 @@ __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
   };
   const Int4Masks masks;
   // What a wave prepares of the next unit: loads retire in order, so with those
-  // of two units still under way its own part of unit u is in LDS.
+  // of one unit still under way its own part of unit u is in LDS.
   auto next = [&](int u) __attribute__((always_inline)) {
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kLoads) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads) : "memory");
     sum_rows(u);
   };
-  auto compute = [&](auto count, int u, const Words& b) __attribute__((always_inline)) {
+  auto compute = [&](auto count, auto shift, int u, const Words& b) __attribute__((always_inline)) {
     float s[4], z[4];
     u32x4_t bw[GU][4];
 #pragma unroll
@@ -191,7 +261,8 @@ __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
     }
     // Without branches: a chunk is read two ahead of its products and added
     // behind the next one's.
-    constexpr int kCount = decltype(count)::value;
+    constexpr int kCount = decltype(count)::value, kHalf = kCount / 2;
+    constexpr bool kLate = decltype(shift)::value;
     u32x4_t a[3][GU];
     f32x4_t sum[3], part[2][4];
 #pragma unroll
@@ -202,42 +273,62 @@ __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
 #pragma unroll
     for (int m = 0; m < kCount; ++m) {
       __builtin_amdgcn_sched_barrier(0);
-      // The loads of unit u + 3 (into the slot that unit u - 1 was read from),
-      // spread over the chunks: a load that the CU's load path cannot take yet
-      // holds up its wave's products.
+      // The loads of the unit two ahead (three for the second half of a late
+      // wave's unit, which is past the barrier), into the slot that every wave
+      // has left; spread over the chunks: a load that the CU's load path cannot
+      // take yet holds up its wave's products.
 #pragma unroll
       for (int i = 0; i < kLoads; ++i)
-        if (i * (kCount - 1) / kLoads == m) load(u + 3, i);
+        if (kLate ? kHalf + i * kHalf / kLoads == m : i * (kCount - 1) / kLoads == m) load(kLate ? u + 3 : u + 2, i);
       if (m + 2 < kCount) {
         chunk_in(u, m + 2, a[(m + 2) % 3]);
         sum[(m + 2) % 3] = sum_in(u, m + 2);
       }
       chunk_mul(a[m % 3], sum[m % 3], bw, z, part[m & 1]);
-      if (m == kCount - 1) next(u + 1);
+      if (m == (kLate ? kHalf : kCount) - 1) {
+        next(u + 1);
+        if (kLate) __syncthreads();
+      }
       if (m > 0) chunk_add(acc[m - 1], part[(m - 1) & 1], s);
     }
     chunk_add(acc[kCount - 1], part[(kCount - 1) & 1], s);
   };
 
+  // Every SIMD has one wave of each half of the workgroup.  The second half runs
+  // half a unit behind: its barriers stand in the middle of a unit, so that one
+  // wave unpacks its weights, and waits, while the other has products to issue.
+  // (T = 4096, G = 64: 595 us in step, 570 like this.  With
+  // zero points and units of two tiles it takes 14 registers too many.)
+  const bool late = !(ZERO && GU == 2) && live && wave >= kGemmWaves / 2;
   load_all(0);
   load_all(1);
-  load_all(2);
   Words b;
   next(0);
   words(0, b);
+  if (late) load_all(2);
   __syncthreads();
   // The wave's own weights it may read at once, the other waves' rows and sums
-  // behind the barrier, where every read of this unit's has returned too.
+  // behind the barrier.  Barrier u stands behind the first waves' unit u and
+  // amid the late ones' (which have read unit u - 1 by then): between barriers
+  // u - 1 and u the slots of u - 1, u and u + 1 are in use, and the loads of u + 2
+  // go to the fourth.
   auto run = [&](auto count) __attribute__((always_inline)) {
-    for (int u = 0; u < nu; ++u) {
-      if (live) {
-        compute(count, u, b);
-      } else {
-        load_all(u + 3);
-        next(u + 1);
+    if (late) {
+      for (int u = 0; u < nu; ++u) {
+        compute(count, std::true_type{}, u, b);
+        words(u + 1, b);
       }
-      words(u + 1, b);
-      __syncthreads();
+    } else {
+      for (int u = 0; u < nu; ++u) {
+        if (live) {
+          compute(count, std::false_type{}, u, b);
+        } else {
+          load_all(u + 2);
+          next(u + 1);
+        }
+        words(u + 1, b);
+        __syncthreads();
+      }
     }
   };
   // an even count of chunks: at most one is computed for nothing
@@ -285,7 +376,8 @@ hipError_t launch(const void* A, const void* Wq, const void* Ws, const void* Wz,
   if ((GATE_UP ? T : S) * K * 2 >= (int64_t)1 << 32) return hipErrorNotSupported;
   const int n_tiles = (N + kBN - 1) / kBN;
   const int64_t m_slots = (S + kBM - 1) / kBM + E;
-  const int64_t grid = (n_tiles * m_slots + kXcds - 1) / kXcds * kXcds;
+  // tile_of rounds each of its three rounds up to the XCDs
+  const int64_t grid = (n_tiles * m_slots + 3 * (kXcds - 1) + kXcds - 1) / kXcds * kXcds;
   if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
   auto kern = G == 32 ? (Wz ? int4_gemm_kernel<GATE_UP, 1, true> : int4_gemm_kernel<GATE_UP, 1, false>)
                       : (Wz ? int4_gemm_kernel<GATE_UP, 2, true> : int4_gemm_kernel<GATE_UP, 2, false>);

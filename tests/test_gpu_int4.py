@@ -227,6 +227,30 @@ def test_few_slots_ties():
     assert len(set(ids[1].tolist())) == k and 0 <= ids[1].min() and ids[1].max() < E and torch.isnan(y[1]).all()
 
 
+def test_few_slots_of_a_rank_with_every_expert():
+    _need_gpu()
+    T, E, H, I, k, G = 3, 64, 128, 96, 4, 32
+    args, z = _gpu_args(_block(T, E, H, I, k, G, True, seed=29))
+    y = binding.moe_forward_int4(*args, k=k, **z)
+    part = binding.moe_forward_ep_int4(*args, 0, k=k, Wgu_z_local=z["Wgu_z"], Wd_z_local=z["Wd_z"])
+    assert torch.equal(part.to(torch.bfloat16), y)
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_infinity_in_a_row_of_h_gives_nan_there(T):
+    _need_gpu()
+    E, H, I, k, G = 16, 64, 128, 1, 64
+    args, z = _gpu_args(_block(T, E, H, I, k, G, True, seed=31))
+    h = dev(d.normal_bf16((T, I), 1.0, 33, 1, T, I))
+    h[T // 2, 3] = float("inf")
+    cnt = torch.zeros(E, dtype=torch.int32, device="cuda")
+    cnt[5] = T
+    off = torch.cat([cnt.new_zeros(1), cnt.cumsum(0).to(torch.int32)])
+    o = binding.moe_down_int4(h, args[6], args[7], args[8], cnt, off, T, k, Wd_z=z["Wd_z"])
+    bad = torch.arange(T, device="cuda") == T // 2
+    assert torch.isnan(o[bad]).all() and torch.isfinite(o[~bad]).all()
+
+
 def test_few_slots_graph_replays():
     """Two captured calls that share a workspace, replayed in turn with eager calls between."""
     _need_gpu()
