@@ -145,6 +145,30 @@ def test_gate_up(T, E, k, K, N, live, G, zeros, path):
                        + 2.0 ** -134, f"expert {e}")
 
 
+@pytest.mark.parametrize("G,zeros", [(32, True), (64, False), (128, True)])
+@pytest.mark.parametrize("counts", [
+    (0, 1, 63, 64, 65, 127, 128, 129, 1100), (1,) * 256, (0,) * 255 + (300,), (16, 17, 31, 33, 80, 81, 96, 97, 112, 113),
+    (1300, 1290, 0, 5)])
+def test_gemm_takes_every_tile(counts, G, zeros):
+    """Long and short last M tiles, whole and cut N tiles, in every mix; each row of every expert is written once."""
+    _need_gpu()
+    E, T, K, N = len(counts), sum(counts), 96, 1160 if len(counts) < 16 else 584
+    m = _matrix(E, K, N, G, zeros, 35)
+    q, s, z = _gpu(m)
+    ids = np.random.default_rng(36).permutation(np.repeat(np.arange(E, dtype=np.int32), counts)).reshape(T, 1)
+    cnt, off, rows, pos = binding.moe_permute(torch.from_numpy(ids).cuda(), E)
+    h = d.normal_bf16((T, K), 3.0, 37, 1, T, K)
+    bd = d.normal_bf16((E, N), 0.5, 38, 1, E, N)
+    o = torch.full((T, N), float("nan"), device="cuda")
+    binding.moe_down_int4(dev(h), q, s, dev(bd), cnt, off, T, 1, Wd_z=z, o=o, path="gemm")
+    got, off = host_f64(o), off.cpu().numpy()
+    for e in range(E):
+        if counts[e]:
+            want, tol = _bound(orc.widen(h[off[e]:off[e + 1]]), m, e, G)
+            b = orc.widen(bd[e])
+            _assert_within(got[off[e]:off[e + 1]], want + b, tol + U * np.abs(want + b), f"expert {e}")
+
+
 def _block(T, E, H, I, k, G, zeros, seed=0, router_bias="normal"):
     cfg = d.small_config(T=T, E=E, H=H, I=I, k=k, x_scale=d.scale_for_hidden(H), router_bias=router_bias)
     x = d.make_activations(cfg, seed)
