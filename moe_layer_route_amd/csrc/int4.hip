@@ -216,33 +216,6 @@ __device__ __forceinline__ void pick_experts(const double* __restrict__ logits, 
   }
 }
 
-// Logits of few tokens: one workgroup per (expert, token), exact products,
-// float64 sums, as the exact router's.
-constexpr int kLogitThreads = 256;
-__global__ __launch_bounds__(kLogitThreads) void slot_logits_kernel(const bf16_t* __restrict__ x,
-                                                                    const bf16_t* __restrict__ Wr,
-                                                                    const bf16_t* __restrict__ br, int H, int E,
-                                                                    double* __restrict__ logits) {
-  __shared__ double part[kLogitThreads / kWave];
-  const int e = blockIdx.x, t = blockIdx.y;
-  const u32x4_t* xr = reinterpret_cast<const u32x4_t*>(x + (size_t)t * H);
-  const u32x4_t* wr = reinterpret_cast<const u32x4_t*>(Wr + (size_t)e * H);
-  double a0 = 0.0, a1 = 0.0;
-  for (int i = threadIdx.x; i < H / 8; i += kLogitThreads) {
-    const u32x4_t a = xr[i], b = wr[i];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      a0 = __builtin_fma((double)bf16lo(a[q]), (double)bf16lo(b[q]), a0);
-      a1 = __builtin_fma((double)bf16hi(a[q]), (double)bf16hi(b[q]), a1);
-    }
-  }
-  const double sum = wave_add(a0 + a1);
-  if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0)
-    logits[(size_t)t * E + e] = ((part[0] + part[1]) + (part[2] + part[3])) + (double)bf16_to_f32(br[e]);
-}
-
 template <bool GATE_UP, int MG, int GS, bool ZERO, int WAVES, int NS, Mode MODE>
 __global__ __launch_bounds__(WAVES * kWave, WAVES == 8 || MG > 1 || NS > GS ? 2 : 3) void int4_stream_kernel(
     const bf16_t* __restrict__ A, const uint8_t* __restrict__ Wq, const uint16_t* __restrict__ Ws,
@@ -573,9 +546,7 @@ hipError_t launch_int4_slots(const void* x, const void* Wr, const void* br, cons
                              const void* Wgu_z, const void* bgu, const void* Wd_q, const void* Wd_s, const void* Wd_z,
                              const void* bd, int64_t T, int H, int E, int k, int I, int G, double* logits, int32_t* ids,
                              float* w, int32_t* pos, void* h, float* o, hipStream_t stream) {
-  hipLaunchKernelGGL(slot_logits_kernel, dim3((unsigned)E, (unsigned)T), dim3(kLogitThreads), 0, stream,
-                     (const bf16_t*)x, (const bf16_t*)Wr, (const bf16_t*)br, H, E, logits);
-  hipError_t e = hipGetLastError();
+  hipError_t e = launch_few_logits(x, Wr, br, T, H, E, logits, stream);
   if (e != hipSuccess) return e;
   const Slots slots{logits, ids, w, pos, k};
   e = launch_slots<true>(x, Wgu_q, Wgu_s, Wgu_z, bgu, T, H, 2 * I, E, G, h, slots, stream);

@@ -95,6 +95,16 @@ hipError_t launch_int4_gate_up(const void* x, const void* Wq, const void* Ws, co
 hipError_t launch_int4_down(const void* h, const void* Wq, const void* Ws, const void* Wz, const void* bd,
                             const int32_t* cnt, const int32_t* off, int64_t T, int H, int E, int k, int I, int G, float* o,
                             hipStream_t stream);
+// Router and permutation of few tokens (takes_few: at most 64) in two launches,
+// with the exact router's decision; slots of tokens from n_valid on (NULL: none)
+// and of experts outside [e_begin, e_begin + n_local) are left out.  logits:
+// scratch of T E doubles, which the o of the same call can hold.
+bool takes_few(int64_t T, int H, int E, int k);
+hipError_t launch_few_logits(const void* x, const void* Wr, const void* br, int64_t T, int H, int E, double* logits,
+                             hipStream_t stream);
+hipError_t launch_few_route(const void* x, const void* Wr, const void* br, int64_t T, int H, int E, int k,
+                            const int32_t* n_valid, int e_begin, int n_local, double* logits, int32_t* ids, float* w,
+                            int32_t* cnt, int32_t* off, int32_t* rows, int32_t* pos, hipStream_t stream);
 // Router, gate_up and down for few tokens, one workgroup column per token slot
 // (h, o in slot order; ids, w and the identity pos written for the combine):
 // the streaming kernels' results without a router and a permutation launch.

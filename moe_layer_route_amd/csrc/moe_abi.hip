@@ -720,6 +720,21 @@ static int run_down_int4(const char* fn, const void* h, const void* Wq, const vo
   return hip_status(fn, moe::launch_int4_down(h, Wq, Ws, Wz, bd, cnt, off, T, H, E, k, I, G, o, s));
 }
 
+// Router, padding and permutation of the int4 blocks and of the FP8 block behind
+// the norm; o is scratch until down writes it.
+static int route_and_permute(const char* fn, const void* x, const void* Wr, const void* br, int64_t T, int32_t H,
+                             int32_t E, int32_t k, const int32_t* n_valid, int32_t e_begin, int32_t n_local, float* o,
+                             int32_t* ids, float* w, int32_t* cnt, int32_t* off, int32_t* rows, int32_t* pos,
+                             hipStream_t s) {
+  if (moe::takes_few(T, H, E, k))
+    return hip_status(fn, moe::launch_few_route(x, Wr, br, T, H, E, k, n_valid, e_begin, n_local,
+                                                reinterpret_cast<double*>(o), ids, w, cnt, off, rows, pos, s));
+  if (int st = hip_status(fn, moe::launch_route(x, Wr, br, T, H, E, k, ids, w, route_method(T), s))) return st;
+  if (n_valid)
+    if (int st = hip_status(fn, moe::launch_mask_padding(ids, w, T, k, n_valid, s))) return st;
+  return hip_status(fn, moe::launch_permute(ids, T, n_local, k, cnt, off, rows, pos, s, e_begin));
+}
+
 // The int4 forward; n_valid (device, optional) marks the rows from *n_valid on
 // as padding, expert_counts_out (optional) receives the per-expert loads.
 static int forward_int4(const char* fn, const void* x, const void* Wr, const void* br, const void* Wgu_q,
@@ -785,17 +800,15 @@ static int forward_int4(const char* fn, const void* x, const void* Wr, const voi
   // T=16 140 against 137), and uneven choices repeat more of them: a quarter.
   // The logits sit where o will be (down writes it when they have been read).
   if (path == MOE_PATH_GEMV && T * k * 4 <= E && !n_valid && !expert_counts_out && n_local == E &&
-      (size_t)T * E * sizeof(double) <= (size_t)T * k * H * 4) {
+      moe::takes_few(T, H, E, k)) {
     if (int st = hip_status(fn, moe::launch_int4_slots(x, Wr, br, Wgu_q, Wgu_s, Wgu_z, bgu, Wd_q, Wd_s, Wd_z, bd, T, H,
                                                        E, k, I, G, reinterpret_cast<double*>(o), ids, w, pos, h, o, s)))
       return st;
     if (int st = hip_status(fn, moe::launch_combine(o, pos, w, T, H, k, y, s, partial))) return st;
     return ok();
   }
-  if (int st = hip_status(fn, moe::launch_route(x, Wr, br, T, H, E, k, ids, w, route_method(T), s))) return st;
-  if (n_valid)
-    if (int st = hip_status(fn, moe::launch_mask_padding(ids, w, T, k, n_valid, s))) return st;
-  if (int st = hip_status(fn, moe::launch_permute(ids, T, n_local, k, cnt, off, rows, pos, s, e_begin))) return st;
+  if (int st = route_and_permute(fn, x, Wr, br, T, H, E, k, n_valid, e_begin, n_local, o, ids, w, cnt, off, rows, pos, s))
+    return st;
   if (int st = run_gate_up_int4(fn, x, Wgu_q, Wgu_s, Wgu_z, bgu, cnt, off, rows, T, H, n_local, k, I, G, h, path, s))
     return st;
   if (int st = run_down_int4(fn, h, Wd_q, Wd_s, Wd_z, bd, cnt, off, T, H, n_local, k, I, G, o, path, s)) return st;
@@ -1044,21 +1057,21 @@ static int forward_fp8(const char* fn, const void* x, const void* Wr, const void
   path = choose_path(path, T, E, k);
   const int64_t S = T * k;
 
-  int method = MOE_ROUTE_AUTO;
   if (norm) {
-    method = route_method(T);
     void* xn = ws + F.total;
     if (int st = hip_status(fn, moe::launch_add_rmsnorm(x, norm->residual, norm->gamma, T, H, norm->eps,
                                                         norm->residual_out, xn, xq, sx, s)))
       return st;
-    x = xn;
-  }
-  if (int st = hip_status(fn, moe::launch_route(x, Wr, br, T, H, E, k, ids, w, method, s))) return st;
-  if (n_valid)
-    if (int st = hip_status(fn, moe::launch_mask_padding(ids, w, T, k, n_valid, s))) return st;
-  if (int st = hip_status(fn, moe::launch_permute(ids, T, n_local, k, cnt, off, rows, pos, s, e_begin))) return st;
-  if (!norm)
+    if (int st = route_and_permute(fn, xn, Wr, br, T, H, E, k, n_valid, e_begin, n_local, o, ids, w, cnt, off, rows,
+                                   pos, s))
+      return st;
+  } else {
+    if (int st = hip_status(fn, moe::launch_route(x, Wr, br, T, H, E, k, ids, w, MOE_ROUTE_AUTO, s))) return st;
+    if (n_valid)
+      if (int st = hip_status(fn, moe::launch_mask_padding(ids, w, T, k, n_valid, s))) return st;
+    if (int st = hip_status(fn, moe::launch_permute(ids, T, n_local, k, cnt, off, rows, pos, s, e_begin))) return st;
     if (int st = hip_status(fn, moe::launch_fp8_quantize_rows(x, T, H, xq, sx, s))) return st;
+  }
   if (int st = run_gate_up_fp8(fn, xq, sx, Wgu_q, Wgu_s, bgu, cnt, off, rows, T, H, n_local, k, I, h, path, s)) return st;
   // only the rows of h the permutation filled (off[n_local] of them; fewer
   // than T*k with padding rows or on an expert-parallel rank)

@@ -44,12 +44,16 @@ __device__ __forceinline__ uint64_t max_moved(uint64_t v) {
   const uint64_t o = (uint64_t)moved<CTRL>((uint32_t)(v >> 32)) << 32 | moved<CTRL>((uint32_t)v);
   return o > v ? o : v;
 }
+// the maximum over a row of 16 lanes, in each of them
+__device__ __forceinline__ uint64_t row_max(uint64_t v) {
+  return max_moved<kMirror>(max_moved<kHalfMirror>(max_moved<kXor2>(max_moved<kXor1>(v))));
+}
 __device__ __forceinline__ uint64_t lane_u64(uint64_t v, int lane) {
   return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane) << 32 |
          (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
 }
 __device__ __forceinline__ uint64_t wave_max(uint64_t v) {
-  v = max_moved<kMirror>(max_moved<kHalfMirror>(max_moved<kXor2>(max_moved<kXor1>(v))));
+  v = row_max(v);
   const uint64_t a = lane_u64(v, 0), b = lane_u64(v, 16), c = lane_u64(v, 32), d = lane_u64(v, 48);
   const uint64_t ab = a > b ? a : b, cd = c > d ? c : d;
   return ab > cd ? ab : cd;

@@ -406,6 +406,36 @@ def test_padded(n, path):
         assert (counts == 0).all()
 
 
+# Up to 64 tokens the router and the permutation take two launches of their own.
+@pytest.mark.parametrize("T,E,k,n,ranks", [
+    (2, 4, 1, 1, 2), (3, 5, 4, 3, 1), (4, 8, 8, 2, 3), (5, 64, 8, 0, 4), (7, 65, 3, 7, 2), (33, 32, 4, 20, 4),
+    (63, 128, 5, 62, 5), (64, 256, 8, 64, 3), (64, 3, 2, 50, 3), (65, 16, 4, 64, 2)])
+def test_few_tokens_route_and_permute(T, E, k, n, ranks):
+    """Ids, weights, loads and rows of padded batches and of expert-parallel ranks, against the router's own call."""
+    _need_gpu()
+    H, I, G = 256, 64, 64
+    b = _block(T, E, H, I, k, G, False, seed=T * E)
+    args, z = _gpu_args(b)
+    want_ids, want_w = binding.moe_route(*args[:3], k, method="exact")
+    ids, w = torch.full_like(want_ids, -7), torch.full_like(want_w, -7.0)
+    counts = torch.full((E,), -1, dtype=torch.int32, device="cuda")
+    valid = torch.tensor([n], dtype=torch.int32, device="cuda")
+    y = binding.moe_forward_padded_int4(*args, k=k, n_valid=valid, expert_counts=counts, topk_ids=ids, topk_w=w, **z)
+    assert torch.equal(ids[:n], want_ids[:n]) and (ids[n:] == -1).all()
+    torch.testing.assert_close(w[:n], want_w[:n], rtol=2 ** -23, atol=0)
+    assert (w[n:] == 0).all() and (y[n:] == 0).all()
+    assert counts.tolist() == np.bincount(want_ids[:n].cpu().numpy().ravel(), minlength=E).tolist()
+    ref = orc.moe_forward_int4(*b, k=k, G=G)
+    if n:
+        assert_y_close(host_f64(y)[:n], ref["y"][:n])
+    cuts = np.linspace(0, E, ranks + 1).astype(int)
+    parts = []
+    for lo, hi in zip(cuts[:-1], cuts[1:]):
+        c = slice(int(lo), int(hi))
+        parts.append(binding.moe_forward_ep_int4(*args[:3], *[a[c].contiguous() for a in args[3:]], int(lo), k=k))
+    assert_y_close(sum(p.double() for p in parts).to(torch.bfloat16).double().cpu().numpy(), ref["y"])
+
+
 @pytest.mark.parametrize("path", PATHS)
 def test_expert_parallel_ranks_sum_to_the_whole(path):
     _need_gpu()
