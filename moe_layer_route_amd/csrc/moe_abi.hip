@@ -794,10 +794,10 @@ static int forward_int4(const char* fn, const void* x, const void* Wr, const voi
   path = choose_path(path, T, E, k);
 
   // Few slots, one by one: no permutation, and the router without its own last
-  // launch.  At H=I=2880, k=4, G=64 and evenly chosen experts: E=32 T=1 21.6 us
-  // against 31.5 in groups, E=128 T=1 22.2 against 44.9, T=8 78 against 94.  At
-  // half as many slots as experts the weights read twice have used that up (E=128
-  // T=16 140 against 137), and uneven choices repeat more of them: a quarter.
+  // launch.  At H=I=2880, k=4, G=64 and evenly chosen experts: E=32 T=1 21.8 us
+  // against 26.7 in groups, T=2 29.8 against 34.2; E=128 T=1 22.2 against 29.9, T=4
+  // 46.7 against 53.1, T=8 78.2 against 78.9.  At half as many slots as experts the
+  // weights read twice cost more than that (E=128 T=16 138 against 123).
   // The logits sit where o will be (down writes it when they have been read).
   if (path == MOE_PATH_GEMV && T * k * 4 <= E && !n_valid && !expert_counts_out && n_local == E &&
       moe::takes_few(T, H, E, k)) {
