@@ -595,7 +595,10 @@ MOE_API int moe_pack_int4(const void* codes_kn, int32_t E, int32_t K, int32_t N,
 /* moe_forward_int4, moe_forward_int4_ex -- moe_forward with these weights
  * (Wgu_z, Wd_z: zero points or NULL, each on its own); every other argument,
  * the workspace (moe_workspace_bytes) and the result's definition as in
- * moe_forward_mxfp4(_ex). */
+ * moe_forward_mxfp4(_ex).  MOE_PATH_AUTO picks a path for each product from
+ * the mean rows per expert r = T*k/E and its columns N (2I or H): streaming up
+ * to r = 32, the grouped GEMM above 128, in between the GEMM where T*k*N is at
+ * least 2^21 (3 * 2^20 with G = 32). */
 MOE_API int moe_forward_int4(const void* x, const void* Wr, const void* br,
                              const void* Wgu_q, const void* Wgu_s, const void* Wgu_z, const void* bgu,
                              const void* Wd_q, const void* Wd_s, const void* Wd_z, const void* bd,

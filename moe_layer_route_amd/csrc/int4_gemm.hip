@@ -7,11 +7,12 @@
 //
 // A workgroup owns 128 rows x 512 columns of one expert: eight waves, two per
 // SIMD, each with a strip of 64 columns (128 accumulators a lane) and all 128
-// rows.  K goes in units of GU tiles that never cross a group of the scales
+// rows; or, where there are few tiles, half of each with four waves, two
+// workgroups on a CU.  K goes in units of GU tiles that never cross a group of the scales
 // (64 values, or 32 where the groups are of 32).  A unit's token rows come into
 // LDS by direct loads, fragment by fragment (a fragment is the 16-row operand
-// of one MFMA, a kilobyte), two units ahead in a ring of four, and so do the
-// wave's own tiles of weights, their scales and zero points.  (Weights loaded
+// of one MFMA, a kilobyte), two or three units ahead in a ring of four, and so
+// do the wave's own tiles of weights, their scales and zero points.  (Weights loaded
 // into registers: 873 against 774 us at the first size below.  The compiler
 // counts only the loads it makes itself, so its waits for them take in the
 // direct loads under way.)  Per 16-row chunk the unit's products go into a
@@ -33,22 +34,18 @@
 namespace moe {
 namespace {
 
-constexpr int kGemmWaves = 8;
-constexpr int kBM = 128, kChunks = kBM / 16;
-static_assert(kChunks == kGemmWaves && kChunks == 8, "a wave brings in one chunk; run() below counts them");
-constexpr int kBN = kGemmWaves * kTileN;
 constexpr int kRing = 4;
 constexpr int kXcds = 8;
 constexpr int kMBlock = 8;   // M tiles that take an N tile together
 constexpr uint32_t kOutOfRange = 0xFFFFFFF0u;
 
-template <int GU>
+template <int GU, int W>
 struct Ring {
-  u32x4_t rows[kRing][GU][kChunks][kWave];      // fragments of the token rows, in lane order
-  u32x4_t w[kGemmWaves][kRing][GU][kWave];      // each wave's tiles
-  uint32_t s[kGemmWaves][kRing][kWave];         // scales of its 64 columns, twice
-  uint32_t z[kGemmWaves][kRing][kWave];         // zero points, four times
-  float sum[4][kChunks][16];                    // of each row's values over a unit, times `flat`
+  u32x4_t rows[kRing][GU][W][kWave];   // fragments of the token rows, in lane order
+  u32x4_t w[W][kRing][GU][kWave];      // each wave's tiles
+  uint32_t s[W][kRing][kWave];         // scales of its 64 columns, twice
+  uint32_t z[W][kRing][kWave];         // zero points, four times
+  float sum[4][W][16];                          // of each row's values over a unit, times `flat`
 };
 
 // Which tile a workgroup takes.  An expert has ceil(M / kBM) M tiles x n_tiles N
@@ -63,6 +60,7 @@ struct Ring {
 // consecutive parts, whose L2 serves the tiles that share rows or weights.
 // Every lane gets the same; false for a block past the last tile (the grid is an
 // upper bound).  Lane l counts experts 4 l .. 4 l + 3: E <= 256.
+template <int kBM>
 __device__ __forceinline__ bool tile_of(const int32_t* __restrict__ cnt, int E, int n_tiles, int wide, int lane, int& e,
                                         int& m0, int& nt) {
   int longer[4], shorter[4];
@@ -117,24 +115,31 @@ __device__ __forceinline__ bool tile_of(const int32_t* __restrict__ cnt, int E, 
   return false;
 }
 
-template <bool GATE_UP, int GU, bool ZERO>
-__global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
+template <bool GATE_UP, int GU, bool ZERO, int W>
+__global__ __launch_bounds__(W * kWave, 2) void int4_gemm_kernel(
     const bf16_t* __restrict__ A, const uint8_t* __restrict__ Wq, const uint16_t* __restrict__ Ws,
     const uint8_t* __restrict__ Wz, const bf16_t* __restrict__ bias, const int32_t* __restrict__ cnt,
     const int32_t* __restrict__ off, const int32_t* __restrict__ rows, int K, int N, int E, int kslots, int64_t a_rows,
     int n_tiles, int units_per_group, void* __restrict__ out) {
-  __shared__ __align__(16) Ring<GU> ring;
+  static_assert(W == 4 || W == 8, "a wave brings in one chunk; run() below counts them");
+  constexpr int kChunks = W, kBM = 16 * kChunks;
+  // Two workgroups of four waves on a CU run out of step by themselves; of eight
+  // waves the second half is shifted (below) where the registers allow it, which
+  // costs a unit of the ring.
+  constexpr bool kShift = W == 8 && !(ZERO && GU == 2);
+  constexpr int kAhead = kShift ? 2 : 3;
+  __shared__ __align__(16) Ring<GU, W> ring;
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   int e, m0, nt;
-  if (!tile_of(cnt, E, n_tiles, (N + kTileN - 1) / kTileN / kGemmWaves, lane, e, m0, nt)) return;   // block-uniform
+  if (!tile_of<kBM>(cnt, E, n_tiles, (N + kTileN - 1) / kTileN / W, lane, e, m0, nt)) return;   // block-uniform
   const int M = cnt[e], row0 = off[e];
   const int nch = min(kChunks, (M - m0 + 15) / 16);   // chunks with rows
   const int g = lane >> 4, c = lane & 15;
   const int nkt = K / kTileK, nu = (nkt + GU - 1) / GU;
   const int ng = (nu + units_per_group - 1) / units_per_group;
   const int strips = (N + kTileN - 1) / kTileN;
-  const int strip = nt * kGemmWaves + wave;
+  const int strip = nt * W + wave;
   const bool live = strip < strips;   // wave-uniform; a wave past the last strip only loads rows
   const int ncol = strip * kTileN + 4 * c;
   const int wstrip = min(strip, strips - 1);
@@ -242,9 +247,9 @@ __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
   };
   const Int4Masks masks;
   // What a wave prepares of the next unit: loads retire in order, so with those
-  // of one unit still under way its own part of unit u is in LDS.
+  // of the units behind it still under way its own part of unit u is in LDS.
   auto next = [&](int u) __attribute__((always_inline)) {
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kAhead - 1) * kLoads) : "memory");
     sum_rows(u);
   };
   auto compute = [&](auto count, auto shift, int u, const Words& b) __attribute__((always_inline)) {
@@ -273,13 +278,13 @@ __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
 #pragma unroll
     for (int m = 0; m < kCount; ++m) {
       __builtin_amdgcn_sched_barrier(0);
-      // The loads of the unit two ahead (three for the second half of a late
-      // wave's unit, which is past the barrier), into the slot that every wave
-      // has left; spread over the chunks: a load that the CU's load path cannot
-      // take yet holds up its wave's products.
+      // The loads of the unit kAhead ahead (one more for the second half of a
+      // late wave's unit, which is past the barrier), into the slot that every
+      // wave has left; spread over the chunks: a load that the CU's load path
+      // cannot take yet holds up its wave's products.
 #pragma unroll
       for (int i = 0; i < kLoads; ++i)
-        if (kLate ? kHalf + i * kHalf / kLoads == m : i * (kCount - 1) / kLoads == m) load(kLate ? u + 3 : u + 2, i);
+        if (kLate ? kHalf + i * kHalf / kLoads == m : i * (kCount - 1) / kLoads == m) load(kLate ? u + kAhead + 1 : u + kAhead, i);
       if (m + 2 < kCount) {
         chunk_in(u, m + 2, a[(m + 2) % 3]);
         sum[(m + 2) % 3] = sum_in(u, m + 2);
@@ -296,22 +301,21 @@ __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
 
   // Every SIMD has one wave of each half of the workgroup.  The second half runs
   // half a unit behind: its barriers stand in the middle of a unit, so that one
-  // wave unpacks its weights, and waits, while the other has products to issue.
-  // (T = 4096, G = 64: 595 us in step, 570 like this.  With
-  // zero points and units of two tiles it takes 14 registers too many.)
-  const bool late = !(ZERO && GU == 2) && live && wave >= kGemmWaves / 2;
-  load_all(0);
-  load_all(1);
+  // wave unpacks its weights, and waits, while the other has products to issue
+  // (T = 4096, G = 64: 595 us in step, 570 like this; with zero points and units
+  // of two tiles it takes 14 registers too many).
+  const bool late = kShift && live && wave >= W / 2;
+  for (int u = 0; u < kAhead; ++u) load_all(u);
   Words b;
   next(0);
   words(0, b);
-  if (late) load_all(2);
+  if (late) load_all(kAhead);
   __syncthreads();
   // The wave's own weights it may read at once, the other waves' rows and sums
   // behind the barrier.  Barrier u stands behind the first waves' unit u and
-  // amid the late ones' (which have read unit u - 1 by then): between barriers
-  // u - 1 and u the slots of u - 1, u and u + 1 are in use, and the loads of u + 2
-  // go to the fourth.
+  // amid the late ones' (which have read unit u - 1 by then): with late waves the
+  // slots of u - 1, u and u + 1 are in use between barriers u - 1 and u, and the
+  // loads of u + 2 go to the fourth; without, u, u + 1 and u + 2, and u + 3.
   auto run = [&](auto count) __attribute__((always_inline)) {
     if (late) {
       for (int u = 0; u < nu; ++u) {
@@ -323,7 +327,7 @@ __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
         if (live) {
           compute(count, std::false_type{}, u, b);
         } else {
-          load_all(u + 2);
+          load_all(u + kAhead);
           next(u + 1);
         }
         words(u + 1, b);
@@ -332,10 +336,10 @@ __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
     }
   };
   // an even count of chunks: at most one is computed for nothing
-  if (nch > 6)
-    run(std::integral_constant<int, 8>{});
-  else if (nch > 4)
-    run(std::integral_constant<int, 6>{});
+  if (W == 8 && nch > 6)
+    run(std::integral_constant<int, W>{});
+  else if (W == 8 && nch > 4)
+    run(std::integral_constant<int, W == 8 ? 6 : 4>{});
   else if (nch > 2)
     run(std::integral_constant<int, 4>{});
   else
@@ -367,6 +371,30 @@ __global__ __launch_bounds__(kGemmWaves * kWave, 2) void int4_gemm_kernel(
     }
 }
 
+template <bool GATE_UP, int W>
+hipError_t launch_tiles(const void* A, const void* Wq, const void* Ws, const void* Wz, const void* bias,
+                        const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T, int K, int N, int E, int k,
+                        int G, void* out, hipStream_t stream) {
+  const int n_tiles = (N + W * kTileN - 1) / (W * kTileN);
+  const int64_t m_slots = (T * k + 16 * W - 1) / (16 * W) + E;
+  // tile_of rounds each of its three rounds up to the XCDs
+  const int64_t grid = (n_tiles * m_slots + 3 * (kXcds - 1) + kXcds - 1) / kXcds * kXcds;
+  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  auto kern = G == 32 ? (Wz ? int4_gemm_kernel<GATE_UP, 1, true, W> : int4_gemm_kernel<GATE_UP, 1, false, W>)
+                      : (Wz ? int4_gemm_kernel<GATE_UP, 2, true, W> : int4_gemm_kernel<GATE_UP, 2, false, W>);
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(W * kWave), 0, stream, (const bf16_t*)A, (const uint8_t*)Wq,
+                     (const uint16_t*)Ws, (const uint8_t*)Wz, (const bf16_t*)bias, cnt, off, rows, K, N, E, k, T, n_tiles,
+                     G == 128 ? 2 : 1, out);
+  return hipGetLastError();
+}
+
+// Two workgroups of small tiles fit a CU.  Where all of them run at once they
+// are done sooner than fewer CUs with large ones, which unpack each weight for
+// half as many rows (K = 2048, N = 4096, G = 64, 104 rows an expert: 8 experts
+// 33 against 56 us, 16 42 against 57, 32, more than fit at once, 88 against 79).
+// Eight rows more than the mean are counted: an expert past 64 has one tile more.
+constexpr int64_t kSmallTiles = 512;
+
 template <bool GATE_UP>
 hipError_t launch(const void* A, const void* Wq, const void* Ws, const void* Wz, const void* bias, const int32_t* cnt,
                   const int32_t* off, const int32_t* rows, int64_t T, int K, int N, int E, int k, int G, void* out,
@@ -374,17 +402,9 @@ hipError_t launch(const void* A, const void* Wq, const void* Ws, const void* Wz,
   const int64_t S = T * k;
   // 32-bit offsets into the token rows (of one expert, for down)
   if ((GATE_UP ? T : S) * K * 2 >= (int64_t)1 << 32) return hipErrorNotSupported;
-  const int n_tiles = (N + kBN - 1) / kBN;
-  const int64_t m_slots = (S + kBM - 1) / kBM + E;
-  // tile_of rounds each of its three rounds up to the XCDs
-  const int64_t grid = (n_tiles * m_slots + 3 * (kXcds - 1) + kXcds - 1) / kXcds * kXcds;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-  auto kern = G == 32 ? (Wz ? int4_gemm_kernel<GATE_UP, 1, true> : int4_gemm_kernel<GATE_UP, 1, false>)
-                      : (Wz ? int4_gemm_kernel<GATE_UP, 2, true> : int4_gemm_kernel<GATE_UP, 2, false>);
-  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(kGemmWaves * kWave), 0, stream, (const bf16_t*)A,
-                     (const uint8_t*)Wq, (const uint16_t*)Ws, (const uint8_t*)Wz, (const bf16_t*)bias, cnt, off, rows, K,
-                     N, E, k, T, n_tiles, G == 128 ? 2 : 1, out);
-  return hipGetLastError();
+  const int64_t small = (N + 4 * kTileN - 1) / (4 * kTileN) * ((S + 72 * (int64_t)E - 1) / (64 * (int64_t)E)) * E;
+  auto run = small <= kSmallTiles ? launch_tiles<GATE_UP, 4> : launch_tiles<GATE_UP, 8>;
+  return run(A, Wq, Ws, Wz, bias, cnt, off, rows, T, K, N, E, k, G, out, stream);
 }
 
 }  // namespace

@@ -701,11 +701,25 @@ int moe_pack_int4(const void* codes_kn, int32_t E, int32_t K, int32_t N, void* c
   return ok();
 }
 
+// The path of one int4 product, `rows` token slots (of the whole layer: E
+// experts) x N columns of which n_local E-ths are here.  Up to 32 rows an expert
+// streaming reads the weights once.  Above, its time grows with rows x columns,
+// while a GEMM of few tiles takes what one tile takes; at G = 32 a tile has twice
+// as many units.  (8 experts, K = N / 2 = 2048, G = 64, 56, 72 and 104 rows an
+// expert: 24, 34 and 46 us streaming against 33, 33 and 33; 32 experts, K = N =
+// 2880, 40 rows: 76 against 53; 8 experts, K = N = 1024, 104 rows: 17.5 against
+// 17.8, 144: 21.7 against 18.1.)
+static int int4_path(int32_t path, int64_t rows, int64_t E, int64_t n_local, int64_t N, int32_t G) {
+  if (path != MOE_PATH_AUTO) return path;
+  if (rows <= 32 * E) return MOE_PATH_GEMV;
+  if (rows > 128 * E) return MOE_PATH_GEMM;
+  return rows * n_local / E * N >= (int64_t)(G == 32 ? 3 : 2) << 20 ? MOE_PATH_GEMM : MOE_PATH_GEMV;
+}
+
 static int run_gate_up_int4(const char* fn, const void* x, const void* Wq, const void* Ws, const void* Wz,
                             const void* bgu, const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T,
                             int32_t H, int32_t E, int32_t k, int32_t I, int32_t G, void* h, int32_t path,
                             hipStream_t s) {
-  path = choose_path(path, T, E, k);
   if (path == MOE_PATH_GEMM)
     return hip_status(fn, moe::launch_gemm_int4_gate_up(x, Wq, Ws, Wz, bgu, cnt, off, rows, T, H, E, k, I, G, h, s));
   return hip_status(fn, moe::launch_int4_gate_up(x, Wq, Ws, Wz, bgu, cnt, off, rows, T, H, E, k, I, G, h, s));
@@ -714,7 +728,6 @@ static int run_gate_up_int4(const char* fn, const void* x, const void* Wq, const
 static int run_down_int4(const char* fn, const void* h, const void* Wq, const void* Ws, const void* Wz, const void* bd,
                          const int32_t* cnt, const int32_t* off, int64_t T, int32_t H, int32_t E, int32_t k, int32_t I,
                          int32_t G, float* o, int32_t path, hipStream_t s) {
-  path = choose_path(path, T, E, k);
   if (path == MOE_PATH_GEMM)
     return hip_status(fn, moe::launch_gemm_int4_down(h, Wq, Ws, Wz, bd, cnt, off, T, H, E, k, I, G, o, s));
   return hip_status(fn, moe::launch_int4_down(h, Wq, Ws, Wz, bd, cnt, off, T, H, E, k, I, G, o, s));
@@ -790,8 +803,8 @@ static int forward_int4(const char* fn, const void* x, const void* Wr, const voi
   void* h = ws + L.h;
   float* o = reinterpret_cast<float*>(ws + L.o);
   hipStream_t s = (hipStream_t)stream;
-  // the expert path follows the whole layer's load per expert, T*k/E
-  path = choose_path(path, T, E, k);
+  const int path_gu = int4_path(path, T * k, E, n_local, 2 * (int64_t)I, G);
+  const int path_d = int4_path(path, T * k, E, n_local, H, G);
 
   // Few slots, one by one: no permutation, and the router without its own last
   // launch.  At H=I=2880, k=4, G=64 and evenly chosen experts: E=32 T=1 21.8 us
@@ -799,7 +812,7 @@ static int forward_int4(const char* fn, const void* x, const void* Wr, const voi
   // 46.7 against 53.1, T=8 78.2 against 78.9.  At half as many slots as experts the
   // weights read twice cost more than that (E=128 T=16 138 against 123).
   // The logits sit where o will be (down writes it when they have been read).
-  if (path == MOE_PATH_GEMV && T * k * 4 <= E && !n_valid && !expert_counts_out && n_local == E &&
+  if (path_gu == MOE_PATH_GEMV && T * k * 4 <= E && !n_valid && !expert_counts_out && n_local == E &&
       moe::takes_few(T, H, E, k)) {
     if (int st = hip_status(fn, moe::launch_int4_slots(x, Wr, br, Wgu_q, Wgu_s, Wgu_z, bgu, Wd_q, Wd_s, Wd_z, bd, T, H,
                                                        E, k, I, G, reinterpret_cast<double*>(o), ids, w, pos, h, o, s)))
@@ -809,9 +822,10 @@ static int forward_int4(const char* fn, const void* x, const void* Wr, const voi
   }
   if (int st = route_and_permute(fn, x, Wr, br, T, H, E, k, n_valid, e_begin, n_local, o, ids, w, cnt, off, rows, pos, s))
     return st;
-  if (int st = run_gate_up_int4(fn, x, Wgu_q, Wgu_s, Wgu_z, bgu, cnt, off, rows, T, H, n_local, k, I, G, h, path, s))
+  if (int st = run_gate_up_int4(fn, x, Wgu_q, Wgu_s, Wgu_z, bgu, cnt, off, rows, T, H, n_local, k, I, G, h, path_gu,
+                                s))
     return st;
-  if (int st = run_down_int4(fn, h, Wd_q, Wd_s, Wd_z, bd, cnt, off, T, H, n_local, k, I, G, o, path, s)) return st;
+  if (int st = run_down_int4(fn, h, Wd_q, Wd_s, Wd_z, bd, cnt, off, T, H, n_local, k, I, G, o, path_d, s)) return st;
   if (int st = hip_status(fn, moe::launch_combine(o, pos, w, T, H, k, y, s, partial))) return st;
   return ok();
 }
@@ -875,8 +889,8 @@ int moe_gate_up_int4(const void* x, const void* Wgu_q, const void* Wgu_s, const 
     return fail(MOE_ERR_INVALID_ARG, "%s: unknown path %d", fn, path);
   if (int st = check_rows(fn, "x", T, H)) return st;
   if (T == 0) return ok();
-  if (int st = run_gate_up_int4(fn, x, Wgu_q, Wgu_s, Wgu_z, bgu, cnt, off, rows, T, H, E, k, I, G, h, path,
-                                (hipStream_t)stream))
+  if (int st = run_gate_up_int4(fn, x, Wgu_q, Wgu_s, Wgu_z, bgu, cnt, off, rows, T, H, E, k, I, G, h,
+                                int4_path(path, T * k, E, E, 2 * (int64_t)I, G), (hipStream_t)stream))
     return st;
   return ok();
 }
@@ -899,7 +913,8 @@ int moe_down_int4(const void* h, const void* Wd_q, const void* Wd_s, const void*
     return fail(MOE_ERR_INVALID_ARG, "%s: unknown path %d", fn, path);
   if (int st = check_rows(fn, "h", T * k, I)) return st;
   if (T == 0) return ok();
-  if (int st = run_down_int4(fn, h, Wd_q, Wd_s, Wd_z, bd, cnt, off, T, H, E, k, I, G, o, path, (hipStream_t)stream))
+  if (int st = run_down_int4(fn, h, Wd_q, Wd_s, Wd_z, bd, cnt, off, T, H, E, k, I, G, o,
+                             int4_path(path, T * k, E, E, H, G), (hipStream_t)stream))
     return st;
   return ok();
 }

@@ -169,6 +169,59 @@ def test_gemm_takes_every_tile(counts, G, zeros):
             _assert_within(got[off[e]:off[e + 1]], want + b, tol + U * np.abs(want + b), f"expert {e}")
 
 
+# 48 experts x 10 column tiles of 256: more small tiles than the card runs at once, so the large ones (128 x 512) run.
+LARGE = (0, 1, 15, 16, 17, 33, 63, 64, 65, 80, 96, 97, 112, 127, 128, 129, 145, 191, 192, 193, 255, 256, 257, 300) * 2
+
+
+@pytest.mark.parametrize("G", [32, 64, 128])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("K", [32, 160, 288])
+def test_gemm_large_tiles(K, zeros, G):
+    """Both products, every count of 16-row chunks, first and last rounds, one to nine tiles of K."""
+    _need_gpu()
+    E, T, N = len(LARGE), sum(LARGE), 2320
+    m = _matrix(E, K, N, G, zeros, 39)
+    q, s, z = _gpu(m)
+    ids = np.random.default_rng(40).permutation(np.repeat(np.arange(E, dtype=np.int32), LARGE)).reshape(T, 1)
+    cnt, off, rows, pos = binding.moe_permute(torch.from_numpy(ids).cuda(), E)
+    x = d.normal_bf16((T, K), 60.0 / np.sqrt(K) / 0.3, 41, 1, T, K)
+    b = d.normal_bf16((E, N), 0.5, 42, 1, E, N)
+    o = torch.full((T, N), float("nan"), device="cuda")
+    h = torch.full((T, N // 2), float("nan"), dtype=torch.bfloat16, device="cuda")
+    binding.moe_down_int4(dev(x), q, s, dev(b), cnt, off, T, 1, Wd_z=z, o=o, path="gemm")
+    binding.moe_gate_up_int4(dev(x), q, s, dev(b), cnt, off, rows, 1, Wgu_z=z, h=h, path="gemm")
+    o, h, off, rows = host_f64(o), host_f64(h), off.cpu().numpy(), rows.cpu().numpy()
+    for e in range(E):
+        if LARGE[e]:
+            r = slice(off[e], off[e + 1])
+            bias = orc.widen(b[e])
+            want, tol = _bound(orc.widen(x[r]), m, e, G)
+            _assert_within(o[r], want + bias, tol + U * np.abs(want + bias), f"down, expert {e}")
+            u, tol = _bound(orc.widen(x[rows[r]]), m, e, G)
+            u = u + bias
+            tol = tol + U * np.abs(u)
+            want = orc.clamped_glu(u)
+            _assert_within(h[r], want, (8.8 * tol[:, 0::2] + 7 * tol[:, 1::2]) * (1 + 2.0 ** -8)
+                           + np.abs(want) * (2.0 ** -8 + 2.0 ** -20) + 2.0 ** -134, f"gate_up, expert {e}")
+
+
+@pytest.mark.parametrize("T,E,k,N,G,path", [
+    (64, 2, 1, 64, 64, "gemv"), (65, 2, 1, 64, 64, "gemv"), (256, 2, 1, 64, 32, "gemv"), (257, 2, 1, 64, 32, "gemm"),
+    (1023, 8, 1, 2048, 64, "gemv"), (1024, 8, 1, 2048, 64, "gemm"), (1024, 8, 1, 2048, 32, "gemv"),
+    (1536, 12, 1, 2048, 32, "gemm"), (1024, 32, 1, 4096, 64, "gemv"), (1025, 32, 1, 4096, 64, "gemm")])
+def test_auto_takes_the_documented_path(T, E, k, N, G, path):
+    """The paths are told apart by their bits: streaming sums four parts of K, the GEMM goes through K in one sequence
+    (at K = 64, one part, they are equal)."""
+    _need_gpu()
+    K = 1024
+    q, s, z = _gpu(_matrix(E, K, N, G, True, 43))
+    ids = _routing(T, E, k, 44)
+    cnt, off, rows, pos = binding.moe_permute(torch.from_numpy(ids).cuda(), E)
+    h, b = dev(d.normal_bf16((T * k, K), 3.0, 45, 1, T, K)), dev(d.normal_bf16((E, N), 0.5, 46, 1, E, N))
+    got = {p: binding.moe_down_int4(h, q, s, b, cnt, off, T, k, Wd_z=z, path=p) for p in ("auto", "gemv", "gemm")}
+    assert not torch.equal(got["gemv"], got["gemm"]) and torch.equal(got["auto"], got[path])
+
+
 def _block(T, E, H, I, k, G, zeros, seed=0, router_bias="normal"):
     cfg = d.small_config(T=T, E=E, H=H, I=I, k=k, x_scale=d.scale_for_hidden(H), router_bias=router_bias)
     x = d.make_activations(cfg, seed)
