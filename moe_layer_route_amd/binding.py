@@ -164,10 +164,21 @@ def _on(t, stream):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _here(t):
     """Raw handle of the current stream of t's device."""
     index = t.get_device()
     return _raw_stream(index) if _raw_stream else torch.cuda.current_stream(index).cuda_stream
+
+
+def _place(t, stream):
+    """_here, if t's device is the current one and stream is not given; None where the caller has to go through _on."""
+    index = t.get_device()
+    if index < 0:
+        _dev(t)   # raises
+    return _here(t) if stream is None and index == _current_device() else None
 
 
 def _at(t):
@@ -176,16 +187,24 @@ def _at(t):
 
 
 def _dev_as(first, *ts):
-    """Every tensor is contiguous and on the device of the first, a GPU."""
-    index = first.get_device()
-    ok = index >= 0 and first.is_contiguous()
+    """Raises: not every tensor is contiguous and on the device of the first, a GPU."""
+    _dev(first, *ts)
+    raise MoEError("tensors are on several devices: "
+                   + ", ".join(sorted({str(t.device) for t in (first, *ts) if t is not None})))
+
+
+def _ats(*ts):
+    """Their addresses (_at), every tensor being contiguous and on the device of the first, a GPU."""
+    index = ts[0].get_device()
+    at = []
     for t in ts:
-        if t is not None and (t.get_device() != index or not t.is_contiguous()):
-            ok = False
-    if not ok:
-        _dev(first, *ts)
-        raise MoEError("tensors are on several devices: "
-                       + ", ".join(sorted({str(t.device) for t in (first, *ts) if t is not None})))
+        if t is None:
+            at.append(None)
+        elif t.get_device() == index and t.is_contiguous() and index >= 0:
+            at.append(t.data_ptr() or 4096)
+        else:
+            _dev_as(*ts)
+    return at
 
 
 # ---------------------------------------------------------------------------
@@ -197,7 +216,7 @@ def _req(t, name, shape, dtype=None, bf16=False):
     """t has exactly this shape (and dtype, or 2-byte elements for bf16 bit patterns)."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape and tuple(t.shape) != tuple(shape):
         raise MoEError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise MoEError(f"{name}: expected {dtype}, got {t.dtype}")
@@ -816,14 +835,17 @@ def moe_add_rmsnorm(x, gamma, residual=None, eps: float = 1e-5, y=None, residual
 
     Without a residual r is x itself.  y and residual_out may be the buffer of x or residual (in place)."""
     T, H = _norm_args(x, gamma, residual, residual_out, y)
-    _dev_as(x, gamma, residual, residual_out, y)
-    with _on(x, stream):
-        if y is None:
-            y = torch.empty_like(x)
-        if residual is not None and residual_out is None:
-            residual_out = torch.empty_like(x)
-        _check(library().moe_add_rmsnorm(_at(x), _at(residual), _at(gamma), T, H, eps, _at(residual_out), _at(y),
-                                         _here(x)), "moe_add_rmsnorm")
+    here = _place(x, stream)
+    if here is None:
+        with _on(x, stream):
+            return moe_add_rmsnorm(x, gamma, residual, eps, y, residual_out)
+    if y is None:
+        y = torch.empty_like(x)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(x)
+    a = _ats(x, residual, gamma, residual_out, y)
+    st = library().moe_add_rmsnorm(a[0], a[1], a[2], T, H, eps, a[3], a[4], here)
+    _check(st, "moe_add_rmsnorm")
     return y, x if residual is None else residual_out
 
 
@@ -834,18 +856,21 @@ def moe_add_rmsnorm_fp8(x, gamma, residual=None, eps: float = 1e-5, y=None, resi
     T, H = _norm_args(x, gamma, residual, residual_out, y)
     _req(codes, "codes", (T, H), torch.uint8)
     _req(scales, "scales", (T,), torch.float32)
-    _dev_as(x, gamma, residual, residual_out, y, codes, scales)
-    with _on(x, stream):
-        if y is None:
-            y = torch.empty_like(x)
-        if residual is not None and residual_out is None:
-            residual_out = torch.empty_like(x)
-        if codes is None:
-            codes = torch.empty((T, H), dtype=torch.uint8, device=x.device)
-        if scales is None:
-            scales = torch.empty((T,), dtype=torch.float32, device=x.device)
-        _check(library().moe_add_rmsnorm_fp8(_at(x), _at(residual), _at(gamma), T, H, eps, _at(residual_out),
-                                             _at(y), _at(codes), _at(scales), _here(x)), "moe_add_rmsnorm_fp8")
+    here = _place(x, stream)
+    if here is None:
+        with _on(x, stream):
+            return moe_add_rmsnorm_fp8(x, gamma, residual, eps, y, residual_out, codes, scales)
+    if y is None:
+        y = torch.empty_like(x)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(x)
+    if codes is None:
+        codes = torch.empty((T, H), dtype=torch.uint8, device=x.device)
+    if scales is None:
+        scales = torch.empty((T,), dtype=torch.float32, device=x.device)
+    a = _ats(x, residual, gamma, residual_out, y, codes, scales)
+    st = library().moe_add_rmsnorm_fp8(a[0], a[1], a[2], T, H, eps, a[3], a[4], a[5], a[6], here)
+    _check(st, "moe_add_rmsnorm_fp8")
     return y, codes, scales, x if residual is None else residual_out
 
 
@@ -865,20 +890,21 @@ def moe_forward_norm_fp8(x, gamma, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, k:
     T, H = _norm_args(x, gamma, residual, residual_out, y)
     _, _, E = _route_args(x, Wr, br, k, topk_ids, topk_w)
     I = _fp8_experts(Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, E, H)
-    _dev_as(x, gamma, residual, residual_out, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, y, workspace, topk_ids, topk_w)
-    with _on(x, stream):
-        if y is None:
-            y = torch.empty_like(x)
-        if residual is not None and residual_out is None:
-            residual_out = torch.empty_like(x)
-        if workspace is None:
-            workspace = alloc_workspace_norm_fp8(T, H, E, k, I, x.device)
-        st = library().moe_forward_norm_fp8(_at(x), _at(residual), _at(gamma), eps, _at(Wr), _at(br), _at(Wgu_q),
-                                            _at(Wgu_s), _at(bgu), _at(Wd_q), _at(Wd_s), _at(bd), T, H, E, k, I,
-                                            _at(residual_out), _at(y), _at(topk_ids), _at(topk_w), _at(workspace),
-                                            workspace.numel() * workspace.element_size(), path_code(path),
-                                            _here(x))
-        _check(st, "moe_forward_norm_fp8")
+    here = _place(x, stream)
+    if here is None:
+        with _on(x, stream):
+            return moe_forward_norm_fp8(x, gamma, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, k, residual, eps, y,
+                                        residual_out, workspace, topk_ids, topk_w, path)
+    if y is None:
+        y = torch.empty_like(x)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(x)
+    if workspace is None:
+        workspace = alloc_workspace_norm_fp8(T, H, E, k, I, x.device)
+    a = _ats(x, residual, gamma, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, residual_out, y, topk_ids, topk_w, workspace)
+    st = library().moe_forward_norm_fp8(a[0], a[1], a[2], eps, *a[3:11], T, H, E, k, I, *a[11:],
+                                        workspace.numel() * workspace.element_size(), path_code(path), here)
+    _check(st, "moe_forward_norm_fp8")
     return y, x if residual is None else residual_out
 
 
@@ -894,7 +920,10 @@ _GROUPS = (32, 64, 128)
 def _int4_group(*pairs):
     """The group size with ceil(K / G) scales for every (K, scales) pair (several fit only where they mean the same)."""
     for G in _GROUPS:
-        if all(-(-K // G) == n for K, n in pairs):
+        for K, n in pairs:
+            if -(-K // G) != n:
+                break
+        else:
             return G
     raise MoEError("scales: no group size of " + ", ".join(map(str, _GROUPS)) + " gives "
                    + " and ".join(f"{n} scales for K={K}" for K, n in pairs))
@@ -905,6 +934,11 @@ def _int4_shape(n, K, N):
 
 
 def _int4_matrix(q, s, z, bias, names, n, K, N):
+    groups = s.shape
+    if (q.shape == (n, -(-N // 64), K // 32, 1024) and q.dtype is torch.uint8 and groups == (n, groups[1], N)
+            and s.dtype is torch.bfloat16 and (z is None or (z.shape == groups and z.dtype is torch.uint8))
+            and bias is not None and bias.shape == (n, N) and bias.element_size() == 2):
+        return
     _req(q, names + "_q", _int4_shape(n, K, N), torch.uint8)
     _req(s, names + "_s", (n, s.shape[1], N), torch.bfloat16)
     _req(z, names + "_z", tuple(s.shape), torch.uint8)
@@ -952,24 +986,32 @@ def moe_pack_int4(codes, stream=None):
     return q
 
 
+def _scalar_or_at(v):
+    return _at(v) if v is None or isinstance(v, torch.Tensor) else v
+
+
 def _forward_int4(name, x, Wr, br, Wgu_q, Wgu_s, Wgu_z, bgu, Wd_q, Wd_s, Wd_z, bd, k, n, y, y_dtype, workspace, topk_ids,
-                  topk_w, path, stream, before=(), between=(), more=()):
+                  topk_w, path, stream, before=(), between=()):
     """The int4 forwards: `before` y come further sizes or inputs, `between` the outputs and the workspace further
-    outputs; `more` are the tensors among them, for the device check."""
+    outputs."""
     T, H, E = _route_args(x, Wr, br, k, topk_ids, topk_w)
     I, G = _int4_experts(Wgu_q, Wgu_s, Wgu_z, bgu, Wd_q, Wd_s, Wd_z, bd, E if n is None else n, H)
     _req(y, "y" if y_dtype == torch.bfloat16 else "y_partial", (T, H), y_dtype)
-    _dev_as(x, Wr, br, Wgu_q, Wgu_s, Wgu_z, bgu, Wd_q, Wd_s, Wd_z, bd, y, workspace, topk_ids, topk_w, *more)
-    with _on(x, stream):
-        if y is None:
-            y = torch.empty((T, H), dtype=y_dtype, device=x.device)
-        if workspace is None:
-            workspace = alloc_workspace(T, H, E, k, I, x.device)
-        st = getattr(library(), name)(_at(x), _at(Wr), _at(br), _at(Wgu_q), _at(Wgu_s), _at(Wgu_z), _at(bgu),
-                                      _at(Wd_q), _at(Wd_s), _at(Wd_z), _at(bd), T, H, E, k, I, G, *before, _at(y),
-                                      _at(topk_ids), _at(topk_w), *between, _at(workspace),
-                                      workspace.numel() * workspace.element_size(), path_code(path), _here(x))
-        _check(st, name.removesuffix("_ex"))
+    here = _place(x, stream)
+    if here is None:
+        with _on(x, stream):
+            return _forward_int4(name, x, Wr, br, Wgu_q, Wgu_s, Wgu_z, bgu, Wd_q, Wd_s, Wd_z, bd, k, n, y, y_dtype,
+                                 workspace, topk_ids, topk_w, path, None, before, between)
+    if y is None:
+        y = torch.empty((T, H), dtype=y_dtype, device=x.device)
+    if workspace is None:
+        workspace = alloc_workspace(T, H, E, k, I, x.device)
+    a = _ats(x, Wr, br, Wgu_q, Wgu_s, Wgu_z, bgu, Wd_q, Wd_s, Wd_z, bd, y, topk_ids, topk_w, workspace,
+             *(t for t in before + between if isinstance(t, torch.Tensor)))
+    st = getattr(library(), name)(*a[:11], T, H, E, k, I, G, *map(_scalar_or_at, before), *a[11:14],
+                                  *map(_scalar_or_at, between), a[14], workspace.numel() * workspace.element_size(),
+                                  path_code(path), here)
+    _check(st, name.removesuffix("_ex"))
     return y
 
 
@@ -987,8 +1029,8 @@ def moe_forward_padded_int4(x, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, k: int
     _dims(Wr, "Wr", 2)
     _padded_args(n_valid, expert_counts, Wr.shape[0])
     return _forward_int4("moe_forward_padded_int4", x, Wr, br, Wgu_q, Wgu_s, Wgu_z, bgu, Wd_q, Wd_s, Wd_z, bd, k, None,
-                         y, torch.bfloat16, workspace, topk_ids, topk_w, path, stream, before=(_at(n_valid),),
-                         between=(_at(expert_counts),), more=(n_valid, expert_counts))
+                         y, torch.bfloat16, workspace, topk_ids, topk_w, path, stream, before=(n_valid,),
+                         between=(expert_counts,))
 
 
 def moe_forward_ep_int4(x, Wr, br, Wgu_q_local, Wgu_s_local, bgu_local, Wd_q_local, Wd_s_local, bd_local, e_begin: int,
@@ -1023,14 +1065,16 @@ def moe_gate_up_int4(x, Wgu_q, Wgu_s, bgu, cnt, off, rows, k: int, Wgu_z=None, h
     G = _int4_group((H, Wgu_s.shape[1]))
     _permutation(cnt, off, rows, E, T * k)
     _req_rows(h, "h", T * k, I, torch.bfloat16)
-    _dev_as(x, Wgu_q, Wgu_s, Wgu_z, bgu, cnt, off, rows, h)
-    with _on(x, stream):
-        if h is None:
-            h = torch.empty((max(T * k, 1), I), dtype=torch.bfloat16, device=x.device)
-        _check(library().moe_gate_up_int4(_at(x), _at(Wgu_q), _at(Wgu_s), _at(Wgu_z), _at(bgu), _at(cnt), _at(off),
-                                          _at(rows), T, H, E, k, I, G, _at(h), path_code(path), _here(x)),
-               "moe_gate_up_int4")
-    return h[:T * k]
+    here = _place(x, stream)
+    if here is None:
+        with _on(x, stream):
+            return moe_gate_up_int4(x, Wgu_q, Wgu_s, bgu, cnt, off, rows, k, Wgu_z, h, path)
+    if h is None:
+        h = torch.empty((max(T * k, 1), I), dtype=torch.bfloat16, device=x.device)
+    a = _ats(x, Wgu_q, Wgu_s, Wgu_z, bgu, cnt, off, rows, h)
+    st = library().moe_gate_up_int4(*a[:8], T, H, E, k, I, G, a[8], path_code(path), here)
+    _check(st, "moe_gate_up_int4")
+    return h if h.shape[0] == T * k else h[:T * k]
 
 
 def moe_down_int4(h, Wd_q, Wd_s, bd, cnt, off, T: int, k: int, Wd_z=None, o=None, path="auto", stream=None):
@@ -1043,13 +1087,16 @@ def moe_down_int4(h, Wd_q, Wd_s, bd, cnt, off, T: int, k: int, Wd_z=None, o=None
     _permutation(cnt, off, None, E, T * k)
     _req_rows(h, "h", T * k, I, torch.bfloat16)
     _req_rows(o, "o", T * k, H, torch.float32)
-    _dev_as(h, Wd_q, Wd_s, Wd_z, bd, cnt, off, o)
-    with _on(h, stream):
-        if o is None:
-            o = torch.empty((max(T * k, 1), H), dtype=torch.float32, device=h.device)
-        _check(library().moe_down_int4(_at(h), _at(Wd_q), _at(Wd_s), _at(Wd_z), _at(bd), _at(cnt), _at(off), T, H,
-                                       E, k, I, G, _at(o), path_code(path), _here(h)), "moe_down_int4")
-    return o[:T * k]
+    here = _place(h, stream)
+    if here is None:
+        with _on(h, stream):
+            return moe_down_int4(h, Wd_q, Wd_s, bd, cnt, off, T, k, Wd_z, o, path)
+    if o is None:
+        o = torch.empty((max(T * k, 1), H), dtype=torch.float32, device=h.device)
+    a = _ats(h, Wd_q, Wd_s, Wd_z, bd, cnt, off, o)
+    st = library().moe_down_int4(*a[:7], T, H, E, k, I, G, a[7], path_code(path), here)
+    _check(st, "moe_down_int4")
+    return o if o.shape[0] == T * k else o[:T * k]
 
 
 # ---------------------------------------------------------------------------
