@@ -590,3 +590,25 @@ def test_no_tokens():
     _need_gpu()
     args, z = _gpu_args(_block(4, 4, 64, 32, 2, 32, False, seed=21))
     assert binding.moe_forward_int4(args[0][:0], *args[1:], k=2, **z).shape == (0, 64)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_stages_on_another_stream(raw):
+    """A torch stream or a raw handle; outputs given and left to the call."""
+    _need_gpu()
+    T, E, H, I, k, G = 9, 8, 96, 64, 2, 32
+    args, z = _gpu_args(_block(T, E, H, I, k, G, True, seed=47))
+    cnt, off, rows, pos = binding.moe_permute(torch.from_numpy(_routing(T, E, k, 48)).cuda(), E)
+    want = binding.moe_gate_up_int4(args[0], *args[3:6], cnt, off, rows, k, Wgu_z=z["Wgu_z"])
+    o = binding.moe_down_int4(want, *args[6:9], cnt, off, T, k, Wd_z=z["Wd_z"])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if raw else side
+    buf = torch.full((T * k + 3, I), 7.0, dtype=torch.bfloat16, device="cuda")   # longer than the rows: left as it was
+    torch.cuda.synchronize()
+    for h in (None, buf):
+        got = binding.moe_gate_up_int4(args[0], *args[3:6], cnt, off, rows, k, Wgu_z=z["Wgu_z"], h=h, stream=stream)
+        got_o = binding.moe_down_int4(got, *args[6:9], cnt, off, T, k, Wd_z=z["Wd_z"], stream=stream)
+        side.synchronize()
+        assert torch.equal(got, want) and torch.equal(got_o, o)
+    assert (buf[T * k:] == 7).all()
