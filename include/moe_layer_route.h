@@ -420,6 +420,8 @@ MOE_API int moe_down_mxfp4(const void* h, const void* Wd_q, const void* Wd_s, co
  * the float32 scale s = amax / 448 and the codes E4M3(a * (448 / amax)),
  * each operation rounded in float32, E4M3 rounding to nearest with ties to
  * the even code and saturating at 448 (NaN -> 0x7F); amax = 0 gives s = 1.
+ * With amax below 2^-119, where 448 / amax leaves float32, a and amax are
+ * taken times 2^64 (exact): finite values have finite codes.
  * The value of a code is E4M3(code) * s.
  *   Weights:     one scale per expert and matrix.
  *   Activations: one scale per row: a token's row of x for gate_up, a (token,

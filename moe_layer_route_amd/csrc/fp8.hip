@@ -9,7 +9,9 @@
 // Format: OCP FP8 E4M3 (bias 7, largest finite 448, S.1111.111 NaN), the
 // format the gfx950 f8f6f4 MFMAs read with format code 0.  A scale is
 // s = amax / 448 and a code is E4M3(a * (448 / amax)), each in float32, with
-// round-to-nearest-even and saturation at 448; amax = 0 takes s = 1.
+// round-to-nearest-even and saturation at 448; amax = 0 takes s = 1.  Below
+// 2^-119, where 448 / amax leaves float32 (and 0 times it would be NaN), a and
+// amax are taken times 2^64, which is exact in bf16 too.
 // Weights have one scale per expert; activations one scale per row (a
 // token's x row for gate_up, a (token, slot) row of h for down).  h is
 // rounded to bf16 by the gate_up epilogue and quantised by the row kernel.
@@ -69,12 +71,18 @@ __device__ __forceinline__ uint32_t e4m3_encode(float v) {
   return v != v ? 0x7Fu : code;
 }
 
+constexpr float kLiftBelow = 0x1p-119f, kLift = 0x1p64f;
+
 // (s, inv) of a float32 maximum: s = amax / 448, inv = 448 / amax, each
-// rounded once; amax = 0 gives (1, 1).
+// rounded once; amax = 0 gives (1, 1).  Below kLiftBelow inv is for values
+// times kLift.
 __device__ __forceinline__ void fp8_scale(float amax, float& s, float& inv) {
   s = amax == 0.0f ? 1.0f : __fdiv_rn(amax, kE4m3Max);
-  inv = amax == 0.0f ? 1.0f : __fdiv_rn(kE4m3Max, amax);
+  inv = amax == 0.0f ? 1.0f : __fdiv_rn(kE4m3Max, amax < kLiftBelow ? amax * kLift : amax);
 }
+
+// two bf16 times kLift
+__device__ __forceinline__ uint32_t lift2(uint32_t v) { return pack_bf16x2(bf16lo(v) * kLift, bf16hi(v) * kLift); }
 
 __device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return a | (b << 8) | (c << 16) | (d << 24);
@@ -130,7 +138,14 @@ __global__ __launch_bounds__(kRowWaves * kWave) void fp8_rows_kernel(const bf16_
   float s, inv;
   fp8_scale(__uint_as_float(m << 16), s, inv);
   u32x2_t* dst = reinterpret_cast<u32x2_t*>(codes + r * K);
-  for (int c = lane; c < nch; c += kWave) dst[c] = encode8(src[c], inv);
+  if ((uint32_t)__builtin_amdgcn_readfirstlane((int)m) << 16 < __float_as_uint(kLiftBelow)) {
+    for (int c = lane; c < nch; c += kWave) {
+      const u32x4_t v = src[c];
+      dst[c] = encode8(u32x4_t{lift2(v[0]), lift2(v[1]), lift2(v[2]), lift2(v[3])}, inv);
+    }
+  } else {
+    for (int c = lane; c < nch; c += kWave) dst[c] = encode8(src[c], inv);
+  }
   if (lane == 0) scales[r] = s;
 }
 
@@ -168,6 +183,7 @@ __global__ __launch_bounds__(256) void fp8_weight_quant_kernel(const bf16_t* __r
   const int t = threadIdx.x;
   float s, inv;
   fp8_scale(__uint_as_float(amax[e]), s, inv);
+  const float lift = __uint_as_float(amax[e]) < kLiftBelow ? kLift : 1.0f;
   const bf16_t* We = W + (size_t)e * K * N;
   // load: thread t covers row k0 + t/8 (+32) and columns n0 + 8(t%8) .. +7
 #pragma unroll
@@ -177,8 +193,8 @@ __global__ __launch_bounds__(256) void fp8_weight_quant_kernel(const bf16_t* __r
     if (k0 + kr < K && n0 + nc < N) v = *reinterpret_cast<const u32x4_t*>(We + (size_t)(k0 + kr) * N + n0 + nc);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      tile[kr][nc + 2 * i] = bf16lo(v[i]);
-      tile[kr][nc + 2 * i + 1] = bf16hi(v[i]);
+      tile[kr][nc + 2 * i] = bf16lo(v[i]) * lift;
+      tile[kr][nc + 2 * i + 1] = bf16hi(v[i]) * lift;
     }
   }
   __syncthreads();

@@ -13,7 +13,9 @@
 //   v = (r * inv) * gamma             (float32, each product rounded)
 //   y = bf16(v)
 //   s = max|v| / 448, code = E4M3(v * (448 / max|v|)): from the float32 values,
-//         not from y, so a code carries one rounding and not two.
+//         not from y, so a code carries one rounding and not two.  Below 2^-119,
+//         where 448 / max|v| leaves float32, v and the maximum are taken times
+//         2^64, which is exact.
 //
 // It is a stream: x and residual are read once, r, y and the codes written
 // once, the row stays in registers between the two reductions.  T = 16384 rows
@@ -28,6 +30,8 @@ namespace moe {
 namespace {
 
 constexpr float kE4m3Max = 448.0f;
+constexpr uint32_t kLiftBelow = 0x04000000u;   // bits of 2^-119
+constexpr float kLift = 0x1p64f;
 
 // E4M3 code of v, nearest with ties to even, saturated at 448, NaN -> 0x7F:
 // with e = max(exponent, -6), q = rint(|v| * 2^(3-e)) counts quanta of
@@ -144,10 +148,11 @@ __global__ __launch_bounds__(kNormMaxWaves * kWave) void add_rmsnorm_kernel(
     }
     const float amax = __uint_as_float(m);
     const float s = m == 0 ? 1.0f : __fdiv_rn(amax, kE4m3Max);
-    const float up = m == 0 ? 1.0f : __fdiv_rn(kE4m3Max, amax);
-    // From 2^-119 on 448 / amax is finite, and |v * up| rounds to 448 at most:
+    const float lift = m < kLiftBelow ? kLift : 1.0f;
+    const float up = m == 0 ? 1.0f : __fdiv_rn(kE4m3Max, amax * lift);
+    // From 2^-119 on nothing is lifted, and |v * up| rounds to 448 at most:
     // the conversion instruction (nearest, ties to even) never overflows.
-    const bool ordinary = __builtin_amdgcn_readfirstlane(m) - 0x04000000u < 0x7F800000u - 0x04000000u;
+    const bool ordinary = __builtin_amdgcn_readfirstlane(m) - kLiftBelow < 0x7F800000u - kLiftBelow;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int i = tid + p * nt;
@@ -161,8 +166,8 @@ __global__ __launch_bounds__(kNormMaxWaves * kWave) void add_rmsnorm_kernel(
       } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          c[h] = e4m3_any(v[p][4 * h] * up) | e4m3_any(v[p][4 * h + 1] * up) << 8 |
-                 e4m3_any(v[p][4 * h + 2] * up) << 16 | e4m3_any(v[p][4 * h + 3] * up) << 24;
+          c[h] = e4m3_any(v[p][4 * h] * lift * up) | e4m3_any(v[p][4 * h + 1] * lift * up) << 8 |
+                 e4m3_any(v[p][4 * h + 2] * lift * up) << 16 | e4m3_any(v[p][4 * h + 3] * lift * up) << 24;
       }
       if (i < np) *reinterpret_cast<u32x2_t*>(codes + base + 8 * (size_t)i) = c;
     }

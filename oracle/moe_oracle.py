@@ -317,7 +317,9 @@ def moe_forward_mxfp4(x, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, k: int, toke
 #       with ties to the even code and saturates to +-448; NaN becomes 0x7F;
 #   F2  a scale is s = amax / 448, and the codes are E4M3(a * (448 / amax)),
 #       each of the three operations in float32 (the precision the codes are
-#       decided in); amax = 0 gives s = 1 and codes of a * 1;
+#       decided in); amax = 0 gives s = 1 and codes of a * 1.  Below 2^-119,
+#       where 448 / amax is past float32, a and amax are first taken times
+#       2^64 (exact), so the codes are a power of two's of a larger tensor;
 #   F3  weights: one scale per expert and matrix (amax over the whole
 #       expert), codes stored K-contiguous [E][N][K];
 #   F4  activations ("A8", not specified further): one dynamic scale per row,
@@ -376,21 +378,29 @@ def fp8_scale(amax):
     return s, inv
 
 
+def _fp8_codes(a, amax):
+    """Codes of float32 a and scales of its maxima amax (which broadcasts against a) (F2)."""
+    lift = np.where(amax < 2.0 ** -119, np.float32(2.0 ** 64), np.float32(1))
+    with np.errstate(over="ignore"):
+        s, _ = fp8_scale(amax)
+    _, inv = fp8_scale(amax * lift)
+    return e4m3_encode(a * lift * inv), s
+
+
 def fp8_quantize_rows(a) -> tuple:
     """float32 [R][K] (bf16 values) -> (codes uint8 [R][K], s float32 [R]):
     one scale per row (F2, F4)."""
     a = np.asarray(a, dtype=np.float32)
-    s, inv = fp8_scale(np.abs(a).max(axis=-1))
-    return e4m3_encode(a * inv[..., None]), s
+    codes, s = _fp8_codes(a, np.abs(a).max(axis=-1, keepdims=True))
+    return codes, s[..., 0]
 
 
 def fp8_quantize_weights(W) -> tuple:
     """bf16 bits [E][K][N] (x.W form) -> (codes uint8 [E][N][K], s float32 [E]):
     one scale per expert (F2, F3)."""
     w = widen(W).astype(np.float32)
-    s, inv = fp8_scale(np.abs(w).reshape(w.shape[0], -1).max(axis=-1))
-    codes = e4m3_encode(w * inv[:, None, None])
-    return np.ascontiguousarray(np.swapaxes(codes, 1, 2)), s
+    codes, s = _fp8_codes(w, np.abs(w).max(axis=(1, 2), keepdims=True))
+    return np.ascontiguousarray(np.swapaxes(codes, 1, 2)), s[:, 0, 0]
 
 
 def fp8_dequantize(codes, s) -> np.ndarray:
