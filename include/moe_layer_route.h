@@ -536,7 +536,8 @@ MOE_API int moe_add_rmsnorm_fp8(const void* x, const void* residual, const void*
  * quantisation launch and no second read of the rows).
  *   x, residual, gamma, eps, residual_out   as in moe_add_rmsnorm
  *   the router, weights, y, topk outputs and path as in moe_forward_fp8_ex
- *   (y: the block's output, written last; it must not overlap residual_out)
+ *   (y: the block's output, written last; it must not overlap residual_out,
+ *   nor x where residual is NULL: x is the residual stream then)
  *   workspace   at least moe_workspace_bytes_norm_fp8(...) bytes
  */
 MOE_API size_t moe_workspace_bytes_norm_fp8(int64_t T, int32_t H, int32_t E, int32_t k, int32_t I);

@@ -833,7 +833,9 @@ def _norm_args(x, gamma, residual, residual_out, y):
 def moe_add_rmsnorm(x, gamma, residual=None, eps: float = 1e-5, y=None, residual_out=None, stream=None):
     """r = bf16(x + residual) and y = RMS norm of r times gamma; returns (y, r).
 
-    Without a residual r is x itself.  y and residual_out may be the buffer of x or residual (in place)."""
+    y and residual_out may be the buffer of x or residual (in place).  Without a residual r is the tensor x itself; with
+    y=x as well (a norm in place that no addition follows, such as a model's last) that tensor then holds y, and the
+    rows as they were are gone."""
     T, H = _norm_args(x, gamma, residual, residual_out, y)
     here = _place(x, stream)
     if here is None:
@@ -852,8 +854,11 @@ def moe_add_rmsnorm(x, gamma, residual=None, eps: float = 1e-5, y=None, residual
 def moe_add_rmsnorm_fp8(x, gamma, residual=None, eps: float = 1e-5, y=None, residual_out=None, codes=None, scales=None,
                         stream=None):
     """moe_add_rmsnorm that also quantises the normalised rows for the FP8 experts; returns (y, codes, scales, r):
-    codes uint8 [T][H] and scales float32 [T] in moe_quantize_rows_fp8's format, from the unrounded values."""
+    codes uint8 [T][H] and scales float32 [T] in moe_quantize_rows_fp8's format, from the unrounded values.  Without a
+    residual r is x itself, which y must not overlap: the block behind these rows adds to it."""
     T, H = _norm_args(x, gamma, residual, residual_out, y)
+    if residual is None and y is not None and abs(y.data_ptr() - x.data_ptr()) < 2 * T * H:
+        raise MoEError("y overlaps x, the residual stream where no residual is given")
     _req(codes, "codes", (T, H), torch.uint8)
     _req(scales, "scales", (T,), torch.float32)
     here = _place(x, stream)
@@ -886,7 +891,8 @@ def alloc_workspace_norm_fp8(T: int, H: int, E: int, k: int, I: int, device=None
 def moe_forward_norm_fp8(x, gamma, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, k: int = 4, residual=None,
                          eps: float = 1e-5, y=None, residual_out=None, workspace=None, topk_ids=None, topk_w=None,
                          path="auto", stream=None):
-    """moe_add_rmsnorm_fp8 and the FP8 block on its rows, in one call; returns (y, r)."""
+    """moe_add_rmsnorm_fp8 and the FP8 block on its rows, in one call; returns (y, r).  Without a residual r is x itself,
+    which y must not overlap."""
     T, H = _norm_args(x, gamma, residual, residual_out, y)
     _, _, E = _route_args(x, Wr, br, k, topk_ids, topk_w)
     I = _fp8_experts(Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, E, H)

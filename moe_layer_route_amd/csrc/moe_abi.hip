@@ -1262,11 +1262,14 @@ int moe_forward_norm_fp8(const void* x, const void* residual, const void* gamma,
   if (int st = check_dims(fn, T, H, E, k, I)) return st;
   CHECK_PTR(y, 16);
   if (int st = check_norm(fn, x, residual, gamma, T, H, eps, residual_out, nullptr, nullptr, nullptr)) return st;
-  // y is written by the last launch: it may be the buffer of x or residual,
-  // which only the first one reads, but would destroy residual_out
+  // y is written by the last launch: beside a residual it may be the buffer of x
+  // or residual, which only the first one reads, but would destroy the new
+  // residual stream, which is residual_out or, without a residual, x itself
   const size_t rows = (size_t)T * H * 2;
   if (residual_out && !disjoint(y, rows, residual_out, rows))
     return fail(MOE_ERR_INVALID_ARG, "%s: y overlaps residual_out", fn);
+  if (!residual_out && !disjoint(y, rows, x, rows))
+    return fail(MOE_ERR_INVALID_ARG, "%s: y overlaps x, the residual stream where no residual is given", fn);
   // Rows that the router and the FP8 kernels address with 32 bits (the codes of a
   // row have half its bytes), refused before anything is enqueued.
   if (int st = check_rows(fn, "x", T, H)) return st;
