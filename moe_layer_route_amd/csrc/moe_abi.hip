@@ -1,5 +1,6 @@
 // C ABI of the MoE block: host-side argument checks, workspace layout and the
 // per-call launch sequence.  Declared in include/moe_layer_route.h.
+#include <float.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
@@ -1195,7 +1196,7 @@ static int check_norm(const char* fn, const void* x, const void* residual, const
   const int step = codes ? 16 : 8;
   if (H < step || H > MOE_MAX_DIM || H % step != 0)
     return fail(MOE_ERR_INVALID_ARG, "%s: H=%d must be a multiple of %d in [%d, %d]", fn, H, step, step, MOE_MAX_DIM);
-  if (!(eps > 0.0f) || eps > 3.4e38f) return fail(MOE_ERR_INVALID_ARG, "%s: eps=%g must be finite and above 0", fn, eps);
+  if (!(eps > 0.0f && eps <= FLT_MAX)) return fail(MOE_ERR_INVALID_ARG, "%s: eps=%g must be finite and above 0", fn, eps);
   CHECK_PTR(x, 16);
   CHECK_PTR(gamma, 16);
   if ((residual == nullptr) != (residual_out == nullptr))

@@ -78,3 +78,9 @@ def test_fp8_norm_does_not_replace_the_stream_it_returns():
     for rows, kw in ((x, {}), (x, dict(y=x, residual=x.clone())), (buf[:4], dict(y=buf[4:8]))):   # these end at the device check
         with pytest.raises(binding.MoEError, match="must be on the GPU"):
             binding.moe_add_rmsnorm_fp8(rows, gamma, **kw)
+
+
+def test_eps_is_any_finite_value_above_zero(lib):
+    x, gamma, y = _p(0), _p(1), _p(2)
+    for eps, want in ((3.4028234663852886e38, 0), (1e-45, 0), (float("inf"), INVALID), (float("nan"), INVALID), (0.0, INVALID)):
+        assert lib.moe_add_rmsnorm(x, None, gamma, 0, 64, eps, None, y, None) == want, eps
