@@ -535,6 +535,11 @@ MOE_API int moe_add_rmsnorm_fp8(const void* x, const void* residual, const void*
  * in one call: the router reads the bf16 rows, gate_up their codes (no
  * quantisation launch and no second read of the rows).
  *   x, residual, gamma, eps, residual_out   as in moe_add_rmsnorm
+ * Accuracy: the block's.  The matrix cores sum FP8 products below float32
+ * precision, so that about 2% of the bf16 values of h and with them 0.1 to 0.2%
+ * of its codes are a neighbour's; y's error against 64 bits (relative norms) is
+ * 2.1e-3 to 2.3e-3 at H = I = 2880, where the rounding of y to bf16 alone is
+ * 1.7e-3.
  *   the router, weights, y, topk outputs and path as in moe_forward_fp8_ex
  *   (y: the block's output, written last; it must not overlap residual_out,
  *   nor x where residual is NULL: x is the residual stream then)

@@ -47,7 +47,9 @@ __device__ __forceinline__ uint32_t int4_store_order(uint32_t w) {
 // q = clamp(rint(v / s), -8, 7) + 8.  With zero points: lo = min(v, 0),
 // hi = max(v, 0), s = bf16(hi / 15 - lo / 15), z = clamp(rint(-lo / s), 0,
 // 15), q = clamp(rint(v / s) + z, 0, 15).  float32, halves to even; s = 0
-// gives q = z (and z = 0 with zero points).
+// gives q = z (and z = 0 with zero points).  Run once when weights are loaded: 32
+// experts of 2880 x 5760 take 1.02 ms at G = 64, 1.05 at G = 128 with zero points,
+// 1.3 TB/s of the weights, codes and scales.
 // ---------------------------------------------------------------------------
 constexpr int kQThreads = 256;
 
@@ -98,7 +100,8 @@ __global__ __launch_bounds__(kQThreads) void int4_quantize_kernel(const bf16_t* 
 }
 
 // Codes [E][N][K/2] (K contiguous, low nibble first) to the tile order: one
-// thread per stored word, which is four consecutive source bytes.
+// thread per stored word, which is four consecutive source bytes.  32 experts of
+// 2880 x 5760 take 0.32 ms, 1.7 TB/s: a tile reads 16 bytes of each of 64 columns.
 __global__ __launch_bounds__(kQThreads) void int4_pack_kernel(const uint8_t* __restrict__ src, int K, int N,
                                                               uint32_t* __restrict__ codes) {
   const int nt_n = (N + kTileN - 1) / kTileN;
@@ -491,6 +494,9 @@ hipError_t launch_group(int G, const void* A, const void* Wq, const void* Ws, co
 // columns and more: gate_up with one strip 33.6, 47.0, 53.5 us, with two 36.6,
 // 46.5, 52.3; T = 256 of 128 experts: down 104 against 98.6 us.  64 rows of 32
 // experts of 1024 x 1536, 384 workgroups of two strips: 8.8 against 10.3 us.)
+// On an expert-parallel rank T * k is the whole layer's and E the rank's: the mean
+// is taken E_layer / E times too high there, and both switches come earlier than
+// the rank's own rows call for.
 // Where no CU would get a second workgroup, eight waves halve each one's share
 // of K.
 constexpr int64_t kOneChunkMeanRows = 10;

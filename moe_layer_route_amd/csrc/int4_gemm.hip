@@ -17,14 +17,19 @@
 // counts only the loads it makes itself, so its waits for them take in the
 // direct loads under way.)  Per 16-row chunk the unit's products go into a
 // fresh accumulator that starts at -(16 + z) sum(a) and is added to the result,
-// times the scale, in float32: no weight is rounded, for 128 more VALU
-// instructions a unit beside its 64 products.
+// times the scale, in float32: no weight is rounded.  A unit of two tiles and
+// 64 products has 198 vector instructions beside them: 128 of these additions
+// (zero points: 128 multiplications more), 56 to unpack the codes, 14 for
+// addresses.
 //
 // T = 4096 of 32 experts, 2880 x 5760 (gate_up), G = 64: 570 us, 954 TFLOP/s;
 // down 324 us, 839 TFLOP/s (a large library product reaches 1155 to 1300 here);
-// T = 16384: 2113 us, 1029 TFLOP/s.  Vector issue binds (each SIMD issues a
-// product and an addition through one port: 48% of all cycles, while the matrix
-// pipes are busy for 44%, at the 1.96 GHz that the card holds under this load).
+// T = 16384: 2113 us, 1029 TFLOP/s.  No unit is saturated: at T = 4096 the matrix
+// pipes are busy for 45% of the cycles (down 38%), vector instructions and
+// products issue in 54% (42%), the LDS is busy for 22%; a wave waits for a load
+// or a barrier for 26% of its time (30%) and for its turn to issue for 30%.  Two
+// waves a SIMD, which is all that 128 accumulators a lane leave room for, do not
+// cover each other's waits.
 #include "device_common.h"
 #include "int4_device.h"
 #include "launch.h"
@@ -393,6 +398,9 @@ hipError_t launch_tiles(const void* A, const void* Wq, const void* Ws, const voi
 // half as many rows (K = 2048, N = 4096, G = 64, 104 rows an expert: 8 experts
 // 33 against 56 us, 16 42 against 57, 32, more than fit at once, 88 against 79).
 // Eight rows more than the mean are counted: an expert past 64 has one tile more.
+// An expert-parallel rank passes the whole layer's T * k with its own E, which
+// counts the layer's rows for the local experts: it takes the large tiles earlier
+// than its own rows call for.
 constexpr int64_t kSmallTiles = 512;
 
 template <bool GATE_UP>

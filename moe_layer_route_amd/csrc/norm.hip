@@ -193,7 +193,8 @@ hipError_t launch_p(const void* x, const void* residual, const void* gamma, int6
 
 // Two pieces a thread: at H = 2880 (three waves a row) T = 64 takes 3.5 us and
 // T = 16384 75.6 us, against 4.0 and 76.2 with one piece (six waves) and 5.4
-// and 82.9 with four (two waves; before the moves above).  Rows that one wave
+// and 82.9 with four (two waves; that one with reductions by lane permutations,
+// which the moves of wave_reduce.h have replaced).  Rows that one wave
 // covers with one piece a thread take that: 8192 x 512 9.1 against 10.1 us.
 // H <= 16384 is 2048 pieces: at most 16 waves a row.
 hipError_t launch_add_rmsnorm(const void* x, const void* residual, const void* gamma, int64_t T, int H, float eps,
