@@ -649,6 +649,83 @@ MOE_API int moe_down_int4(const void* h, const void* Wd_q, const void* Wd_s, con
                           int64_t T, int32_t H, int32_t E, int32_t k, int32_t I, int32_t G, float* o,
                           int32_t path, void* stream);
 
+/*
+ * MXFP4 on both sides (W4A4) -- xserv "Phase 19: gpt-oss-20b MoE support",
+ * section 5: the experts' products of MXFP4 rows and MXFP4 weights on the
+ * scaled matrix instructions.  Weights as in "MXFP4 expert weights" above.
+ *
+ * Rows a [R][K] (a token's row of x for gate_up, a (token, slot) row of h for
+ * down), K % 32 == 0:
+ *   codes  uint8 [R][K/2]             as a weight's: k = 2i in bits 0-3 of byte
+ *                                     i, k = 2i+1 in bits 4-7
+ *   scales uint8 [ceil(K/128)][R][4]  scales[b / 4][r][b % 4] = s is the power
+ *                                     2^(s - 127) of values 32b .. 32b+31 of
+ *                                     row r; 255 is NaN.  The bytes of blocks
+ *                                     past K/32 are never read; the quantiser
+ *                                     writes 0 there, moe_gate_up_w4a4 nothing.
+ * Quantisation is that of moe_quantize_mxfp4, one block of a row at a time: s =
+ * floor(log2 max |v|) - 2 + 127, clamped at 0, and the nearest E2M1 value of v
+ * 2^(127 - s), ties to the even code, above 6 to 6.  A block with a NaN or an
+ * infinity takes s = 255 and codes 0: it is NaN, and so is what it is
+ * multiplied into.  Code arrays 16-byte aligned, scale arrays 4-byte aligned.
+ */
+
+/* moe_quantize_rows_mxfp4 -- bf16 rows a [R][K] to codes and scales.  K % 32 ==
+ * 0, 32 <= K <= MOE_MAX_DIM, R below 2^31; R = 0 is a no-op. */
+MOE_API int moe_quantize_rows_mxfp4(const void* a, int64_t R, int32_t K, void* codes, void* scales, void* stream);
+
+/* moe_dequantize_rows_mxfp4 -- the rows' values in bf16 [R][K] (exact: every
+ * value of the format up to 2^127 is a bf16; a larger one, from scales above
+ * 252, which the quantiser does not write, is infinite). */
+MOE_API int moe_dequantize_rows_mxfp4(const void* codes, const void* scales, int64_t R, int32_t K, void* out,
+                                      void* stream);
+
+/* Bytes of workspace moe_forward_w4a4 and its variants need. */
+MOE_API size_t moe_workspace_bytes_w4a4(int64_t T, int32_t H, int32_t E, int32_t k, int32_t I);
+
+/*
+ * moe_forward_w4a4 -- moe_forward with MXFP4 expert weights (arguments as in
+ * moe_forward_mxfp4) and activations quantised to MXFP4 inside the call: x for
+ * gate_up (the router reads the bf16 x), and h, rounded to bf16, for down.
+ * Products are exact and summed in float32.  H % 32 == 0 and I % 32 == 0;
+ * moe_workspace_bytes_w4a4 bytes of workspace; path: MOE_PATH_GEMV streams the
+ * weights, MOE_PATH_GEMM is the LDS-tiled grouped GEMM, AUTO picks from T*k/E.
+ * x, h and one expert's matrix must take fewer than 2^32 values each
+ * (MOE_ERR_UNSUPPORTED, before anything is enqueued).
+ */
+MOE_API int moe_forward_w4a4(const void* x, const void* Wr, const void* br, const void* Wgu_q, const void* Wgu_s,
+                             const void* bgu, const void* Wd_q, const void* Wd_s, const void* bd,
+                             int64_t T, int32_t H, int32_t E, int32_t k, int32_t I,
+                             void* y, int32_t* topk_ids_out, float* topk_w_out,
+                             void* workspace, size_t workspace_bytes, int32_t path, void* stream);
+
+/* moe_forward_padded_w4a4, moe_forward_ep_w4a4 -- moe_forward_padded and
+ * moe_forward_ep with MXFP4 on both sides. */
+MOE_API int moe_forward_padded_w4a4(const void* x, const void* Wr, const void* br, const void* Wgu_q, const void* Wgu_s,
+                                    const void* bgu, const void* Wd_q, const void* Wd_s, const void* bd,
+                                    int64_t T, int32_t H, int32_t E, int32_t k, int32_t I, const int32_t* n_valid,
+                                    void* y, int32_t* topk_ids_out, float* topk_w_out, int32_t* expert_counts_out,
+                                    void* workspace, size_t workspace_bytes, int32_t path, void* stream);
+MOE_API int moe_forward_ep_w4a4(const void* x, const void* Wr, const void* br, const void* Wgu_q_local,
+                                const void* Wgu_s_local, const void* bgu_local, const void* Wd_q_local,
+                                const void* Wd_s_local, const void* bd_local, int64_t T, int32_t H, int32_t E,
+                                int32_t k, int32_t I, int32_t e_begin, int32_t n_local, float* y_partial,
+                                int32_t* topk_ids_out, float* topk_w_out, void* workspace, size_t workspace_bytes,
+                                int32_t path, void* stream);
+
+/* Stage calls of moe_forward_w4a4, permuted order as in moe_gate_up and
+ * moe_down: gate_up takes x as MXFP4 rows [T] and leaves h as MXFP4 rows [T*k]
+ * (hq uint8 [T*k][I/2], sh uint8 [ceil(I/128)][T*k][4]); down takes those.
+ * Rows from off[E] on (slots of no expert) are neither read nor written. */
+MOE_API int moe_gate_up_w4a4(const void* xq, const void* sx, const void* Wgu_q, const void* Wgu_s, const void* bgu,
+                             const int32_t* cnt, const int32_t* off, const int32_t* rows,
+                             int64_t T, int32_t H, int32_t E, int32_t k, int32_t I, void* hq, void* sh,
+                             int32_t path, void* stream);
+MOE_API int moe_down_w4a4(const void* hq, const void* sh, const void* Wd_q, const void* Wd_s, const void* bd,
+                          const int32_t* cnt, const int32_t* off,
+                          int64_t T, int32_t H, int32_t E, int32_t k, int32_t I, float* o,
+                          int32_t path, void* stream);
+
 /* ---------------------------------------------------------------------------
  * Measurement probes.  They are not part of the block: they measure what a
  * plain hand-written kernel gets from the matrix cores and from HBM on this

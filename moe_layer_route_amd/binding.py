@@ -34,7 +34,9 @@ EXPORTS = ("moe_abi_version", "moe_status_str", "moe_last_error", "moe_workspace
            "moe_forward_noalloc",
            "moe_add_rmsnorm", "moe_add_rmsnorm_fp8", "moe_workspace_bytes_norm_fp8", "moe_forward_norm_fp8",
            "moe_quantize_int4", "moe_pack_int4", "moe_forward_int4", "moe_forward_int4_ex", "moe_gate_up_int4",
-           "moe_down_int4", "moe_forward_padded_int4", "moe_forward_ep_int4")
+           "moe_down_int4", "moe_forward_padded_int4", "moe_forward_ep_int4",
+           "moe_quantize_rows_mxfp4", "moe_dequantize_rows_mxfp4", "moe_workspace_bytes_w4a4", "moe_forward_w4a4",
+           "moe_forward_padded_w4a4", "moe_forward_ep_w4a4", "moe_gate_up_w4a4", "moe_down_w4a4")
 
 
 class MoEError(RuntimeError):
@@ -99,6 +101,14 @@ _SIGS = {
     "moe_forward_ep_int4": (ctypes.c_int, [_vp] * 11 + [_i64] + [_i32] * 7 + [_vp] * 4 + [_sz, _i32, _vp]),
     "moe_gate_up_int4": (ctypes.c_int, [_vp] * 8 + [_i64] + [_i32] * 5 + [_vp, _i32, _vp]),
     "moe_down_int4": (ctypes.c_int, [_vp] * 7 + [_i64] + [_i32] * 5 + [_vp, _i32, _vp]),
+    "moe_quantize_rows_mxfp4": (ctypes.c_int, [_vp, _i64, _i32, _vp, _vp, _vp]),
+    "moe_dequantize_rows_mxfp4": (ctypes.c_int, [_vp, _vp, _i64, _i32, _vp, _vp]),
+    "moe_workspace_bytes_w4a4": (_sz, [_i64, _i32, _i32, _i32, _i32]),
+    "moe_forward_w4a4": (ctypes.c_int, [_vp] * 9 + [_i64] + [_i32] * 4 + [_vp] * 4 + [_sz, _i32, _vp]),
+    "moe_forward_padded_w4a4": (ctypes.c_int, [_vp] * 9 + [_i64] + [_i32] * 4 + [_vp] * 6 + [_sz, _i32, _vp]),
+    "moe_forward_ep_w4a4": (ctypes.c_int, [_vp] * 9 + [_i64] + [_i32] * 6 + [_vp] * 4 + [_sz, _i32, _vp]),
+    "moe_gate_up_w4a4": (ctypes.c_int, [_vp] * 8 + [_i64] + [_i32] * 4 + [_vp, _vp, _i32, _vp]),
+    "moe_down_w4a4": (ctypes.c_int, [_vp] * 7 + [_i64] + [_i32] * 4 + [_vp, _i32, _vp]),
 }
 
 
@@ -1102,6 +1112,171 @@ def moe_down_int4(h, Wd_q, Wd_s, bd, cnt, off, T: int, k: int, Wd_z=None, o=None
     a = _ats(h, Wd_q, Wd_s, Wd_z, bd, cnt, off, o)
     st = library().moe_down_int4(*a[:7], T, H, E, k, I, G, a[7], path_code(path), here)
     _check(st, "moe_down_int4")
+    return o if o.shape[0] == T * k else o[:T * k]
+
+
+# ---------------------------------------------------------------------------
+# MXFP4 on both sides: rows as codes uint8 [R][K/2] and scales uint8
+# [ceil(K/128)][R][4], weights as in the MXFP4 section above
+# ---------------------------------------------------------------------------
+def _mx_rows(codes, scales, name, R, K):
+    """Codes and scales of exactly R rows (the scales' layout goes by their number)."""
+    _req(codes, name + "q", (R, K // 2), torch.uint8)
+    _req(scales, "s" + name, (-(-K // 128), R, 4), torch.uint8)
+
+
+def _mx_matrix(q, s, bias, names, E, K, N):
+    _req(q, names + "_q", (E, N, K // 2), torch.uint8)
+    _req(s, names + "_s", (E, K // 32, N), torch.uint8)
+    _req(bias, "b" + names[1:], (E, N), bf16=True)
+
+
+def moe_quantize_rows_mxfp4(a, codes=None, scales=None, stream=None):
+    """bf16 rows [R][K] -> (codes uint8 [R][K/2], scales uint8 [ceil(K/128)][R][4])."""
+    _dims(a, "a", 2)
+    R, K = a.shape
+    _req(a, "a", (R, K), torch.bfloat16)
+    _req(codes, "codes", (R, K // 2), torch.uint8)
+    _req(scales, "scales", (-(-K // 128), R, 4), torch.uint8)
+    here = _place(a, stream)
+    if here is None:
+        with _on(a, stream):
+            return moe_quantize_rows_mxfp4(a, codes, scales)
+    if codes is None:
+        codes = torch.empty((R, K // 2), dtype=torch.uint8, device=a.device)
+    if scales is None:
+        scales = torch.empty((-(-K // 128), R, 4), dtype=torch.uint8, device=a.device)
+    at = _ats(a, codes, scales)
+    _check(library().moe_quantize_rows_mxfp4(at[0], R, K, at[1], at[2], here), "moe_quantize_rows_mxfp4")
+    return codes, scales
+
+
+def moe_dequantize_rows_mxfp4(codes, scales, out=None, stream=None):
+    """Codes and scales of rows -> their values, bf16 [R][K] (exact)."""
+    _dims(codes, "codes", 2)
+    R, K = codes.shape[0], 2 * codes.shape[1]
+    _req(codes, "codes", (R, K // 2), torch.uint8)
+    _req(scales, "scales", (-(-K // 128), R, 4), torch.uint8)
+    _req(out, "out", (R, K), torch.bfloat16)
+    here = _place(codes, stream)
+    if here is None:
+        with _on(codes, stream):
+            return moe_dequantize_rows_mxfp4(codes, scales, out)
+    if out is None:
+        out = torch.empty((R, K), dtype=torch.bfloat16, device=codes.device)
+    at = _ats(codes, scales, out)
+    _check(library().moe_dequantize_rows_mxfp4(at[0], at[1], R, K, at[2], here), "moe_dequantize_rows_mxfp4")
+    return out
+
+
+def workspace_bytes_w4a4(T: int, H: int, E: int, k: int, I: int) -> int:
+    return int(library().moe_workspace_bytes_w4a4(T, H, E, k, I))
+
+
+def alloc_workspace_w4a4(T: int, H: int, E: int, k: int, I: int, device=None) -> torch.Tensor:
+    n = workspace_bytes_w4a4(T, H, E, k, I)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device or "cuda")
+
+
+def _forward_w4a4(name, x, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, k, n, y, y_dtype, workspace, topk_ids, topk_w,
+                  path, stream, before=(), between=()):
+    """The forwards with MXFP4 on both sides: `before` y come further sizes or inputs, `between` the outputs and the
+    workspace further outputs."""
+    T, H, E = _route_args(x, Wr, br, k, topk_ids, topk_w)
+    I = _mxfp4_experts(Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, E if n is None else n, H)
+    _req(y, "y" if y_dtype == torch.bfloat16 else "y_partial", (T, H), y_dtype)
+    here = _place(x, stream)
+    if here is None:
+        with _on(x, stream):
+            return _forward_w4a4(name, x, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, k, n, y, y_dtype, workspace,
+                                 topk_ids, topk_w, path, None, before, between)
+    if y is None:
+        y = torch.empty((T, H), dtype=y_dtype, device=x.device)
+    if workspace is None:
+        workspace = alloc_workspace_w4a4(T, H, E, k, I, x.device)
+    a = _ats(x, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, y, topk_ids, topk_w, workspace,
+             *(t for t in before + between if isinstance(t, torch.Tensor)))
+    st = getattr(library(), name)(*a[:9], T, H, E, k, I, *map(_scalar_or_at, before), *a[9:12],
+                                  *map(_scalar_or_at, between), a[12], workspace.numel() * workspace.element_size(),
+                                  path_code(path), here)
+    _check(st, name)
+    return y
+
+
+def moe_forward_w4a4(x, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, k: int = 4, y=None, workspace=None, topk_ids=None,
+                     topk_w=None, path="auto", stream=None):
+    """moe_forward with MXFP4 weights and MXFP4 activations; returns y (bf16 [T,H])."""
+    return _forward_w4a4("moe_forward_w4a4", x, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, k, None, y, torch.bfloat16,
+                         workspace, topk_ids, topk_w, path, stream)
+
+
+def moe_forward_padded_w4a4(x, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, k: int = 4, n_valid=None, y=None,
+                            workspace=None, topk_ids=None, topk_w=None, expert_counts=None, path="auto", stream=None):
+    """moe_forward_padded with MXFP4 weights and MXFP4 activations; returns y (bf16 [T,H])."""
+    _dims(Wr, "Wr", 2)
+    _padded_args(n_valid, expert_counts, Wr.shape[0])
+    return _forward_w4a4("moe_forward_padded_w4a4", x, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, k, None, y,
+                         torch.bfloat16, workspace, topk_ids, topk_w, path, stream, before=(n_valid,),
+                         between=(expert_counts,))
+
+
+def moe_forward_ep_w4a4(x, Wr, br, Wgu_q_local, Wgu_s_local, bgu_local, Wd_q_local, Wd_s_local, bd_local, e_begin: int,
+                        k: int = 4, y_partial=None, workspace=None, topk_ids=None, topk_w=None, path="auto",
+                        stream=None):
+    """moe_forward_ep with MXFP4 weights and MXFP4 activations (the rank's n_local = Wgu_q_local.shape[0] experts from
+    e_begin); returns y_partial (float32 [T,H])."""
+    _dims(Wr, "Wr", 2)
+    _dims(Wgu_q_local, "Wgu_q_local", 3)
+    n_local = Wgu_q_local.shape[0]
+    _local_experts(e_begin, n_local, Wr.shape[0])
+    return _forward_w4a4("moe_forward_ep_w4a4", x, Wr, br, Wgu_q_local, Wgu_s_local, bgu_local, Wd_q_local, Wd_s_local,
+                         bd_local, k, n_local, y_partial, torch.float32, workspace, topk_ids, topk_w, path, stream,
+                         before=(e_begin, n_local))
+
+
+def moe_gate_up_w4a4(xq, sx, Wgu_q, Wgu_s, bgu, cnt, off, rows, k: int, hq=None, sh=None, path="auto", stream=None):
+    """gate_up + bias + GLU of MXFP4 rows; returns (hq uint8 [T*k, I/2], sh uint8 [ceil(I/128), T*k, 4]): h as MXFP4
+    rows, permuted order."""
+    _dims(xq, "xq", 2)
+    _dims(Wgu_q, "Wgu_q", 3)
+    T, H = xq.shape[0], 2 * xq.shape[1]
+    E, I = Wgu_q.shape[0], Wgu_q.shape[1] // 2
+    _mx_rows(xq, sx, "x", T, H)
+    _mx_matrix(Wgu_q, Wgu_s, bgu, "Wgu", E, H, 2 * I)
+    _permutation(cnt, off, rows, E, T * k)
+    _mx_rows(hq, sh, "h", T * k, I)
+    here = _place(xq, stream)
+    if here is None:
+        with _on(xq, stream):
+            return moe_gate_up_w4a4(xq, sx, Wgu_q, Wgu_s, bgu, cnt, off, rows, k, hq, sh, path)
+    if hq is None:
+        hq = torch.empty((T * k, I // 2), dtype=torch.uint8, device=xq.device)
+    if sh is None:
+        sh = torch.empty((-(-I // 128), T * k, 4), dtype=torch.uint8, device=xq.device)
+    a = _ats(xq, sx, Wgu_q, Wgu_s, bgu, cnt, off, rows, hq, sh)
+    st = library().moe_gate_up_w4a4(*a[:8], T, H, E, k, I, a[8], a[9], path_code(path), here)
+    _check(st, "moe_gate_up_w4a4")
+    return hq, sh
+
+
+def moe_down_w4a4(hq, sh, Wd_q, Wd_s, bd, cnt, off, T: int, k: int, o=None, path="auto", stream=None):
+    """down + bias of MXFP4 rows h; returns o (float32 [T*k, H], permuted order)."""
+    _dims(hq, "hq", 2)
+    _dims(Wd_q, "Wd_q", 3)
+    E, H, I = Wd_q.shape[0], Wd_q.shape[1], 2 * hq.shape[1]
+    _mx_rows(hq, sh, "h", T * k, I)
+    _mx_matrix(Wd_q, Wd_s, bd, "Wd", E, I, H)
+    _permutation(cnt, off, None, E, T * k)
+    _req_rows(o, "o", T * k, H, torch.float32)
+    here = _place(hq, stream)
+    if here is None:
+        with _on(hq, stream):
+            return moe_down_w4a4(hq, sh, Wd_q, Wd_s, bd, cnt, off, T, k, o, path)
+    if o is None:
+        o = torch.empty((T * k, H), dtype=torch.float32, device=hq.device)
+    a = _ats(hq, sh, Wd_q, Wd_s, bd, cnt, off, o)
+    st = library().moe_down_w4a4(*a[:7], T, H, E, k, I, a[7], path_code(path), here)
+    _check(st, "moe_down_w4a4")
     return o if o.shape[0] == T * k else o[:T * k]
 
 

@@ -1286,6 +1286,241 @@ int moe_forward_norm_fp8(const void* x, const void* residual, const void* gamma,
 }
 
 // ---------------------------------------------------------------------------
+// MXFP4 on both sides
+// ---------------------------------------------------------------------------
+// Rows of the quantiser and its inverse, and where their buffers may not meet.
+static int check_mx_rows(const char* fn, const char* a_name, const void* a, int64_t R, int32_t K, const void* codes,
+                         const void* scales) {
+  if (R < 0 || R >= (int64_t)1 << 31)
+    return fail(MOE_ERR_INVALID_ARG, "%s: R=%lld outside [0, 2^31)", fn, (long long)R);
+  if (K < 32 || K > MOE_MAX_DIM || K % 32 != 0)
+    return fail(MOE_ERR_INVALID_ARG, "%s: K=%d must be a multiple of 32 in [32, %d]", fn, K, MOE_MAX_DIM);
+  if (a == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: %s is NULL", fn, a_name);
+  if (!aligned(a, 16)) return fail(MOE_ERR_INVALID_ARG, "%s: %s is not 16-byte aligned", fn, a_name);
+  CHECK_PTR(codes, 16);
+  CHECK_PTR(scales, 4);
+  const size_t an = (size_t)R * K * 2, cn = (size_t)R * K / 2, sn = (size_t)((K + 127) / 128) * R * 4;
+  if (!disjoint(a, an, codes, cn)) return fail(MOE_ERR_INVALID_ARG, "%s: codes overlaps %s", fn, a_name);
+  if (!disjoint(a, an, scales, sn)) return fail(MOE_ERR_INVALID_ARG, "%s: scales overlaps %s", fn, a_name);
+  if (!disjoint(codes, cn, scales, sn)) return fail(MOE_ERR_INVALID_ARG, "%s: scales overlaps codes", fn);
+  return MOE_OK;
+}
+
+int moe_quantize_rows_mxfp4(const void* a, int64_t R, int32_t K, void* codes, void* scales, void* stream) {
+  const char* fn = "moe_quantize_rows_mxfp4";
+  if (int st = check_mx_rows(fn, "a", a, R, K, codes, scales)) return st;
+  if (R == 0) return ok();
+  if (int st = hip_status(fn, moe::launch_mxfp4_rows(a, R, K, codes, scales, (hipStream_t)stream))) return st;
+  return ok();
+}
+
+int moe_dequantize_rows_mxfp4(const void* codes, const void* scales, int64_t R, int32_t K, void* out, void* stream) {
+  const char* fn = "moe_dequantize_rows_mxfp4";
+  if (int st = check_mx_rows(fn, "out", out, R, K, codes, scales)) return st;
+  if (R == 0) return ok();
+  if (int st = hip_status(fn, moe::launch_mxfp4_rows_back(codes, scales, R, K, out, (hipStream_t)stream))) return st;
+  return ok();
+}
+
+struct W4a4Layout {
+  Layout base;   // h is not used
+  size_t xq, sx, hq, sh, total;
+};
+
+static size_t mx_scale_bytes(int64_t R, int32_t K) { return (size_t)((K + 127) / 128) * (size_t)R * 4; }
+
+static W4a4Layout w4a4_layout(int64_t T, int32_t H, int32_t E, int32_t k, int32_t I) {
+  W4a4Layout L;
+  const size_t S = (size_t)T * k;
+  size_t cur = 0;
+  L.base.ids = take(cur, S * 4);
+  L.base.w = take(cur, S * 4);
+  L.base.cnt = take(cur, (size_t)E * 4);
+  L.base.off = take(cur, (size_t)(E + 1) * 4);
+  L.base.rows = take(cur, S * 4);
+  L.base.pos = take(cur, S * 4);
+  L.base.h = 0;
+  L.base.o = take(cur, S * H * 4);
+  L.base.total = cur;
+  L.xq = take(cur, (size_t)T * H / 2);
+  L.sx = take(cur, mx_scale_bytes(T, H));
+  L.hq = take(cur, S * I / 2);
+  L.sh = take(cur, mx_scale_bytes(S, I));
+  L.total = cur;
+  return L;
+}
+
+size_t moe_workspace_bytes_w4a4(int64_t T, int32_t H, int32_t E, int32_t k, int32_t I) {
+  if (check_dims("moe_workspace_bytes_w4a4", T, H, E, k, I) != MOE_OK) return 0;
+  if (check_mx_dims("moe_workspace_bytes_w4a4", H, I) != MOE_OK) return 0;
+  if (T == 0) return 0;
+  return w4a4_layout(T, H, E, k, I).total;
+}
+
+// The kernels address rows of codes with 32 bits; the router reads x's bytes.
+static int check_w4a4_rows(const char* fn, const char* name, int64_t rows, int32_t K) {
+  if (rows * K >= (int64_t)1 << 32)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: %s of %lld rows of %d has 2^32 values or more: split the batch", fn, name,
+                (long long)rows, K);
+  return MOE_OK;
+}
+
+static int run_gate_up_w4a4(const char* fn, const void* xq, const void* sx, const void* Wgu_q, const void* Wgu_s,
+                            const void* bgu, const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T,
+                            int32_t H, int32_t E, int32_t k, int32_t I, void* hq, void* sh, int32_t path,
+                            hipStream_t s) {
+  return hip_status(fn, moe::launch_w4a4_gate_up(xq, sx, Wgu_q, Wgu_s, bgu, cnt, off, rows, T, H, E, k, I, hq, sh, s));
+}
+
+static int run_down_w4a4(const char* fn, const void* hq, const void* sh, const void* Wd_q, const void* Wd_s,
+                         const void* bd, const int32_t* cnt, const int32_t* off, int64_t T, int32_t H, int32_t E,
+                         int32_t k, int32_t I, float* o, int32_t path, hipStream_t s) {
+  return hip_status(fn, moe::launch_w4a4_down(hq, sh, Wd_q, Wd_s, bd, cnt, off, T, H, E, k, I, o, s));
+}
+
+// The forward with MXFP4 on both sides: the experts [e_begin, e_begin + n_local)
+// of E; n_valid (device, optional) marks the rows from *n_valid on as padding.
+static int forward_w4a4(const char* fn, const void* x, const void* Wr, const void* br, const void* Wgu_q,
+                        const void* Wgu_s, const void* bgu, const void* Wd_q, const void* Wd_s, const void* bd,
+                        int64_t T, int32_t H, int32_t E, int32_t k, int32_t I, int32_t e_begin, int32_t n_local,
+                        const int32_t* n_valid, void* y, bool partial, int32_t* topk_ids_out, float* topk_w_out,
+                        int32_t* expert_counts_out, void* workspace, size_t workspace_bytes, int32_t path,
+                        void* stream) {
+  if (int st = check_dims(fn, T, H, E, k, I)) return st;
+  if (int st = check_mx_dims(fn, H, I)) return st;
+  if (n_local < 1 || e_begin < 0 || e_begin > E - n_local)
+    return fail(MOE_ERR_INVALID_ARG, "%s: local experts [%d, %d + %d) outside [0, E=%d)", fn, e_begin, e_begin,
+                n_local, E);
+  CHECK_PTR(x, 16);
+  CHECK_PTR(Wr, 16);
+  CHECK_PTR(br, 2);
+  CHECK_PTR(Wgu_q, 16);
+  CHECK_PTR(Wgu_s, 16);
+  CHECK_PTR(bgu, 4);
+  CHECK_PTR(Wd_q, 16);
+  CHECK_PTR(Wd_s, 16);
+  CHECK_PTR(bd, 4);
+  CHECK_PTR(y, 16);
+  if (topk_ids_out && !aligned(topk_ids_out, 4))
+    return fail(MOE_ERR_INVALID_ARG, "%s: topk_ids_out is not 4-byte aligned", fn);
+  if (topk_w_out && !aligned(topk_w_out, 4))
+    return fail(MOE_ERR_INVALID_ARG, "%s: topk_w_out is not 4-byte aligned", fn);
+  if (n_valid && !aligned(n_valid, 4)) return fail(MOE_ERR_INVALID_ARG, "%s: n_valid is not 4-byte aligned", fn);
+  if (expert_counts_out && !aligned(expert_counts_out, 4))
+    return fail(MOE_ERR_INVALID_ARG, "%s: expert_counts_out is not 4-byte aligned", fn);
+  if (path < MOE_PATH_AUTO || path > MOE_PATH_GEMM)
+    return fail(MOE_ERR_INVALID_ARG, "%s: unknown path %d", fn, path);
+  if (int st = check_rows(fn, "x", T, H)) return st;
+  if (int st = check_w4a4_rows(fn, "h", T * k, I)) return st;
+  if (T == 0) return ok();
+  const W4a4Layout F = w4a4_layout(T, H, E, k, I);
+  if (workspace == nullptr || workspace_bytes < F.total)
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace of %zu bytes given, %zu needed", fn,
+                workspace ? workspace_bytes : (size_t)0, F.total);
+  if (!aligned(workspace, 256))
+    return fail(MOE_ERR_INVALID_ARG, "%s: workspace is not 256-byte aligned", fn);
+
+  char* ws = static_cast<char*>(workspace);
+  const Layout& L = F.base;
+  int32_t* ids = topk_ids_out ? topk_ids_out : reinterpret_cast<int32_t*>(ws + L.ids);
+  float* w = topk_w_out ? topk_w_out : reinterpret_cast<float*>(ws + L.w);
+  int32_t* cnt = expert_counts_out ? expert_counts_out : reinterpret_cast<int32_t*>(ws + L.cnt);
+  int32_t* off = reinterpret_cast<int32_t*>(ws + L.off);
+  int32_t* rows = reinterpret_cast<int32_t*>(ws + L.rows);
+  int32_t* pos = reinterpret_cast<int32_t*>(ws + L.pos);
+  float* o = reinterpret_cast<float*>(ws + L.o);
+  void *xq = ws + F.xq, *sx = ws + F.sx, *hq = ws + F.hq, *sh = ws + F.sh;
+  hipStream_t s = (hipStream_t)stream;
+
+  if (int st = route_and_permute(fn, x, Wr, br, T, H, E, k, n_valid, e_begin, n_local, o, ids, w, cnt, off, rows, pos, s))
+    return st;
+  if (int st = hip_status(fn, moe::launch_mxfp4_rows(x, T, H, xq, sx, s))) return st;
+  if (int st = run_gate_up_w4a4(fn, xq, sx, Wgu_q, Wgu_s, bgu, cnt, off, rows, T, H, n_local, k, I, hq, sh, path, s))
+    return st;
+  if (int st = run_down_w4a4(fn, hq, sh, Wd_q, Wd_s, bd, cnt, off, T, H, n_local, k, I, o, path, s)) return st;
+  if (int st = hip_status(fn, moe::launch_combine(o, pos, w, T, H, k, y, s, partial))) return st;
+  return ok();
+}
+
+int moe_forward_w4a4(const void* x, const void* Wr, const void* br, const void* Wgu_q, const void* Wgu_s,
+                     const void* bgu, const void* Wd_q, const void* Wd_s, const void* bd, int64_t T, int32_t H,
+                     int32_t E, int32_t k, int32_t I, void* y, int32_t* topk_ids_out, float* topk_w_out,
+                     void* workspace, size_t workspace_bytes, int32_t path, void* stream) {
+  return forward_w4a4("moe_forward_w4a4", x, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, T, H, E, k, I, 0, E, nullptr,
+                      y, false, topk_ids_out, topk_w_out, nullptr, workspace, workspace_bytes, path, stream);
+}
+
+int moe_forward_padded_w4a4(const void* x, const void* Wr, const void* br, const void* Wgu_q, const void* Wgu_s,
+                            const void* bgu, const void* Wd_q, const void* Wd_s, const void* bd, int64_t T, int32_t H,
+                            int32_t E, int32_t k, int32_t I, const int32_t* n_valid, void* y, int32_t* topk_ids_out,
+                            float* topk_w_out, int32_t* expert_counts_out, void* workspace, size_t workspace_bytes,
+                            int32_t path, void* stream) {
+  return forward_w4a4("moe_forward_padded_w4a4", x, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, T, H, E, k, I, 0, E,
+                      n_valid, y, false, topk_ids_out, topk_w_out, expert_counts_out, workspace, workspace_bytes, path,
+                      stream);
+}
+
+int moe_forward_ep_w4a4(const void* x, const void* Wr, const void* br, const void* Wgu_q_local, const void* Wgu_s_local,
+                        const void* bgu_local, const void* Wd_q_local, const void* Wd_s_local, const void* bd_local,
+                        int64_t T, int32_t H, int32_t E, int32_t k, int32_t I, int32_t e_begin, int32_t n_local,
+                        float* y_partial, int32_t* topk_ids_out, float* topk_w_out, void* workspace,
+                        size_t workspace_bytes, int32_t path, void* stream) {
+  return forward_w4a4("moe_forward_ep_w4a4", x, Wr, br, Wgu_q_local, Wgu_s_local, bgu_local, Wd_q_local, Wd_s_local,
+                      bd_local, T, H, E, k, I, e_begin, n_local, nullptr, y_partial, true, topk_ids_out, topk_w_out,
+                      nullptr, workspace, workspace_bytes, path, stream);
+}
+
+int moe_gate_up_w4a4(const void* xq, const void* sx, const void* Wgu_q, const void* Wgu_s, const void* bgu,
+                     const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T, int32_t H, int32_t E,
+                     int32_t k, int32_t I, void* hq, void* sh, int32_t path, void* stream) {
+  const char* fn = "moe_gate_up_w4a4";
+  if (int st = check_dims(fn, T, H, E, k, I)) return st;
+  if (int st = check_mx_dims(fn, H, I)) return st;
+  CHECK_PTR(xq, 16);
+  CHECK_PTR(sx, 4);
+  CHECK_PTR(Wgu_q, 16);
+  CHECK_PTR(Wgu_s, 16);
+  CHECK_PTR(bgu, 4);
+  CHECK_PTR(cnt, 4);
+  CHECK_PTR(off, 4);
+  CHECK_PTR(rows, 4);
+  CHECK_PTR(hq, 16);
+  CHECK_PTR(sh, 4);
+  if (path < MOE_PATH_AUTO || path > MOE_PATH_GEMM)
+    return fail(MOE_ERR_INVALID_ARG, "%s: unknown path %d", fn, path);
+  if (int st = check_w4a4_rows(fn, "x", T, H)) return st;
+  if (int st = check_w4a4_rows(fn, "h", T * k, I)) return st;
+  if (T == 0) return ok();
+  if (int st = run_gate_up_w4a4(fn, xq, sx, Wgu_q, Wgu_s, bgu, cnt, off, rows, T, H, E, k, I, hq, sh, path,
+                                (hipStream_t)stream))
+    return st;
+  return ok();
+}
+
+int moe_down_w4a4(const void* hq, const void* sh, const void* Wd_q, const void* Wd_s, const void* bd,
+                  const int32_t* cnt, const int32_t* off, int64_t T, int32_t H, int32_t E, int32_t k, int32_t I,
+                  float* o, int32_t path, void* stream) {
+  const char* fn = "moe_down_w4a4";
+  if (int st = check_dims(fn, T, H, E, k, I)) return st;
+  if (int st = check_mx_dims(fn, H, I)) return st;
+  CHECK_PTR(hq, 16);
+  CHECK_PTR(sh, 4);
+  CHECK_PTR(Wd_q, 16);
+  CHECK_PTR(Wd_s, 16);
+  CHECK_PTR(bd, 4);
+  CHECK_PTR(cnt, 4);
+  CHECK_PTR(off, 4);
+  CHECK_PTR(o, 16);
+  if (path < MOE_PATH_AUTO || path > MOE_PATH_GEMM)
+    return fail(MOE_ERR_INVALID_ARG, "%s: unknown path %d", fn, path);
+  if (int st = check_w4a4_rows(fn, "h", T * k, I)) return st;
+  if (T == 0) return ok();
+  if (int st = run_down_w4a4(fn, hq, sh, Wd_q, Wd_s, bd, cnt, off, T, H, E, k, I, o, path, (hipStream_t)stream))
+    return st;
+  return ok();
+}
+
+// ---------------------------------------------------------------------------
 // measurement probes
 // ---------------------------------------------------------------------------
 int moe_probe_mfma_bf16(int32_t iters, int32_t workgroups, float* out, void* stream) {

@@ -17,6 +17,7 @@
 // magnitudes are 0, 0.5, 1, 1.5, 2, 3, 4, 6.
 #include "device_common.h"
 #include "launch.h"
+#include "mxfp4_device.h"
 
 namespace moe {
 namespace {
@@ -118,26 +119,6 @@ constexpr int kMxWaves = 4;
 constexpr int kMxNJ = 4;                 // columns per lane (calls j)
 constexpr int kMxCols = 16 * kMxNJ;      // 64 columns per workgroup
 constexpr int64_t kMxOneChunkMeanRows = 10;
-
-typedef __bf16 bf16x2_v __attribute__((ext_vector_type(2)));
-
-// UE8M0 byte -> float32 scale 2^(s - 127) (s = 0 is the subnormal 2^-127, 255 NaN)
-__device__ __forceinline__ float ue8m0_to_f32(uint32_t s) {
-  uint32_t u = s << 23;
-  u = s == 0 ? 0x00400000u : u;
-  u = s == 255 ? 0x7FC00000u : u;
-  return __uint_as_float(u);
-}
-
-// eight E2M1 codes (one dword, k = 0..7 from the low nibble up) -> eight bf16 * scale
-__device__ __forceinline__ u32x4_t dequant8(uint32_t w, float s) {
-  const bf16x2_v a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0);
-  const bf16x2_v b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1);
-  const bf16x2_v c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2);
-  const bf16x2_v d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3);
-  return u32x4_t{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, c),
-                 __builtin_bit_cast(uint32_t, d)};
-}
 
 // one double step's weight loads: 8 coalesced code pieces and the scales of
 // the lane's two blocks (u = 0, 1)

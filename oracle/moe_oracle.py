@@ -561,6 +561,48 @@ def moe_forward_norm_fp8(x, residual, gamma, eps, Wr, br, Wgu_q, Wgu_s, bgu, Wd_
 
 
 # --------------------------------------------------------------------------
+# MXFP4 on both sides (W4A4): rows in the format of the weights, the scales of
+# four neighbouring blocks of a row side by side.  Readings:
+#   A1  a row block is quantised as a weight block (M1-M3); one that holds a
+#       NaN or an infinity takes scale 255 and codes 0, and is NaN as a whole;
+#   A2  x is quantised as it is; h is rounded to bf16, the type activations are
+#       kept in, and then quantised.
+# --------------------------------------------------------------------------
+def mxfp4_quantize_rows(a):
+    """float [R][K] (K % 32 == 0) -> (codes uint8 [R][K/2], scales uint8 [ceil(K/128)][R][4])."""
+    a = np.asarray(a, dtype=np.float64)
+    R, K = a.shape
+    bad = ~np.isfinite(a.reshape(R, K // 32, 32)).all(axis=2)                   # [R][K/32]
+    codes, s = mxfp4_quantize(np.where(np.repeat(bad, 32, axis=1), 0.0, a))     # s [K/32][R]
+    scales = np.zeros((-(-K // 128) * 4, R), np.uint8)
+    scales[:K // 32] = np.where(bad.T, 255, s)
+    return codes, np.ascontiguousarray(scales.reshape(-1, 4, R).transpose(0, 2, 1))
+
+
+def mxfp4_dequantize_rows(codes, scales):
+    """codes uint8 [R][K/2], scales uint8 [ceil(K/128)][R][4] -> float64 [R][K]."""
+    nb = codes.shape[1] // 16
+    return mxfp4_dequantize(codes, scales.transpose(0, 2, 1).reshape(-1, codes.shape[0])[:nb])
+
+
+def moe_forward_w4a4(x, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, k: int, experts=None):
+    """The forward with MXFP4 weights and activations; experts: only the slots of these (an expert-parallel share)."""
+    ids, w, _ = route(x, Wr, br, k)
+    xv = mxfp4_dequantize_rows(*mxfp4_quantize_rows(widen(x)))
+    y = np.zeros((x.shape[0], Wd_q.shape[1]))
+    for e in range(Wgu_q.shape[0]) if experts is None else experts:
+        t, j = np.nonzero(ids == e)
+        if not t.size:
+            continue
+        i = e if experts is None else e - experts[0]
+        h = clamped_glu(xv[t] @ mxfp4_dequantize(Wgu_q[i], Wgu_s[i]).T + widen(bgu[i]))
+        h = mxfp4_dequantize_rows(*mxfp4_quantize_rows(bf16_round(h)))
+        o = h @ mxfp4_dequantize(Wd_q[i], Wd_s[i]).T + widen(bd[i])
+        np.add.at(y, t, w[t, j][:, None] * o)
+    return {"y": y, "ids": ids, "w": w}
+
+
+# --------------------------------------------------------------------------
 # Second formulation: every expert on every token, then select (the dense
 # "replicate to all local experts" pipeline of section 2).  Small shapes only.
 # --------------------------------------------------------------------------
