@@ -726,6 +726,45 @@ MOE_API int moe_down_w4a4(const void* hq, const void* sh, const void* Wd_q, cons
                           int64_t T, int32_t H, int32_t E, int32_t k, int32_t I, float* o,
                           int32_t path, void* stream);
 
+/*
+ * moe_backward -- the gradients of moe_forward (bf16 weights): for a loss whose
+ * gradient with respect to y is dy, from the inputs of the forward call and the
+ * routing decision it left.  gate, up and h are recomputed; nothing but
+ * topk_ids and topk_w is kept from the forward pass.
+ *
+ *   dy   bf16 [T][H]         gradient of y
+ *   x, Wr, Wgu, bgu, Wd, bd  as given to moe_forward
+ *   topk_ids int32 [T][k], topk_w float [T][k]   as moe_forward (or moe_route,
+ *                            moe_forward_padded) returned them.  A slot whose id
+ *                            lies outside [0, E) is skipped (a padding token
+ *                            gets dx = 0 and adds nothing); the ids of a row are
+ *                            otherwise different.
+ *   dx   bf16 [T][H]    out  through the experts and through the router
+ *   dWr  bf16 [E][H], dbr bf16 [E]   out, both NULL to skip
+ *   dWgu bf16 [E][H][2I], dbgu bf16 [E][2I], dWd bf16 [E][I][H], dbd bf16 [E][H]
+ *                       out, all four NULL to skip; an expert without slots gets 0
+ * Formulas (e, w, slot s of token t; z = sigmoid(1.702 g), g and u clamped):
+ *   d = dy . Wd[e]^T;  h = (u + 1) g z;  dw = h . d + bd[e] . dy
+ *   dgate = w d (u + 1) z (1 + 1.702 g (1 - z)), 0 where gate > 7
+ *   dup   = w d g z, 0 where up > 7 or up < -7
+ *   dl_j  = w_j (dw_j - sum_i w_i dw_i)
+ *   dx[t] = sum_j [dgate, dup]_j . Wgu[e_j]^T + dl_j Wr[e_j]
+ *   dWgu[e] = sum x^T [dgate, dup], dWd[e] = sum (w h)^T dy, dWr[e] = sum dl x,
+ *   and the biases' gradients the sums of [dgate, dup], w dy and dl.
+ * bf16 operands ([dgate, dup] and w h are rounded to bf16), float32 sums in a
+ * fixed order, each gradient rounded once to bf16 (not accumulated into).
+ * Outputs overlap neither inputs nor each other nor the workspace
+ * (MOE_ERR_INVALID_ARG, as far as it is checked: outputs against inputs and each
+ * other).  x and dy must take less than 2 GiB each (MOE_ERR_UNSUPPORTED).  T = 0
+ * is a valid call that enqueues nothing: the weights' gradients stay as they are.
+ */
+MOE_API size_t moe_workspace_bytes_backward(int64_t T, int32_t H, int32_t E, int32_t k, int32_t I);
+MOE_API int moe_backward(const void* dy, const void* x, const void* Wr, const void* Wgu, const void* bgu,
+                         const void* Wd, const void* bd, const int32_t* topk_ids, const float* topk_w,
+                         int64_t T, int32_t H, int32_t E, int32_t k, int32_t I,
+                         void* dx, void* dWr, void* dbr, void* dWgu, void* dbgu, void* dWd, void* dbd,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---------------------------------------------------------------------------
  * Measurement probes.  They are not part of the block: they measure what a
  * plain hand-written kernel gets from the matrix cores and from HBM on this

@@ -36,7 +36,8 @@ EXPORTS = ("moe_abi_version", "moe_status_str", "moe_last_error", "moe_workspace
            "moe_quantize_int4", "moe_pack_int4", "moe_forward_int4", "moe_forward_int4_ex", "moe_gate_up_int4",
            "moe_down_int4", "moe_forward_padded_int4", "moe_forward_ep_int4",
            "moe_quantize_rows_mxfp4", "moe_dequantize_rows_mxfp4", "moe_workspace_bytes_w4a4", "moe_forward_w4a4",
-           "moe_forward_padded_w4a4", "moe_forward_ep_w4a4", "moe_gate_up_w4a4", "moe_down_w4a4")
+           "moe_forward_padded_w4a4", "moe_forward_ep_w4a4", "moe_gate_up_w4a4", "moe_down_w4a4",
+           "moe_workspace_bytes_backward", "moe_backward")
 
 
 class MoEError(RuntimeError):
@@ -107,6 +108,8 @@ _SIGS = {
     "moe_forward_w4a4": (ctypes.c_int, [_vp] * 9 + [_i64] + [_i32] * 4 + [_vp] * 4 + [_sz, _i32, _vp]),
     "moe_forward_padded_w4a4": (ctypes.c_int, [_vp] * 9 + [_i64] + [_i32] * 4 + [_vp] * 6 + [_sz, _i32, _vp]),
     "moe_forward_ep_w4a4": (ctypes.c_int, [_vp] * 9 + [_i64] + [_i32] * 6 + [_vp] * 4 + [_sz, _i32, _vp]),
+    "moe_workspace_bytes_backward": (_sz, [_i64, _i32, _i32, _i32, _i32]),
+    "moe_backward": (ctypes.c_int, [_vp] * 9 + [_i64] + [_i32] * 4 + [_vp] * 8 + [_sz, _vp]),
     "moe_gate_up_w4a4": (ctypes.c_int, [_vp] * 8 + [_i64] + [_i32] * 4 + [_vp, _vp, _i32, _vp]),
     "moe_down_w4a4": (ctypes.c_int, [_vp] * 7 + [_i64] + [_i32] * 4 + [_vp, _i32, _vp]),
 }
@@ -1278,6 +1281,64 @@ def moe_down_w4a4(hq, sh, Wd_q, Wd_s, bd, cnt, off, T: int, k: int, o=None, path
     st = library().moe_down_w4a4(*a[:7], T, H, E, k, I, a[7], path_code(path), here)
     _check(st, "moe_down_w4a4")
     return o if o.shape[0] == T * k else o[:T * k]
+
+
+# ---------------------------------------------------------------------------
+# the backward pass of the block with bf16 weights
+# ---------------------------------------------------------------------------
+def workspace_bytes_backward(T: int, H: int, E: int, k: int, I: int) -> int:
+    return int(library().moe_workspace_bytes_backward(T, H, E, k, I))
+
+
+def alloc_workspace_backward(T: int, H: int, E: int, k: int, I: int, device=None) -> torch.Tensor:
+    n = workspace_bytes_backward(T, H, E, k, I)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device or "cuda")
+
+
+def moe_backward(dy, x, Wr, Wgu, bgu, Wd, bd, topk_ids, topk_w, router=True, experts=True, dx=None, dWr=None, dbr=None,
+                 dWgu=None, dbgu=None, dWd=None, dbd=None, workspace=None, stream=None):
+    """Gradients of moe_forward for the gradient dy of y; topk_ids and topk_w as the forward call left them.  Returns a
+    dict of bf16 tensors: dx; dWr and dbr unless router is False; dWgu, dbgu, dWd and dbd unless experts is False
+    (frozen weights: their products are not run).  No tokens: the weights' gradients are 0."""
+    _dims(topk_ids, "topk_ids", 2)
+    k = topk_ids.shape[1]
+    _dims(Wr, "Wr", 2)
+    E = Wr.shape[0]
+    T, H, E = _route_args(x, Wr, None, k, topk_ids, topk_w)
+    if topk_w is None:
+        raise MoEError("topk_w: needed")
+    I = _bf16_experts(Wgu, bgu, Wd, bd, E, H)
+    bf16 = torch.bfloat16
+    _req(dy, "dy", (T, H), bf16)
+    shapes = {"dx": (T, H)}
+    if router:
+        shapes |= {"dWr": (E, H), "dbr": (E,)}
+    if experts:
+        shapes |= {"dWgu": (E, H, 2 * I), "dbgu": (E, 2 * I), "dWd": (E, I, H), "dbd": (E, H)}
+    grads = {"dx": dx, "dWr": dWr, "dbr": dbr, "dWgu": dWgu, "dbgu": dbgu, "dWd": dWd, "dbd": dbd}
+    for name, g in grads.items():
+        if g is not None:
+            if name not in shapes:
+                raise MoEError(f"{name}: given, but not asked for")
+            _req(g, name, shapes[name], bf16)
+    here = _place(x, stream)
+    if here is None:
+        with _on(x, stream):
+            return moe_backward(dy, x, Wr, Wgu, bgu, Wd, bd, topk_ids, topk_w, router, experts, dx, dWr, dbr, dWgu, dbgu,
+                                dWd, dbd, workspace)
+    for name, shape in shapes.items():
+        if grads[name] is None:
+            grads[name] = torch.empty(shape, dtype=bf16, device=x.device)
+    if workspace is None:
+        workspace = alloc_workspace_backward(T, H, E, k, I, x.device)
+    a = _ats(x, dy, Wr, Wgu, bgu, Wd, bd, topk_ids, topk_w, *grads.values(), workspace)
+    st = library().moe_backward(a[1], a[0], *a[2:9], T, H, E, k, I, *a[9:17], workspace.numel() * workspace.element_size(),
+                                here)
+    _check(st, "moe_backward")
+    if T == 0:
+        for name in shapes:
+            grads[name].zero_()
+    return {name: grads[name] for name in shapes}
 
 
 # ---------------------------------------------------------------------------

@@ -1521,6 +1521,131 @@ int moe_down_w4a4(const void* hq, const void* sh, const void* Wd_q, const void* 
 }
 
 // ---------------------------------------------------------------------------
+// The backward pass
+// ---------------------------------------------------------------------------
+struct BackwardLayout {
+  size_t cnt, off, rows, pos, dw_part, dl, wide, wh, dgu, total;
+};
+
+// d [S][I] and dxs [S][H] share `wide`: d is read for the last time before dxs
+// is first written.
+static BackwardLayout backward_layout(int64_t T, int32_t H, int32_t E, int32_t k, int32_t I) {
+  BackwardLayout L;
+  const size_t S = (size_t)T * k;
+  size_t cur = 0;
+  L.cnt = take(cur, (size_t)E * 4);
+  L.off = take(cur, (size_t)(E + 1) * 4);
+  L.rows = take(cur, S * 4);
+  L.pos = take(cur, S * 4);
+  L.dw_part = take(cur, S * moe::backward_dw_parts(I) * 4);
+  L.dl = take(cur, S * 4);
+  L.wide = take(cur, S * (H > I ? H : I) * 4);
+  L.wh = take(cur, S * I * 2);
+  L.dgu = take(cur, S * I * 4);
+  L.total = cur;
+  return L;
+}
+
+size_t moe_workspace_bytes_backward(int64_t T, int32_t H, int32_t E, int32_t k, int32_t I) {
+  if (check_dims("moe_workspace_bytes_backward", T, H, E, k, I) != MOE_OK) return 0;
+  if (T == 0) return 0;
+  return backward_layout(T, H, E, k, I).total;
+}
+
+int moe_backward(const void* dy, const void* x, const void* Wr, const void* Wgu, const void* bgu, const void* Wd,
+                 const void* bd, const int32_t* topk_ids, const float* topk_w, int64_t T, int32_t H, int32_t E,
+                 int32_t k, int32_t I, void* dx, void* dWr, void* dbr, void* dWgu, void* dbgu, void* dWd, void* dbd,
+                 void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_backward";
+  if (int st = check_dims(fn, T, H, E, k, I)) return st;
+  CHECK_PTR(dy, 16);
+  CHECK_PTR(x, 16);
+  CHECK_PTR(Wr, 16);
+  CHECK_PTR(Wgu, 16);
+  CHECK_PTR(bgu, 4);
+  CHECK_PTR(Wd, 16);
+  CHECK_PTR(bd, 16);
+  CHECK_PTR(topk_ids, 4);
+  CHECK_PTR(topk_w, 4);
+  CHECK_PTR(dx, 16);
+  if ((dWr == nullptr) != (dbr == nullptr))
+    return fail(MOE_ERR_INVALID_ARG, "%s: dWr and dbr are both given or both NULL", fn);
+  const bool experts = dWgu != nullptr;
+  if ((dbgu != nullptr) != experts || (dWd != nullptr) != experts || (dbd != nullptr) != experts)
+    return fail(MOE_ERR_INVALID_ARG, "%s: dWgu, dbgu, dWd and dbd are all given or all NULL", fn);
+  if (dWr) {
+    CHECK_PTR(dWr, 16);
+    CHECK_PTR(dbr, 2);
+  }
+  if (experts) {
+    CHECK_PTR(dWgu, 16);
+    CHECK_PTR(dbgu, 16);
+    CHECK_PTR(dWd, 16);
+    CHECK_PTR(dbd, 16);
+  }
+  const size_t row = (size_t)T * H * 2, S = (size_t)T * k, wgu = (size_t)E * H * I * 4;
+  const struct { const char* name; const void* p; size_t n; } ins[] = {
+      {"dy", dy, row}, {"x", x, row}, {"Wr", Wr, (size_t)E * H * 2}, {"Wgu", Wgu, wgu}, {"bgu", bgu, (size_t)E * I * 4},
+      {"Wd", Wd, wgu / 2}, {"bd", bd, (size_t)E * H * 2}, {"topk_ids", topk_ids, S * 4}, {"topk_w", topk_w, S * 4}};
+  const struct { const char* name; const void* p; size_t n; } outs[] = {
+      {"dx", dx, row}, {"dWr", dWr, (size_t)E * H * 2}, {"dbr", dbr, (size_t)E * 2}, {"dWgu", dWgu, wgu},
+      {"dbgu", dbgu, (size_t)E * I * 4}, {"dWd", dWd, wgu / 2}, {"dbd", dbd, (size_t)E * H * 2}};
+  for (int i = 0; i < 7; ++i) {
+    if (!outs[i].p) continue;
+    for (const auto& in : ins)
+      if (!disjoint(outs[i].p, outs[i].n, in.p, in.n))
+        return fail(MOE_ERR_INVALID_ARG, "%s: %s overlaps %s", fn, outs[i].name, in.name);
+    for (int j = 0; j < i; ++j)
+      if (outs[j].p && !disjoint(outs[i].p, outs[i].n, outs[j].p, outs[j].n))
+        return fail(MOE_ERR_INVALID_ARG, "%s: %s overlaps %s", fn, outs[i].name, outs[j].name);
+  }
+  // the products gather rows of x and dy with 31-bit byte offsets
+  if (T * (int64_t)H * 2 >= (int64_t)1 << 31)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: x and dy of %lld rows of %d take 2 GiB or more: split the batch", fn,
+                (long long)T, H);
+  if (T == 0) return ok();
+  const BackwardLayout L = backward_layout(T, H, E, k, I);
+  if (workspace == nullptr || workspace_bytes < L.total)
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace of %zu bytes given, %zu needed", fn,
+                workspace ? workspace_bytes : (size_t)0, L.total);
+  if (!aligned(workspace, 256))
+    return fail(MOE_ERR_INVALID_ARG, "%s: workspace is not 256-byte aligned", fn);
+
+  char* ws = static_cast<char*>(workspace);
+  int32_t* cnt = reinterpret_cast<int32_t*>(ws + L.cnt);
+  int32_t* off = reinterpret_cast<int32_t*>(ws + L.off);
+  int32_t* rows = reinterpret_cast<int32_t*>(ws + L.rows);
+  int32_t* pos = reinterpret_cast<int32_t*>(ws + L.pos);
+  float* dw_part = reinterpret_cast<float*>(ws + L.dw_part);
+  float* dl = reinterpret_cast<float*>(ws + L.dl);
+  float* wide = reinterpret_cast<float*>(ws + L.wide);
+  void *wh = ws + L.wh, *dgu = ws + L.dgu;
+  hipStream_t s = (hipStream_t)stream;
+
+  if (int st = hip_status(fn, moe::launch_permute(topk_ids, T, E, k, cnt, off, rows, pos, s))) return st;
+  if (int st = hip_status(fn, moe::launch_backward_d(dy, Wd, cnt, off, rows, T, H, E, k, I, wide, s))) return st;
+  if (int st = hip_status(fn, moe::launch_backward_gu(x, Wgu, bgu, topk_w, wide, cnt, off, rows, T, H, E, k, I, dgu, wh,
+                                                      dw_part, s)))
+    return st;
+  if (int st = hip_status(fn, moe::launch_backward_dl(dy, bd, topk_ids, pos, topk_w, dw_part,
+                                                      moe::backward_dw_parts(I), T, H, k, dl, s)))
+    return st;
+  if (int st = hip_status(fn, moe::launch_backward_dx(dgu, Wgu, cnt, off, T, H, E, k, I, wide, s))) return st;
+  if (experts) {
+    if (int st = hip_status(fn, moe::launch_backward_wgu(x, dgu, cnt, off, rows, T, H, E, k, I, dWgu, s))) return st;
+    if (int st = hip_status(fn, moe::launch_backward_wd(wh, dy, cnt, off, rows, T, H, E, k, I, dWd, s))) return st;
+    if (int st = hip_status(fn, moe::launch_backward_column_sum(dgu, nullptr, cnt, off, rows, E, 2 * I, k, dbgu, nullptr, s)))
+      return st;
+    if (int st = hip_status(fn, moe::launch_backward_column_sum(dy, topk_w, cnt, off, rows, E, H, k, dbd, nullptr, s)))
+      return st;
+  }
+  if (dWr)
+    if (int st = hip_status(fn, moe::launch_backward_column_sum(x, dl, cnt, off, rows, E, H, k, dWr, dbr, s))) return st;
+  if (int st = hip_status(fn, moe::launch_backward_dx_sum(wide, topk_ids, pos, dl, Wr, T, H, k, dx, s))) return st;
+  return ok();
+}
+
+// ---------------------------------------------------------------------------
 // measurement probes
 // ---------------------------------------------------------------------------
 int moe_probe_mfma_bf16(int32_t iters, int32_t workgroups, float* out, void* stream) {

@@ -603,6 +603,50 @@ def moe_forward_w4a4(x, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, k: int, exper
 
 
 # --------------------------------------------------------------------------
+# The backward pass of the block: gradients for a given dy and routing decision.
+# Readings:
+#   B1  the clamps pass the gradient up to and on their bounds and stop it
+#       beyond (gate above 7; up above 7 or below -7);
+#   B2  the pick of experts has no gradient, the softmax over the picks has;
+#   B3  slots whose id lies outside [0, E) are skipped: they are no term of y,
+#       and their weights' gradients count as 0 in the softmax's.
+# --------------------------------------------------------------------------
+def moe_backward(dy, x, Wr, Wgu, bgu, Wd, bd, ids, w):
+    """Gradients in float64, nothing rounded: a dict of dx, dWr, dbr, dWgu, dbgu, dWd, dbd."""
+    dyv, xv, w = widen(dy), widen(x), np.asarray(w, np.float64)
+    T, H = xv.shape
+    E, I = Wd.shape[:2]
+    g = {"dx": np.zeros((T, H)), "dWr": np.zeros((E, H)), "dbr": np.zeros(E), "dWgu": np.zeros((E, H, 2 * I)),
+         "dbgu": np.zeros((E, 2 * I)), "dWd": np.zeros((E, I, H)), "dbd": np.zeros((E, H))}
+    dw = np.zeros_like(w)
+    for e in range(E):
+        t, j = np.nonzero(ids == e)
+        if not t.size:
+            continue
+        Wg, Wo = widen(Wgu[e]), widen(Wd[e])
+        u = xv[t] @ Wg + widen(bgu[e])
+        gate, up = np.minimum(u[:, 0::2], GLU_LIMIT), np.clip(u[:, 1::2], -GLU_LIMIT, GLU_LIMIT)
+        with np.errstate(over="ignore"):
+            z = 1.0 / (1.0 + np.exp(-GLU_ALPHA * gate))
+        h = (up + 1.0) * gate * z
+        wt = w[t, j][:, None]
+        dw[t, j] = np.sum((h @ Wo + widen(bd[e])) * dyv[t], axis=1)
+        dh = wt * dyv[t] @ Wo.T
+        du = np.empty_like(u)
+        du[:, 0::2] = np.where(u[:, 0::2] > GLU_LIMIT, 0.0, dh * (up + 1.0) * (z + GLU_ALPHA * gate * z * (1.0 - z)))
+        du[:, 1::2] = np.where(np.abs(u[:, 1::2]) > GLU_LIMIT, 0.0, dh * gate * z)
+        np.add.at(g["dx"], t, du @ Wg.T)
+        g["dWgu"][e], g["dbgu"][e] = xv[t].T @ du, du.sum(axis=0)
+        g["dWd"][e], g["dbd"][e] = (wt * h).T @ dyv[t], (wt * dyv[t]).sum(axis=0)
+    dl = w * (dw - np.sum(w * dw, axis=1, keepdims=True))
+    for e in range(E):
+        t, j = np.nonzero(ids == e)
+        np.add.at(g["dx"], t, dl[t, j][:, None] * widen(Wr[e])[None])
+        g["dWr"][e], g["dbr"][e] = dl[t, j] @ xv[t], dl[t, j].sum()
+    return g
+
+
+# --------------------------------------------------------------------------
 # Second formulation: every expert on every token, then select (the dense
 # "replicate to all local experts" pipeline of section 2).  Small shapes only.
 # --------------------------------------------------------------------------
