@@ -76,6 +76,14 @@ hipError_t launch_w4a4_down(const void* hq, const void* sh, const void* Wq, cons
                             const int32_t* cnt, const int32_t* off, int64_t T, int H, int E, int k, int I, float* o,
                             hipStream_t stream);
 
+// the LDS-tiled grouped GEMMs (w4a4_gemm.hip)
+hipError_t launch_gemm_w4a4_gate_up(const void* xq, const void* sx, const void* Wq, const void* Ws, const void* bgu,
+                                    const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T, int H, int E,
+                                    int k, int I, void* hq, void* sh, hipStream_t stream);
+hipError_t launch_gemm_w4a4_down(const void* hq, const void* sh, const void* Wq, const void* Ws, const void* bd,
+                                 const int32_t* cnt, const int32_t* off, int64_t T, int H, int E, int k, int I, float* o,
+                                 hipStream_t stream);
+
 // FP8 W8A8 (OCP E4M3): weight codes [E][N][K] with one float32 scale per
 // expert; activation codes [R][K] with one scale per row (K % 16 == 0)
 // R_live (device int32, optional): only rows below *R_live are quantised
