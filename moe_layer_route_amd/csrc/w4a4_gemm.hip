@@ -35,23 +35,25 @@ namespace {
 #define LDS3 __attribute__((address_space(3)))
 
 constexpr int kThreads = 256;
-constexpr int kTile = 256;
-constexpr int kStage = 256;                    // codes per K stage
-constexpr int kRowBytes = kStage / 2;          // 128
-constexpr int kOpBytes = kTile * kRowBytes;    // 32 KB: one operand of one stage
-constexpr int kA = 0;                          // A of buffer b at b * 32 KB
-constexpr int kB = 2 * kOpBytes;
-constexpr int kAs = 4 * kOpBytes;              // row scales of buffer b: 2 groups x 256 rows x 4 bytes
-constexpr int kAsBytes = 2 * kTile * 4;
-constexpr int kBs = kAs + 2 * kAsBytes;        // weight scales of buffer b: 8 blocks x 256 columns
-constexpr int kBsBytes = 8 * kTile;
-constexpr int kLds = kBs + 2 * kBsBytes;       // 136 KB
+constexpr int kBM = 128, kBN = 256;
+constexpr int kStage = 128;                    // codes per K stage: one word of row scales
+constexpr int kRowBytes = kStage / 2;          // 64
+constexpr int kRing = 3;                       // stage buffers; the loads run kRing - 1 stages ahead
+constexpr int kABytes = kBM * kRowBytes;       // 8 KB
+constexpr int kBBytes = kBN * kRowBytes;       // 16 KB
+constexpr int kA = 0;                          // A of buffer b at b * 8 KB
+constexpr int kB = kRing * kABytes;
+constexpr int kAs = kB + kRing * kBBytes;      // row scales of buffer b: 32 words for each wave, 256 bytes apart
+constexpr int kAsBytes = 1024;
+constexpr int kBs = kAs + kRing * kAsBytes;    // weight scales of buffer b: 4 blocks x 256 columns
+constexpr int kBsBytes = 4 * kBN;
+constexpr int kLds = kBs + kRing * kBsBytes;   // 78 KB: two workgroups a CU
 constexpr int kMBlock = 1024;                  // M tiles per block of the tile order: all of an expert's
 constexpr int kXcds = 8;
 constexpr uint32_t kOOR = 0x80000000u;         // beyond every descriptor's range
 
 template <bool GATE_UP>
-__global__ __launch_bounds__(kThreads, 1) void w4a4_gemm_kernel(
+__global__ __launch_bounds__(kThreads, 2) void w4a4_gemm_kernel(
     const uint8_t* __restrict__ A,       // gate_up: x codes [T][K/2]; down: h codes [S][K/2] (permuted order)
     const uint8_t* __restrict__ As,      // [ceil(K/128)][a_rows][4]
     const uint8_t* __restrict__ Wq,      // [E][N][K/2]
@@ -72,85 +74,86 @@ __global__ __launch_bounds__(kThreads, 1) void w4a4_gemm_kernel(
   const int wm = wave >> 1, wn = wave & 1;
 
   int e, m0, nt;
-  if (!grouped_gemm_tile(cnt, E, kTile, n_tiles, kMBlock, lane, e, m0, nt)) return;   // workgroup-uniform
-  const int n0 = nt * kTile;
+  if (!grouped_gemm_tile(cnt, E, kBM, n_tiles, kMBlock, lane, e, m0, nt)) return;   // workgroup-uniform
+  const int n0 = nt * kBN;
   const int M = cnt[e];
   const int row0 = off[e];
   const int Kb = K / 2;
   const int nblk = K / 32;
-  const int ns = (nblk + 7) / 8;
+  const int ns = (nblk + 3) / 4;
 
-  // ---- direct-load assignments: wave w fills rows 64w .. 64w + 63 of both
-  // tiles, eight rows an instruction; lane l takes row 8i + l / 8 of its
-  // instruction i and chunk c = (l % 8) ^ ((r >> 1) & 7) of it.  What is past the
-  // edges is sent out of range and lands as 0. ----
+  // ---- direct-load assignments: wave w fills rows 32w .. 32w + 31 of A and 64w
+  // .. 64w + 63 of B, sixteen rows an instruction; lane l takes row 16i + l / 4 of
+  // its instruction i and chunk c = (l % 4) ^ ((r >> 2) & 3) of it.  What is past
+  // the edges is sent out of range and lands as 0. ----
   const u32x4_t a_rs = rsrc_words(A, 0x7FFFFFFFu);
   const u32x4_t b_rs = rsrc_words(Wq + (size_t)e * N * Kb, 0x7FFFFFFFu);
   const u32x4_t as_rs = rsrc_words(As, 0x7FFFFFFFu);
   const u32x4_t bs_rs = rsrc_words(Ws + (size_t)e * nblk * N, 0x7FFFFFFFu);
-  const int lc[2] = {(lane & 7) ^ ((lane >> 4) & 7), (lane & 7) ^ (((lane >> 4) + 4) & 7)};  // even, odd i
-  uint32_t a_off[8], b_off[8];
+  const int lc = (lane & 3) ^ ((lane >> 4) & 3);
+  uint32_t a_off[2], b_off[4];
+  auto row_of = [&](int m) {
+    return GATE_UP ? (uint32_t)(rows[row0 + m] / kslots) : (uint32_t)(row0 + m);
+  };
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = 64 * wave + 8 * i + (lane >> 3);
-    const uint32_t c16 = 16u * (uint32_t)lc[i & 1];
-    const int m = m0 + r;
-    if (m < M) {
-      const uint32_t row = GATE_UP ? (uint32_t)(rows[row0 + m] / kslots) : (uint32_t)(row0 + m);
-      a_off[i] = row * (uint32_t)Kb + c16;
-    } else {
-      a_off[i] = kOOR;
-    }
-    const int n = n0 + (r & ~127) + 4 * (r & 31) + ((r >> 5) & 3);
-    b_off[i] = n < N ? (uint32_t)n * (uint32_t)Kb + c16 : kOOR;
+  for (int i = 0; i < 2; ++i) {
+    const int m = m0 + 32 * wave + 16 * i + (lane >> 2);
+    a_off[i] = m < M ? row_of(m) * (uint32_t)Kb + 16u * lc : kOOR;
   }
-  // row scales: wave w, group h of the stage: rows 64w + lane
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 64 * wave + 16 * i + (lane >> 2);
+    const int n = n0 + (r & ~127) + 4 * (r & 31) + ((r >> 5) & 3);
+    b_off[i] = n < N ? (uint32_t)n * (uint32_t)Kb + 16u * lc : kOOR;
+  }
+  // row scales: rows 32w + lane of the first 32 lanes (the others fill the gap
+  // behind them); weight scales: block w of the stage, four columns a lane
   uint32_t as_off = kOOR;
   {
-    const int m = m0 + 64 * wave + lane;
-    if (m < M) as_off = 4u * (GATE_UP ? (uint32_t)(rows[row0 + m] / kslots) : (uint32_t)(row0 + m));
+    const int m = m0 + 32 * wave + lane;
+    if (lane < 32 && m < M) as_off = 4u * row_of(m);
   }
-  // weight scales: waves 0 and 1, four blocks each: block 4w + l / 16, 16 columns
-  const int bs_col = n0 + 16 * (lane & 15);
-  const uint32_t bs_off = bs_col < N ? (uint32_t)(4 * (wave & 1) + (lane >> 4)) * (uint32_t)N + (uint32_t)bs_col : kOOR;
+  const uint32_t bs_off = n0 + 4 * lane < N ? (uint32_t)wave * (uint32_t)N + (uint32_t)(n0 + 4 * lane) : kOOR;
 
-  auto dma = [&](int st, int buf, int i, bool b_side) {
+  // eight loads a wave and stage (the waits below count them); a stage past the
+  // last is out of range
+  auto dma = [&](int st, int buf, int i) {   // 0, 1: A; 2 .. 5: B; 6, 7: scales
     const int k0 = st * kRowBytes;
-    const uint32_t base = b_side ? b_off[i] : a_off[i];
-    const uint32_t voff = k0 + 16 * lc[i & 1] < Kb ? base : kOOR;
-    const uint32_t lds = lds0 + (b_side ? kB : kA) + buf * kOpBytes + (64 * wave + 8 * i) * kRowBytes;
-    dma16(b_side ? b_rs : a_rs, voff, (uint32_t)k0, lds);
-  };
-  auto dma_scales = [&](int st, int buf) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int group = 2 * st + h;
-      dma4(as_rs, 4 * group < nblk ? as_off : kOOR, (uint32_t)group * (uint32_t)a_rows * 4u,
-           lds0 + kAs + buf * kAsBytes + h * kTile * 4 + 64 * wave * 4);
-    }
-    if (wave < 2)   // wave-uniform
-      dma16(bs_rs, 8 * st + 4 * wave + (lane >> 4) < nblk ? bs_off : kOOR, (uint32_t)(8 * st) * (uint32_t)N,
-            lds0 + kBs + buf * kBsBytes + wave * 4 * kTile);
+    if (i < 2)
+      dma16(a_rs, k0 + 16 * lc < Kb ? a_off[i] : kOOR, (uint32_t)k0,
+            lds0 + kA + buf * kABytes + (32 * wave + 16 * i) * kRowBytes);
+    else if (i < 6)
+      dma16(b_rs, k0 + 16 * lc < Kb ? b_off[i - 2] : kOOR, (uint32_t)k0,
+            lds0 + kB + buf * kBBytes + (64 * wave + 16 * (i - 2)) * kRowBytes);
+    else if (i == 6)
+      dma4(as_rs, 4 * st < nblk ? as_off : kOOR, (uint32_t)st * (uint32_t)a_rows * 4u,
+           lds0 + kAs + buf * kAsBytes + 256 * wave);
+    else
+      dma4(bs_rs, 4 * st + wave < nblk ? bs_off : kOOR, (uint32_t)(4 * st) * (uint32_t)N,
+           lds0 + kBs + buf * kBsBytes + wave * kBN);
   };
 
-  // ---- fragment reads: step j has chunk j (lanes 0-31) or 4 + j (lanes 32-63) ----
+  // ---- fragment reads: step j has chunk j (lanes 0-31) or 2 + j (lanes 32-63) ----
   const int fr = lane & 31, fg = lane >> 5;
-  uint32_t a_rd[4], b_rd[4];
+  uint32_t a_rd[2], b_rd[2];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t xo = 16u * (uint32_t)((4 * fg + j) ^ ((fr >> 1) & 7));
-    a_rd[j] = (uint32_t)(kA + (128 * wm + fr) * kRowBytes) + xo;
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t xo = 16u * (uint32_t)((2 * fg + j) ^ ((fr >> 2) & 3));
+    a_rd[j] = (uint32_t)(kA + (64 * wm + fr) * kRowBytes) + xo;
     b_rd[j] = (uint32_t)(kB + (128 * wn + fr) * kRowBytes) + xo;
   }
-  auto read_frag = [&](int buf, int j, int q, bool b_side) -> u32x4_t {
-    return *(const LDS3 u32x4_t*)(smem + (b_side ? b_rd[j] : a_rd[j]) + buf * kOpBytes + q * 32 * kRowBytes);
+  auto read_a = [&](int buf, int j, int i) -> u32x4_t {
+    return *(const LDS3 u32x4_t*)(smem + a_rd[j] + buf * kABytes + i * 32 * kRowBytes);
   };
-  const uint32_t as_rd = (uint32_t)(kAs + fg * kTile * 4 + (128 * wm + fr) * 4);
-  const uint32_t bs_rd = (uint32_t)(kBs + 4 * fg * kTile + 128 * wn + 4 * fr);
+  auto read_b = [&](int buf, int j, int q) -> u32x4_t {
+    return *(const LDS3 u32x4_t*)(smem + b_rd[j] + buf * kBBytes + q * 32 * kRowBytes);
+  };
+  const uint32_t as_rd = (uint32_t)(kAs + 512 * wm + fr * 4);
+  const uint32_t bs_rd = (uint32_t)(kBs + 2 * fg * kBN + 128 * wn + 4 * fr);
 
-  f32x16_t acc[4][4];
+  f32x16_t acc[2][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -158,87 +161,88 @@ __global__ __launch_bounds__(kThreads, 1) void w4a4_gemm_kernel(
 
   // a stage's scale words: row block i (byte: step), step j (byte: column block)
   struct Scales {
-    uint32_t a[4], b[4];
+    uint32_t a[2], b[2];
   };
   Scales sc = {}, last;
   auto read_scales = [&](int s, int buf) {
     // no byte past K is used: it is a caller's, and 255 would be a NaN
-    const int live = nblk - 8 * s - 4 * fg;
-    const uint32_t mask = live >= 4 ? 0xFFFFFFFFu : live <= 0 ? 0u : (1u << (8 * live)) - 1u;
+    const int live = nblk - 4 * s;
+    const uint32_t mask = live >= 4 ? 0xFFFFFFFFu : (1u << (8 * live)) - 1u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      sc.a[i] = *(const LDS3 uint32_t*)(smem + as_rd + buf * kAsBytes + i * 32 * 4) & mask;
-      sc.b[i] = *(const LDS3 uint32_t*)(smem + bs_rd + buf * kBsBytes + i * kTile);
+    for (int i = 0; i < 2; ++i) {
+      sc.a[i] = (*(const LDS3 uint32_t*)(smem + as_rd + buf * kAsBytes + i * 256) & mask) >> (16 * fg);
+      sc.b[i] = *(const LDS3 uint32_t*)(smem + bs_rd + buf * kBsBytes + i * kBN);
     }
   };
-  // fragments in the order they are read (a0 b0 a1 b1 ...), each product as soon
-  // as both its operands are there: slot u of four
+  // fragments in the order they are read (a0 b0 a1 b1 b2 b3), two products behind
+  // each, in three slots
 #define MX_MFMA(J, I, Q) acc[I][Q] = mfma_fp4_32<J, Q>(fa[I], fb[Q], acc[I][Q], s4.a[I], s4.b[J])
-#define MX_SLOT(J)                                                            \
-  if (u == 0) {                                                               \
-    MX_MFMA(J, 0, 0); MX_MFMA(J, 0, 1); MX_MFMA(J, 1, 0); MX_MFMA(J, 1, 1);   \
-  } else if (u == 1) {                                                        \
-    MX_MFMA(J, 0, 2); MX_MFMA(J, 1, 2); MX_MFMA(J, 2, 0); MX_MFMA(J, 2, 1);   \
-  } else if (u == 2) {                                                        \
-    MX_MFMA(J, 2, 2); MX_MFMA(J, 0, 3); MX_MFMA(J, 1, 3); MX_MFMA(J, 2, 3);   \
-  } else {                                                                    \
-    MX_MFMA(J, 3, 0); MX_MFMA(J, 3, 1); MX_MFMA(J, 3, 2); MX_MFMA(J, 3, 3);   \
+#define MX_SLOT(J)                                          \
+  if (u == 0) {                                             \
+    MX_MFMA(J, 0, 0);                                       \
+    MX_MFMA(J, 1, 0);                                       \
+  } else if (u == 1) {                                      \
+    MX_MFMA(J, 0, 1); MX_MFMA(J, 1, 1); MX_MFMA(J, 0, 2);   \
+  } else {                                                  \
+    MX_MFMA(J, 1, 2); MX_MFMA(J, 0, 3); MX_MFMA(J, 1, 3);   \
   }
-  auto slot = [&](int j, int u, const u32x4_t (&fa)[4], const u32x4_t (&fb)[4], const Scales& s4) {
+  auto slot = [&](int j, int u, const u32x4_t (&fa)[2], const u32x4_t (&fb)[4], const Scales& s4) {
     if (j == 0) {
       MX_SLOT(0)
-    } else if (j == 1) {
-      MX_SLOT(1)
-    } else if (j == 2) {
-      MX_SLOT(2)
     } else {
-      MX_SLOT(3)
+      MX_SLOT(1)
     }
   };
 
-  // prologue: stage 0 into buffer 0
+  // prologue: stages 0 .. kRing - 2
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    dma(0, 0, i, false);
-    dma(0, 0, i, true);
-  }
-  dma_scales(0, 0);
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  for (int st = 0; st < kRing - 1; ++st)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dma(st, st, i);
+  asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
   __builtin_amdgcn_s_barrier();
 
-  u32x4_t fa0[4], fb0[4], fa1[4], fb1[4];
-  // Step j of stage s in four slots: slot u reads fragments u of both operands
-  // for step j and issues four products of the step before; the slots of the
-  // first two steps also issue the loads of stage s + 1 (past the last: none).
-  auto step = [&](int s, int buf, int j, u32x4_t (&fa_rd)[4], u32x4_t (&fb_rd)[4], const u32x4_t (&fa_mm)[4],
+  u32x4_t fa0[2], fb0[4], fa1[2], fb1[4];
+  // Step j of stage s in three slots: slot u reads two fragments for step j,
+  // issues loads of stage s + kRing - 1 into the buffer that stage s - 1 left at
+  // the last barrier, and products of the step before.
+  auto step = [&](int s, int buf, int nbuf, int j, u32x4_t (&fa_rd)[2], u32x4_t (&fb_rd)[4], const u32x4_t (&fa_mm)[2],
                   const u32x4_t (&fb_mm)[4], const Scales& s4, bool do_mfma) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (j < 2) {
-        dma(s + 1, buf ^ 1, 4 * j + u, false);
-        dma(s + 1, buf ^ 1, 4 * j + u, true);
-        if (j == 1 && u == 3) dma_scales(s + 1, buf ^ 1);
-      }
+    for (int u = 0; u < 3; ++u) {
+      dma(s + kRing - 1, nbuf, 4 * j + u);
+      if (u == 2) dma(s + kRing - 1, nbuf, 4 * j + 3);
       __builtin_amdgcn_sched_barrier(0);
-      fa_rd[u] = read_frag(buf, j, u, false);
-      fb_rd[u] = read_frag(buf, j, u, true);
-      if (do_mfma) slot((j + 3) & 3, u, fa_mm, fb_mm, s4);
+      if (u == 0) {
+        fa_rd[0] = read_a(buf, j, 0);
+        fb_rd[0] = read_b(buf, j, 0);
+      } else if (u == 1) {
+        fa_rd[1] = read_a(buf, j, 1);
+        fb_rd[1] = read_b(buf, j, 1);
+      } else {
+        fb_rd[2] = read_b(buf, j, 2);
+        fb_rd[3] = read_b(buf, j, 3);
+      }
+      if (do_mfma) slot(j ^ 1, u, fa_mm, fb_mm, s4);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
+  int buf = 0, nbuf = kRing - 1;
   for (int s = 0; s < ns; ++s) {
-    const int buf = s & 1;
     last = sc;
     read_scales(s, buf);
-    step(s, buf, 0, fa0, fb0, fa1, fb1, last, s > 0);
-    step(s, buf, 1, fa1, fb1, fa0, fb0, sc, true);
-    step(s, buf, 2, fa0, fb0, fa1, fb1, sc, true);
-    step(s, buf, 3, fa1, fb1, fa0, fb0, sc, true);
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    step(s, buf, nbuf, 0, fa0, fb0, fa1, fb1, last, s > 0);
+    step(s, buf, nbuf, 1, fa1, fb1, fa0, fb0, sc, true);
+    // stage s + 1 has landed when only the loads of the stage behind it are out
+    asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
+    nbuf = buf;
+    buf = buf == kRing - 1 ? 0 : buf + 1;
   }
 #pragma unroll
-  for (int u = 0; u < 4; ++u) slot(3, u, fa1, fb1, sc);
+  for (int u = 0; u < 3; ++u) slot(1, u, fa1, fb1, sc);
+  // the loads past the last stage wrote zeros into LDS that nothing reads; they end before the wave does
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
   // ---- epilogue.  Lane l, element v of block (i, q): row 32i + 8 (v / 4) + 4 (l
   // / 32) + v % 4, column 4 (l % 32) + q of the wave's 128. ----
@@ -255,10 +259,10 @@ __global__ __launch_bounds__(kThreads, 1) void w4a4_gemm_kernel(
     const uint32_t pick = 0x01010101u * (uint32_t)l4 + 0x04000400u;   // bytes l4 of two words, twice
     uint8_t* codes = reinterpret_cast<uint8_t*>(out);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int v4 = 0; v4 < 4; ++v4) {
-        const int m4 = m0 + 128 * wm + 32 * i + 8 * v4 + 4 * fg;     // rows m4 .. m4 + 3
+        const int m4 = m0 + 64 * wm + 32 * i + 8 * v4 + 4 * fg;     // rows m4 .. m4 + 3
         uint32_t c4 = 0, s4 = 0;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -284,10 +288,10 @@ __global__ __launch_bounds__(kThreads, 1) void w4a4_gemm_kernel(
   } else {
     if (ncol >= N) return;                                   // N % 32 == 0: four columns are all in or all out
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
-        const int m = m0 + 128 * wm + 32 * i + 8 * (v >> 2) + 4 * fg + (v & 3);
+        const int m = m0 + 64 * wm + 32 * i + 8 * (v >> 2) + 4 * fg + (v & 3);
         if (m < M)
           *reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(out) + (size_t)(row0 + m) * N + ncol) =
               f32x4_t{acc[i][0][v] + bb[0], acc[i][1][v] + bb[1], acc[i][2][v] + bb[2], acc[i][3][v] + bb[3]};
@@ -302,9 +306,9 @@ hipError_t launch(const void* A, const void* As, const void* Wq, const void* Ws,
   const int64_t S = T * k, a_rows = GATE_UP ? T : S;
   // 32-bit buffer offsets: the token codes and one expert's codes below 2 GiB
   if (a_rows * K / 2 >= ((int64_t)1 << 31) || (int64_t)N * K / 2 >= ((int64_t)1 << 31)) return hipErrorNotSupported;
-  const int n_tiles = (N + kTile - 1) / kTile;
-  // at most sum_e ceil(cnt_e / 256) <= S / 256 + min(E, S) M tiles
-  const int64_t tiles = (S / kTile + (S < E ? S : E)) * n_tiles;
+  const int n_tiles = (N + kBN - 1) / kBN;
+  // at most sum_e ceil(cnt_e / 128) <= S / 128 + min(E, S) M tiles
+  const int64_t tiles = (S / kBM + (S < E ? S : E)) * n_tiles;
   const int64_t grid = (tiles + kXcds - 1) / kXcds * kXcds;
   if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
   hipLaunchKernelGGL((w4a4_gemm_kernel<GATE_UP>), dim3((unsigned)grid), dim3(kThreads), 0, stream, (const uint8_t*)A,
