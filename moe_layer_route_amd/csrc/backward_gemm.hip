@@ -28,12 +28,17 @@
 // buffers of 64 KB; fragments of the second kind are read by the transposing LDS
 // read (ds_read_b64_tr_b16: 16 lanes read 4 k's x 16 columns and each gets the
 // four k's of one column).
+//   Tile heights: an expert's rows are split evenly over its tiles of at most 256,
+//   in steps of 64, and a tile of 64 ni rows has ni row blocks a wave: the loop
+//   is built for each ni.  530 rows cost three tiles of 192 and not of 256.
 //   Stage layout, K contiguous: row r's 16-byte chunk c at slot c ^ ((r >> 1) &
 //   7) of its 128 bytes.  Rows contiguous: run k's 32-byte piece p at p ^ 2 (k &
 //   3) of its 512 bytes: the four k's of a transposing read fall on different
 //   banks.
 #include "device_common.h"
 #include "launch.h"
+
+#include <type_traits>
 
 namespace moe {
 namespace {
@@ -83,6 +88,7 @@ __global__ __launch_bounds__(kThreads, 1) void backward_gemm_kernel(const Args p
   constexpr bool kAT = kWeightGrad, kBT = kWeightGrad || KIND == kGU;   // rows / columns contiguous
   constexpr bool kAGather = KIND == kD || KIND == kGU || KIND == kWGU, kBGather = KIND == kWD;
   __shared__ __align__(1024) char smem_g[4 * kOpBytes];
+  __shared__ float s_w[KIND == kGU ? kTile : 1];   // the rows' routing weights
   LDS3 char* smem = (LDS3 char*)smem_g;
   const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
 
@@ -112,6 +118,19 @@ __global__ __launch_bounds__(kThreads, 1) void backward_gemm_kernel(const Args p
   const int K = kWeightGrad ? rows_e : p.K;
   const int N = p.N;
   const int ns = (K + kBK - 1) / kBK;
+  // the tile's rows: an expert's split evenly over its tiles, in steps of 64
+  int height = kTile;
+  if (!kWeightGrad) {
+    const int tiles = (M + kTile - 1) / kTile;
+    height = (M + 64 * tiles - 1) / (64 * tiles) * 64;
+    m0 = m0 / kTile * height;
+  }
+  const int m_end = min(M, m0 + height);
+  const int ni = (m_end - m0 + 63) / 64;            // row blocks of 32 a wave, 1 .. 4
+  if constexpr (KIND == kGU) {
+    const int m = m0 + tid;
+    s_w[tid] = m < m_end ? p.w[p.rows[row0 + m]] : 0.f;
+  }
 
   // ---- direct-load assignments.  K contiguous: wave w fills rows 64w .. 64w +
   // 63, eight rows an instruction: lane l takes row 8i + l / 8 and the 16-byte
@@ -134,7 +153,7 @@ __global__ __launch_bounds__(kThreads, 1) void backward_gemm_kernel(const Args p
       const int r = 64 * wave + 8 * i + (lane >> 3);
       const uint32_t c16 = 16u * (uint32_t)lc[i & 1];
       const uint32_t row = kAGather ? (uint32_t)(p.rows[row0 + min(m0 + r, M - 1)] / p.kslots) : (uint32_t)r;
-      a_off[i] = m0 + r < M ? row * (uint32_t)K * 2u + c16 : kOOR;
+      a_off[i] = m0 + r < m_end ? row * (uint32_t)K * 2u + c16 : kOOR;
     }
   }
   if (!kBT) {
@@ -151,7 +170,7 @@ __global__ __launch_bounds__(kThreads, 1) void backward_gemm_kernel(const Args p
   for (int par = 0; par < 2; ++par) {
     const int f = 2 * ((2 * par + (lane >> 5)) & 3);
     const int col = 16 * (((lane & 31) >> 1) ^ f) + 8 * (lane & 1);
-    a_col[par] = m0 + col < M ? 2u * (uint32_t)(m0 + col) : kOOR;
+    a_col[par] = m0 + col < m_end ? 2u * (uint32_t)(m0 + col) : kOOR;
     b_col[par] = n0 + col < N ? 2u * (uint32_t)(n0 + col) : kOOR;
   }
   if (kBT && !kWeightGrad) Be += (size_t)e * N * K;                            // Wgu[e] [H][2I]
@@ -204,8 +223,8 @@ __global__ __launch_bounds__(kThreads, 1) void backward_gemm_kernel(const Args p
     const uint32_t xo = 16u * (uint32_t)((2 * j + fg) ^ ((fr >> 1) & 7));
     const int r = (lane & 15) >> 2, half16 = (lane >> 4) & 1;
     const uint32_t run = (uint32_t)(8 * fg + r) * 512u + 8u * (uint32_t)(lane & 3);
-    a_rd[j] = kAT ? (uint32_t)kA + run + 32u * (uint32_t)((8 * wm + 2 * j + half16) ^ (2 * r))
-                  : (uint32_t)(kA + (128 * wm + fr) * 128) + xo;
+    a_rd[j] = kAT ? (uint32_t)kA + run + 32u * (uint32_t)((2 * ni * wm + 2 * j + half16) ^ (2 * r))
+                  : (uint32_t)(kA + (32 * ni * wm + fr) * 128) + xo;
     b_rd[j] = kBT ? (uint32_t)kB + run + 32u * (uint32_t)((8 * wn + 2 * j + half16) ^ (2 * r))
                   : (uint32_t)(kB + (128 * wn + fr) * 128) + xo;
   }
@@ -231,33 +250,17 @@ __global__ __launch_bounds__(kThreads, 1) void backward_gemm_kernel(const Args p
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-  // fragments in the order they are read (a0 b0 a1 b1 ...), each product as soon
-  // as both its operands are there
-  constexpr int kOrd[16][2] = {{0, 0}, {0, 1}, {1, 0}, {1, 1}, {0, 2}, {1, 2}, {2, 0}, {2, 1},
-                               {2, 2}, {0, 3}, {1, 3}, {2, 3}, {3, 0}, {3, 1}, {3, 2}, {3, 3}};
-  auto mfma_at = [&](int t, const u32x4_t (&fa)[4], const u32x4_t (&fb)[4]) {
-    const int i = kOrd[t][0], j = kOrd[t][1];
-    acc[i][j] = mfma32x32x16(fa[i], fb[j], acc[i][j]);
-  };
-
-  if (ns > 0) {
-    // prologue: stage 0 into buffer 0
-    if (kWeightGrad) {
-      tok = tokens(0);
-      tok_next = tokens(1);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      dma(0, 0, i, false);
-      dma(0, 0, i, true);
-    }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-
+  // The loop for NI row blocks.  Step j of a stage in four slots: slot u reads row
+  // fragment u (of the first NI) and column fragment u for step j and issues the
+  // products of row block u of the step before; the slots of the first two steps
+  // also issue the loads of stage s + 1 (past the last: none).
+  auto loop = [&](auto ni_c) {
+    constexpr int NI = decltype(ni_c)::value;
     u32x4_t fa0[4], fb0[4], fa1[4], fb1[4];
-    // Step j of stage s in four slots: slot u reads fragments u of both operands
-    // for step j and issues four products of the step before; the slots of the
-    // first two steps also issue the loads of stage s + 1 (past the last: none).
+    auto multiply = [&](int u, const u32x4_t (&fa)[4], const u32x4_t (&fb)[4]) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[u][j] = mfma32x32x16(fa[u], fb[j], acc[u][j]);
+    };
     auto step = [&](int s, int buf, int j, u32x4_t (&fa_rd)[4], u32x4_t (&fb_rd)[4], const u32x4_t (&fa_mm)[4],
                     const u32x4_t (&fb_mm)[4], bool do_mfma) {
 #pragma unroll
@@ -267,12 +270,9 @@ __global__ __launch_bounds__(kThreads, 1) void backward_gemm_kernel(const Args p
           dma(s + 1, buf ^ 1, 4 * j + u, true);
         }
         __builtin_amdgcn_sched_barrier(0);
-        fa_rd[u] = read_a(buf, j, u);
+        if (u < NI) fa_rd[u] = read_a(buf, j, u);
         fb_rd[u] = read_b(buf, j, u);
-        if (do_mfma) {
-#pragma unroll
-          for (int t = 4 * u; t < 4 * u + 4; ++t) mfma_at(t, fa_mm, fb_mm);
-        }
+        if (u < NI && do_mfma) multiply(u, fa_mm, fb_mm);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
@@ -290,52 +290,106 @@ __global__ __launch_bounds__(kThreads, 1) void backward_gemm_kernel(const Args p
       __builtin_amdgcn_s_barrier();
     }
 #pragma unroll
-    for (int t = 0; t < 16; ++t) mfma_at(t, fa1, fb1);
+    for (int u = 0; u < NI; ++u) multiply(u, fa1, fb1);
+  };
+  if (ns > 0) {
+    // prologue: stage 0 into buffer 0
+    if (kWeightGrad) {
+      tok = tokens(0);
+      tok_next = tokens(1);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      dma(0, 0, i, false);
+      dma(0, 0, i, true);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    if (ni == 4) loop(std::integral_constant<int, 4>{});
+    else if (ni == 3) loop(std::integral_constant<int, 3>{});
+    else if (ni == 2) loop(std::integral_constant<int, 2>{});
+    else loop(std::integral_constant<int, 1>{});
   }
 
   // ---- epilogue.  Lane l, element v of block (i, j): row 32i + 8 (v / 4) + 4 (l
-  // / 32) + v % 4, column 32j + l % 32.  Where a pair of columns belongs
-  // together, lanes l and l ^ 1 exchange halves of two rows: the even lane gets
-  // both columns of row v, the odd one those of row v + 1. ----
+  // / 32) + v % 4 of the wave's, column 32j + l % 32 of its 128.  Where a pair of
+  // columns belongs together, lanes l and l ^ 1 exchange halves of two rows: the
+  // even lane gets both columns of row v, the odd one those of row v + 1.
+  // bf16 results go through LDS (the stage buffers are free behind the last
+  // barrier), whose rows of 512 bytes then leave whole: 16-byte chunk c of row r
+  // at c ^ 4 (r % 2 + 2 (r / 4 % 2)), as the four rows that a wave touches at once
+  // would otherwise share their banks. ----
+  const int row_w = 32 * ni * wm + 4 * fg;       // + 32 i + 8 (v / 4) + v % 4
   const bool odd = lane & 1;
   auto pair_of = [&](float v0, float v1, float& first, float& second) {
     const float got = xor1(odd ? v0 : v1);
     first = odd ? got : v0;
     second = odd ? v1 : got;
   };
+  auto swizzle = [](int r) { return 4 * ((r & 1) + 2 * ((r >> 2) & 1)); };
+  // word w (a pair of bf16, or a float) of row r: 128 words a row
+  auto word_at = [&](int r, int w) { return (uint32_t)(r * 512 + 16 * ((w >> 2) ^ swizzle(r)) + 4 * (w & 3)); };
+  // rows of 256 bf16 from LDS to out, which points at row m0, column n0
+  auto flush = [&](bf16_t* out, int ld) {
+#pragma unroll 8
+    for (int i = 0; i < 32; ++i) {
+      const int r = 64 * wave + 2 * i + (lane >> 5);
+      const int c = 8 * ((lane & 31) ^ swizzle(r));
+      const u32x4_t v = *(const LDS3 u32x4_t*)(smem + r * 512 + 16 * (lane & 31));
+      if (m0 + r < m_end && n0 + c < N) *reinterpret_cast<u32x4_t*>(out + (size_t)r * ld + c) = v;
+    }
+  };
   if constexpr (KIND == kD || KIND == kDX) {
     float* out = reinterpret_cast<float*>(p.out);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i) {
+      if (i < ni) {
 #pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int m = m0 + 128 * wm + 32 * i + 8 * (v >> 2) + 4 * fg + (v & 3);
-        if (m < M) {
+        for (int v = 0; v < 16; ++v) {
+          const int m = m0 + row_w + 32 * i + 8 * (v >> 2) + (v & 3);
+          if (m < m_end) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int n = n0 + 128 * wn + 32 * j + fr;
-            if (n < N) out[(size_t)(row0 + m) * N + n] = acc[i][j][v];
+            for (int j = 0; j < 4; ++j) {
+              const int n = n0 + 128 * wn + 32 * j + fr;
+              if (n < N) out[(size_t)(row0 + m) * N + n] = acc[i][j][v];
+            }
           }
         }
       }
+    }
   } else if constexpr (kWeightGrad) {
-    bf16_t* out = reinterpret_cast<bf16_t*>(p.out) + (size_t)e * M * N;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i) {
+      if (i < ni) {
 #pragma unroll
-      for (int v = 0; v < 16; v += 2) {
-        const int m = m0 + 128 * wm + 32 * i + 8 * (v >> 2) + 4 * fg + (v & 3) + (odd ? 1 : 0);
+        for (int v = 0; v < 16; v += 2) {
+          const int r = row_w + 32 * i + 8 * (v >> 2) + (v & 3) + (odd ? 1 : 0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float a, b;
-          pair_of(acc[i][j][v], acc[i][j][v + 1], a, b);
-          const int n = n0 + 128 * wn + 32 * j + (fr & ~1);
-          if (m < M && n < N) *reinterpret_cast<uint32_t*>(out + (size_t)m * N + n) = pack_bf16x2(a, b);
+          for (int j = 0; j < 4; ++j) {
+            float a, b;
+            pair_of(acc[i][j][v], acc[i][j][v + 1], a, b);
+            *(LDS3 uint32_t*)(smem + word_at(r, 64 * wn + 16 * j + (fr >> 1))) = pack_bf16x2(a, b);
+          }
         }
       }
+    }
+    __syncthreads();
+    flush(reinterpret_cast<bf16_t*>(p.out) + ((size_t)e * M + m0) * N + n0, N);
   } else {
     const int I = N / 2;
-    bf16_t* dgu = reinterpret_cast<bf16_t*>(p.out);
+    // the tile of d: 256 rows x 128 floats, in the place that dgu takes
+    {
+      const u32x4_t d_rs = rsrc_words(p.d + (size_t)(row0 + m0) * I, 0x7FFFFFFFu);
+#pragma unroll 8
+      for (int i = 0; i < 32; ++i) {
+        const int r = 64 * wave + 2 * i + (lane >> 5);
+        const int c = n0 / 2 + 4 * ((lane & 31) ^ swizzle(r));
+        dma16(d_rs, m0 + r < m_end && c < I ? ((uint32_t)r * (uint32_t)I + (uint32_t)c) * 4u : kOOR, 0u,
+              lds0 + (64 * wave + 2 * i) * 512);
+      }
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();
+    }
     float bg[4], bu[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -344,23 +398,23 @@ __global__ __launch_bounds__(kThreads, 1) void backward_gemm_kernel(const Args p
       bg[j] = bf16lo(b);
       bu[j] = bf16hi(b);
     }
+    uint32_t wh[4][8][2];   // pairs j = 0, 1 and j = 2, 3
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i) {
+      if (i < ni) {
 #pragma unroll
-      for (int v = 0; v < 16; v += 2) {
-        const int m = m0 + 128 * wm + 32 * i + 8 * (v >> 2) + 4 * fg + (v & 3) + (odd ? 1 : 0);
-        const size_t row = (size_t)(row0 + min(m, M - 1));
-        const float w = p.w[p.rows[row]];
-        float dw = 0.f;
+        for (int v = 0; v < 16; v += 2) {
+          const int r = row_w + 32 * i + 8 * (v >> 2) + (v & 3) + (odd ? 1 : 0);
+          const float w = s_w[r];
+          float dw = 0.f, whv[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float gate, up;
-          pair_of(acc[i][j][v], acc[i][j][v + 1], gate, up);
-          gate += bg[j];
-          up += bu[j];
-          const int n = n0 + 128 * wn + 32 * j + (fr & ~1);
-          if (n < N) {
-            const float d = p.d[row * I + n / 2];
+          for (int j = 0; j < 4; ++j) {
+            float gate, up;
+            pair_of(acc[i][j][v], acc[i][j][v + 1], gate, up);
+            gate += bg[j];
+            up += bu[j];
+            LDS3 uint32_t* at = (LDS3 uint32_t*)(smem + word_at(r, 64 * wn + 16 * j + (fr >> 1)));
+            const float d = __uint_as_float(*at);   // 0 past the last row or column
             // compare-selects, so that a NaN stays one
             const float g = gate > 7.0f ? 7.0f : gate;
             const float u = up > 7.0f ? 7.0f : (up < -7.0f ? -7.0f : up);
@@ -371,19 +425,47 @@ __global__ __launch_bounds__(kThreads, 1) void backward_gemm_kernel(const Args p
             const float wd = w * d;
             const float dgate = gate > 7.0f ? 0.0f : wd * (u + 1.0f) * (z + 1.702f * gz * (1.0f - z));
             const float dup = up > 7.0f || up < -7.0f ? 0.0f : wd * gz;
-            if (m < M) {
-              *reinterpret_cast<uint32_t*>(dgu + row * N + n) = pack_bf16x2(dgate, dup);
-              p.wh[row * I + n / 2] = (bf16_t)f32_to_bf16(w * h);
-            }
+            *at = pack_bf16x2(dgate, dup);
+            whv[j] = w * h;
+          }
+          wh[i][v / 2][0] = pack_bf16x2(whv[0], whv[1]);
+          wh[i][v / 2][1] = pack_bf16x2(whv[2], whv[3]);
+          // lanes of one parity hold one row: sum over them, and over both halves of 32 lanes' columns
+          dw = add_dpp<0x4E>(dw);    // quad_perm [2 3 0 1]
+          dw = add_dpp<0x124>(dw);   // row_ror 4
+          dw = add_dpp<0x128>(dw);   // row_ror 8
+          dw += __shfl_xor(dw, 16, kWave);
+          if (m0 + r < m_end && (lane & 30) == 0) p.dw_part[(size_t)(2 * nt + wn) * p.S + row0 + m0 + r] = dw;
+        }
+      }
+    }
+    __syncthreads();
+    flush(reinterpret_cast<bf16_t*>(p.out) + (size_t)(row0 + m0) * N + n0, N);
+    __syncthreads();
+    // wh: rows of 128 bf16, 16-byte chunk c of row r at c ^ 2 (r % 2 + 2 (r / 4 % 2))
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i < ni) {
+#pragma unroll
+        for (int v = 0; v < 16; v += 2) {
+          const int r = row_w + 32 * i + 8 * (v >> 2) + (v & 3) + (odd ? 1 : 0);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int c = 64 * wn + 16 * j + (fr >> 1);
+            *(LDS3 uint16_t*)(smem + r * 256 + 16 * ((c >> 3) ^ (swizzle(r) / 2)) + 2 * (c & 7)) =
+                (uint16_t)(wh[i][v / 2][j / 2] >> (16 * (j & 1)));
           }
         }
-        // lanes of one parity hold one row: sum over them, and over both halves of 32 lanes' columns
-        dw = add_dpp<0x4E>(dw);    // quad_perm [2 3 0 1]
-        dw = add_dpp<0x124>(dw);   // row_ror 4
-        dw = add_dpp<0x128>(dw);   // row_ror 8
-        dw += __shfl_xor(dw, 16, kWave);
-        if (m < M && (lane & 30) == 0) p.dw_part[(size_t)(2 * nt + wn) * p.S + row] = dw;
       }
+    }
+    __syncthreads();
+#pragma unroll 8
+    for (int i = 0; i < 16; ++i) {
+      const int r = 64 * wave + 4 * i + (lane >> 4);
+      const int c = n0 / 2 + 8 * ((lane & 15) ^ (swizzle(r) / 2));
+      const u32x4_t v = *(const LDS3 u32x4_t*)(smem + r * 256 + 16 * (lane & 15));
+      if (m0 + r < m_end && c < I) *reinterpret_cast<u32x4_t*>(p.wh + (size_t)(row0 + m0 + r) * I + c) = v;
+    }
   }
 }
 
