@@ -19,22 +19,23 @@
 // operands of bf16 products, as h is in the forward pass; d stays float32, it
 // is multiplied elementwise.
 //
-// One kernel for the five: tiles of 256 x 256, K stages of 64, four waves of 128
-// x 128 = 4 x 4 blocks of v_mfma_f32_32x32x16_bf16.  An operand lies in memory
-// either with K contiguous (rows of a stage are 128-byte lines) or with its rows
-// or columns contiguous (a stage is 64 runs of 512 bytes, one for each k: Wgu in
-// GU, all operands of the weight gradients, whose K is the expert's rows).  Both
-// kinds go from HBM/L2 to LDS by direct loads of 16 bytes a lane, two stage
-// buffers of 64 KB; fragments of the second kind are read by the transposing LDS
-// read (ds_read_b64_tr_b16: 16 lanes read 4 k's x 16 columns and each gets the
-// four k's of one column).
-//   Tile heights: an expert's rows are split evenly over its tiles of at most 256,
-//   in steps of 64, and a tile of 64 ni rows has ni row blocks a wave: the loop
-//   is built for each ni.  530 rows cost three tiles of 192 and not of 256.
-//   Stage layout, K contiguous: row r's 16-byte chunk c at slot c ^ ((r >> 1) &
-//   7) of its 128 bytes.  Rows contiguous: run k's 32-byte piece p at p ^ 2 (k &
-//   3) of its 512 bytes: the four k's of a transposing read fall on different
-//   banks.
+// One kernel for the five: tiles of 128 x 256, K stages of 32, four waves in a 2 x
+// 2 grid, each 64 x 128 = 2 x 4 blocks of v_mfma_f32_32x32x16_bf16; two workgroups
+// a CU, so that one's loads, exchange and stores run beside the other's products.
+// An operand lies in memory either with K contiguous (a stage has 64 bytes of
+// every row) or with its rows or columns contiguous (a stage is 32 runs of 256 or
+// 512 bytes, one for each k: Wgu in GU, all operands of the weight gradients,
+// whose K is the expert's rows).  Both kinds go from HBM/L2 to LDS by direct loads
+// of 16 bytes a lane into a ring of three stages; fragments of the second kind are
+// read by the transposing LDS read (ds_read_b64_tr_b16: 16 lanes read 4 k's x 16
+// columns and each gets the four k's of one column).
+//   Stage layout, K contiguous: row r's 16-byte chunk c at slot c ^ ((r >> 2) &
+//   3) of its 64 bytes.  Rows contiguous: run k's 32-byte piece p at p ^ 2 (k & 3)
+//   of its run: the four k's of a transposing read fall on different banks.
+//   Tile heights: an expert's rows are split evenly over its tiles of at most 128,
+//   in steps of 64, and a tile of 64 ni rows has ni row blocks a wave: the loop is
+//   built for each ni, and once more for the tiles that reach past the last
+//   column, whose waves leave out the column blocks without any.
 #include "device_common.h"
 #include "launch.h"
 
@@ -50,11 +51,15 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 enum Kind { kD, kGU, kDX, kWGU, kWD };
 
 constexpr int kThreads = 256;
-constexpr int kTile = 256;
-constexpr int kBK = 64;
-constexpr int kOpBytes = kTile * kBK * 2;   // 32 KB: one operand of one stage
-constexpr int kA = 0;                       // A of buffer b at b * 32 KB
-constexpr int kB = 2 * kOpBytes;            // B of buffer b at 64 KB + b * 32 KB
+constexpr int kBM = 128, kBN = 256;
+constexpr int kBK = 32;
+constexpr int kRing = 3;                      // stage buffers; the loads run kRing - 1 stages ahead
+constexpr int kABytes = kBM * kBK * 2;        // 8 KB
+constexpr int kBBytes = kBN * kBK * 2;        // 16 KB
+constexpr int kA = 0;                         // A of buffer b at b * 8 KB
+constexpr int kB = kRing * kABytes;
+constexpr int kLds = kB + kRing * kBBytes;    // 72 KB; the epilogue's tile of 128 x 512 bytes fits in
+constexpr int kALoads = 2, kBLoads = 4;       // a wave and stage
 constexpr int kXcds = 8;
 constexpr int kMBlock = 1024;               // M tiles per block of the tile order: all of an expert's
 constexpr uint32_t kOOR = 0x80000000u;      // beyond every descriptor's range
@@ -64,7 +69,8 @@ struct Args {
   const bf16_t* B;
   const int32_t *cnt, *off, *rows;
   int M, N, K;           // D, GU, DX: M unused; WGU, WD: K unused (the expert's rows)
-  int E, kslots, tiles_m, tiles_n;
+  int E, tiles_m, tiles_n;
+  uint32_t per_token;    // slot / k = umulhi(slot, per_token); 0: k = 1
   void* out;
   // GU
   const bf16_t* bias;
@@ -83,12 +89,12 @@ __device__ __forceinline__ float add_dpp(float v) {
 }
 
 template <int KIND>
-__global__ __launch_bounds__(kThreads, 1) void backward_gemm_kernel(const Args p) {
+__global__ __launch_bounds__(kThreads, 2) void backward_gemm_kernel(const Args p) {
   constexpr bool kWeightGrad = KIND == kWGU || KIND == kWD;
   constexpr bool kAT = kWeightGrad, kBT = kWeightGrad || KIND == kGU;   // rows / columns contiguous
   constexpr bool kAGather = KIND == kD || KIND == kGU || KIND == kWGU, kBGather = KIND == kWD;
-  __shared__ __align__(1024) char smem_g[4 * kOpBytes];
-  __shared__ float s_w[KIND == kGU ? kTile : 1];   // the rows' routing weights
+  __shared__ __align__(1024) char smem_g[kLds];
+  __shared__ float s_w[KIND == kGU ? kBM : 1];   // the rows' routing weights
   LDS3 char* smem = (LDS3 char*)smem_g;
   const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
 
@@ -107,11 +113,11 @@ __global__ __launch_bounds__(kThreads, 1) void backward_gemm_kernel(const Args p
     e = t / (p.tiles_m * p.tiles_n);
     const int r = t - e * p.tiles_m * p.tiles_n;
     nt = r / p.tiles_m;
-    m0 = (r - nt * p.tiles_m) * kTile;
+    m0 = (r - nt * p.tiles_m) * kBM;
   } else {
-    if (!grouped_gemm_tile(p.cnt, p.E, kTile, p.tiles_n, kMBlock, lane, e, m0, nt)) return;   // workgroup-uniform
+    if (!grouped_gemm_tile(p.cnt, p.E, kBM, p.tiles_n, kMBlock, lane, e, m0, nt)) return;   // workgroup-uniform
   }
-  const int n0 = nt * kTile;
+  const int n0 = nt * kBN;
   const int rows_e = p.cnt[e];
   const int row0 = p.off[e];
   const int M = kWeightGrad ? p.M : rows_e;
@@ -119,196 +125,217 @@ __global__ __launch_bounds__(kThreads, 1) void backward_gemm_kernel(const Args p
   const int N = p.N;
   const int ns = (K + kBK - 1) / kBK;
   // the tile's rows: an expert's split evenly over its tiles, in steps of 64
-  int height = kTile;
+  int height = kBM;
   if (!kWeightGrad) {
-    const int tiles = (M + kTile - 1) / kTile;
+    const int tiles = (M + kBM - 1) / kBM;
     height = (M + 64 * tiles - 1) / (64 * tiles) * 64;
-    m0 = m0 / kTile * height;
+    m0 = m0 / kBM * height;
   }
   const int m_end = min(M, m0 + height);
-  const int ni = (m_end - m0 + 63) / 64;            // row blocks of 32 a wave, 1 .. 4
+  const int ni = m_end - m0 > 64 ? 2 : 1;           // row blocks of 32 a wave
+  auto token = [&](int slot) {
+    return p.per_token ? __umulhi((uint32_t)slot, p.per_token) : (uint32_t)slot;
+  };
   if constexpr (KIND == kGU) {
-    const int m = m0 + tid;
-    s_w[tid] = m < m_end ? p.w[p.rows[row0 + m]] : 0.f;
+    if (tid < kBM) s_w[tid] = m0 + tid < m_end ? p.w[p.rows[row0 + m0 + tid]] : 0.f;
   }
 
-  // ---- direct-load assignments.  K contiguous: wave w fills rows 64w .. 64w +
-  // 63, eight rows an instruction: lane l takes row 8i + l / 8 and the 16-byte
-  // chunk (l % 8) ^ ((r >> 1) & 7).  Rows contiguous: wave w fills the runs of k
-  // = 16w .. 16w + 15, two an instruction: lane l takes k = 16w + 2i + l / 32
-  // and 16 bytes of piece ((l % 32) / 2) ^ 2 (k & 3).  What is past the edges is
-  // sent out of range and lands as 0. ----
-  const int lc[2] = {(lane & 7) ^ ((lane >> 4) & 7), (lane & 7) ^ (((lane >> 4) + 4) & 7)};   // even, odd i
-  uint32_t a_off[8], b_off[8];
-  u32x4_t a_rs, b_rs;
-  uint32_t a_col[2], b_col[2];
+  // ---- direct-load assignments.  K contiguous: wave w fills rows 32w .. of A and
+  // 64w .. of B, sixteen an instruction: lane l takes row 16i + l / 4 and the
+  // 16-byte chunk (l % 4) ^ ((r >> 2) & 3).  Rows contiguous: wave w fills the
+  // runs of k = 8w .. 8w + 7, four (A) or two (B) an instruction: a lane takes 16
+  // bytes of piece p ^ 2 (k & 3).  What is past the edges is sent out of range and
+  // lands as 0. ----
+  const int lc = (lane & 3) ^ ((lane >> 4) & 3);
   const bf16_t* Ae = p.A;
   const bf16_t* Be = p.B;
-  if (!kAT) {
-    // A rows: tokens' rows of dy or x, or the expert's rows of dgu from m0 on
-    if (!kAGather) Ae += (size_t)(row0 + m0) * K;
-    a_rs = rsrc_words(Ae, 0x7FFFFFFFu);
+  // of instruction i: K contiguous, the row's offset; rows contiguous, the column's
+  uint32_t a_off[kALoads], b_off[kBLoads];
+  int a_k[kALoads], b_k[kBLoads];   // rows contiguous: k of the stage
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = 64 * wave + 8 * i + (lane >> 3);
-      const uint32_t c16 = 16u * (uint32_t)lc[i & 1];
-      const uint32_t row = kAGather ? (uint32_t)(p.rows[row0 + min(m0 + r, M - 1)] / p.kslots) : (uint32_t)r;
-      a_off[i] = m0 + r < m_end ? row * (uint32_t)K * 2u + c16 : kOOR;
+  for (int i = 0; i < kALoads; ++i) {
+    if (kAT) {
+      a_k[i] = 8 * wave + 4 * i + (lane >> 4);
+      const int col = m0 + 16 * (((lane & 15) >> 1) ^ (2 * (a_k[i] & 3))) + 8 * (lane & 1);
+      a_off[i] = col < m_end ? 2u * (uint32_t)col : kOOR;
+    } else {
+      const int m = m0 + 32 * wave + 16 * i + (lane >> 2);
+      const uint32_t row = kAGather ? token(p.rows[row0 + min(m, M - 1)]) : (uint32_t)(m - m0);
+      a_off[i] = m < m_end ? row * (uint32_t)K * 2u + 16u * (uint32_t)lc : kOOR;
     }
   }
-  if (!kBT) {
-    Be += (size_t)e * N * K;
-    b_rs = rsrc_words(Be, 0x7FFFFFFFu);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int n = n0 + 64 * wave + 8 * i + (lane >> 3);
-      b_off[i] = n < N ? (uint32_t)n * (uint32_t)K * 2u + 16u * (uint32_t)lc[i & 1] : kOOR;
+  for (int i = 0; i < kBLoads; ++i) {
+    if (kBT) {
+      b_k[i] = 8 * wave + 2 * i + (lane >> 5);
+      const int col = n0 + 16 * (((lane & 31) >> 1) ^ (2 * (b_k[i] & 3))) + 8 * (lane & 1);
+      b_off[i] = col < N ? 2u * (uint32_t)col : kOOR;
+    } else {
+      const int n = n0 + 64 * wave + 16 * i + (lane >> 2);
+      b_off[i] = n < N ? (uint32_t)n * (uint32_t)K * 2u + 16u * (uint32_t)lc : kOOR;
     }
   }
-  const int t_k = 16 * wave + (lane >> 5);          // k of instruction i: t_k + 2i
-#pragma unroll
-  for (int par = 0; par < 2; ++par) {
-    const int f = 2 * ((2 * par + (lane >> 5)) & 3);
-    const int col = 16 * (((lane & 31) >> 1) ^ f) + 8 * (lane & 1);
-    a_col[par] = m0 + col < m_end ? 2u * (uint32_t)(m0 + col) : kOOR;
-    b_col[par] = n0 + col < N ? 2u * (uint32_t)(n0 + col) : kOOR;
-  }
-  if (kBT && !kWeightGrad) Be += (size_t)e * N * K;                            // Wgu[e] [H][2I]
-  if (kAT && !kAGather) Ae += (size_t)row0 * p.M;                              // wh of the expert's rows
+  if (KIND == kDX) Ae += (size_t)(row0 + m0) * K;                              // dgu of the tile's rows
+  if (kWeightGrad && !kAGather) Ae += (size_t)row0 * p.M;                      // wh of the expert's rows
   if (kWeightGrad && !kBGather) Be += (size_t)row0 * N;                        // dgu of the expert's rows
+  if (!kWeightGrad) Be += (size_t)e * N * K;                                   // the expert's weight
 
-  // The tokens of the 16 k's that this wave loads at stage s (weight gradients)
-  auto tokens = [&](int s) {
-    const int k = s * kBK + 16 * wave + (lane & 15);
-    return k < K ? (int)((uint32_t)p.rows[row0 + k] / (uint32_t)p.kslots) : 0;
-  };
-  int tok = 0, tok_next = 0;
-
-  // one operand's instruction i of stage st
-  auto dma_k = [&](u32x4_t rs, const uint32_t (&base)[8], int region, int st, int buf, int i) {
-    const int k0 = st * kBK;
-    const uint32_t voff = k0 + 8 * lc[i & 1] < K ? base[i] : kOOR;
-    dma16(rs, voff, (uint32_t)k0 * 2u, lds0 + region + buf * kOpBytes + (64 * wave + 8 * i) * 128);
-  };
-  auto dma_t = [&](const bf16_t* base, int ld, const uint32_t (&col)[2], bool gather, int region, int st, int buf, int i) {
-    const int k = st * kBK + t_k + 2 * i;
-    uint32_t voff;
-    u32x4_t rs;
-    if (gather) {
-      const int t0 = __builtin_amdgcn_readlane(tok, 2 * i), t1 = __builtin_amdgcn_readlane(tok, 2 * i + 1);
-      voff = (uint32_t)(lane < 32 ? t0 : t1) * (uint32_t)ld * 2u + col[i & 1];
-      rs = rsrc_words(base, 0x7FFFFFFFu);
-    } else {
-      voff = (uint32_t)(t_k + 2 * i) * (uint32_t)ld * 2u + col[i & 1];
-      rs = rsrc_words(base + (size_t)st * kBK * ld, 0x7FFFFFFFu);
+  // The tokens of a wave's eight k's of a stage (weight gradients), loaded a stage
+  // ahead as scalars: vector loads would be counted with the direct loads, and the
+  // wait for them would drain those.  From the last row on, up to seven words
+  // behind the expert's rows are read and not used.
+  uint32_t tok[8] = {}, tok_next[8] = {};
+  const __attribute__((address_space(4))) int32_t* const rows_s =
+      (const __attribute__((address_space(4))) int32_t*)(p.rows + row0);
+  auto tokens = [&](int s, uint32_t (&t)[8]) {
+    if constexpr (kWeightGrad) {
+      const int k = min(s * kBK + 8 * wave, K - 1);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = token(rows_s[k + i]);
     }
-    voff = k < K && col[i & 1] != kOOR ? voff : kOOR;
-    dma16(rs, voff, 0u, lds0 + region + buf * kOpBytes + (16 * wave + 2 * i) * 512);
   };
-  auto dma = [&](int st, int buf, int i, bool b_side) {
-    if (b_side) {
-      if constexpr (kBT) dma_t(Be, N, b_col, kBGather, kB, st, buf, i);
-      else dma_k(b_rs, b_off, kB, st, buf, i);
+  auto pick_a = [&](int i) {   // of the lane's k of A's instruction i
+    const int g = lane >> 4;
+    const uint32_t lo = g == 0 ? tok[4 * i] : tok[4 * i + 1], hi = g == 2 ? tok[4 * i + 2] : tok[4 * i + 3];
+    return g < 2 ? lo : hi;
+  };
+  auto pick_b = [&](int i) { return lane < 32 ? tok[2 * i] : tok[2 * i + 1]; };
+
+  // load q of a wave's six of stage st: A, then B; a stage past the last is out of range
+  auto load = [&](const bf16_t* base, int ld, bool t, bool gather, uint32_t off, int k_in, uint32_t token_row, int st,
+                  uint32_t lds) {
+    const int k0 = st * kBK;
+    if (!t) {
+      dma16(rsrc_words(base, 0x7FFFFFFFu), k0 + 8 * lc < K ? off : kOOR, (uint32_t)k0 * 2u, lds);
+    } else if (gather) {
+      const uint32_t voff = token_row * (uint32_t)ld * 2u + off;
+      dma16(rsrc_words(base, 0x7FFFFFFFu), k0 + k_in < K && off != kOOR ? voff : kOOR, 0u, lds);
     } else {
-      if constexpr (kAT) dma_t(Ae, p.M, a_col, kAGather, kA, st, buf, i);
-      else dma_k(a_rs, a_off, kA, st, buf, i);
+      const uint32_t voff = (uint32_t)k_in * (uint32_t)ld * 2u + off;
+      dma16(rsrc_words(base + (size_t)k0 * ld, 0x7FFFFFFFu), k0 + k_in < K && off != kOOR ? voff : kOOR, 0u, lds);
+    }
+  };
+  auto dma = [&](int st, int buf, int q) {
+    if (q < kALoads) {
+      load(Ae, p.M, kAT, kAGather, a_off[q], a_k[q], kAT && kAGather ? pick_a(q) : 0u, st,
+           lds0 + kA + buf * kABytes + (kAT ? (8 * wave + 4 * q) * 256 : (32 * wave + 16 * q) * 64));
+    } else {
+      const int i = q - kALoads;
+      load(Be, N, kBT, kBGather, b_off[i], b_k[i], kBT && kBGather ? pick_b(i) : 0u, st,
+           lds0 + kB + buf * kBBytes + (kBT ? (8 * wave + 2 * i) * 512 : (64 * wave + 16 * i) * 64));
     }
   };
 
   // ---- fragment reads: step j has k = 16j .. 16j + 15 of the stage ----
   const int fr = lane & 31, fg = lane >> 5;
-  uint32_t a_rd[4], b_rd[4];   // K contiguous: of step j; rows contiguous: of fragment q
+  uint32_t a_rd[2], b_rd[4];   // K contiguous: of step j; rows contiguous: of fragment q
+  const int t_r = (lane & 15) >> 2, t_half = (lane >> 4) & 1;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t xo = 16u * (uint32_t)((2 * j + fg) ^ ((fr >> 1) & 7));
-    const int r = (lane & 15) >> 2, half16 = (lane >> 4) & 1;
-    const uint32_t run = (uint32_t)(8 * fg + r) * 512u + 8u * (uint32_t)(lane & 3);
-    a_rd[j] = kAT ? (uint32_t)kA + run + 32u * (uint32_t)((2 * ni * wm + 2 * j + half16) ^ (2 * r))
-                  : (uint32_t)(kA + (32 * ni * wm + fr) * 128) + xo;
-    b_rd[j] = kBT ? (uint32_t)kB + run + 32u * (uint32_t)((8 * wn + 2 * j + half16) ^ (2 * r))
-                  : (uint32_t)(kB + (128 * wn + fr) * 128) + xo;
+  for (int q = 0; q < 2; ++q) {
+    const uint32_t xo = 16u * (uint32_t)((2 * q + fg) ^ ((fr >> 2) & 3));
+    a_rd[q] = kAT ? (uint32_t)kA + (uint32_t)(8 * fg + t_r) * 256u + 8u * (uint32_t)(lane & 3) +
+                        32u * (uint32_t)((2 * ni * wm + 2 * q + t_half) ^ (2 * t_r))
+                  : (uint32_t)(kA + (32 * ni * wm + fr) * 64) + xo;
+    if (!kBT) b_rd[q] = (uint32_t)(kB + (128 * wn + fr) * 64) + xo;
   }
-  auto read_t = [&](uint32_t at) -> u32x4_t {
+  if (kBT) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      b_rd[q] = (uint32_t)kB + (uint32_t)(8 * fg + t_r) * 512u + 8u * (uint32_t)(lane & 3) +
+                32u * (uint32_t)((8 * wn + 2 * q + t_half) ^ (2 * t_r));
+  }
+  auto read_t = [&](uint32_t at, int run) -> u32x4_t {
     const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS3 s16x4_t*)(smem + at));
-    const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS3 s16x4_t*)(smem + at + 4 * 512));
+    const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS3 s16x4_t*)(smem + at + 4 * run));
     const u32x2_t l = __builtin_bit_cast(u32x2_t, lo), h = __builtin_bit_cast(u32x2_t, hi);
     return u32x4_t{l.x, l.y, h.x, h.y};
   };
   auto read_a = [&](int buf, int j, int q) -> u32x4_t {
-    if constexpr (kAT) return read_t(a_rd[q] + buf * kOpBytes + j * 16 * 512);
-    else return *(const LDS3 u32x4_t*)(smem + a_rd[j] + buf * kOpBytes + q * 32 * 128);
+    if constexpr (kAT) return read_t(a_rd[q] + buf * kABytes + j * 16 * 256, 256);
+    else return *(const LDS3 u32x4_t*)(smem + a_rd[j] + buf * kABytes + q * 32 * 64);
   };
   auto read_b = [&](int buf, int j, int q) -> u32x4_t {
-    if constexpr (kBT) return read_t(b_rd[q] + buf * kOpBytes + j * 16 * 512);
-    else return *(const LDS3 u32x4_t*)(smem + b_rd[j] + buf * kOpBytes + q * 32 * 128);
+    if constexpr (kBT) return read_t(b_rd[q] + buf * kBBytes + j * 16 * 512, 512);
+    else return *(const LDS3 u32x4_t*)(smem + b_rd[j] + buf * kBBytes + q * 32 * 64);
   };
 
-  f32x16_t acc[4][4];
+  f32x16_t acc[2][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-  // The loop for NI row blocks.  Step j of a stage in four slots: slot u reads row
-  // fragment u (of the first NI) and column fragment u for step j and issues the
-  // products of row block u of the step before; the slots of the first two steps
-  // also issue the loads of stage s + 1 (past the last: none).
-  auto loop = [&](auto ni_c) {
+  // The loop for NI row blocks.  Step j of a stage in four slots: slot u reads the
+  // row fragment u (of the first NI) and the column fragment u for step j, issues
+  // a load of the stage kRing - 1 ahead, into the buffer that the stage before left
+  // at the last barrier, and the products of column block u of the step before.
+  // PART: only the first nj column blocks have columns.
+  const int nj = min(4, max(0, (N - n0 - 128 * wn + 31) / 32));
+  auto loop = [&](auto ni_c, auto part_c) {
     constexpr int NI = decltype(ni_c)::value;
-    u32x4_t fa0[4], fb0[4], fa1[4], fb1[4];
-    auto multiply = [&](int u, const u32x4_t (&fa)[4], const u32x4_t (&fb)[4]) {
+    constexpr bool PART = decltype(part_c)::value;
+    u32x4_t fa0[2], fb0[4], fa1[2], fb1[4];
+    auto multiply = [&](int u, const u32x4_t (&fa)[2], const u32x4_t (&fb)[4]) {
+      if (PART && u >= nj) return;   // wave-uniform
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[u][j] = mfma32x32x16(fa[u], fb[j], acc[u][j]);
+      for (int i = 0; i < NI; ++i) acc[i][u] = mfma32x32x16(fa[i], fb[u], acc[i][u]);
     };
-    auto step = [&](int s, int buf, int j, u32x4_t (&fa_rd)[4], u32x4_t (&fb_rd)[4], const u32x4_t (&fa_mm)[4],
+    auto step = [&](int s, int buf, int nbuf, int j, u32x4_t (&fa_rd)[2], u32x4_t (&fb_rd)[4], const u32x4_t (&fa_mm)[2],
                     const u32x4_t (&fb_mm)[4], bool do_mfma) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        if (j < 2) {
-          dma(s + 1, buf ^ 1, 4 * j + u, false);
-          dma(s + 1, buf ^ 1, 4 * j + u, true);
-        }
+        if (4 * j + u < kALoads + kBLoads) dma(s + kRing - 1, nbuf, 4 * j + u);
         __builtin_amdgcn_sched_barrier(0);
         if (u < NI) fa_rd[u] = read_a(buf, j, u);
         fb_rd[u] = read_b(buf, j, u);
-        if (u < NI && do_mfma) multiply(u, fa_mm, fb_mm);
+        if (do_mfma) multiply(u, fa_mm, fb_mm);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
+    int buf = 0, nbuf = kRing - 1;
     for (int s = 0; s < ns; ++s) {
-      const int buf = s & 1;
       if (kWeightGrad) {
-        tok = tok_next;
-        tok_next = tokens(s + 2);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) tok[i] = tok_next[i];
+        tokens(s + kRing, tok_next);
       }
-      step(s, buf, 0, fa0, fb0, fa1, fb1, s > 0);
-      step(s, buf, 1, fa1, fb1, fa0, fb0, true);
-      step(s, buf, 2, fa0, fb0, fa1, fb1, true);
-      step(s, buf, 3, fa1, fb1, fa0, fb0, true);
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      step(s, buf, nbuf, 0, fa0, fb0, fa1, fb1, s > 0);
+      step(s, buf, nbuf, 1, fa1, fb1, fa0, fb0, true);
+      // stage s + 1 has landed when only the loads of the stage behind it are out
+      asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)" ::: "memory");
       __builtin_amdgcn_s_barrier();
+      nbuf = buf;
+      buf = buf == kRing - 1 ? 0 : buf + 1;
     }
 #pragma unroll
-    for (int u = 0; u < NI; ++u) multiply(u, fa1, fb1);
+    for (int u = 0; u < 4; ++u) multiply(u, fa1, fb1);
+    // the loads past the last stage wrote zeros: they end before the epilogue writes there
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   };
   if (ns > 0) {
-    // prologue: stage 0 into buffer 0
-    if (kWeightGrad) {
-      tok = tokens(0);
-      tok_next = tokens(1);
-    }
+    // prologue: stages 0 and 1
+    static_assert(kRing == 3 && kALoads + kBLoads == 6, "the waits count the six loads of one stage");
+    tokens(0, tok);
+    tokens(1, tok_next);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      dma(0, 0, i, false);
-      dma(0, 0, i, true);
-    }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    for (int q = 0; q < kALoads + kBLoads; ++q) dma(0, 0, q);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) tok[i] = tok_next[i];
+    tokens(2, tok_next);
+#pragma unroll
+    for (int q = 0; q < kALoads + kBLoads; ++q) dma(1, 1, q);
+    asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
     __builtin_amdgcn_s_barrier();
-    if (ni == 4) loop(std::integral_constant<int, 4>{});
-    else if (ni == 3) loop(std::integral_constant<int, 3>{});
-    else if (ni == 2) loop(std::integral_constant<int, 2>{});
-    else loop(std::integral_constant<int, 1>{});
+    using std::integral_constant;
+    if (n0 + kBN <= N) {
+      if (ni == 2) loop(integral_constant<int, 2>{}, std::false_type{});
+      else loop(integral_constant<int, 1>{}, std::false_type{});
+    } else {
+      if (ni == 2) loop(integral_constant<int, 2>{}, std::true_type{});
+      else loop(integral_constant<int, 1>{}, std::true_type{});
+    }
+    __syncthreads();
   }
 
   // ---- epilogue.  Lane l, element v of block (i, j): row 32i + 8 (v / 4) + 4 (l
@@ -332,8 +359,8 @@ __global__ __launch_bounds__(kThreads, 1) void backward_gemm_kernel(const Args p
   // rows of 256 bf16 from LDS to out, which points at row m0, column n0
   auto flush = [&](bf16_t* out, int ld) {
 #pragma unroll 8
-    for (int i = 0; i < 32; ++i) {
-      const int r = 64 * wave + 2 * i + (lane >> 5);
+    for (int i = 0; i < 16; ++i) {
+      const int r = 32 * wave + 2 * i + (lane >> 5);
       const int c = 8 * ((lane & 31) ^ swizzle(r));
       const u32x4_t v = *(const LDS3 u32x4_t*)(smem + r * 512 + 16 * (lane & 31));
       if (m0 + r < m_end && n0 + c < N) *reinterpret_cast<u32x4_t*>(out + (size_t)r * ld + c) = v;
@@ -342,7 +369,7 @@ __global__ __launch_bounds__(kThreads, 1) void backward_gemm_kernel(const Args p
   if constexpr (KIND == kD || KIND == kDX) {
     float* out = reinterpret_cast<float*>(p.out);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       if (i < ni) {
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
@@ -359,7 +386,7 @@ __global__ __launch_bounds__(kThreads, 1) void backward_gemm_kernel(const Args p
     }
   } else if constexpr (kWeightGrad) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       if (i < ni) {
 #pragma unroll
         for (int v = 0; v < 16; v += 2) {
@@ -377,15 +404,15 @@ __global__ __launch_bounds__(kThreads, 1) void backward_gemm_kernel(const Args p
     flush(reinterpret_cast<bf16_t*>(p.out) + ((size_t)e * M + m0) * N + n0, N);
   } else {
     const int I = N / 2;
-    // the tile of d: 256 rows x 128 floats, in the place that dgu takes
+    // the tile of d: 128 rows x 128 floats, in the place that dgu takes
     {
       const u32x4_t d_rs = rsrc_words(p.d + (size_t)(row0 + m0) * I, 0x7FFFFFFFu);
 #pragma unroll 8
-      for (int i = 0; i < 32; ++i) {
-        const int r = 64 * wave + 2 * i + (lane >> 5);
+      for (int i = 0; i < 16; ++i) {
+        const int r = 32 * wave + 2 * i + (lane >> 5);
         const int c = n0 / 2 + 4 * ((lane & 31) ^ swizzle(r));
         dma16(d_rs, m0 + r < m_end && c < I ? ((uint32_t)r * (uint32_t)I + (uint32_t)c) * 4u : kOOR, 0u,
-              lds0 + (64 * wave + 2 * i) * 512);
+              lds0 + (32 * wave + 2 * i) * 512);
       }
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
@@ -398,9 +425,9 @@ __global__ __launch_bounds__(kThreads, 1) void backward_gemm_kernel(const Args p
       bg[j] = bf16lo(b);
       bu[j] = bf16hi(b);
     }
-    uint32_t wh[4][8][2];   // pairs j = 0, 1 and j = 2, 3
+    uint32_t wh[2][8][2];   // pairs j = 0, 1 and j = 2, 3
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       if (i < ni) {
 #pragma unroll
         for (int v = 0; v < 16; v += 2) {
@@ -444,7 +471,7 @@ __global__ __launch_bounds__(kThreads, 1) void backward_gemm_kernel(const Args p
     __syncthreads();
     // wh: rows of 128 bf16, 16-byte chunk c of row r at c ^ 2 (r % 2 + 2 (r / 4 % 2))
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       if (i < ni) {
 #pragma unroll
         for (int v = 0; v < 16; v += 2) {
@@ -460,8 +487,8 @@ __global__ __launch_bounds__(kThreads, 1) void backward_gemm_kernel(const Args p
     }
     __syncthreads();
 #pragma unroll 8
-    for (int i = 0; i < 16; ++i) {
-      const int r = 64 * wave + 4 * i + (lane >> 4);
+    for (int i = 0; i < 8; ++i) {
+      const int r = 32 * wave + 4 * i + (lane >> 4);
       const int c = n0 / 2 + 8 * ((lane & 15) ^ (swizzle(r) / 2));
       const u32x4_t v = *(const LDS3 u32x4_t*)(smem + r * 256 + 16 * (lane & 15));
       if (m0 + r < m_end && c < I) *reinterpret_cast<u32x4_t*>(p.wh + (size_t)(row0 + m0 + r) * I + c) = v;
@@ -469,16 +496,20 @@ __global__ __launch_bounds__(kThreads, 1) void backward_gemm_kernel(const Args p
   }
 }
 
+// slot / k for the slots that can be (T H below 2^30 and H >= 8: below 2^30) as the
+// high word of slot times 2^32 / k rounded up: off by less than slot / 2^30 / k
+uint32_t per_token(int k) { return k == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + k - 1) / k); }
+
 template <int KIND>
 hipError_t launch(Args a, int64_t S, hipStream_t stream) {
-  a.tiles_n = (a.N + kTile - 1) / kTile;
+  a.tiles_n = (a.N + kBN - 1) / kBN;
   int64_t tiles;
   if (KIND == kWGU || KIND == kWD) {
-    a.tiles_m = (a.M + kTile - 1) / kTile;
+    a.tiles_m = (a.M + kBM - 1) / kBM;
     tiles = (int64_t)a.E * a.tiles_m * a.tiles_n;
   } else {
-    // at most sum_e ceil(cnt_e / 256) <= S / 256 + min(E, S) tiles of rows
-    tiles = (S / kTile + (S < a.E ? S : a.E)) * a.tiles_n;
+    // at most sum_e ceil(cnt_e / 128) <= S / 128 + min(E, S) tiles of rows
+    tiles = (S / kBM + (S < a.E ? S : a.E)) * a.tiles_n;
   }
   const int64_t grid = (tiles + kXcds - 1) / kXcds * kXcds;
   if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
@@ -494,18 +525,18 @@ hipError_t launch_backward_d(const void* dy, const void* Wd, const int32_t* cnt,
                              int64_t T, int H, int E, int k, int I, float* d, hipStream_t stream) {
   Args a{};
   a.A = (const bf16_t*)dy, a.B = (const bf16_t*)Wd, a.cnt = cnt, a.off = off, a.rows = rows;
-  a.N = I, a.K = H, a.E = E, a.kslots = k, a.out = d;
+  a.N = I, a.K = H, a.E = E, a.per_token = per_token(k), a.out = d;
   return launch<kD>(a, T * k, stream);
 }
 
-int backward_dw_parts(int I) { return (2 * I + kTile - 1) / kTile * 2; }
+int backward_dw_parts(int I) { return (2 * I + kBN - 1) / kBN * 2; }
 
 hipError_t launch_backward_gu(const void* x, const void* Wgu, const void* bgu, const float* w, const float* d,
                               const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T, int H, int E,
                               int k, int I, void* dgu, void* wh, float* dw_part, hipStream_t stream) {
   Args a{};
   a.A = (const bf16_t*)x, a.B = (const bf16_t*)Wgu, a.cnt = cnt, a.off = off, a.rows = rows;
-  a.N = 2 * I, a.K = H, a.E = E, a.kslots = k, a.out = dgu;
+  a.N = 2 * I, a.K = H, a.E = E, a.per_token = per_token(k), a.out = dgu;
   a.bias = (const bf16_t*)bgu, a.d = d, a.w = w, a.wh = (bf16_t*)wh, a.dw_part = dw_part;
   return launch<kGU>(a, T * k, stream);
 }
@@ -514,7 +545,7 @@ hipError_t launch_backward_dx(const void* dgu, const void* Wgu, const int32_t* c
                               int E, int k, int I, float* dxs, hipStream_t stream) {
   Args a{};
   a.A = (const bf16_t*)dgu, a.B = (const bf16_t*)Wgu, a.cnt = cnt, a.off = off;
-  a.N = H, a.K = 2 * I, a.E = E, a.kslots = k, a.out = dxs;
+  a.N = H, a.K = 2 * I, a.E = E, a.per_token = per_token(k), a.out = dxs;
   return launch<kDX>(a, T * k, stream);
 }
 
@@ -523,7 +554,7 @@ hipError_t launch_backward_wgu(const void* x, const void* dgu, const int32_t* cn
                                hipStream_t stream) {
   Args a{};
   a.A = (const bf16_t*)x, a.B = (const bf16_t*)dgu, a.cnt = cnt, a.off = off, a.rows = rows;
-  a.M = H, a.N = 2 * I, a.E = E, a.kslots = k, a.out = dWgu;
+  a.M = H, a.N = 2 * I, a.E = E, a.per_token = per_token(k), a.out = dWgu;
   return launch<kWGU>(a, T * k, stream);
 }
 
@@ -532,7 +563,7 @@ hipError_t launch_backward_wd(const void* wh, const void* dy, const int32_t* cnt
                               hipStream_t stream) {
   Args a{};
   a.A = (const bf16_t*)wh, a.B = (const bf16_t*)dy, a.cnt = cnt, a.off = off, a.rows = rows;
-  a.M = I, a.N = H, a.E = E, a.kslots = k, a.out = dWd;
+  a.M = I, a.N = H, a.E = E, a.per_token = per_token(k), a.out = dWd;
   return launch<kWD>(a, T * k, stream);
 }
 

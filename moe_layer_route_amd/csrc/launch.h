@@ -150,7 +150,8 @@ hipError_t launch_add_rmsnorm(const void* x, const void* residual, const void* g
 // then dgu, wh and the parts of dw [backward_dw_parts(I)][S]; dxs [S][H]; the
 // weights' gradients; dl [T][k]; the sums over an expert's slots of rows of V [..][C]
 // (factor of the slot: rows of its token; NULL: rows in permuted order; out_factor:
-// the sum of the factors, or NULL); and dx
+// the sum of the factors, or NULL); and dx.  The weights' gradients read up to 28
+// bytes behind rows (other parts of the workspace) without using them.
 hipError_t launch_backward_d(const void* dy, const void* Wd, const int32_t* cnt, const int32_t* off, const int32_t* rows,
                              int64_t T, int H, int E, int k, int I, float* d, hipStream_t stream);
 int backward_dw_parts(int I);
