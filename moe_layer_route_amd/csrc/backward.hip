@@ -69,10 +69,11 @@ __global__ __launch_bounds__(kDlWaves * kWave) void backward_dl_kernel(
 
 // ---------------------------------------------------------------------------
 // Column sums over an expert's slots, of rows V[..] times a factor of the slot:
-// one workgroup per expert and 512 columns, its four waves take every fourth
-// row, eight columns a lane; the four sums meet in LDS.
+// one workgroup per expert and 512 columns, its sixteen waves take every sixteenth
+// row, eight columns a lane, four rows in flight; the sums meet in LDS.
 // ---------------------------------------------------------------------------
-constexpr int kSumWaves = 4;
+constexpr int kSumWaves = 16;
+constexpr int kSumAhead = 4;
 constexpr int kSumCols = 8 * kWave;
 
 // GATHER: row of V is the slot's token, else its place in the permuted order.
@@ -90,20 +91,28 @@ __global__ __launch_bounds__(kSumWaves * kWave) void backward_column_sum_kernel(
   const int col = blockIdx.x * kSumCols + 8 * lane;
   const int at = min(col, C - 8);   // C % 8 == 0
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum_f = 0.f;
-  for (int m = wave; m < n; m += kSumWaves) {
-    float f = 1.f;
-    size_t row = (size_t)(row0 + m);
-    if (GATHER) {
-      const int slot = rows[row0 + m];
-      row = (size_t)(slot / kslots);
-      f = factor[slot];
-      sum_f += f;
-    }
-    const u32x4_t v = ld16(V + row * C + at);
+  for (int m0 = wave; m0 < n; m0 += kSumWaves * kSumAhead) {
+    u32x4_t v[kSumAhead];
+    float f[kSumAhead];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      sum[2 * q] = fmaf(f, bf16lo(v[q]), sum[2 * q]);
-      sum[2 * q + 1] = fmaf(f, bf16hi(v[q]), sum[2 * q + 1]);
+    for (int i = 0; i < kSumAhead; ++i) {
+      const int m = m0 + kSumWaves * i;
+      const int at_m = row0 + min(m, n - 1);
+      const int slot = GATHER ? rows[at_m] : 0;
+      const size_t row = GATHER ? (size_t)(slot / kslots) : (size_t)at_m;
+      f[i] = GATHER ? factor[slot] : 1.f;
+      v[i] = ld16(V + row * C + at);
+    }
+#pragma unroll
+    for (int i = 0; i < kSumAhead; ++i) {
+      if (m0 + kSumWaves * i < n) {   // wave-uniform
+        sum_f += f[i];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          sum[2 * q] = fmaf(f[i], bf16lo(v[i][q]), sum[2 * q]);
+          sum[2 * q + 1] = fmaf(f[i], bf16hi(v[i][q]), sum[2 * q + 1]);
+        }
+      }
     }
   }
 #pragma unroll
@@ -113,12 +122,20 @@ __global__ __launch_bounds__(kSumWaves * kWave) void backward_column_sum_kernel(
   if (wave == 0) {
     float s[8];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) s[q] = ((part[0][q][lane] + part[1][q][lane]) + part[2][q][lane]) + part[3][q][lane];
+    for (int q = 0; q < 8; ++q) {
+      s[q] = part[0][q][lane];
+#pragma unroll
+      for (int w = 1; w < kSumWaves; ++w) s[q] += part[w][q][lane];
+    }
     if (col < C)
       *reinterpret_cast<u32x4_t*>(out + (size_t)e * C + col) =
           u32x4_t{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7])};
-    if (out_factor && blockIdx.x == 0 && lane == 0)
-      out_factor[e] = (bf16_t)f32_to_bf16(((part_f[0] + part_f[1]) + part_f[2]) + part_f[3]);
+    if (out_factor && blockIdx.x == 0 && lane == 0) {
+      float f = part_f[0];
+#pragma unroll
+      for (int w = 1; w < kSumWaves; ++w) f += part_f[w];
+      out_factor[e] = (bf16_t)f32_to_bf16(f);
+    }
   }
 }
 

@@ -133,6 +133,8 @@ SIZES = [
     (520, 2, 1, 40, 512, None),     # one K stage that is not full; two tiles of rows
     (33, 2, 2, 2880, 104, None),    # the full hidden size
     (20, 2, 1, 104, 2880, None),    # the full intermediate size
+    (400, 1, 1, 328, 200, None),    # 400 rows of one expert: wide tiles of the gradients, ragged both ways
+    (777, 3, 2, 712, 392, None),    # several of them in both directions
 ]
 
 
