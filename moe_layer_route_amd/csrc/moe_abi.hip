@@ -1365,16 +1365,23 @@ static int check_w4a4_rows(const char* fn, const char* name, int64_t rows, int32
   return MOE_OK;
 }
 
-static int w4a4_path(int32_t path, int64_t S, int32_t E) {
+// The tiles cost about the same up to 64 rows an expert, the streaming kernel more
+// with every chunk of 16.  Where the tiles (256 columns, at least one an expert)
+// fill the card's 512 places twice over they win from 14 rows on, else from 24
+// (gate_up of 2880 x 5760, streaming against tiles: 128 experts, 8 rows each 262 us
+// against 263, 16 rows 300 against 273; 32 experts, 16 rows 78 against 87, 24 rows
+// 82 against 88, 32 rows 112 against 90).
+static int w4a4_path(int32_t path, int64_t S, int32_t E, int32_t N) {
   if (path != MOE_PATH_AUTO) return path;
-  return S > 48 * (int64_t)E ? MOE_PATH_GEMM : MOE_PATH_GEMV;
+  const int64_t tiles = (int64_t)E * ((N + 255) / 256);
+  return S > (tiles < 1024 ? 24 : 14) * (int64_t)E ? MOE_PATH_GEMM : MOE_PATH_GEMV;
 }
 
 static int run_gate_up_w4a4(const char* fn, const void* xq, const void* sx, const void* Wgu_q, const void* Wgu_s,
                             const void* bgu, const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T,
                             int32_t H, int32_t E, int32_t k, int32_t I, void* hq, void* sh, int32_t path,
                             hipStream_t s) {
-  if (w4a4_path(path, T * k, E) == MOE_PATH_GEMM)
+  if (w4a4_path(path, T * k, E, 2 * I) == MOE_PATH_GEMM)
     return hip_status(fn, moe::launch_gemm_w4a4_gate_up(xq, sx, Wgu_q, Wgu_s, bgu, cnt, off, rows, T, H, E, k, I, hq, sh, s));
   return hip_status(fn, moe::launch_w4a4_gate_up(xq, sx, Wgu_q, Wgu_s, bgu, cnt, off, rows, T, H, E, k, I, hq, sh, s));
 }
@@ -1382,7 +1389,7 @@ static int run_gate_up_w4a4(const char* fn, const void* xq, const void* sx, cons
 static int run_down_w4a4(const char* fn, const void* hq, const void* sh, const void* Wd_q, const void* Wd_s,
                          const void* bd, const int32_t* cnt, const int32_t* off, int64_t T, int32_t H, int32_t E,
                          int32_t k, int32_t I, float* o, int32_t path, hipStream_t s) {
-  if (w4a4_path(path, T * k, E) == MOE_PATH_GEMM)
+  if (w4a4_path(path, T * k, E, H) == MOE_PATH_GEMM)
     return hip_status(fn, moe::launch_gemm_w4a4_down(hq, sh, Wd_q, Wd_s, bd, cnt, off, T, H, E, k, I, o, s));
   return hip_status(fn, moe::launch_w4a4_down(hq, sh, Wd_q, Wd_s, bd, cnt, off, T, H, E, k, I, o, s));
 }
