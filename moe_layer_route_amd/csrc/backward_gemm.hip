@@ -201,7 +201,7 @@ __global__ __launch_bounds__(kThreads, 2) void backward_gemm_kernel(const Args p
   };
   auto pick_b = [&](int i) { return lane < 32 ? tok[2 * i] : tok[2 * i + 1]; };
 
-  // load q of a wave's six of stage st: A, then B; a stage past the last is out of range
+  // load q of a wave's six of stage st: A, then B
   auto load = [&](const bf16_t* base, int ld, bool t, bool gather, uint32_t off, int k_in, uint32_t token_row, int st,
                   uint32_t lds) {
     const int k0 = st * kBK;
@@ -285,7 +285,7 @@ __global__ __launch_bounds__(kThreads, 2) void backward_gemm_kernel(const Args p
                     const u32x4_t (&fb_mm)[4], bool do_mfma) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        if (4 * j + u < kALoads + kBLoads) dma(s + kRing - 1, nbuf, 4 * j + u);
+        if (4 * j + u < kALoads + kBLoads && s + kRing - 1 < ns) dma(s + kRing - 1, nbuf, 4 * j + u);
         __builtin_amdgcn_sched_barrier(0);
         if (u < NI) fa_rd[u] = read_a(buf, j, u);
         fb_rd[u] = read_b(buf, j, u);
@@ -302,16 +302,15 @@ __global__ __launch_bounds__(kThreads, 2) void backward_gemm_kernel(const Args p
       }
       step(s, buf, nbuf, 0, fa0, fb0, fa1, fb1, s > 0);
       step(s, buf, nbuf, 1, fa1, fb1, fa0, fb0, true);
-      // stage s + 1 has landed when only the loads of the stage behind it are out
-      asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)" ::: "memory");
+      // stage s + 1 has landed when only the loads of the stage behind it, if any, are out
+      if (s + kRing - 1 < ns) asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)" ::: "memory");
+      else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
       __builtin_amdgcn_s_barrier();
       nbuf = buf;
       buf = buf == kRing - 1 ? 0 : buf + 1;
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) multiply(u, fa1, fb1);
-    // the loads past the last stage wrote zeros: they end before the epilogue writes there
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   };
   if (ns > 0) {
     // prologue: stages 0 and 1
@@ -324,7 +323,7 @@ __global__ __launch_bounds__(kThreads, 2) void backward_gemm_kernel(const Args p
     for (int i = 0; i < 8; ++i) tok[i] = tok_next[i];
     tokens(2, tok_next);
 #pragma unroll
-    for (int q = 0; q < kALoads + kBLoads; ++q) dma(1, 1, q);
+    for (int q = 0; q < kALoads + kBLoads; ++q) dma(1, 1, q);   // (out of range where there is one stage)
     asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     using std::integral_constant;
@@ -385,23 +384,28 @@ __global__ __launch_bounds__(kThreads, 2) void backward_gemm_kernel(const Args p
       }
     }
   } else if constexpr (kWeightGrad) {
+    // rows v and v + 1 packed, then lanes l and l ^ 1 trade halves: the even lane has
+    // both columns of row v, the odd one those of row v + 1
+    const uint32_t pick = odd ? 0x03020706u : 0x05040100u;
+    bf16_t* out = reinterpret_cast<bf16_t*>(p.out) + ((size_t)e * M + m0 + row_w + (odd ? 1 : 0)) * N + n0 + 128 * wn + (fr & ~1);
+    const int rows_left = m_end - m0 - row_w - (odd ? 1 : 0), cols_left = N - n0 - 128 * wn - (fr & ~1);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (i < ni) {
 #pragma unroll
         for (int v = 0; v < 16; v += 2) {
-          const int r = row_w + 32 * i + 8 * (v >> 2) + (v & 3) + (odd ? 1 : 0);
+          const int r = 32 * i + 8 * (v >> 2) + (v & 3);
+          bf16_t* at = out + (size_t)r * N;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            float a, b;
-            pair_of(acc[i][j][v], acc[i][j][v + 1], a, b);
-            *(LDS3 uint32_t*)(smem + word_at(r, 64 * wn + 16 * j + (fr >> 1))) = pack_bf16x2(a, b);
+            const uint32_t two = pack_bf16x2(acc[i][j][v], acc[i][j][v + 1]);
+            const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)two, 0xB1, 0xF, 0xF, true);
+            const uint32_t word = perm_b32(got, two, pick);
+            if (r < rows_left && 32 * j < cols_left) __builtin_nontemporal_store(word, reinterpret_cast<uint32_t*>(at + 32 * j));
           }
         }
       }
     }
-    __syncthreads();
-    flush(reinterpret_cast<bf16_t*>(p.out) + ((size_t)e * M + m0) * N + n0, N);
   } else {
     const int I = N / 2;
     // the tile of d: 128 rows x 128 floats, in the place that dgu takes
