@@ -13,12 +13,20 @@
 // scales, the token rows' codes and scale, and four matrix instructions per 16
 // rows.
 //
-// A workgroup owns one expert and 64 columns; its four waves split K.  Lane
-// (g = lane / 16, c = lane % 16), column block j: column n0 + 4c + j, block 4s +
-// g of step s.  So a lane's four accumulators are neighbouring columns (gate and
-// up of two pairs), their scales one word of the block-major scales, and the 16
-// lanes of a row hold the 32 values of one block of h: its maximum is four lane
-// moves away, and h leaves as MXFP4 rows without a pass of its own.
+// A workgroup owns one expert and 64 columns and walks K in stages of 512 values.
+// Codes and scales go from HBM to LDS by direct loads, 256 bytes of a column an
+// instruction row: reading 4 columns x 256 bytes at a time reaches 6.9 TB/s from
+// registers alone, 16 columns x 64 bytes (the operand's own shape) 5.7, as columns
+// of 1440 bytes begin anywhere in a cache line.  Wave w multiplies the w-th 128
+// values of a stage.
+//   Lane (g = lane / 16, c = lane % 16), column block j: column n0 + 4c + j, block
+//   g of the wave's four.  So a lane's four accumulators are neighbouring columns
+//   (gate and up of two pairs), their scales one word of the block-major scales,
+//   and the 16 lanes of a row hold the 32 values of one block of h: its maximum is
+//   four lane moves away, and h leaves as MXFP4 rows without a pass of its own.
+//   In LDS a column (or row) has 256 bytes of a stage, its 16-byte chunk k at k ^ 4
+//   (column / 4 % 4) (a row's at k ^ 4 (row % 4)): a wave's reads spread over all
+//   banks.
 // The partial sums of the waves are added in LDS in a fixed order.
 #include "launch.h"
 #include "mxfp4_device.h"
@@ -26,25 +34,24 @@
 namespace moe {
 namespace {
 
-typedef __amdgpu_buffer_rsrc_t rsrc_t;
-__device__ __forceinline__ rsrc_t make_rsrc(const void* base, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
-}
-__device__ __forceinline__ u32x4_t buf_ld16(rsrc_t r, uint32_t voff) {
-  return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)voff, 0, 0));
-}
 constexpr uint32_t kOutOfRange = 0x80000000u;   // any offset at or past this reads 0
+
+#define LDS3 __attribute__((address_space(3)))
 
 constexpr int kWaves = 4;
 constexpr int kCols = 64;
+constexpr int kStageBlocks = 16;                // blocks of 32 values a stage
+constexpr int kColBytes = 16 * kStageBlocks;    // 256
 
-// one step's loads: codes and scales of the lane's four columns, and of MG rows
+// MG chunks of 16 rows a pass
 template <int MG>
-struct Step {
-  u32x4_t w[4];
-  uint32_t ws;
-  u32x4_t a[MG];
-  uint32_t as[MG];
+struct Shape {
+  static constexpr int kRing = 2;               // stage buffers; the loads run a stage ahead
+  static constexpr int kWBytes = kCols * kColBytes, kABytes = 16 * MG * kColBytes;
+  static constexpr int kW = 0, kA = kW + kWBytes, kWs = kA + kABytes, kAs = kWs + kCols * kStageBlocks;
+  static constexpr int kStage = kAs + 256 * kWaves;    // 22 or 26 KB
+  static constexpr int kLds = kRing * kStage;          // three workgroups a CU
+  static constexpr int kLoads = 6 + MG;                // a wave and stage
 };
 
 // The y-th expert with rows (every lane of the wave gets it), -1 past the last.
@@ -67,9 +74,8 @@ __device__ __forceinline__ int live_expert(const int32_t* __restrict__ cnt, int 
   return __builtin_amdgcn_readfirstlane(__shfl(found, __ffsll((unsigned long long)who) - 1, kWave));
 }
 
-// MG: chunks of 16 rows a pass; D: steps in flight; WG: workgroups a CU.
-template <bool GATE_UP, int MG, int D, int WG>
-__global__ __launch_bounds__(kWaves * kWave, WG) void w4a4_stream_kernel(
+template <bool GATE_UP, int MG>
+__global__ __launch_bounds__(kWaves * kWave) void w4a4_stream_kernel(
     const uint8_t* __restrict__ A,       // gate_up: x codes [T][K/2]; down: h codes [S][K/2] (permuted order)
     const uint8_t* __restrict__ As,      // [ceil(K/128)][a_rows][4]
     const uint8_t* __restrict__ Wq,      // [E][N][K/2]
@@ -80,7 +86,10 @@ __global__ __launch_bounds__(kWaves * kWave, WG) void w4a4_stream_kernel(
     int K, int N, int E, int kslots, int a_rows, int64_t S,
     void* __restrict__ out,              // gate_up: h codes [S][I/2]; down: float32 [S][N]
     uint8_t* __restrict__ out_s) {       // gate_up: h scales [ceil(I/128)][S][4]
-  __shared__ float red[kWaves][4][4][kWave];   // 16 KB: one chunk's partial sums per wave
+  using C = Shape<MG>;
+  __shared__ __align__(1024) char smem_g[C::kLds];
+  LDS3 char* smem = (LDS3 char*)smem_g;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
 
   const int lane = threadIdx.x & (kWave - 1);
   const int e = S < E ? live_expert(cnt, E, blockIdx.y, lane) : (int)blockIdx.y;
@@ -95,75 +104,114 @@ __global__ __launch_bounds__(kWaves * kWave, WG) void w4a4_stream_kernel(
   const int ncol = n0 + 4 * c;
   // N % 32 == 0: a lane's four columns are all in range or all out of it
   const bool col_ok = ncol < N;
-
   const uint32_t row_bytes = (uint32_t)K / 2;
-  const rsrc_t w_rs = make_rsrc(Wq + (size_t)e * N * row_bytes, (uint32_t)N * row_bytes);
-  const rsrc_t ws_rs = make_rsrc(Ws + (size_t)e * nblk * N, (uint32_t)(nblk * N));
-  const rsrc_t a_rs = make_rsrc(A, (uint32_t)((size_t)a_rows * row_bytes));
-  const int steps = (nblk + 3) / 4;
-  const rsrc_t as_rs = make_rsrc(As, (uint32_t)((size_t)steps * a_rows * 4));
-  const uint32_t s_col = (uint32_t)min(ncol, N - 4);
+  const int ns = (nblk + kStageBlocks - 1) / kStageBlocks;
+
+  // ---- direct-load assignments: wave w fills columns 16w .. 16w + 15, four an
+  // instruction (column 16w + 4i + l / 16, chunk l % 16 ^ 4 i), the rows 4 MG w ..
+  // likewise, its own blocks' weight scales (block l / 16, four columns a lane) and
+  // its rows' scales (row l / 4, group l % 4 of the stage, the first 16 MG lanes).
+  // What is past the edges is sent out of range and lands as 0. ----
+  const u32x4_t w_rs = rsrc_words(Wq + (size_t)e * N * row_bytes, 0x7FFFFFFFu);
+  const u32x4_t ws_rs = rsrc_words(Ws + (size_t)e * nblk * N, 0x7FFFFFFFu);
+  const u32x4_t a_rs = rsrc_words(A, 0x7FFFFFFFu);
+  const u32x4_t as_rs = rsrc_words(As, 0x7FFFFFFFu);
   uint32_t w_off[4];
+  int w_chunk[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) w_off[j] = (uint32_t)min(ncol + j, N - 1) * row_bytes + 16u * g;
-  const int begin = steps * wave / kWaves, end = steps * (wave + 1) / kWaves;
+  for (int i = 0; i < 4; ++i) {
+    const int n = n0 + 16 * wave + 4 * i + g;
+    w_chunk[i] = c ^ (4 * i);
+    w_off[i] = n < N ? (uint32_t)n * row_bytes + 16u * (uint32_t)w_chunk[i] : kOutOfRange;
+  }
+  const uint32_t s_col = (uint32_t)min(ncol, N - 4);
+  const uint32_t ws_off = col_ok ? (uint32_t)g * (uint32_t)N + (uint32_t)ncol : kOutOfRange;
+  const int a_chunk = c ^ (4 * g);
 
   for (int r0 = 0; r0 < M; r0 += 16 * MG) {
     const int nch = min(MG, (M - r0 + 15) / 16);           // block-uniform
+    auto load_w = [&](int s, int buf) {
+      const uint32_t at = lds0 + buf * C::kStage;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        dma16(w_rs, kStageBlocks * s + w_chunk[i] < nblk ? w_off[i] : kOutOfRange, (uint32_t)(kColBytes * s),
+              at + C::kW + (16 * wave + 4 * i) * kColBytes);
+      const int b = kStageBlocks * s + 4 * wave;
+      dma4(ws_rs, b + g < nblk ? ws_off : kOutOfRange, (uint32_t)b * (uint32_t)N, at + C::kWs + 256 * wave);
+    };
+    // the first stage's weights are asked for ahead of the rows
+    load_w(0, 0);
+    // The wave's rows, as scalars (vector loads would be counted with the direct
+    // loads): 4 MG of them; rows past M feed outputs that are not stored.
+    uint32_t a_off[MG], as_off = kOutOfRange;
+#pragma unroll
+    for (int q = 0; q < MG; ++q) {
+      uint32_t row[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int m = row0 + min(r0 + 4 * MG * wave + 4 * q + i, M - 1);
+        row[i] = GATE_UP ? (uint32_t)(((const __attribute__((address_space(4))) int32_t*)rows)[m] / kslots) : (uint32_t)m;
+      }
+      auto pick = [&](int i) {
+        const uint32_t lo = i == 0 ? row[0] : row[1], hi = i == 2 ? row[2] : row[3];
+        return i < 2 ? lo : hi;
+      };
+      a_off[q] = pick(g) * row_bytes + 16u * (uint32_t)a_chunk;
+      if (lane >> 4 == q) as_off = ((uint32_t)(lane & 3) * (uint32_t)a_rows + pick((lane >> 2) & 3)) * 4u;
+    }
+    auto load_a = [&](int s, int buf) {
+      const uint32_t at = lds0 + buf * C::kStage;
+#pragma unroll
+      for (int q = 0; q < MG; ++q)
+        dma16(a_rs, kStageBlocks * s + a_chunk < nblk ? a_off[q] : kOutOfRange, (uint32_t)(kColBytes * s),
+              at + C::kA + (4 * MG * wave + 4 * q) * kColBytes);
+      dma4(as_rs, kStageBlocks * s + 4 * (lane & 3) < nblk ? as_off : kOutOfRange, (uint32_t)(4 * s) * (uint32_t)a_rows * 4u,
+           at + C::kAs + 256 * wave);
+    };
+    load_a(0, 0);
+
     f32x4_t acc[MG][4];
 #pragma unroll
     for (int q = 0; q < MG; ++q)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[q][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-    // Blocks past K and steps past this wave's are sent out of range: codes and
-    // scales 0 (no caller's padding byte, which may be a NaN, is read).
-    auto load_w = [&](int s, Step<MG>& t) {
-      const bool in = s < end && 4 * s + g < nblk;
+    for (int s = 0; s < ns; ++s) {
+      const int buf = s & 1;
+      // stage s + 1 into the other buffer (its reads ended before the last barrier);
+      // past the last stage the loads are out of range
+      load_w(s + 1, buf ^ 1);
+      load_a(s + 1, buf ^ 1);
+      if constexpr (MG == 1) asm volatile("s_waitcnt vmcnt(7)" ::: "memory");
+      else asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+      static_assert(C::kLoads == 6 + MG, "the waits count the loads of one stage");
+      __builtin_amdgcn_s_barrier();
+      const LDS3 char* at = smem + buf * C::kStage;
+      const bool in = kStageBlocks * s + 4 * wave + g < nblk;   // no caller's byte past K is used: 255 would be a NaN
+      u32x4_t w[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) t.w[j] = buf_ld16(w_rs, in ? w_off[j] + 64u * s : kOutOfRange);
-      t.ws = __builtin_amdgcn_raw_buffer_load_b32(ws_rs, (int)(in ? (uint32_t)(4 * s + g) * N + s_col : kOutOfRange), 0, 0);
-    };
-    uint32_t a_row[MG];
-// the first steps' weights are asked for ahead of the rows
-    Step<MG> ring[D];
-#pragma unroll
-    for (int i = 0; i < D; ++i) load_w(begin + i, ring[i]);
-#pragma unroll
-    for (int q = 0; q < MG; ++q) {
-      const int m = min(r0 + 16 * q + c, M - 1);           // rows past M feed outputs that are not stored
-      a_row[q] = GATE_UP ? (uint32_t)(rows[row0 + m] / kslots) : (uint32_t)(row0 + m);
-    }
-    auto load_a = [&](int s, Step<MG>& t) {
-      const bool in = s < end && 4 * s + g < nblk;
+      for (int j = 0; j < 4; ++j)
+        w[j] = *(const LDS3 u32x4_t*)(at + C::kW + (4 * c + j) * kColBytes + 16 * ((4 * wave + g) ^ (4 * (c & 3))));
+      const uint32_t sw = *(const LDS3 uint32_t*)(at + C::kWs + (4 * wave + g) * kCols + 4 * c);
 #pragma unroll
       for (int q = 0; q < MG; ++q) {
-        t.a[q] = buf_ld16(a_rs, in ? a_row[q] * row_bytes + 64u * s + 16u * g : kOutOfRange);
-        t.as[q] = __builtin_amdgcn_raw_buffer_load_b8(
-            as_rs, (int)(in ? ((uint32_t)s * a_rows + a_row[q]) * 4u + g : kOutOfRange), 0, 0);
+        const int r = 16 * q + c;
+        const u32x4_t a = *(const LDS3 u32x4_t*)(at + C::kA + r * kColBytes + 16 * ((4 * wave + g) ^ (4 * (r & 3))));
+        uint32_t sa = *(const LDS3 uint8_t*)(at + C::kAs + 256 * (r / (4 * MG)) + 16 * (r % (4 * MG)) + 4 * wave + g);
+        sa = in ? sa : 0u;
+        acc[q][0] = mfma_fp4_16<0, 0>(a, w[0], acc[q][0], sa, sw);
+        acc[q][1] = mfma_fp4_16<0, 1>(a, w[1], acc[q][1], sa, sw);
+        acc[q][2] = mfma_fp4_16<0, 2>(a, w[2], acc[q][2], sa, sw);
+        acc[q][3] = mfma_fp4_16<0, 3>(a, w[3], acc[q][3], sa, sw);
       }
-    };
-    auto multiply = [&](const Step<MG>& t) {
-#pragma unroll
-      for (int q = 0; q < MG; ++q) {
-        if (q == 0 || q < nch) {
-          acc[q][0] = mfma_fp4_16<0, 0>(t.a[q], t.w[0], acc[q][0], t.as[q], t.ws);
-          acc[q][1] = mfma_fp4_16<0, 1>(t.a[q], t.w[1], acc[q][1], t.as[q], t.ws);
-          acc[q][2] = mfma_fp4_16<0, 2>(t.a[q], t.w[2], acc[q][2], t.as[q], t.ws);
-          acc[q][3] = mfma_fp4_16<0, 3>(t.a[q], t.w[3], acc[q][3], t.as[q], t.ws);
-        }
-      }
-    };
-#pragma unroll
-    for (int i = 0; i < D; ++i) load_a(begin + i, ring[i]);
-    for (int s = begin; s < end; s += D) {
-#pragma unroll
-      for (int i = 0; i < D; ++i) {
-        multiply(ring[i]);
-        load_w(s + i + D, ring[i]);
-        load_a(s + i + D, ring[i]);
-      }
+      // every wave has read its part before the next stage's loads go there
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    // the stage buffers now hold one chunk's partial sums a wave
+    LDS3 float (*red)[4][4][kWave] = (LDS3 float (*)[4][4][kWave])smem;
 
     float bb[4];
     {
@@ -217,10 +265,7 @@ hipError_t launch(const void* A, const void* As, const void* Wq, const void* Ws,
   // so an offset at kOutOfRange never comes back into range
   if (a_rows * K / 2 >= ((int64_t)1 << 31) || (int64_t)N * K / 2 >= ((int64_t)1 << 31)) return hipErrorNotSupported;
   const dim3 grid((unsigned)((N + kCols - 1) / kCols), (unsigned)(S < E ? S : E));
-  // Up to twelve rows an expert in the mean most fit one pass of 16; beyond, two
-  // chunks a pass save the second reading of the weights (32 experts of 2880 x 5760:
-  // T = 64 68.6 us against 74.1, T = 96 74.1 against 76.4, T = 128 96.8 against 78.8).
-  auto kern = S <= 12 * (int64_t)E ? w4a4_stream_kernel<GATE_UP, 1, 3, 3> : w4a4_stream_kernel<GATE_UP, 2, 3, 2>;
+  auto kern = S <= 12 * (int64_t)E ? w4a4_stream_kernel<GATE_UP, 1> : w4a4_stream_kernel<GATE_UP, 2>;
   hipLaunchKernelGGL(kern, grid, dim3(kWaves * kWave), 0, stream, (const uint8_t*)A, (const uint8_t*)As,
                      (const uint8_t*)Wq, (const uint8_t*)Ws, (const bf16_t*)bias, cnt, off, rows, K, N, E, k,
                      (int)a_rows, S, out, (uint8_t*)out_s);
