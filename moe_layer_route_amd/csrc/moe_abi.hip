@@ -1367,14 +1367,14 @@ static int check_w4a4_rows(const char* fn, const char* name, int64_t rows, int32
 
 // The tiles cost about the same up to 64 rows an expert, the streaming kernel more
 // with every chunk of 16.  Where the tiles (256 columns, at least one an expert)
-// fill the card's 512 places twice over they win from 14 rows on, else from 24
-// (gate_up of 2880 x 5760, streaming against tiles: 128 experts, 8 rows each 262 us
-// against 263, 16 rows 300 against 273; 32 experts, 16 rows 78 against 87, 24 rows
-// 82 against 88, 32 rows 112 against 90).
+// fill the card's 512 places twice over they win from 36 rows on, else from 56
+// (gate_up of 2880 x 5760, streaming against tiles: 128 experts, 32 rows each 278 us
+// against 287, 64 rows 397 against 313; 32 experts, 48 rows 77 against 82, 64 rows
+// 105 against 84).
 static int w4a4_path(int32_t path, int64_t S, int32_t E, int32_t N) {
   if (path != MOE_PATH_AUTO) return path;
   const int64_t tiles = (int64_t)E * ((N + 255) / 256);
-  return S > (tiles < 1024 ? 24 : 14) * (int64_t)E ? MOE_PATH_GEMM : MOE_PATH_GEMV;
+  return S > (tiles < 1024 ? 56 : 36) * (int64_t)E ? MOE_PATH_GEMM : MOE_PATH_GEMV;
 }
 
 static int run_gate_up_w4a4(const char* fn, const void* xq, const void* sx, const void* Wgu_q, const void* Wgu_s,

@@ -49,8 +49,8 @@ struct Shape {
   static constexpr int kRing = 2;               // stage buffers; the loads run a stage ahead
   static constexpr int kWBytes = kCols * kColBytes, kABytes = 16 * MG * kColBytes;
   static constexpr int kW = 0, kA = kW + kWBytes, kWs = kA + kABytes, kAs = kWs + kCols * kStageBlocks;
-  static constexpr int kStage = kAs + 256 * kWaves;    // 22 or 26 KB
-  static constexpr int kLds = kRing * kStage;          // three workgroups a CU
+  static constexpr int kStage = kAs + 256 * kWaves;    // 22, 26 or 34 KB
+  static constexpr int kLds = kRing * kStage;          // three, three or two workgroups a CU
   static constexpr int kLoads = 6 + MG;                // a wave and stage
 };
 
@@ -183,7 +183,8 @@ __global__ __launch_bounds__(kWaves * kWave) void w4a4_stream_kernel(
       load_w(s + 1, buf ^ 1);
       load_a(s + 1, buf ^ 1);
       if constexpr (MG == 1) asm volatile("s_waitcnt vmcnt(7)" ::: "memory");
-      else asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+      else if constexpr (MG == 2) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+      else asm volatile("s_waitcnt vmcnt(10)" ::: "memory");
       static_assert(C::kLoads == 6 + MG, "the waits count the loads of one stage");
       __builtin_amdgcn_s_barrier();
       const LDS3 char* at = smem + buf * C::kStage;
@@ -265,7 +266,15 @@ hipError_t launch(const void* A, const void* As, const void* Wq, const void* Ws,
   // so an offset at kOutOfRange never comes back into range
   if (a_rows * K / 2 >= ((int64_t)1 << 31) || (int64_t)N * K / 2 >= ((int64_t)1 << 31)) return hipErrorNotSupported;
   const dim3 grid((unsigned)((N + kCols - 1) / kCols), (unsigned)(S < E ? S : E));
-  auto kern = S <= 12 * (int64_t)E ? w4a4_stream_kernel<GATE_UP, 1> : w4a4_stream_kernel<GATE_UP, 2>;
+  // Rows a pass by the mean rows an expert: 16, 32 or 64.  More rows cost LDS (two
+  // instead of three workgroups a CU at 64) and reads of rows that are not there;
+  // fewer cost another pass over the weights.  gate_up of 2880 x 5760, 16 / 32 / 64:
+  // 32 experts, 8 rows each 51 / 54 / 66 us, 12: 58 / 54 / 64, 24: 92 / 63 / 69, 32:
+  // 105 / 78 / 72; 128 experts, 8: 196 / 200 / 236, 16: 265 / 219 / 251, 32: 408 /
+  // 301 / 278.
+  auto kern = S <= 10 * (int64_t)E   ? w4a4_stream_kernel<GATE_UP, 1>
+              : S <= 27 * (int64_t)E ? w4a4_stream_kernel<GATE_UP, 2>
+                                     : w4a4_stream_kernel<GATE_UP, 4>;
   hipLaunchKernelGGL(kern, grid, dim3(kWaves * kWave), 0, stream, (const uint8_t*)A, (const uint8_t*)As,
                      (const uint8_t*)Wq, (const uint8_t*)Ws, (const bf16_t*)bias, cnt, off, rows, K, N, E, k,
                      (int)a_rows, S, out, (uint8_t*)out_s);

@@ -5,27 +5,25 @@
 // batched launch), section 2 (gate_up -> bias -> GLU, down -> bias), section 4
 // (early exits only when the whole workgroup leaves together; masked tails).
 //
-// Tile: 256 rows x 256 columns, K stages of 256 codes (one 128-byte line of
-// every row and column), four waves in a 2 x 2 grid, each 128 x 128 = 4 x 4
-// blocks of v_mfma_scale_f32_32x32x64_f8f6f4 (256 float32 accumulators a lane).
-//   Staging: codes and scales HBM/L2 -> LDS by direct loads, two stage buffers
-//   of 64 KB of codes and 4 KB of scales.  Row r's 16-byte chunk c (one block of
-//   32 values) sits at slot c ^ ((r >> 1) & 7) of its 128 bytes.  LDS row 32q +
-//   t of a wave's 128 columns is column 4t + q, so that accumulator blocks q = 0
-//   .. 3 of a lane are four neighbouring columns: two (gate, up) pairs, one
-//   16-byte store of down, and one word of the block-major weight scales.
-//   Steps: step j of a stage has the blocks j (lanes 0-31) and 4 + j (lanes
-//   32-63) of the stage's eight; the product only needs both operands to agree.
-//   So a lane's four row scales of a stage are one word of the rows' scale
-//   layout (its group of four blocks), step j takes byte j of it, and column
-//   block q takes byte q of the weight scales' word of block 4 (l / 32) + j:
-//   8 scale words a lane and stage, picked by the instruction itself.
-//   Stage s: after the barrier that ends stage s - 1, the loads of stage s + 1 go
-//   into the other buffer; each wave waits for its own at the end of the stage
-//   and the barrier makes all of them visible.
-// Epilogue of gate_up: 16 lanes hold one block of h for a row: maximum by lane
-// moves, codes by the conversion instruction, then a 4 x 4 byte transpose in each
-// quad of lanes makes a lane's four bytes those of one row.
+// Tile: 128 rows x 256 columns, K stages of 128 codes (64 bytes of every row and
+// column), four waves in a 2 x 2 grid, each 64 x 128 = 2 x 4 blocks of
+// v_mfma_scale_f32_32x32x64_f8f6f4 (128 float32 accumulators a lane).  A second
+// kernel below has tiles of 128 x 128 for launches of few tiles.
+//   Staging: codes and scales HBM/L2 -> LDS by direct loads into a ring of three
+//   stage buffers (24 KB of codes, 2 KB of scales each), two stages ahead; 78 KB, so
+//   two workgroups share a CU and one multiplies while the other starts or ends.
+//   Row r's 16-byte chunk c (one block of 32 values) sits at slot c ^ ((r >> 2) & 3)
+//   of its 64 bytes.  LDS row 32q + t of a wave's 128 columns is column 4t + q, so
+//   that accumulator blocks q = 0 .. 3 of a lane are four neighbouring columns: two
+//   (gate, up) pairs, one 16-byte store of down, and one word of the block-major
+//   weight scales.
+//   Steps: step j of a stage has the blocks j (lanes 0-31) and 2 + j (lanes 32-63)
+//   of the stage's four; the product only needs both operands to agree.  A lane's
+//   row scales of a stage are one word of the rows' layout, shifted once by its
+//   half, step j takes byte j of it, and column block q takes byte q of the weight
+//   scales' word of block 2 (l / 32) + j: picked by the instruction itself.
+//   Stage s: its loads were issued during stage s - 2; each wave waits for its own
+//   at the end of stage s - 1 and the barrier makes all of them visible.
 #include "launch.h"
 #include "mxfp4_device.h"
 
@@ -51,6 +49,38 @@ constexpr int kLds = kBs + kRing * kBsBytes;   // 78 KB: two workgroups a CU
 constexpr int kMBlock = 1024;                  // M tiles per block of the tile order: all of an expert's
 constexpr int kXcds = 8;
 constexpr uint32_t kOOR = 0x80000000u;         // beyond every descriptor's range
+
+// Four rows m4 .. m4 + 3 of h from a lane's four neighbouring columns (two gate, up
+// pairs) of each, p[column][row] without the bias.  16 lanes hold one block of h for
+// a row: maximum by lane moves, codes by the conversion instruction, then a 4 x 4
+// byte transpose in each quad of lanes makes a lane's four bytes those of one row.
+__device__ __forceinline__ void store_glu_quad(const f32x4_t (&p)[4], const float (&bb)[4], int m4, int M, int row0,
+                                               int ncol, int N, int lane, uint8_t* __restrict__ codes,
+                                               uint8_t* __restrict__ out_s, int64_t S) {
+  const int b = ncol / 64;                                 // this lane's block of h
+  const int l4 = lane & 3;
+  const uint32_t pick = 0x01010101u * (uint32_t)l4 + 0x04000400u;   // bytes l4 of two words, twice
+  uint32_t c4 = 0, s4 = 0;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const uint32_t h = pack_bf16x2(clamped_glu(p[0][r] + bb[0], p[1][r] + bb[1]),
+                                   clamped_glu(p[2][r] + bb[2], p[3][r] + bb[3]));
+    const uint32_t s = mx_scale_byte(row16_max(abs_max2(h)));
+    const uint32_t c = s == 255 ? 0u : encode2<0>(0u, h, ue8m0_to_f32(s)) & 0xFFu;
+    c4 |= c << (8 * r);
+    s4 |= s << (8 * r);
+  }
+  // lane l4 of a quad: byte l4 (row m4 + l4) of the quad's four words
+  const uint32_t q0 = moved<0x00>(c4), q1 = moved<0x55>(c4), q2 = moved<0xAA>(c4), q3 = moved<0xFF>(c4);
+  const uint32_t lo = perm_b32(q1, q0, pick), hi = perm_b32(q3, q2, pick);
+  const uint32_t word = pack_lo(lo, hi);
+  const int m = m4 + l4;
+  if (m < M && ncol < N) {
+    const size_t orow = (size_t)(row0 + m);
+    *reinterpret_cast<uint32_t*>(codes + orow * (N / 4) + (ncol & ~15) / 4) = word;
+    if ((lane & 15) < 4) out_s[((size_t)(b / 4) * S + orow) * 4 + b % 4] = (uint8_t)(s4 >> (8 * l4));
+  }
+}
 
 template <bool GATE_UP>
 __global__ __launch_bounds__(kThreads, 2) void w4a4_gemm_kernel(
@@ -254,36 +284,17 @@ __global__ __launch_bounds__(kThreads, 2) void w4a4_gemm_kernel(
     bb[0] = bf16lo(b01), bb[1] = bf16hi(b01), bb[2] = bf16lo(b23), bb[3] = bf16hi(b23);
   }
   if (GATE_UP) {
-    const int b = (n0 + 128 * wn) / 64 + (fr >> 4);          // this lane's block of h
-    const int l4 = lane & 3;
-    const uint32_t pick = 0x01010101u * (uint32_t)l4 + 0x04000400u;   // bytes l4 of two words, twice
-    uint8_t* codes = reinterpret_cast<uint8_t*>(out);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int v4 = 0; v4 < 4; ++v4) {
-        const int m4 = m0 + 64 * wm + 32 * i + 8 * v4 + 4 * fg;     // rows m4 .. m4 + 3
-        uint32_t c4 = 0, s4 = 0;
+        f32x4_t quad[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int v = 4 * v4 + r;
-          const uint32_t h = pack_bf16x2(clamped_glu(acc[i][0][v] + bb[0], acc[i][1][v] + bb[1]),
-                                         clamped_glu(acc[i][2][v] + bb[2], acc[i][3][v] + bb[3]));
-          const uint32_t s = mx_scale_byte(row16_max(abs_max2(h)));
-          const uint32_t c = s == 255 ? 0u : encode2<0>(0u, h, ue8m0_to_f32(s)) & 0xFFu;
-          c4 |= c << (8 * r);
-          s4 |= s << (8 * r);
-        }
-        // lane l4 of a quad: byte l4 (row m4 + l4) of the quad's four words
-        const uint32_t q0 = moved<0x00>(c4), q1 = moved<0x55>(c4), q2 = moved<0xAA>(c4), q3 = moved<0xFF>(c4);
-        const uint32_t lo = perm_b32(q1, q0, pick), hi = perm_b32(q3, q2, pick);
-        const uint32_t word = pack_lo(lo, hi);
-        const int m = m4 + l4;
-        if (m < M && ncol < N) {
-          const size_t orow = (size_t)(row0 + m);
-          *reinterpret_cast<uint32_t*>(codes + orow * (N / 4) + (ncol & ~15) / 4) = word;
-          if ((lane & 15) < 4) out_s[((size_t)(b / 4) * S + orow) * 4 + b % 4] = (uint8_t)(s4 >> (8 * l4));
-        }
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) quad[q][r] = acc[i][q][4 * v4 + r];
+        store_glu_quad(quad, bb, m0 + 64 * wm + 32 * i + 8 * v4 + 4 * fg, M, row0, ncol, N, lane,
+                       reinterpret_cast<uint8_t*>(out), out_s, S);
       }
   } else {
     if (ncol >= N) return;                                   // N % 32 == 0: four columns are all in or all out
@@ -299,6 +310,166 @@ __global__ __launch_bounds__(kThreads, 2) void w4a4_gemm_kernel(
   }
 }
 
+// ---- the same product by tiles of 128 x 128 with K stages of 256 codes: a whole
+// 128-byte line of every row and column at a time.  Two stage buffers of 34 KB, two
+// workgroups a CU; four waves in a 2 x 2 grid, each 64 x 64 = 4 x 4 blocks of
+// v_mfma_scale_f32_16x16x128_f8f6f4, two steps of 128 values a stage.
+//   LDS row 16j + t of a wave's 64 columns is column 4t + j, so a lane's four column
+//   blocks are neighbouring columns, as in the tiles above; chunk c of row r sits at
+//   slot c ^ ((r >> 1) & 7).
+//   Lane (g = lane / 16, c = lane % 16) has block g of a step's four; its scales are
+//   byte g of the row's word and the word of the four columns. ----
+constexpr int kMidBN = 128;
+constexpr int kMidRow = 128;                       // bytes of a row and stage
+constexpr int kMidA = 0, kMidB = kMidA + kBM * kMidRow, kMidAs = kMidB + kMidBN * kMidRow, kMidBs = kMidAs + 1024;
+constexpr int kMidStage = kMidBs + 1024;           // 34 KB
+
+template <bool GATE_UP>
+__global__ __launch_bounds__(kThreads, 2) void w4a4_mid_kernel(
+    const uint8_t* __restrict__ A, const uint8_t* __restrict__ As, const uint8_t* __restrict__ Wq,
+    const uint8_t* __restrict__ Ws, const bf16_t* __restrict__ bias, const int32_t* __restrict__ cnt,
+    const int32_t* __restrict__ off, const int32_t* __restrict__ rows, int K, int N, int E, int kslots, int a_rows,
+    int64_t S, int n_tiles, void* __restrict__ out, uint8_t* __restrict__ out_s) {
+  __shared__ __align__(1024) char smem_g[2 * kMidStage];
+  LDS3 char* smem = (LDS3 char*)smem_g;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
+
+  const int tid = threadIdx.x;
+  const int lane = tid & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int g = lane >> 4, c = lane & 15;
+
+  int e, m0, nt;
+  if (!grouped_gemm_tile(cnt, E, kBM, n_tiles, kMBlock, lane, e, m0, nt)) return;   // workgroup-uniform
+  const int n0 = nt * kMidBN;
+  const int M = cnt[e];
+  const int row0 = off[e];
+  const int Kb = K / 2;
+  const int nblk = K / 32;
+  const int ns = (nblk + 7) / 8;
+
+  // ---- direct-load assignments: wave w fills rows 32w .. 32w + 31 of A and of B,
+  // eight an instruction (row 8i + l / 8, chunk (l % 8) ^ ((r >> 1) & 7)) ----
+  const u32x4_t a_rs = rsrc_words(A, 0x7FFFFFFFu);
+  const u32x4_t b_rs = rsrc_words(Wq + (size_t)e * N * Kb, 0x7FFFFFFFu);
+  const u32x4_t as_rs = rsrc_words(As, 0x7FFFFFFFu);
+  const u32x4_t bs_rs = rsrc_words(Ws + (size_t)e * nblk * N, 0x7FFFFFFFu);
+  auto row_of = [&](int m) {
+    return GATE_UP ? (uint32_t)(rows[row0 + m] / kslots) : (uint32_t)(row0 + m);
+  };
+  uint32_t a_off[4], b_off[4];
+  int chunk[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 32 * wave + 8 * i + (lane >> 3);
+    chunk[i] = (lane & 7) ^ ((r >> 1) & 7);
+    const int n = n0 + (r & ~63) + 4 * (r & 15) + ((r >> 4) & 3);
+    b_off[i] = n < N ? (uint32_t)n * (uint32_t)Kb + 16u * chunk[i] : kOOR;
+  }
+  // weight scales: blocks 2w and 2w + 1 of the stage, four columns a lane
+  const int bs_n = n0 + 4 * (lane & 31), bs_b = 2 * wave + (lane >> 5);
+  const uint32_t bs_off = bs_n < N ? (uint32_t)bs_b * (uint32_t)N + (uint32_t)bs_n : kOOR;
+  // row scales: rows 32w + l / 2, word l % 2 of the stage's two
+  uint32_t as_off = kOOR;
+
+  auto load_b = [&](int st, int buf) {
+    const uint32_t k0 = (uint32_t)st * kMidRow, at = lds0 + buf * kMidStage;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      dma16(b_rs, 8 * st + chunk[i] < nblk ? b_off[i] : kOOR, k0, at + kMidB + (32 * wave + 8 * i) * kMidRow);
+    dma4(bs_rs, 8 * st + bs_b < nblk ? bs_off : kOOR, (uint32_t)(8 * st) * (uint32_t)N, at + kMidBs + 256 * wave);
+  };
+  auto load_a = [&](int st, int buf) {
+    const uint32_t k0 = (uint32_t)st * kMidRow, at = lds0 + buf * kMidStage;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      dma16(a_rs, 8 * st + chunk[i] < nblk ? a_off[i] : kOOR, k0, at + kMidA + (32 * wave + 8 * i) * kMidRow);
+    dma4(as_rs, 8 * st + 4 * (lane & 1) < nblk ? as_off : kOOR, (uint32_t)(2 * st) * (uint32_t)a_rows * 4u,
+         at + kMidAs + 256 * wave);
+  };
+  load_b(0, 0);   // ahead of the rows
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int m = m0 + 32 * wave + 8 * i + (lane >> 3);
+    a_off[i] = m < M ? row_of(m) * (uint32_t)Kb + 16u * chunk[i] : kOOR;
+  }
+  {
+    const int m = m0 + 32 * wave + (lane >> 1);
+    if (m < M) as_off = ((uint32_t)(lane & 1) * (uint32_t)a_rows + row_of(m)) * 4u;
+  }
+  load_a(0, 0);
+
+  f32x4_t acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  const uint32_t xr = (uint32_t)((c >> 1) & 7);
+  const uint32_t a_rd = kMidA + (64 * wm + c) * kMidRow, b_rd = kMidB + (64 * wn + c) * kMidRow;
+  const bool live = m0 + 64 * wm < M;                      // wave-uniform: some of its rows are there
+  for (int s = 0; s < ns; ++s) {
+    const int buf = s & 1;
+    // stage s has landed, and every wave is done with stage s - 1's buffer
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    if (s + 1 < ns) {
+      load_b(s + 1, buf ^ 1);
+      load_a(s + 1, buf ^ 1);
+    }
+    if (!live) continue;
+    const LDS3 char* at = smem + buf * kMidStage;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const bool in = 8 * s + 4 * t + g < nblk;            // no caller's byte past K is used: 255 would be a NaN
+      const uint32_t xo = 16u * ((uint32_t)(4 * t + g) ^ xr);
+      u32x4_t b[4], a[4];
+      uint32_t sa[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[j] = *(const LDS3 u32x4_t*)(at + b_rd + xo + 16 * j * kMidRow);
+      const uint32_t sb = *(const LDS3 uint32_t*)(at + kMidBs + (4 * t + g) * kMidBN + 64 * wn + 4 * c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[i] = *(const LDS3 u32x4_t*)(at + a_rd + xo + 16 * i * kMidRow);
+        sa[i] = *(const LDS3 uint8_t*)(at + kMidAs + 8 * (64 * wm + 16 * i + c) + 4 * t + g);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t si = in ? sa[i] : 0u;
+        acc[i][0] = mfma_fp4_16<0, 0>(a[i], b[0], acc[i][0], si, sb);
+        acc[i][1] = mfma_fp4_16<0, 1>(a[i], b[1], acc[i][1], si, sb);
+        acc[i][2] = mfma_fp4_16<0, 2>(a[i], b[2], acc[i][2], si, sb);
+        acc[i][3] = mfma_fp4_16<0, 3>(a[i], b[3], acc[i][3], si, sb);
+      }
+    }
+  }
+  if (!live) return;
+
+  // ---- epilogue: lane (g, c), element v of block (i, j): row 16i + 4g + v, column
+  // 4c + j of the wave's 64 ----
+  const int ncol = n0 + 64 * wn + 4 * c;
+  float bb[4];
+  {
+    const uint32_t* bp = reinterpret_cast<const uint32_t*>(bias + (size_t)e * N + min(ncol, N - 4));
+    const uint32_t b01 = bp[0], b23 = bp[1];
+    bb[0] = bf16lo(b01), bb[1] = bf16hi(b01), bb[2] = bf16lo(b23), bb[3] = bf16hi(b23);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int m4 = m0 + 64 * wm + 16 * i + 4 * g;          // rows m4 .. m4 + 3
+    if constexpr (GATE_UP) {
+      store_glu_quad(acc[i], bb, m4, M, row0, ncol, N, lane, reinterpret_cast<uint8_t*>(out), out_s, S);
+    } else {
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        if (m4 + v < M && ncol < N)
+          *reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(out) + (size_t)(row0 + m4 + v) * N + ncol) =
+              f32x4_t{acc[i][0][v] + bb[0], acc[i][1][v] + bb[1], acc[i][2][v] + bb[2], acc[i][3][v] + bb[3]};
+    }
+  }
+}
+
 template <bool GATE_UP>
 hipError_t launch(const void* A, const void* As, const void* Wq, const void* Ws, const void* bias, const int32_t* cnt,
                   const int32_t* off, const int32_t* rows, int64_t T, int K, int N, int E, int k, void* out, void* out_s,
@@ -306,12 +477,20 @@ hipError_t launch(const void* A, const void* As, const void* Wq, const void* Ws,
   const int64_t S = T * k, a_rows = GATE_UP ? T : S;
   // 32-bit buffer offsets: the token codes and one expert's codes below 2 GiB
   if (a_rows * K / 2 >= ((int64_t)1 << 31) || (int64_t)N * K / 2 >= ((int64_t)1 << 31)) return hipErrorNotSupported;
-  const int n_tiles = (N + kBN - 1) / kBN;
+  // Tiles of 128 x 128 where those of 128 x 256 are few: 512 run at a time, and the
+  // last round is seldom full.  2880 x 5760 and 2880 x 2880, 32 experts, 128 x 128
+  // against 128 x 256: 64 rows each 84 and 48 us against 96 and 51, 128 rows 113 and
+  // 60 against 117 and 75, 192 rows 144 and 72 against 131 and 80, 512 rows 284 and
+  // 166 against 253 and 174; 128 experts, 32 rows 299 and 150 against 287 and 152.
+  const int64_t big = (S / kBM + (S < E ? S : E)) * ((N + kBN - 1) / kBN);
+  const bool mid = big < 1792;
+  const int n_tiles = (N + (mid ? kMidBN : kBN) - 1) / (mid ? kMidBN : kBN);
   // at most sum_e ceil(cnt_e / 128) <= S / 128 + min(E, S) M tiles
   const int64_t tiles = (S / kBM + (S < E ? S : E)) * n_tiles;
   const int64_t grid = (tiles + kXcds - 1) / kXcds * kXcds;
   if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((w4a4_gemm_kernel<GATE_UP>), dim3((unsigned)grid), dim3(kThreads), 0, stream, (const uint8_t*)A,
+  auto kern = mid ? w4a4_mid_kernel<GATE_UP> : w4a4_gemm_kernel<GATE_UP>;
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(kThreads), 0, stream, (const uint8_t*)A,
                      (const uint8_t*)As, (const uint8_t*)Wq, (const uint8_t*)Ws, (const bf16_t*)bias, cnt, off, rows, K,
                      N, E, k, (int)a_rows, S, n_tiles, out, (uint8_t*)out_s);
   return hipGetLastError();
