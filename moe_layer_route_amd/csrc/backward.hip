@@ -68,78 +68,6 @@ __global__ __launch_bounds__(kDlWaves * kWave) void backward_dl_kernel(
 }
 
 // ---------------------------------------------------------------------------
-// Column sums over an expert's slots, of rows V[..] times a factor of the slot:
-// one workgroup per expert and 512 columns, its sixteen waves take every sixteenth
-// row, eight columns a lane, four rows in flight; the sums meet in LDS.
-// ---------------------------------------------------------------------------
-constexpr int kSumWaves = 16;
-constexpr int kSumAhead = 4;
-constexpr int kSumCols = 8 * kWave;
-
-// GATHER: row of V is the slot's token, else its place in the permuted order.
-template <bool GATHER>
-__global__ __launch_bounds__(kSumWaves * kWave) void backward_column_sum_kernel(
-    const bf16_t* __restrict__ V, const float* __restrict__ factor, const int32_t* __restrict__ cnt,
-    const int32_t* __restrict__ off, const int32_t* __restrict__ rows, int C, int kslots, bf16_t* __restrict__ out,
-    bf16_t* __restrict__ out_factor) {
-  __shared__ float part[kSumWaves][8][kWave];
-  __shared__ float part_f[kSumWaves];
-  const int lane = threadIdx.x & (kWave - 1);
-  const int wave = threadIdx.x / kWave;
-  const int e = blockIdx.y;
-  const int n = cnt[e], row0 = off[e];
-  const int col = blockIdx.x * kSumCols + 8 * lane;
-  const int at = min(col, C - 8);   // C % 8 == 0
-  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum_f = 0.f;
-  for (int m0 = wave; m0 < n; m0 += kSumWaves * kSumAhead) {
-    u32x4_t v[kSumAhead];
-    float f[kSumAhead];
-#pragma unroll
-    for (int i = 0; i < kSumAhead; ++i) {
-      const int m = m0 + kSumWaves * i;
-      const int at_m = row0 + min(m, n - 1);
-      const int slot = GATHER ? rows[at_m] : 0;
-      const size_t row = GATHER ? (size_t)(slot / kslots) : (size_t)at_m;
-      f[i] = GATHER ? factor[slot] : 1.f;
-      v[i] = ld16(V + row * C + at);
-    }
-#pragma unroll
-    for (int i = 0; i < kSumAhead; ++i) {
-      if (m0 + kSumWaves * i < n) {   // wave-uniform
-        sum_f += f[i];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          sum[2 * q] = fmaf(f[i], bf16lo(v[i][q]), sum[2 * q]);
-          sum[2 * q + 1] = fmaf(f[i], bf16hi(v[i][q]), sum[2 * q + 1]);
-        }
-      }
-    }
-  }
-#pragma unroll
-  for (int q = 0; q < 8; ++q) part[wave][q][lane] = sum[q];
-  if (lane == 0) part_f[wave] = sum_f;
-  __syncthreads();
-  if (wave == 0) {
-    float s[8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      s[q] = part[0][q][lane];
-#pragma unroll
-      for (int w = 1; w < kSumWaves; ++w) s[q] += part[w][q][lane];
-    }
-    if (col < C)
-      *reinterpret_cast<u32x4_t*>(out + (size_t)e * C + col) =
-          u32x4_t{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7])};
-    if (out_factor && blockIdx.x == 0 && lane == 0) {
-      float f = part_f[0];
-#pragma unroll
-      for (int w = 1; w < kSumWaves; ++w) f += part_f[w];
-      out_factor[e] = (bf16_t)f32_to_bf16(f);
-    }
-  }
-}
-
-// ---------------------------------------------------------------------------
 // dx: one thread per four columns of a token.
 // ---------------------------------------------------------------------------
 constexpr int kDxThreads = 256;
@@ -189,16 +117,6 @@ hipError_t launch_backward_dl(const void* dy, const void* bd, const int32_t* ids
                               hipStream_t stream) {
   hipLaunchKernelGGL(backward_dl_kernel, dim3((unsigned)((T + kDlWaves - 1) / kDlWaves)), dim3(kDlWaves * kWave), 0,
                      stream, (const bf16_t*)dy, (const bf16_t*)bd, ids, pos, w, dw_part, parts, T, H, k, dl);
-  return hipGetLastError();
-}
-
-hipError_t launch_backward_column_sum(const void* V, const float* factor, const int32_t* cnt, const int32_t* off,
-                                      const int32_t* rows, int E, int C, int k, void* out, void* out_factor,
-                                      hipStream_t stream) {
-  const dim3 grid((unsigned)((C + kSumCols - 1) / kSumCols), (unsigned)E);
-  auto kern = factor ? backward_column_sum_kernel<true> : backward_column_sum_kernel<false>;
-  hipLaunchKernelGGL(kern, grid, dim3(kSumWaves * kWave), 0, stream, (const bf16_t*)V, factor, cnt, off, rows, C, k,
-                     (bf16_t*)out, (bf16_t*)out_factor);
   return hipGetLastError();
 }
 

@@ -88,14 +88,12 @@ __device__ __forceinline__ float add_dpp(float v) {
   return v + __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xF, 0xF, true));
 }
 
+// One tile; block is the launch's number of it, s_w GU's place for the rows' weights.
 template <int KIND>
-__global__ __launch_bounds__(kThreads, 2) void backward_gemm_kernel(const Args p) {
+__device__ __forceinline__ void product(const Args& p, int block, LDS3 char* smem, LDS3 float* s_w) {
   constexpr bool kWeightGrad = KIND == kWGU || KIND == kWD;
   constexpr bool kAT = kWeightGrad, kBT = kWeightGrad || KIND == kGU;   // rows / columns contiguous
   constexpr bool kAGather = KIND == kD || KIND == kGU || KIND == kWGU, kBGather = KIND == kWD;
-  __shared__ __align__(1024) char smem_g[kLds];
-  __shared__ float s_w[KIND == kGU ? kBM : 1];   // the rows' routing weights
-  LDS3 char* smem = (LDS3 char*)smem_g;
   const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
 
   const int tid = threadIdx.x;
@@ -108,14 +106,14 @@ __global__ __launch_bounds__(kThreads, 2) void backward_gemm_kernel(const Args p
   if (kWeightGrad) {
     // consecutive tiles of an expert on one XCD
     const int total = p.E * p.tiles_m * p.tiles_n, q = (total + kXcds - 1) / kXcds;
-    const int t = (int)(blockIdx.x % kXcds) * q + (int)blockIdx.x / kXcds;
-    if ((int)blockIdx.x / kXcds >= q || t >= total) return;   // workgroup-uniform
+    const int t = block % kXcds * q + block / kXcds;
+    if (block / kXcds >= q || t >= total) return;   // workgroup-uniform
     e = t / (p.tiles_m * p.tiles_n);
     const int r = t - e * p.tiles_m * p.tiles_n;
     nt = r / p.tiles_m;
     m0 = (r - nt * p.tiles_m) * kBM;
   } else {
-    if (!grouped_gemm_tile(p.cnt, p.E, kBM, p.tiles_n, kMBlock, lane, e, m0, nt)) return;   // workgroup-uniform
+    if (!grouped_gemm_tile(p.cnt, p.E, kBM, p.tiles_n, kMBlock, block, lane, e, m0, nt)) return;   // workgroup-uniform
   }
   const int n0 = nt * kBN;
   const int rows_e = p.cnt[e];
@@ -500,12 +498,128 @@ __global__ __launch_bounds__(kThreads, 2) void backward_gemm_kernel(const Args p
   }
 }
 
+// ---------------------------------------------------------------------------
+// Column sums over an expert's slots, of rows V[..] times a factor of the slot: one
+// workgroup per expert and 512 columns, its four waves take every fourth row, eight
+// columns a lane, eight rows in flight; the sums meet in LDS in a fixed order.
+// ---------------------------------------------------------------------------
+constexpr int kSumWaves = kThreads / kWave;
+constexpr int kSumAhead = 8;
+constexpr int kSumCols = 8 * kWave;
+
+struct Sum {
+  const bf16_t* V;
+  const float* factor;   // of the slot; null: 1, and V has the rows of the permuted order, else the tokens'
+  int C, parts;          // columns, pieces of 512 of them (0: not asked for)
+  bf16_t *out, *out_factor;   // [E][C]; [E], the sum of the factors, or null
+};
+
+template <bool GATHER>
+__device__ __forceinline__ void column_sum(const Sum& p, const Args& a, int e, int piece, LDS3 char* smem) {
+  LDS3 float (*part)[8][kWave] = (LDS3 float (*)[8][kWave])smem;
+  LDS3 float* part_f = (LDS3 float*)(smem + kSumWaves * 8 * kWave * 4);
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int n = a.cnt[e], row0 = a.off[e], C = p.C;
+  const int col = piece * kSumCols + 8 * lane;
+  const int at = min(col, C - 8);   // C % 8 == 0
+  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum_f = 0.f;
+  for (int m0 = wave; m0 < n; m0 += kSumWaves * kSumAhead) {
+    u32x4_t v[kSumAhead];
+    float f[kSumAhead];
+#pragma unroll
+    for (int i = 0; i < kSumAhead; ++i) {
+      const int at_m = row0 + min(m0 + kSumWaves * i, n - 1);
+      const uint32_t slot = GATHER ? (uint32_t)a.rows[at_m] : 0u;
+      const size_t row = GATHER ? (a.per_token ? __umulhi(slot, a.per_token) : slot) : (size_t)at_m;
+      f[i] = GATHER ? p.factor[slot] : 1.f;
+      v[i] = ld16(p.V + row * C + at);
+    }
+#pragma unroll
+    for (int i = 0; i < kSumAhead; ++i) {
+      if (m0 + kSumWaves * i < n) {   // wave-uniform
+        sum_f += f[i];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          sum[2 * q] = fmaf(f[i], bf16lo(v[i][q]), sum[2 * q]);
+          sum[2 * q + 1] = fmaf(f[i], bf16hi(v[i][q]), sum[2 * q + 1]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 8; ++q) part[wave][q][lane] = sum[q];
+  if (lane == 0) part_f[wave] = sum_f;
+  __syncthreads();
+  if (wave == 0) {
+    float s[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      s[q] = part[0][q][lane];
+#pragma unroll
+      for (int w = 1; w < kSumWaves; ++w) s[q] += part[w][q][lane];
+    }
+    if (col < C)
+      *reinterpret_cast<u32x4_t*>(p.out + (size_t)e * C + col) =
+          u32x4_t{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7])};
+    if (p.out_factor && piece == 0 && lane == 0) {
+      float f = part_f[0];
+#pragma unroll
+      for (int w = 1; w < kSumWaves; ++w) f += part_f[w];
+      p.out_factor[e] = (bf16_t)f32_to_bf16(f);
+    }
+  }
+}
+
+template <int KIND>
+__global__ __launch_bounds__(kThreads, 2) void backward_gemm_kernel(const Args p) {
+  __shared__ __align__(1024) char smem[kLds];
+  __shared__ float s_w[KIND == kGU ? kBM : 1];   // the rows' routing weights
+  product<KIND>(p, blockIdx.x, (LDS3 char*)smem, (LDS3 float*)s_w);
+}
+
+// What only needs dgu, wh and dl, in one launch: DX's tiles, which are long, the
+// column sums, then the tiles of the weight gradients, which are short and fill the
+// places that DX's last round leaves.  Blocks come in groups of eight, one a XCD.
+struct Tail {
+  Args dx, wgu, wd;
+  Sum sum[3];            // dbgu, dbd, dWr
+  int begin[4];          // first group of the sums, WGU, WD, and the end
+};
+
+__global__ __launch_bounds__(kThreads, 2) void backward_tail_kernel(const Tail p) {
+  __shared__ __align__(1024) char smem_g[kLds];
+  LDS3 char* smem = (LDS3 char*)smem_g;
+  const int group = blockIdx.x / kXcds;
+  if (group < p.begin[0]) {
+    product<kDX>(p.dx, blockIdx.x, smem, nullptr);
+  } else if (group < p.begin[1]) {
+    int item = blockIdx.x - p.begin[0] * kXcds;
+    const int parts = p.sum[0].parts + p.sum[1].parts + p.sum[2].parts;
+    const int e = item / parts;
+    if (e >= p.dx.E) return;                       // workgroup-uniform
+    item -= e * parts;
+    if (item < p.sum[0].parts) {
+      column_sum<false>(p.sum[0], p.wgu, e, item, smem);
+    } else {
+      item -= p.sum[0].parts;
+      const bool second = item >= p.sum[1].parts;
+      column_sum<true>(p.sum[second ? 2 : 1], p.wgu, e, second ? item - p.sum[1].parts : item, smem);
+    }
+  } else if (group < p.begin[2]) {
+    product<kWGU>(p.wgu, blockIdx.x - p.begin[1] * kXcds, smem, nullptr);
+  } else {
+    product<kWD>(p.wd, blockIdx.x - p.begin[2] * kXcds, smem, nullptr);
+  }
+}
+
 // slot / k for the slots that can be (T H below 2^30 and H >= 8: below 2^30) as the
 // high word of slot times 2^32 / k rounded up: off by less than slot / 2^30 / k
 uint32_t per_token(int k) { return k == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + k - 1) / k); }
 
+// groups of eight blocks of a product; fills in the tile counts
 template <int KIND>
-hipError_t launch(Args a, int64_t S, hipStream_t stream) {
+int64_t groups(Args& a, int64_t S) {
   a.tiles_n = (a.N + kBN - 1) / kBN;
   int64_t tiles;
   if (KIND == kWGU || KIND == kWD) {
@@ -515,10 +629,15 @@ hipError_t launch(Args a, int64_t S, hipStream_t stream) {
     // at most sum_e ceil(cnt_e / 128) <= S / 128 + min(E, S) tiles of rows
     tiles = (S / kBM + (S < a.E ? S : a.E)) * a.tiles_n;
   }
-  const int64_t grid = (tiles + kXcds - 1) / kXcds * kXcds;
+  a.S = S;
+  return (tiles + kXcds - 1) / kXcds;
+}
+
+template <int KIND>
+hipError_t launch(Args a, int64_t S, hipStream_t stream) {
+  const int64_t grid = groups<KIND>(a, S) * kXcds;
   if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
   if (grid == 0) return hipSuccess;
-  a.S = S;
   hipLaunchKernelGGL((backward_gemm_kernel<KIND>), dim3((unsigned)grid), dim3(kThreads), 0, stream, a);
   return hipGetLastError();
 }
@@ -545,30 +664,35 @@ hipError_t launch_backward_gu(const void* x, const void* Wgu, const void* bgu, c
   return launch<kGU>(a, T * k, stream);
 }
 
-hipError_t launch_backward_dx(const void* dgu, const void* Wgu, const int32_t* cnt, const int32_t* off, int64_t T, int H,
-                              int E, int k, int I, float* dxs, hipStream_t stream) {
+hipError_t launch_backward_tail(const void* dy, const void* x, const void* Wgu, const float* w, const void* dgu,
+                                const void* wh, const float* dl, const int32_t* cnt, const int32_t* off,
+                                const int32_t* rows, int64_t T, int H, int E, int k, int I, float* dxs, void* dWgu,
+                                void* dbgu, void* dWd, void* dbd, void* dWr, void* dbr, hipStream_t stream) {
+  const int64_t S = T * k;
+  Tail p{};
   Args a{};
-  a.A = (const bf16_t*)dgu, a.B = (const bf16_t*)Wgu, a.cnt = cnt, a.off = off;
-  a.N = H, a.K = 2 * I, a.E = E, a.per_token = per_token(k), a.out = dxs;
-  return launch<kDX>(a, T * k, stream);
-}
-
-hipError_t launch_backward_wgu(const void* x, const void* dgu, const int32_t* cnt, const int32_t* off,
-                               const int32_t* rows, int64_t T, int H, int E, int k, int I, void* dWgu,
-                               hipStream_t stream) {
-  Args a{};
-  a.A = (const bf16_t*)x, a.B = (const bf16_t*)dgu, a.cnt = cnt, a.off = off, a.rows = rows;
-  a.M = H, a.N = 2 * I, a.E = E, a.per_token = per_token(k), a.out = dWgu;
-  return launch<kWGU>(a, T * k, stream);
-}
-
-hipError_t launch_backward_wd(const void* wh, const void* dy, const int32_t* cnt, const int32_t* off,
-                              const int32_t* rows, int64_t T, int H, int E, int k, int I, void* dWd,
-                              hipStream_t stream) {
-  Args a{};
-  a.A = (const bf16_t*)wh, a.B = (const bf16_t*)dy, a.cnt = cnt, a.off = off, a.rows = rows;
-  a.M = I, a.N = H, a.E = E, a.per_token = per_token(k), a.out = dWd;
-  return launch<kWD>(a, T * k, stream);
+  a.cnt = cnt, a.off = off, a.rows = rows, a.E = E, a.per_token = per_token(k);
+  p.dx = p.wgu = p.wd = a;
+  p.dx.A = (const bf16_t*)dgu, p.dx.B = (const bf16_t*)Wgu, p.dx.N = H, p.dx.K = 2 * I, p.dx.out = dxs;
+  p.wgu.A = (const bf16_t*)x, p.wgu.B = (const bf16_t*)dgu, p.wgu.M = H, p.wgu.N = 2 * I, p.wgu.out = dWgu;
+  p.wd.A = (const bf16_t*)wh, p.wd.B = (const bf16_t*)dy, p.wd.M = I, p.wd.N = H, p.wd.out = dWd;
+  auto sum = [](const void* V, const float* factor, int C, void* out, void* out_factor) {
+    return Sum{(const bf16_t*)V, factor, C, out ? (C + kSumCols - 1) / kSumCols : 0, (bf16_t*)out, (bf16_t*)out_factor};
+  };
+  p.sum[0] = sum(dgu, nullptr, 2 * I, dbgu, nullptr);
+  p.sum[1] = sum(dy, w, H, dbd, nullptr);
+  p.sum[2] = sum(x, dl, H, dWr, dbr);
+  const int64_t sums = (int64_t)E * (p.sum[0].parts + p.sum[1].parts + p.sum[2].parts);
+  int64_t at = groups<kDX>(p.dx, S);
+  const int64_t after[4] = {0, (sums + kXcds - 1) / kXcds, dWgu ? groups<kWGU>(p.wgu, S) : 0, dWd ? groups<kWD>(p.wd, S) : 0};
+  for (int i = 0; i < 4; ++i) {
+    at += after[i];
+    if (at * kXcds > 0x7FFFFFFF) return hipErrorInvalidValue;
+    p.begin[i] = (int)at;
+  }
+  if (at == 0) return hipSuccess;
+  hipLaunchKernelGGL(backward_tail_kernel, dim3((unsigned)(at * kXcds)), dim3(kThreads), 0, stream, p);
+  return hipGetLastError();
 }
 
 }  // namespace moe

@@ -146,31 +146,23 @@ hipError_t launch_gemm_int4_down(const void* h, const void* Wq, const void* Ws, 
 hipError_t launch_add_rmsnorm(const void* x, const void* residual, const void* gamma, int64_t T, int H, float eps,
                               void* residual_out, void* y, void* codes, float* scales, hipStream_t stream);
 
-// The backward pass (backward_gemm.hip, backward.hip): d [S][I] = dy . Wd^T;
-// then dgu, wh and the parts of dw [backward_dw_parts(I)][S]; dxs [S][H]; the
-// weights' gradients; dl [T][k]; the sums over an expert's slots of rows of V [..][C]
-// (factor of the slot: rows of its token; NULL: rows in permuted order; out_factor:
-// the sum of the factors, or NULL); and dx.  The weights' gradients read up to 28
-// bytes behind rows (other parts of the workspace) without using them.
+// The backward pass (backward_gemm.hip, backward.hip): d [S][I] = dy . Wd^T; then
+// dgu, wh and the parts of dw [backward_dw_parts(I)][S]; dl [T][k]; dxs [S][H] with
+// the gradients of the weights (the experts' four or the router's two may be NULL);
+// and dx.  The weights' gradients read up to 28 bytes behind rows (other parts of
+// the workspace) without using them.
 hipError_t launch_backward_d(const void* dy, const void* Wd, const int32_t* cnt, const int32_t* off, const int32_t* rows,
                              int64_t T, int H, int E, int k, int I, float* d, hipStream_t stream);
 int backward_dw_parts(int I);
 hipError_t launch_backward_gu(const void* x, const void* Wgu, const void* bgu, const float* w, const float* d,
                               const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T, int H, int E,
                               int k, int I, void* dgu, void* wh, float* dw_part, hipStream_t stream);
-hipError_t launch_backward_dx(const void* dgu, const void* Wgu, const int32_t* cnt, const int32_t* off, int64_t T, int H,
-                              int E, int k, int I, float* dxs, hipStream_t stream);
-hipError_t launch_backward_wgu(const void* x, const void* dgu, const int32_t* cnt, const int32_t* off,
-                               const int32_t* rows, int64_t T, int H, int E, int k, int I, void* dWgu,
-                               hipStream_t stream);
-hipError_t launch_backward_wd(const void* wh, const void* dy, const int32_t* cnt, const int32_t* off,
-                              const int32_t* rows, int64_t T, int H, int E, int k, int I, void* dWd,
-                              hipStream_t stream);
 hipError_t launch_backward_dl(const void* dy, const void* bd, const int32_t* ids, const int32_t* pos, const float* w,
                               const float* dw_part, int parts, int64_t T, int H, int k, float* dl, hipStream_t stream);
-hipError_t launch_backward_column_sum(const void* V, const float* factor, const int32_t* cnt, const int32_t* off,
-                                      const int32_t* rows, int E, int C, int k, void* out, void* out_factor,
-                                      hipStream_t stream);
+hipError_t launch_backward_tail(const void* dy, const void* x, const void* Wgu, const float* w, const void* dgu,
+                                const void* wh, const float* dl, const int32_t* cnt, const int32_t* off,
+                                const int32_t* rows, int64_t T, int H, int E, int k, int I, float* dxs, void* dWgu,
+                                void* dbgu, void* dWd, void* dbd, void* dWr, void* dbr, hipStream_t stream);
 hipError_t launch_backward_dx_sum(const float* dxs, const int32_t* ids, const int32_t* pos, const float* dl,
                                   const void* Wr, int64_t T, int H, int k, void* dx, hipStream_t stream);
 

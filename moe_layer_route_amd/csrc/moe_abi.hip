@@ -1646,17 +1646,9 @@ int moe_backward(const void* dy, const void* x, const void* Wr, const void* Wgu,
   if (int st = hip_status(fn, moe::launch_backward_dl(dy, bd, topk_ids, pos, topk_w, dw_part,
                                                       moe::backward_dw_parts(I), T, H, k, dl, s)))
     return st;
-  if (int st = hip_status(fn, moe::launch_backward_dx(dgu, Wgu, cnt, off, T, H, E, k, I, wide, s))) return st;
-  if (experts) {
-    if (int st = hip_status(fn, moe::launch_backward_wgu(x, dgu, cnt, off, rows, T, H, E, k, I, dWgu, s))) return st;
-    if (int st = hip_status(fn, moe::launch_backward_wd(wh, dy, cnt, off, rows, T, H, E, k, I, dWd, s))) return st;
-    if (int st = hip_status(fn, moe::launch_backward_column_sum(dgu, nullptr, cnt, off, rows, E, 2 * I, k, dbgu, nullptr, s)))
-      return st;
-    if (int st = hip_status(fn, moe::launch_backward_column_sum(dy, topk_w, cnt, off, rows, E, H, k, dbd, nullptr, s)))
-      return st;
-  }
-  if (dWr)
-    if (int st = hip_status(fn, moe::launch_backward_column_sum(x, dl, cnt, off, rows, E, H, k, dWr, dbr, s))) return st;
+  if (int st = hip_status(fn, moe::launch_backward_tail(dy, x, Wgu, topk_w, dgu, wh, dl, cnt, off, rows, T, H, E, k, I,
+                                                        wide, dWgu, dbgu, dWd, dbd, dWr, dbr, s)))
+    return st;
   if (int st = hip_status(fn, moe::launch_backward_dx_sum(wide, topk_ids, pos, dl, Wr, T, H, k, dx, s))) return st;
   return ok();
 }
