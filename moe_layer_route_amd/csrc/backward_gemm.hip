@@ -11,7 +11,7 @@
 //        h = (u + 1) g z
 //        dgu[s]    = w d * (dh/dgate, dh/dup)              [S][2I] (bf16)
 //        wh[s]     = w h                                   [S][I]  (bf16)
-//        dw[s]     = sum over i of h d   (+ bd . dy)       in parts of 64 i
+//        dw[s]     = sum over i of h d   (+ bd . dy)       in parts of 48 i
 //   DX   dxs[s]    = dgu[s] . Wgu[e]^T                     [S][H]  (float32)
 //   WGU  dWgu[e]   = sum over e's slots of x[t]^T dgu[s]   [H][2I] (bf16)
 //   WD   dWd[e]    = sum over e's slots of wh[s]^T dy[t]   [I][H]  (bf16)
@@ -51,15 +51,26 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 enum Kind { kD, kGU, kDX, kWGU, kWD };
 
 constexpr int kThreads = 256;
-constexpr int kBM = 128, kBN = 256;
-constexpr int kBK = 32;
-constexpr int kRing = 3;                      // stage buffers; the loads run kRing - 1 stages ahead
-constexpr int kABytes = kBM * kBK * 2;        // 8 KB
-constexpr int kBBytes = kBN * kBK * 2;        // 16 KB
-constexpr int kA = 0;                         // A of buffer b at b * 8 KB
-constexpr int kB = kRing * kABytes;
-constexpr int kLds = kB + kRing * kBBytes;    // 72 KB; the epilogue's tile of 128 x 512 bytes fits in
-constexpr int kALoads = 2, kBLoads = 4;       // a wave and stage
+constexpr int kBM = 128;
+
+// The tile's columns, K stage and ring of a kind
+template <int BN_, int BK_, int RING_, int PER_SLOT_>
+struct Tile {
+  static constexpr int BN = BN_, WN = BN / 2, NB = WN / 32;   // columns; of a wave; their blocks of 32
+  static constexpr int BK = BK_, STEPS = BK / 16, WK = BK / 4;   // a stage's k's; of a wave's runs
+  static constexpr int RING = RING_;                    // stage buffers; the loads run RING - 1 stages ahead
+  static constexpr int PER_SLOT = PER_SLOT_;            // loads a slot of the loop
+  static constexpr int ABYTES = kBM * BK * 2, BBYTES = BN * BK * 2;
+  static constexpr int A = 0, B = RING * ABYTES;        // A and B of buffer b at b * ABYTES, b * BBYTES
+  static constexpr int LDS = B + RING * BBYTES;
+  static constexpr int ROW = BK * 2;                    // K contiguous: bytes of a row and stage
+  static constexpr int ROWS_I = 1024 / ROW;             // and rows an instruction
+  static constexpr int RUN_A = kBM * 2, RUN_B = BN * 2; // rows contiguous: bytes of a run
+  static constexpr int ALOADS = ABYTES / 4096, BLOADS = BBYTES / 4096;   // a wave and stage
+};
+template <int KIND>
+using TileOf = std::conditional_t<KIND == kD || KIND == kDX || KIND == kGU, Tile<192, 64, 2, 4>, Tile<256, 32, 3, 1>>;
+constexpr int kLds = 81920;                   // of the largest: two workgroups a CU
 constexpr int kXcds = 8;
 constexpr int kMBlock = 1024;               // M tiles per block of the tile order: all of an expert's
 constexpr uint32_t kOOR = 0x80000000u;      // beyond every descriptor's range
@@ -76,7 +87,7 @@ struct Args {
   const bf16_t* bias;
   const float *d, *w;    // w [T][k]
   bf16_t* wh;
-  float* dw_part;        // [ceil(2I / 128)][S]
+  float* dw_part;        // [backward_dw_parts(I)][S]
   int64_t S;
 };
 
@@ -88,10 +99,12 @@ __device__ __forceinline__ float add_dpp(float v) {
   return v + __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xF, 0xF, true));
 }
 
-// One tile; block is the launch's number of it, s_w GU's place for the rows' weights.
+// One tile; block is the launch's number of it.
 template <int KIND>
-__device__ __forceinline__ void product(const Args& p, int block, LDS3 char* smem, LDS3 float* s_w) {
+__device__ __forceinline__ void product(const Args& p, int block, LDS3 char* smem) {
   constexpr bool kWeightGrad = KIND == kWGU || KIND == kWD;
+  using C = TileOf<KIND>;
+  static_assert(C::LDS <= kLds, "");
   constexpr bool kAT = kWeightGrad, kBT = kWeightGrad || KIND == kGU;   // rows / columns contiguous
   constexpr bool kAGather = KIND == kD || KIND == kGU || KIND == kWGU, kBGather = KIND == kWD;
   const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
@@ -115,13 +128,13 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
   } else {
     if (!grouped_gemm_tile(p.cnt, p.E, kBM, p.tiles_n, kMBlock, block, lane, e, m0, nt)) return;   // workgroup-uniform
   }
-  const int n0 = nt * kBN;
+  const int n0 = nt * C::BN;
   const int rows_e = p.cnt[e];
   const int row0 = p.off[e];
   const int M = kWeightGrad ? p.M : rows_e;
   const int K = kWeightGrad ? rows_e : p.K;
   const int N = p.N;
-  const int ns = (K + kBK - 1) / kBK;
+  const int ns = (K + C::BK - 1) / C::BK;
   // the tile's rows: an expert's split evenly over its tiles, in steps of 64
   int height = kBM;
   if (!kWeightGrad) {
@@ -134,43 +147,45 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
   auto token = [&](int slot) {
     return p.per_token ? __umulhi((uint32_t)slot, p.per_token) : (uint32_t)slot;
   };
-  if constexpr (KIND == kGU) {
-    if (tid < kBM) s_w[tid] = m0 + tid < m_end ? p.w[p.rows[row0 + m0 + tid]] : 0.f;
-  }
 
-  // ---- direct-load assignments.  K contiguous: wave w fills rows 32w .. of A and
-  // 64w .. of B, sixteen an instruction: lane l takes row 16i + l / 4 and the
-  // 16-byte chunk (l % 4) ^ ((r >> 2) & 3).  Rows contiguous: wave w fills the
-  // runs of k = 8w .. 8w + 7, four (A) or two (B) an instruction: a lane takes 16
-  // bytes of piece p ^ 2 (k & 3).  What is past the edges is sent out of range and
-  // lands as 0. ----
-  const int lc = (lane & 3) ^ ((lane >> 4) & 3);
+  // ---- direct-load assignments.  K contiguous: wave w fills the w-th quarter of the
+  // rows, 1 KB an instruction, a lane 16 bytes: chunk c of a row is at c ^ ((r >> 1)
+  // & 7) of its 128 bytes (c ^ ((r >> 2) & 3) of 64).  Rows contiguous: wave w fills
+  // the w-th quarter of the runs; 32-byte piece p of run k is at p ^ 2 (k & 3), in
+  // runs of 384 bytes, where two k's are half the banks apart, at p ^ (k & 2).  What
+  // is past the edges is sent out of range and lands as 0. ----
   const bf16_t* Ae = p.A;
   const bf16_t* Be = p.B;
+  auto row_i = [&](int i) { return C::ROWS_I * i + lane / (C::ROW / 16); };   // of the wave's rows
+  auto chunk = [&](int i) {
+    return C::ROW == 128 ? (lane & 7) ^ ((row_i(i) >> 1) & 7) : (lane & 3) ^ ((row_i(i) >> 2) & 3);
+  };
+  constexpr int kRunChunksA = C::RUN_A / 16, kRunChunksB = C::RUN_B / 16;
+  auto run_a = [&](int i) { return C::WK * wave + (64 * i + lane) / kRunChunksA; };
+  auto run_b = [&](int i) { return C::WK * wave + (64 * i + lane) / kRunChunksB; };
+  auto swizzle_b = [](int k) { return C::RUN_B == 512 ? 2 * (k & 3) : k & 2; };
   // of instruction i: K contiguous, the row's offset; rows contiguous, the column's
-  uint32_t a_off[kALoads], b_off[kBLoads];
-  int a_k[kALoads], b_k[kBLoads];   // rows contiguous: k of the stage
+  uint32_t a_off[C::ALOADS], b_off[C::BLOADS];
 #pragma unroll
-  for (int i = 0; i < kALoads; ++i) {
+  for (int i = 0; i < C::ALOADS; ++i) {
     if (kAT) {
-      a_k[i] = 8 * wave + 4 * i + (lane >> 4);
-      const int col = m0 + 16 * (((lane & 15) >> 1) ^ (2 * (a_k[i] & 3))) + 8 * (lane & 1);
+      const int col = m0 + 16 * (((lane & 15) >> 1) ^ (2 * (run_a(i) & 3))) + 8 * (lane & 1);
       a_off[i] = col < m_end ? 2u * (uint32_t)col : kOOR;
     } else {
-      const int m = m0 + 32 * wave + 16 * i + (lane >> 2);
+      const int m = m0 + kBM / 4 * wave + row_i(i);
       const uint32_t row = kAGather ? token(p.rows[row0 + min(m, M - 1)]) : (uint32_t)(m - m0);
-      a_off[i] = m < m_end ? row * (uint32_t)K * 2u + 16u * (uint32_t)lc : kOOR;
+      a_off[i] = m < m_end ? row * (uint32_t)K * 2u + 16u * (uint32_t)chunk(i) : kOOR;
     }
   }
 #pragma unroll
-  for (int i = 0; i < kBLoads; ++i) {
+  for (int i = 0; i < C::BLOADS; ++i) {
     if (kBT) {
-      b_k[i] = 8 * wave + 2 * i + (lane >> 5);
-      const int col = n0 + 16 * (((lane & 31) >> 1) ^ (2 * (b_k[i] & 3))) + 8 * (lane & 1);
+      const int c = (64 * i + lane) % kRunChunksB;
+      const int col = n0 + 16 * ((c >> 1) ^ swizzle_b(run_b(i))) + 8 * (c & 1);
       b_off[i] = col < N ? 2u * (uint32_t)col : kOOR;
     } else {
-      const int n = n0 + 64 * wave + 16 * i + (lane >> 2);
-      b_off[i] = n < N ? (uint32_t)n * (uint32_t)K * 2u + 16u * (uint32_t)lc : kOOR;
+      const int n = n0 + C::BN / 4 * wave + row_i(i);
+      b_off[i] = n < N ? (uint32_t)n * (uint32_t)K * 2u + 16u * (uint32_t)chunk(i) : kOOR;
     }
   }
   if (KIND == kDX) Ae += (size_t)(row0 + m0) * K;                              // dgu of the tile's rows
@@ -178,33 +193,34 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
   if (kWeightGrad && !kBGather) Be += (size_t)row0 * N;                        // dgu of the expert's rows
   if (!kWeightGrad) Be += (size_t)e * N * K;                                   // the expert's weight
 
-  // The tokens of a wave's eight k's of a stage (weight gradients), loaded a stage
-  // ahead as scalars: vector loads would be counted with the direct loads, and the
-  // wait for them would drain those.  From the last row on, up to seven words
-  // behind the expert's rows are read and not used.
-  uint32_t tok[8] = {}, tok_next[8] = {};
+  // The tokens of a wave's k's of a stage (weight gradients), loaded as scalars when
+  // the stage before has been asked for: vector loads would be counted with the
+  // direct loads, and the wait for them would drain those.  From the last row on, up
+  // to WK - 1 words behind the expert's rows are read and not used.
+  uint32_t tok[C::WK] = {};
   const __attribute__((address_space(4))) int32_t* const rows_s =
       (const __attribute__((address_space(4))) int32_t*)(p.rows + row0);
-  auto tokens = [&](int s, uint32_t (&t)[8]) {
+  auto tokens = [&](int s) {
     if constexpr (kWeightGrad) {
-      const int k = min(s * kBK + 8 * wave, K - 1);
+      const int k = min(s * C::BK + C::WK * wave, K - 1);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = token(rows_s[k + i]);
+      for (int i = 0; i < C::WK; ++i) tok[i] = token(rows_s[k + i]);
     }
   };
-  auto pick_a = [&](int i) {   // of the lane's k of A's instruction i
+  auto pick_a = [&](int i) {   // of the lane's k of A's instruction i: four runs
     const int g = lane >> 4;
     const uint32_t lo = g == 0 ? tok[4 * i] : tok[4 * i + 1], hi = g == 2 ? tok[4 * i + 2] : tok[4 * i + 3];
     return g < 2 ? lo : hi;
   };
-  auto pick_b = [&](int i) { return lane < 32 ? tok[2 * i] : tok[2 * i + 1]; };
+  auto pick_b = [&](int i) { return lane < 32 ? tok[2 * i] : tok[2 * i + 1]; };   // of B's: two runs
+  static_assert(!kWeightGrad || (C::RUN_A == 256 && C::RUN_B == 512), "the picks count the runs of an instruction");
 
-  // load q of a wave's six of stage st: A, then B
+  // load q of a wave's of stage st: A, then B
   auto load = [&](const bf16_t* base, int ld, bool t, bool gather, uint32_t off, int k_in, uint32_t token_row, int st,
-                  uint32_t lds) {
-    const int k0 = st * kBK;
+                  uint32_t lds) {   // k_in: the first k in the stage of the lane's bytes
+    const int k0 = st * C::BK;
     if (!t) {
-      dma16(rsrc_words(base, 0x7FFFFFFFu), k0 + 8 * lc < K ? off : kOOR, (uint32_t)k0 * 2u, lds);
+      dma16(rsrc_words(base, 0x7FFFFFFFu), k0 + k_in < K ? off : kOOR, (uint32_t)k0 * 2u, lds);
     } else if (gather) {
       const uint32_t voff = token_row * (uint32_t)ld * 2u + off;
       dma16(rsrc_words(base, 0x7FFFFFFFu), k0 + k_in < K && off != kOOR ? voff : kOOR, 0u, lds);
@@ -214,34 +230,32 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
     }
   };
   auto dma = [&](int st, int buf, int q) {
-    if (q < kALoads) {
-      load(Ae, p.M, kAT, kAGather, a_off[q], a_k[q], kAT && kAGather ? pick_a(q) : 0u, st,
-           lds0 + kA + buf * kABytes + (kAT ? (8 * wave + 4 * q) * 256 : (32 * wave + 16 * q) * 64));
+    if (q < C::ALOADS) {
+      load(Ae, p.M, kAT, kAGather, a_off[q], kAT ? run_a(q) : 8 * chunk(q), kAT && kAGather ? pick_a(q) : 0u, st,
+           lds0 + C::A + buf * C::ABYTES + wave * (C::ABYTES / 4) + 1024 * q);
     } else {
-      const int i = q - kALoads;
-      load(Be, N, kBT, kBGather, b_off[i], b_k[i], kBT && kBGather ? pick_b(i) : 0u, st,
-           lds0 + kB + buf * kBBytes + (kBT ? (8 * wave + 2 * i) * 512 : (64 * wave + 16 * i) * 64));
+      const int i = q - C::ALOADS;
+      load(Be, N, kBT, kBGather, b_off[i], kBT ? run_b(i) : 8 * chunk(i), kBT && kBGather ? pick_b(i) : 0u, st,
+           lds0 + C::B + buf * C::BBYTES + wave * (C::BBYTES / 4) + 1024 * i);
     }
   };
 
   // ---- fragment reads: step j has k = 16j .. 16j + 15 of the stage ----
   const int fr = lane & 31, fg = lane >> 5;
-  uint32_t a_rd[2], b_rd[4];   // K contiguous: of step j; rows contiguous: of fragment q
   const int t_r = (lane & 15) >> 2, t_half = (lane >> 4) & 1;
+  // K contiguous: of step 0, the others at ^ 32 j; rows contiguous: of fragment q
+  uint32_t a_rd[2], b_rd[C::NB];
+  const uint32_t xo = 16u * (uint32_t)(fg ^ (C::ROW == 128 ? (fr >> 1) & 7 : (fr >> 2) & 3));
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const uint32_t xo = 16u * (uint32_t)((2 * q + fg) ^ ((fr >> 2) & 3));
-    a_rd[q] = kAT ? (uint32_t)kA + (uint32_t)(8 * fg + t_r) * 256u + 8u * (uint32_t)(lane & 3) +
-                        32u * (uint32_t)((2 * ni * wm + 2 * q + t_half) ^ (2 * t_r))
-                  : (uint32_t)(kA + (32 * ni * wm + fr) * 64) + xo;
-    if (!kBT) b_rd[q] = (uint32_t)(kB + (128 * wn + fr) * 64) + xo;
-  }
-  if (kBT) {
+  for (int q = 0; q < 2; ++q)
+    a_rd[q] = kAT ? (uint32_t)(C::A + (8 * fg + t_r) * C::RUN_A + 8 * (lane & 3) +
+                               32 * ((2 * ni * wm + 2 * q + t_half) ^ (2 * t_r)))
+                  : (uint32_t)(C::A + (32 * ni * wm + fr) * C::ROW) + xo;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      b_rd[q] = (uint32_t)kB + (uint32_t)(8 * fg + t_r) * 512u + 8u * (uint32_t)(lane & 3) +
-                32u * (uint32_t)((8 * wn + 2 * q + t_half) ^ (2 * t_r));
-  }
+  for (int q = 0; q < C::NB; ++q)
+    b_rd[q] = kBT ? (uint32_t)(C::B + (8 * fg + t_r) * C::RUN_B + 8 * (lane & 3) +
+                               32 * ((C::WN / 16 * wn + 2 * q + t_half) ^ swizzle_b(t_r)))
+                  : (uint32_t)(C::B + (C::WN * wn + fr) * C::ROW) + xo;
   auto read_t = [&](uint32_t at, int run) -> u32x4_t {
     const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS3 s16x4_t*)(smem + at));
     const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS3 s16x4_t*)(smem + at + 4 * run));
@@ -249,83 +263,83 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
     return u32x4_t{l.x, l.y, h.x, h.y};
   };
   auto read_a = [&](int buf, int j, int q) -> u32x4_t {
-    if constexpr (kAT) return read_t(a_rd[q] + buf * kABytes + j * 16 * 256, 256);
-    else return *(const LDS3 u32x4_t*)(smem + a_rd[j] + buf * kABytes + q * 32 * 64);
+    if constexpr (kAT) return read_t(a_rd[q] + buf * C::ABYTES + j * 16 * C::RUN_A, C::RUN_A);
+    else return *(const LDS3 u32x4_t*)(smem + (a_rd[0] ^ (32 * j)) + buf * C::ABYTES + q * 32 * C::ROW);
   };
   auto read_b = [&](int buf, int j, int q) -> u32x4_t {
-    if constexpr (kBT) return read_t(b_rd[q] + buf * kBBytes + j * 16 * 512, 512);
-    else return *(const LDS3 u32x4_t*)(smem + b_rd[j] + buf * kBBytes + q * 32 * 64);
+    if constexpr (kBT) return read_t(b_rd[q] + buf * C::BBYTES + j * 16 * C::RUN_B, C::RUN_B);
+    else return *(const LDS3 u32x4_t*)(smem + (b_rd[0] ^ (32 * j)) + buf * C::BBYTES + q * 32 * C::ROW);
   };
 
-  f32x16_t acc[2][4];
+  f32x16_t acc[2][C::NB];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < C::NB; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-  // The loop for NI row blocks.  Step j of a stage in four slots: slot u reads the
+  // The loop for NI row blocks.  Step j of a stage in NB slots: slot u reads the
   // row fragment u (of the first NI) and the column fragment u for step j, issues
-  // a load of the stage kRing - 1 ahead, into the buffer that the stage before left
-  // at the last barrier, and the products of column block u of the step before.
+  // loads of the stage RING - 1 ahead, into the buffer that the stage before left at
+  // the last barrier, and the products of column block u of the step before.
   // PART: only the first nj column blocks have columns.
-  const int nj = min(4, max(0, (N - n0 - 128 * wn + 31) / 32));
+  const int nj = min(C::NB, max(0, (N - n0 - C::WN * wn + 31) / 32));
+  constexpr int kLoads = C::ALOADS + C::BLOADS;
+  static_assert(C::RING == 2 || (C::RING == 3 && kLoads == 6), "the waits count the loads of a stage");
+  static_assert(C::PER_SLOT * C::STEPS * C::NB >= kLoads, "every load has a slot");
   auto loop = [&](auto ni_c, auto part_c) {
     constexpr int NI = decltype(ni_c)::value;
     constexpr bool PART = decltype(part_c)::value;
-    u32x4_t fa0[2], fb0[4], fa1[2], fb1[4];
-    auto multiply = [&](int u, const u32x4_t (&fa)[2], const u32x4_t (&fb)[4]) {
+    u32x4_t fa[2][2], fb[2][C::NB];
+    auto multiply = [&](int u, int f) {
       if (PART && u >= nj) return;   // wave-uniform
 #pragma unroll
-      for (int i = 0; i < NI; ++i) acc[i][u] = mfma32x32x16(fa[i], fb[u], acc[i][u]);
+      for (int i = 0; i < NI; ++i) acc[i][u] = mfma32x32x16(fa[f][i], fb[f][u], acc[i][u]);
     };
-    auto step = [&](int s, int buf, int nbuf, int j, u32x4_t (&fa_rd)[2], u32x4_t (&fb_rd)[4], const u32x4_t (&fa_mm)[2],
-                    const u32x4_t (&fb_mm)[4], bool do_mfma) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (4 * j + u < kALoads + kBLoads && s + kRing - 1 < ns) dma(s + kRing - 1, nbuf, 4 * j + u);
-        __builtin_amdgcn_sched_barrier(0);
-        if (u < NI) fa_rd[u] = read_a(buf, j, u);
-        fb_rd[u] = read_b(buf, j, u);
-        if (do_mfma) multiply(u, fa_mm, fb_mm);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    };
-    int buf = 0, nbuf = kRing - 1;
+    int buf = 0, nbuf = C::RING - 1;
     for (int s = 0; s < ns; ++s) {
-      if (kWeightGrad) {
+      const bool more = s + C::RING - 1 < ns;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) tok[i] = tok_next[i];
-        tokens(s + kRing, tok_next);
+      for (int j = 0; j < C::STEPS; ++j) {
+#pragma unroll
+        for (int u = 0; u < C::NB; ++u) {
+          if (more) {
+#pragma unroll
+            for (int q = 0; q < C::PER_SLOT; ++q)
+              if (C::PER_SLOT * (C::NB * j + u) + q < kLoads) dma(s + C::RING - 1, nbuf, C::PER_SLOT * (C::NB * j + u) + q);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          if (u < NI) fa[j & 1][u] = read_a(buf, j, u);
+          fb[j & 1][u] = read_b(buf, j, u);
+          if (j > 0 || s > 0) multiply(u, (j & 1) ^ 1);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
-      step(s, buf, nbuf, 0, fa0, fb0, fa1, fb1, s > 0);
-      step(s, buf, nbuf, 1, fa1, fb1, fa0, fb0, true);
-      // stage s + 1 has landed when only the loads of the stage behind it, if any, are out
-      if (s + kRing - 1 < ns) asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)" ::: "memory");
+      tokens(s + C::RING);
+      // stage s is read, and stage s + 1 has landed: with a ring of three when only the
+      // loads of the stage behind it, if any, are out
+      if (C::RING == 3 && more) asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)" ::: "memory");
       else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
       __builtin_amdgcn_s_barrier();
       nbuf = buf;
-      buf = buf == kRing - 1 ? 0 : buf + 1;
+      buf = buf == C::RING - 1 ? 0 : buf + 1;
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) multiply(u, fa1, fb1);
+    for (int u = 0; u < C::NB; ++u) multiply(u, 1);
   };
   if (ns > 0) {
-    // prologue: stages 0 and 1
-    static_assert(kRing == 3 && kALoads + kBLoads == 6, "the waits count the six loads of one stage");
-    tokens(0, tok);
-    tokens(1, tok_next);
 #pragma unroll
-    for (int q = 0; q < kALoads + kBLoads; ++q) dma(0, 0, q);
+    for (int st = 0; st < C::RING - 1; ++st) {   // (out of range past the last stage)
+      tokens(st);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) tok[i] = tok_next[i];
-    tokens(2, tok_next);
-#pragma unroll
-    for (int q = 0; q < kALoads + kBLoads; ++q) dma(1, 1, q);   // (out of range where there is one stage)
-    asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
+      for (int q = 0; q < kLoads; ++q) dma(st, st, q);
+    }
+    tokens(C::RING - 1);
+    if (C::RING == 3) asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     using std::integral_constant;
-    if (n0 + kBN <= N) {
+    if (n0 + C::BN <= N) {
       if (ni == 2) loop(integral_constant<int, 2>{}, std::false_type{});
       else loop(integral_constant<int, 1>{}, std::false_type{});
     } else {
@@ -336,13 +350,13 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
   }
 
   // ---- epilogue.  Lane l, element v of block (i, j): row 32i + 8 (v / 4) + 4 (l
-  // / 32) + v % 4 of the wave's, column 32j + l % 32 of its 128.  Where a pair of
+  // / 32) + v % 4 of the wave's, column 32j + l % 32 of its WN.  Where a pair of
   // columns belongs together, lanes l and l ^ 1 exchange halves of two rows: the
   // even lane gets both columns of row v, the odd one those of row v + 1.
-  // bf16 results go through LDS (the stage buffers are free behind the last
-  // barrier), whose rows of 512 bytes then leave whole: 16-byte chunk c of row r
-  // at c ^ 4 (r % 2 + 2 (r / 4 % 2)), as the four rows that a wave touches at once
-  // would otherwise share their banks. ----
+  // GU's results go through LDS (the stage buffers are free behind the last
+  // barrier), whose rows of 2 BN bytes then leave whole: 16-byte chunk c of row r at
+  // c ^ swizzle(r), as some of the four rows that a wave touches at once would
+  // otherwise share their banks. ----
   const int row_w = 32 * ni * wm + 4 * fg;       // + 32 i + 8 (v / 4) + v % 4
   const bool odd = lane & 1;
   auto pair_of = [&](float v0, float v1, float& first, float& second) {
@@ -350,19 +364,10 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
     first = odd ? got : v0;
     second = odd ? v1 : got;
   };
-  auto swizzle = [](int r) { return 4 * ((r & 1) + 2 * ((r >> 2) & 1)); };
-  // word w (a pair of bf16, or a float) of row r: 128 words a row
-  auto word_at = [&](int r, int w) { return (uint32_t)(r * 512 + 16 * ((w >> 2) ^ swizzle(r)) + 4 * (w & 3)); };
-  // rows of 256 bf16 from LDS to out, which points at row m0, column n0
-  auto flush = [&](bf16_t* out, int ld) {
-#pragma unroll 8
-    for (int i = 0; i < 16; ++i) {
-      const int r = 32 * wave + 2 * i + (lane >> 5);
-      const int c = 8 * ((lane & 31) ^ swizzle(r));
-      const u32x4_t v = *(const LDS3 u32x4_t*)(smem + r * 512 + 16 * (lane & 31));
-      if (m0 + r < m_end && n0 + c < N) *reinterpret_cast<u32x4_t*>(out + (size_t)r * ld + c) = v;
-    }
-  };
+  constexpr int kEpi = 2 * C::BN;                  // bytes of a row of d and of dgu
+  auto swizzle = [](int r) { return kEpi == 512 ? 4 * ((r & 1) + 2 * ((r >> 2) & 1)) : r & 4; };
+  // word w (a pair of bf16, or a float) of row r
+  auto word_at = [&](int r, int w) { return (uint32_t)(r * kEpi + 16 * ((w >> 2) ^ swizzle(r)) + 4 * (w & 3)); };
   if constexpr (KIND == kD || KIND == kDX) {
     float* out = reinterpret_cast<float*>(p.out);
 #pragma unroll
@@ -373,8 +378,8 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
           const int m = m0 + row_w + 32 * i + 8 * (v >> 2) + (v & 3);
           if (m < m_end) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int n = n0 + 128 * wn + 32 * j + fr;
+            for (int j = 0; j < C::NB; ++j) {
+              const int n = n0 + C::WN * wn + 32 * j + fr;
               if (n < N) out[(size_t)(row0 + m) * N + n] = acc[i][j][v];
             }
           }
@@ -385,8 +390,8 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
     // rows v and v + 1 packed, then lanes l and l ^ 1 trade halves: the even lane has
     // both columns of row v, the odd one those of row v + 1
     const uint32_t pick = odd ? 0x03020706u : 0x05040100u;
-    bf16_t* out = reinterpret_cast<bf16_t*>(p.out) + ((size_t)e * M + m0 + row_w + (odd ? 1 : 0)) * N + n0 + 128 * wn + (fr & ~1);
-    const int rows_left = m_end - m0 - row_w - (odd ? 1 : 0), cols_left = N - n0 - 128 * wn - (fr & ~1);
+    bf16_t* out = reinterpret_cast<bf16_t*>(p.out) + ((size_t)e * M + m0 + row_w + (odd ? 1 : 0)) * N + n0 + C::WN * wn + (fr & ~1);
+    const int rows_left = m_end - m0 - row_w - (odd ? 1 : 0), cols_left = N - n0 - C::WN * wn - (fr & ~1);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (i < ni) {
@@ -395,7 +400,7 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
           const int r = 32 * i + 8 * (v >> 2) + (v & 3);
           bf16_t* at = out + (size_t)r * N;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < C::NB; ++j) {
             const uint32_t two = pack_bf16x2(acc[i][j][v], acc[i][j][v + 1]);
             const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)two, 0xB1, 0xF, 0xF, true);
             const uint32_t word = perm_b32(got, two, pick);
@@ -406,28 +411,32 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
     }
   } else {
     const int I = N / 2;
-    // the tile of d: 128 rows x 128 floats, in the place that dgu takes
+    constexpr int kChunks = kEpi / 16;
+    static_assert(kBM * (kEpi + 4) <= kLds, "");
+    LDS3 float* const s_w = (LDS3 float*)(smem + kBM * kEpi);
+    // the tile of d, 128 rows x BN / 2 floats in the place that dgu takes, and the rows' weights
     {
       const u32x4_t d_rs = rsrc_words(p.d + (size_t)(row0 + m0) * I, 0x7FFFFFFFu);
-#pragma unroll 8
-      for (int i = 0; i < 16; ++i) {
-        const int r = 32 * wave + 2 * i + (lane >> 5);
-        const int c = n0 / 2 + 4 * ((lane & 31) ^ swizzle(r));
+#pragma unroll 6
+      for (int i = 0; i < kChunks / 2; ++i) {
+        const int at = 64 * (kChunks / 2 * wave + i) + lane, r = at / kChunks;
+        const int c = n0 / 2 + 4 * ((at - r * kChunks) ^ swizzle(r));
         dma16(d_rs, m0 + r < m_end && c < I ? ((uint32_t)r * (uint32_t)I + (uint32_t)c) * 4u : kOOR, 0u,
-              lds0 + (32 * wave + 2 * i) * 512);
+              lds0 + 1024 * (kChunks / 2 * wave + i));
       }
+      if (tid < kBM) s_w[tid] = m0 + tid < m_end ? p.w[p.rows[row0 + m0 + tid]] : 0.f;
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
     }
-    float bg[4], bu[4];
+    float bg[C::NB], bu[C::NB];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = min(n0 + 128 * wn + 32 * j + (fr & ~1), N - 2);
+    for (int j = 0; j < C::NB; ++j) {
+      const int n = min(n0 + C::WN * wn + 32 * j + (fr & ~1), N - 2);
       const uint32_t b = *reinterpret_cast<const uint32_t*>(p.bias + (size_t)e * N + n);
       bg[j] = bf16lo(b);
       bu[j] = bf16hi(b);
     }
-    uint32_t wh[2][8][2];   // pairs j = 0, 1 and j = 2, 3
+    uint32_t wh[2][8][2];   // of two column blocks each
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (i < ni) {
@@ -435,14 +444,14 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
         for (int v = 0; v < 16; v += 2) {
           const int r = row_w + 32 * i + 8 * (v >> 2) + (v & 3) + (odd ? 1 : 0);
           const float w = s_w[r];
-          float dw = 0.f, whv[4];
+          float dw = 0.f, whv[4] = {};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < C::NB; ++j) {
             float gate, up;
             pair_of(acc[i][j][v], acc[i][j][v + 1], gate, up);
             gate += bg[j];
             up += bu[j];
-            LDS3 uint32_t* at = (LDS3 uint32_t*)(smem + word_at(r, 64 * wn + 16 * j + (fr >> 1)));
+            LDS3 uint32_t* at = (LDS3 uint32_t*)(smem + word_at(r, C::WN / 2 * wn + 16 * j + (fr >> 1)));
             const float d = __uint_as_float(*at);   // 0 past the last row or column
             // compare-selects, so that a NaN stays one
             const float g = gate > 7.0f ? 7.0f : gate;
@@ -469,9 +478,15 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
       }
     }
     __syncthreads();
-    flush(reinterpret_cast<bf16_t*>(p.out) + (size_t)(row0 + m0) * N + n0, N);
+    bf16_t* const dgu = reinterpret_cast<bf16_t*>(p.out) + (size_t)(row0 + m0) * N + n0;
+#pragma unroll 6
+    for (int i = 0; i < kChunks / 2; ++i) {
+      const int at = kThreads * i + tid, r = at / kChunks, c = 8 * ((at - r * kChunks) ^ swizzle(r));
+      const u32x4_t v = *(const LDS3 u32x4_t*)(smem + 16 * at);
+      if (m0 + r < m_end && n0 + c < N) *reinterpret_cast<u32x4_t*>(dgu + (size_t)r * N + c) = v;
+    }
     __syncthreads();
-    // wh: rows of 128 bf16, 16-byte chunk c of row r at c ^ 2 (r % 2 + 2 (r / 4 % 2))
+    // wh: rows of BN / 2 bf16, 16-byte chunk c of row r at c ^ swizzle(r) / 2
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (i < ni) {
@@ -479,20 +494,20 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
         for (int v = 0; v < 16; v += 2) {
           const int r = row_w + 32 * i + 8 * (v >> 2) + (v & 3) + (odd ? 1 : 0);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int c = 64 * wn + 16 * j + (fr >> 1);
-            *(LDS3 uint16_t*)(smem + r * 256 + 16 * ((c >> 3) ^ (swizzle(r) / 2)) + 2 * (c & 7)) =
+          for (int j = 0; j < C::NB; ++j) {
+            const int c = C::WN / 2 * wn + 16 * j + (fr >> 1);
+            *(LDS3 uint16_t*)(smem + r * C::BN + 16 * ((c >> 3) ^ (swizzle(r) / 2)) + 2 * (c & 7)) =
                 (uint16_t)(wh[i][v / 2][j / 2] >> (16 * (j & 1)));
           }
         }
       }
     }
     __syncthreads();
-#pragma unroll 8
-    for (int i = 0; i < 8; ++i) {
-      const int r = 32 * wave + 4 * i + (lane >> 4);
-      const int c = n0 / 2 + 8 * ((lane & 15) ^ (swizzle(r) / 2));
-      const u32x4_t v = *(const LDS3 u32x4_t*)(smem + r * 256 + 16 * (lane & 15));
+#pragma unroll
+    for (int i = 0; i < kChunks / 4; ++i) {
+      const int at = kThreads * i + tid, r = at / (kChunks / 2);
+      const int c = n0 / 2 + 8 * ((at - r * (kChunks / 2)) ^ (swizzle(r) / 2));
+      const u32x4_t v = *(const LDS3 u32x4_t*)(smem + 16 * at);
       if (m0 + r < m_end && c < I) *reinterpret_cast<u32x4_t*>(p.wh + (size_t)(row0 + m0 + r) * I + c) = v;
     }
   }
@@ -574,8 +589,7 @@ __device__ __forceinline__ void column_sum(const Sum& p, const Args& a, int e, i
 template <int KIND>
 __global__ __launch_bounds__(kThreads, 2) void backward_gemm_kernel(const Args p) {
   __shared__ __align__(1024) char smem[kLds];
-  __shared__ float s_w[KIND == kGU ? kBM : 1];   // the rows' routing weights
-  product<KIND>(p, blockIdx.x, (LDS3 char*)smem, (LDS3 float*)s_w);
+  product<KIND>(p, blockIdx.x, (LDS3 char*)smem);
 }
 
 // What only needs dgu, wh and dl, in one launch: DX's tiles, which are long, the
@@ -592,7 +606,7 @@ __global__ __launch_bounds__(kThreads, 2) void backward_tail_kernel(const Tail p
   LDS3 char* smem = (LDS3 char*)smem_g;
   const int group = blockIdx.x / kXcds;
   if (group < p.begin[0]) {
-    product<kDX>(p.dx, blockIdx.x, smem, nullptr);
+    product<kDX>(p.dx, blockIdx.x, smem);
   } else if (group < p.begin[1]) {
     int item = blockIdx.x - p.begin[0] * kXcds;
     const int parts = p.sum[0].parts + p.sum[1].parts + p.sum[2].parts;
@@ -607,9 +621,9 @@ __global__ __launch_bounds__(kThreads, 2) void backward_tail_kernel(const Tail p
       column_sum<true>(p.sum[second ? 2 : 1], p.wgu, e, second ? item - p.sum[1].parts : item, smem);
     }
   } else if (group < p.begin[2]) {
-    product<kWGU>(p.wgu, blockIdx.x - p.begin[1] * kXcds, smem, nullptr);
+    product<kWGU>(p.wgu, blockIdx.x - p.begin[1] * kXcds, smem);
   } else {
-    product<kWD>(p.wd, blockIdx.x - p.begin[2] * kXcds, smem, nullptr);
+    product<kWD>(p.wd, blockIdx.x - p.begin[2] * kXcds, smem);
   }
 }
 
@@ -620,7 +634,8 @@ uint32_t per_token(int k) { return k == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32)
 // groups of eight blocks of a product; fills in the tile counts
 template <int KIND>
 int64_t groups(Args& a, int64_t S) {
-  a.tiles_n = (a.N + kBN - 1) / kBN;
+  constexpr int BN = TileOf<KIND>::BN;
+  a.tiles_n = (a.N + BN - 1) / BN;
   int64_t tiles;
   if (KIND == kWGU || KIND == kWD) {
     a.tiles_m = (a.M + kBM - 1) / kBM;
@@ -652,7 +667,10 @@ hipError_t launch_backward_d(const void* dy, const void* Wd, const int32_t* cnt,
   return launch<kD>(a, T * k, stream);
 }
 
-int backward_dw_parts(int I) { return (2 * I + kBN - 1) / kBN * 2; }
+int backward_dw_parts(int I) {
+  constexpr int BN = TileOf<kGU>::BN;
+  return (2 * I + BN - 1) / BN * 2;
+}
 
 hipError_t launch_backward_gu(const void* x, const void* Wgu, const void* bgu, const float* w, const float* d,
                               const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T, int H, int E,
