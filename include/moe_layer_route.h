@@ -675,8 +675,8 @@ MOE_API int moe_down_int4(const void* h, const void* Wd_q, const void* Wd_s, con
 MOE_API int moe_quantize_rows_mxfp4(const void* a, int64_t R, int32_t K, void* codes, void* scales, void* stream);
 
 /* moe_dequantize_rows_mxfp4 -- the rows' values in bf16 [R][K] (exact: every
- * value of the format up to 2^127 is a bf16; a larger one, from scales above
- * 252, which the quantiser does not write, is infinite). */
+ * value of the format below 2^128 is a bf16; a larger one, which only scales above
+ * 252 reach and the quantiser does not write, is infinite). */
 MOE_API int moe_dequantize_rows_mxfp4(const void* codes, const void* scales, int64_t R, int32_t K, void* out,
                                       void* stream);
 

@@ -1,6 +1,5 @@
-// The block's backward pass beside its products: gradients of the routing
-// weights and the router's logits, column sums (biases and router), and the sum
-// of a token's input gradients.
+// The block's backward pass beside its products and column sums: gradients of the
+// routing weights and the router's logits, and the sum of a token's input gradients.
 //
 // xserv "Phase 19: gpt-oss-20b MoE support", section 2 (router -> top-k softmax
 // -> experts -> weighted sum).  For token t with picks j, weights w_j = softmax
@@ -8,9 +7,9 @@
 //   dw_j = o_j . dy = sum over i of h_j d_j + bd[e_j] . dy    (o_j = h_j . Wd + bd)
 //   dl_j = w_j (dw_j - sum over i of w_i dw_i)
 //   dx   = sum over j of dxs_j + dl_j Wr[e_j]
-//   dWr[e] = sum over e's slots of dl x, dbr[e] = sum of dl,
-//   dbd[e] = sum of w dy, dbgu[e] = sum of dgu.
 // All sums are float32 in a fixed order; the gradients are rounded once to bf16.
+// Both are bound by bytes: 16384 slots of H = 2880, dl 25 us (a wave a token, each
+// reads dy once and four rows of bd), dx 43 us, 5 TB/s.
 #include "device_common.h"
 #include "launch.h"
 

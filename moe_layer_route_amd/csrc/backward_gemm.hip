@@ -19,23 +19,35 @@
 // operands of bf16 products, as h is in the forward pass; d stays float32, it
 // is multiplied elementwise.
 //
-// One kernel for the five: tiles of 128 x 256, K stages of 32, four waves in a 2 x
-// 2 grid, each 64 x 128 = 2 x 4 blocks of v_mfma_f32_32x32x16_bf16; two workgroups
-// a CU, so that one's loads, exchange and stores run beside the other's products.
-// An operand lies in memory either with K contiguous (a stage has 64 bytes of
-// every row) or with its rows or columns contiguous (a stage is 32 runs of 256 or
-// 512 bytes, one for each k: Wgu in GU, all operands of the weight gradients,
-// whose K is the expert's rows).  Both kinds go from HBM/L2 to LDS by direct loads
-// of 16 bytes a lane into a ring of three stages; fragments of the second kind are
-// read by the transposing LDS read (ds_read_b64_tr_b16: 16 lanes read 4 k's x 16
-// columns and each gets the four k's of one column).
-//   Stage layout, K contiguous: row r's 16-byte chunk c at slot c ^ ((r >> 2) &
-//   3) of its 64 bytes.  Rows contiguous: run k's 32-byte piece p at p ^ 2 (k & 3)
-//   of its run: the four k's of a transposing read fall on different banks.
+// One kernel for the five: four waves in a 2 x 2 grid, each 64 rows x 96 or 128
+// columns = 2 x 3 or 2 x 4 blocks of v_mfma_f32_32x32x16_bf16; two workgroups a CU,
+// so that one's loads, exchange and stores run beside the other's products.
+//   An operand lies in memory either with K contiguous or with its rows or columns
+//   contiguous (a run for each k: Wgu in GU, both operands of the weight gradients,
+//   whose K is the expert's rows).  Both kinds go from HBM/L2 to LDS by direct loads
+//   of 16 bytes a lane; fragments of the second kind are read by the transposing LDS
+//   read (ds_read_b64_tr_b16: 16 lanes read 4 k's x 16 columns and each gets the four
+//   k's of one column).
+//   D, GU, DX: tiles of 128 x 192, K stages of 64, a ring of two (80 KB).  A stage
+//   has 128 bytes of a row: with stages of 32 every load of 64 bytes is a request to
+//   L2 of its own (D of T = 4096, E = 32: 54 M requests and 392 us, against 29 M and
+//   331).
+//   WGU, WD: tiles of 128 x 256, K stages of 32, a ring of three (72 KB): runs are
+//   whole lines anyway, an expert's rows are few stages, and the columns of the wider
+//   tile are read by fewer of them (with 128 x 192 and 64: T = 4096 all gradients of
+//   weights 1.25 -> 1.6 ms).
+//   Measured against both and not kept: 256 x 256 by eight waves, one workgroup a CU,
+//   stages of 64 (ring of two) or 32 (ring of four): the whole pass at T = 4096, E =
+//   32 2.82 and 2.85 ms against 2.84, at T = 512 1.19 and 1.12 against 0.99.
 //   Tile heights: an expert's rows are split evenly over its tiles of at most 128,
 //   in steps of 64, and a tile of 64 ni rows has ni row blocks a wave: the loop is
 //   built for each ni, and once more for the tiles that reach past the last
 //   column, whose waves leave out the column blocks without any.
+// What bounds it (H = I = 2880, E = 32): at T = 4096, 512 rows an expert, the load
+// path and the clock (1.9 to 2.0 GHz of 2.4): D 331 us (820 TFLOP/s), GU 668 (814), the
+// rest 1.85 ms with the column sums (735), matrix pipes 38 to 43% busy, without the
+// products 376 / 609 / 1714 us (measured before D, GU and DX had the tiles above).  At
+// T = 512, 64 rows, memory: 4.2 GB of weights read and gradients written in 0.95 ms.
 #include "device_common.h"
 #include "launch.h"
 
@@ -64,7 +76,6 @@ struct Tile {
   static constexpr int A = 0, B = RING * ABYTES;        // A and B of buffer b at b * ABYTES, b * BBYTES
   static constexpr int LDS = B + RING * BBYTES;
   static constexpr int ROW = BK * 2;                    // K contiguous: bytes of a row and stage
-  static constexpr int ROWS_I = 1024 / ROW;             // and rows an instruction
   static constexpr int RUN_A = kBM * 2, RUN_B = BN * 2; // rows contiguous: bytes of a run
   static constexpr int ALOADS = ABYTES / 4096, BLOADS = BBYTES / 4096;   // a wave and stage
 };
@@ -104,7 +115,7 @@ template <int KIND>
 __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* smem) {
   constexpr bool kWeightGrad = KIND == kWGU || KIND == kWD;
   using C = TileOf<KIND>;
-  static_assert(C::LDS <= kLds, "");
+  static_assert(C::LDS <= kLds, "two workgroups a CU");
   constexpr bool kAT = kWeightGrad, kBT = kWeightGrad || KIND == kGU;   // rows / columns contiguous
   constexpr bool kAGather = KIND == kD || KIND == kGU || KIND == kWGU, kBGather = KIND == kWD;
   const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
@@ -150,16 +161,16 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
 
   // ---- direct-load assignments.  K contiguous: wave w fills the w-th quarter of the
   // rows, 1 KB an instruction, a lane 16 bytes: chunk c of a row is at c ^ ((r >> 1)
-  // & 7) of its 128 bytes (c ^ ((r >> 2) & 3) of 64).  Rows contiguous: wave w fills
-  // the w-th quarter of the runs; 32-byte piece p of run k is at p ^ 2 (k & 3), in
-  // runs of 384 bytes, where two k's are half the banks apart, at p ^ (k & 2).  What
-  // is past the edges is sent out of range and lands as 0. ----
+  // & 7) of its 128 bytes.  Rows contiguous: wave w fills the w-th quarter of the
+  // runs; 32-byte piece p of run k is at p ^ 2 (k & 3), in runs of 384 bytes, where
+  // two k's are half the banks apart, at p ^ (k & 2): a transposing read's four k's
+  // fall on different banks.  What is past the edges is sent out of range and lands
+  // as 0. ----
   const bf16_t* Ae = p.A;
   const bf16_t* Be = p.B;
-  auto row_i = [&](int i) { return C::ROWS_I * i + lane / (C::ROW / 16); };   // of the wave's rows
-  auto chunk = [&](int i) {
-    return C::ROW == 128 ? (lane & 7) ^ ((row_i(i) >> 1) & 7) : (lane & 3) ^ ((row_i(i) >> 2) & 3);
-  };
+  auto row_i = [&](int i) { return 8 * i + (lane >> 3); };   // of the wave's rows
+  auto chunk = [&](int i) { return (lane & 7) ^ ((row_i(i) >> 1) & 7); };
+  static_assert(kWeightGrad || C::ROW == 128, "eight rows an instruction");
   constexpr int kRunChunksA = C::RUN_A / 16, kRunChunksB = C::RUN_B / 16;
   auto run_a = [&](int i) { return C::WK * wave + (64 * i + lane) / kRunChunksA; };
   auto run_b = [&](int i) { return C::WK * wave + (64 * i + lane) / kRunChunksB; };
@@ -245,7 +256,7 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
   const int t_r = (lane & 15) >> 2, t_half = (lane >> 4) & 1;
   // K contiguous: of step 0, the others at ^ 32 j; rows contiguous: of fragment q
   uint32_t a_rd[2], b_rd[C::NB];
-  const uint32_t xo = 16u * (uint32_t)(fg ^ (C::ROW == 128 ? (fr >> 1) & 7 : (fr >> 2) & 3));
+  const uint32_t xo = 16u * (uint32_t)(fg ^ ((fr >> 1) & 7));
 #pragma unroll
   for (int q = 0; q < 2; ++q)
     a_rd[q] = kAT ? (uint32_t)(C::A + (8 * fg + t_r) * C::RUN_A + 8 * (lane & 3) +
@@ -354,9 +365,10 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
   // columns belongs together, lanes l and l ^ 1 exchange halves of two rows: the
   // even lane gets both columns of row v, the odd one those of row v + 1.
   // GU's results go through LDS (the stage buffers are free behind the last
-  // barrier), whose rows of 2 BN bytes then leave whole: 16-byte chunk c of row r at
-  // c ^ swizzle(r), as some of the four rows that a wave touches at once would
-  // otherwise share their banks. ----
+  // barrier), whose rows of 384 bytes then leave whole: 16-byte chunk c of row r at
+  // c ^ (r & 4), as two of the four rows that a wave touches at once would otherwise
+  // share their banks.  The weights' gradients leave from the registers, 64 bytes a
+  // row and instruction, past the caches (through LDS: the same time). ----
   const int row_w = 32 * ni * wm + 4 * fg;       // + 32 i + 8 (v / 4) + v % 4
   const bool odd = lane & 1;
   auto pair_of = [&](float v0, float v1, float& first, float& second) {
@@ -365,9 +377,8 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
     second = odd ? v1 : got;
   };
   constexpr int kEpi = 2 * C::BN;                  // bytes of a row of d and of dgu
-  auto swizzle = [](int r) { return kEpi == 512 ? 4 * ((r & 1) + 2 * ((r >> 2) & 1)) : r & 4; };
   // word w (a pair of bf16, or a float) of row r
-  auto word_at = [&](int r, int w) { return (uint32_t)(r * kEpi + 16 * ((w >> 2) ^ swizzle(r)) + 4 * (w & 3)); };
+  auto word_at = [&](int r, int w) { return (uint32_t)(r * kEpi + 16 * ((w >> 2) ^ (r & 4)) + 4 * (w & 3)); };
   if constexpr (KIND == kD || KIND == kDX) {
     float* out = reinterpret_cast<float*>(p.out);
 #pragma unroll
@@ -420,7 +431,7 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
 #pragma unroll 6
       for (int i = 0; i < kChunks / 2; ++i) {
         const int at = 64 * (kChunks / 2 * wave + i) + lane, r = at / kChunks;
-        const int c = n0 / 2 + 4 * ((at - r * kChunks) ^ swizzle(r));
+        const int c = n0 / 2 + 4 * ((at - r * kChunks) ^ (r & 4));
         dma16(d_rs, m0 + r < m_end && c < I ? ((uint32_t)r * (uint32_t)I + (uint32_t)c) * 4u : kOOR, 0u,
               lds0 + 1024 * (kChunks / 2 * wave + i));
       }
@@ -481,12 +492,12 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
     bf16_t* const dgu = reinterpret_cast<bf16_t*>(p.out) + (size_t)(row0 + m0) * N + n0;
 #pragma unroll 6
     for (int i = 0; i < kChunks / 2; ++i) {
-      const int at = kThreads * i + tid, r = at / kChunks, c = 8 * ((at - r * kChunks) ^ swizzle(r));
+      const int at = kThreads * i + tid, r = at / kChunks, c = 8 * ((at - r * kChunks) ^ (r & 4));
       const u32x4_t v = *(const LDS3 u32x4_t*)(smem + 16 * at);
       if (m0 + r < m_end && n0 + c < N) *reinterpret_cast<u32x4_t*>(dgu + (size_t)r * N + c) = v;
     }
     __syncthreads();
-    // wh: rows of BN / 2 bf16, 16-byte chunk c of row r at c ^ swizzle(r) / 2
+    // wh: rows of BN / 2 bf16, 16-byte chunk c of row r at c ^ (r / 2 & 2)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (i < ni) {
@@ -496,7 +507,7 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
 #pragma unroll
           for (int j = 0; j < C::NB; ++j) {
             const int c = C::WN / 2 * wn + 16 * j + (fr >> 1);
-            *(LDS3 uint16_t*)(smem + r * C::BN + 16 * ((c >> 3) ^ (swizzle(r) / 2)) + 2 * (c & 7)) =
+            *(LDS3 uint16_t*)(smem + r * C::BN + 16 * ((c >> 3) ^ ((r >> 1) & 2)) + 2 * (c & 7)) =
                 (uint16_t)(wh[i][v / 2][j / 2] >> (16 * (j & 1)));
           }
         }
@@ -506,7 +517,7 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
 #pragma unroll
     for (int i = 0; i < kChunks / 4; ++i) {
       const int at = kThreads * i + tid, r = at / (kChunks / 2);
-      const int c = n0 / 2 + 8 * ((at - r * (kChunks / 2)) ^ (swizzle(r) / 2));
+      const int c = n0 / 2 + 8 * ((at - r * (kChunks / 2)) ^ ((r >> 1) & 2));
       const u32x4_t v = *(const LDS3 u32x4_t*)(smem + 16 * at);
       if (m0 + r < m_end && c < I) *reinterpret_cast<u32x4_t*>(p.wh + (size_t)(row0 + m0 + r) * I + c) = v;
     }
@@ -514,8 +525,9 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
 }
 
 // ---------------------------------------------------------------------------
-// Column sums over an expert's slots, of rows V[..] times a factor of the slot: one
-// workgroup per expert and 512 columns, its four waves take every fourth row, eight
+// Column sums over an expert's slots, of rows V[..] times a factor of the slot: dbgu
+// sums dgu, dbd w dy, dWr dl x and dbr dl.  One workgroup per expert and 512
+// columns, its four waves take every fourth row, eight
 // columns a lane, eight rows in flight; the sums meet in LDS in a fixed order.
 // ---------------------------------------------------------------------------
 constexpr int kSumWaves = kThreads / kWave;
@@ -594,7 +606,9 @@ __global__ __launch_bounds__(kThreads, 2) void backward_gemm_kernel(const Args p
 
 // What only needs dgu, wh and dl, in one launch: DX's tiles, which are long, the
 // column sums, then the tiles of the weight gradients, which are short and fill the
-// places that DX's last round leaves.  Blocks come in groups of eight, one a XCD.
+// places that DX's last round leaves (DX and others in turns: no gain; five launches:
+// T = 512, E = 32 1155 -> 1080 us, T = 2047, E = 128 4257 -> 4059).  Blocks come in
+// groups of eight, one a XCD.
 struct Tail {
   Args dx, wgu, wd;
   Sum sum[3];            // dbgu, dbd, dWr

@@ -149,7 +149,7 @@ hipError_t launch_add_rmsnorm(const void* x, const void* residual, const void* g
 // The backward pass (backward_gemm.hip, backward.hip): d [S][I] = dy . Wd^T; then
 // dgu, wh and the parts of dw [backward_dw_parts(I)][S]; dl [T][k]; dxs [S][H] with
 // the gradients of the weights (the experts' four or the router's two may be NULL);
-// and dx.  The weights' gradients read up to 60 bytes behind rows (other parts of
+// and dx.  The weights' gradients read up to 28 bytes behind rows (other parts of
 // the workspace) without using them.
 hipError_t launch_backward_d(const void* dy, const void* Wd, const int32_t* cnt, const int32_t* off, const int32_t* rows,
                              int64_t T, int H, int E, int k, int I, float* d, hipStream_t stream);

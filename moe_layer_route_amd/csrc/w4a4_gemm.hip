@@ -24,6 +24,12 @@
 //   scales' word of block 2 (l / 32) + j: picked by the instruction itself.
 //   Stage s: its loads were issued during stage s - 2; each wave waits for its own
 //   at the end of stage s - 1 and the barrier makes all of them visible.
+// What bounds it: the load path and the products in turn.  2880 x 5760, 512 rows an
+// expert, 32 experts: 253 us, 2.1 PFLOP/s, matrix pipes 26% busy at 2.1 GHz, a wave
+// waiting for 28% of its time and for its turn to issue for 38% (down 170 us, 1.6
+// PFLOP/s).  One expert of 16384 rows: 222 us, without the loads 143, without the
+// products 176, without both 89.  Tiles of 256 x 256 by four waves took 316 us where
+// these take 256, by eight 293.
 #include "launch.h"
 #include "mxfp4_device.h"
 
