@@ -367,8 +367,8 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
   // GU's results go through LDS (the stage buffers are free behind the last
   // barrier), whose rows of 384 bytes then leave whole: 16-byte chunk c of row r at
   // c ^ (r & 4), as two of the four rows that a wave touches at once would otherwise
-  // share their banks.  The weights' gradients leave from the registers, 64 bytes a
-  // row and instruction, past the caches (through LDS: the same time). ----
+  // share their banks.  The weights' gradients leave from the registers, past the
+  // caches (through LDS: the same time). ----
   const int row_w = 32 * ni * wm + 4 * fg;       // + 32 i + 8 (v / 4) + v % 4
   const bool odd = lane & 1;
   auto pair_of = [&](float v0, float v1, float& first, float& second) {
@@ -398,11 +398,14 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
       }
     }
   } else if constexpr (kWeightGrad) {
-    // rows v and v + 1 packed, then lanes l and l ^ 1 trade halves: the even lane has
-    // both columns of row v, the odd one those of row v + 1
-    const uint32_t pick = odd ? 0x03020706u : 0x05040100u;
-    bf16_t* out = reinterpret_cast<bf16_t*>(p.out) + ((size_t)e * M + m0 + row_w + (odd ? 1 : 0)) * N + n0 + C::WN * wn + (fr & ~1);
-    const int rows_left = m_end - m0 - row_w - (odd ? 1 : 0), cols_left = N - n0 - C::WN * wn - (fr & ~1);
+    // Of two column blocks j, j + 1 the even lane of a pair takes both columns of block
+    // j, the odd one those of j + 1: an instruction stores whole lines, 64 columns of a
+    // row.  Rows v and v + 1 are packed, so one exchange serves both.
+    static_assert(C::NB % 2 == 0, "pairs of column blocks");
+    const uint32_t pick_a = odd ? 0x01000504u : 0x05040100u, pick_b = odd ? 0x03020706u : 0x07060302u;
+    const int col = C::WN * wn + (odd ? 32 : 0) + (fr & ~1);
+    bf16_t* out = reinterpret_cast<bf16_t*>(p.out) + ((size_t)e * M + m0 + row_w) * N + n0 + col;
+    const int rows_left = m_end - m0 - row_w, cols_left = N - n0 - col;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (i < ni) {
@@ -411,11 +414,16 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
           const int r = 32 * i + 8 * (v >> 2) + (v & 3);
           bf16_t* at = out + (size_t)r * N;
 #pragma unroll
-          for (int j = 0; j < C::NB; ++j) {
-            const uint32_t two = pack_bf16x2(acc[i][j][v], acc[i][j][v + 1]);
-            const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)two, 0xB1, 0xF, 0xF, true);
-            const uint32_t word = perm_b32(got, two, pick);
-            if (r < rows_left && 32 * j < cols_left) __builtin_nontemporal_store(word, reinterpret_cast<uint32_t*>(at + 32 * j));
+          for (int j = 0; j < C::NB; j += 2) {
+            const uint32_t t0 = pack_bf16x2(acc[i][j][v], acc[i][j][v + 1]);
+            const uint32_t t1 = pack_bf16x2(acc[i][j + 1][v], acc[i][j + 1][v + 1]);
+            const uint32_t mine = odd ? t1 : t0;
+            const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)(odd ? t0 : t1), 0xB1, 0xF, 0xF, true);
+            if (32 * j < cols_left) {
+              if (r < rows_left) __builtin_nontemporal_store(perm_b32(got, mine, pick_a), reinterpret_cast<uint32_t*>(at + 32 * j));
+              if (r + 1 < rows_left)
+                __builtin_nontemporal_store(perm_b32(got, mine, pick_b), reinterpret_cast<uint32_t*>(at + N + 32 * j));
+            }
           }
         }
       }
