@@ -135,6 +135,9 @@ SIZES = [
     (20, 2, 1, 104, 2880, None),    # the full intermediate size
     (400, 1, 1, 328, 200, None),    # 400 rows of one expert: wide tiles of the gradients, ragged both ways
     (777, 3, 2, 712, 392, None),    # several of them in both directions
+    (50, 2, 1, 192, 96, None),      # exactly a tile of 192 columns
+    (130, 2, 2, 200, 192, None),    # two rows past a tile of 128; eight columns past a tile
+    (65, 1, 1, 448, 288, None),     # one row past half a tile; whole K stages
 ]
 
 
@@ -286,3 +289,48 @@ def test_repeats_graph_and_other_stream():
         graph.replay()
         torch.cuda.synchronize()
         same(g)
+
+
+def test_same_expert_twice_in_a_row():
+    """A token that names an expert twice has two slots there."""
+    _need_gpu()
+    T, E, k, H, I = 60, 3, 3, 136, 104
+    inputs, (ids, w) = _inputs(T, E, H, I, 35), _routing(T, E, k, 36)
+    ids[::2, 2] = ids[::2, 0]
+    _check(inputs, ids, w, _run(inputs, ids, w))
+
+
+def test_two_calls_at_once():
+    """Two streams, each with its own workspace, in turn without a wait between them."""
+    _need_gpu()
+    E, k, H, I = 4, 2, 264, 136
+    calls = []
+    for T in (90, 333):
+        inputs, (ids, w) = _inputs(T, E, H, I, 37), _routing(T, E, k, 38)
+        calls.append([dev(v) for v in inputs] + [torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda()])
+    want = [{n: bf16_bits(v) for n, v in binding.moe_backward(*c).items()} for c in calls]
+    spaces = [binding.alloc_workspace_backward(c[0].shape[0], H, E, k, I) for c in calls]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[binding.moe_backward(*c, workspace=ws, stream=s) for c, ws, s in zip(calls, spaces, streams)] for _ in range(6)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for g, bits in zip(pair, want):
+            assert all((bf16_bits(g[n]) == bits[n]).all() for n in NAMES)
+
+
+def test_rows_past_four_gib():
+    """Slots whose rows of d and of its gradients lie beyond 2^32 bytes: the last tokens' dx, alone and at the end of a
+    batch, are the same bits (every row is summed in the same order)."""
+    _need_gpu()
+    T, n, E, k, H, I = 200000, 100, 2, 2, 64, 2880
+    small, (ids, w) = _inputs(n, E, H, I, 39), _routing(n, E, k, 40)
+    part = [dev(v) for v in small] + [torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda()]
+    alone = bf16_bits(binding.moe_backward(*part, router=False, experts=False)["dx"])
+    dy, x = (torch.randn((T, H), device="cuda").bfloat16() for _ in range(2))
+    ids_all = torch.tensor([0, 1], dtype=torch.int32, device="cuda").repeat(T, 1)
+    w_all = torch.full((T, k), 0.5, device="cuda")
+    for whole, piece in ((dy, part[0]), (x, part[1]), (ids_all, part[7]), (w_all, part[8])):
+        whole[T - n:] = piece
+    got = binding.moe_backward(dy, x, *part[2:7], ids_all, w_all, router=False, experts=False)["dx"]
+    assert (bf16_bits(got[T - n:]) == alone).all()

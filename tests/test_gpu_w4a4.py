@@ -420,3 +420,95 @@ def test_other_stream():
     s.synchronize()
     assert (bf16_bits(y) == want).all() and (bf16_bits(y2) == want).all()
     assert (host_f64(back) == orc.mxfp4_dequantize_rows(*orc.mxfp4_quantize_rows(host_f64(g[0])))).all()
+
+
+@pytest.mark.parametrize("K", [32, 672])
+def test_products_of_many_tiles(K):
+    """So many tiles that the GEMM takes its wide ones: ragged experts, some of one row, against 64 bits."""
+    _need_gpu()
+    T, E, k, N = 4096, 32, 4, 2880
+    rng = np.random.default_rng(K)
+    # experts of very different size: the first few take most of the tokens
+    p = 1.0 / (1.0 + np.arange(E)) ** 1.5
+    ids = np.argsort(rng.gumbel(size=(T, E)) + np.log(p), axis=1)[:, -k:].astype(np.int32)
+    ids[ids == E - 1] = -1
+    ids[5, 0] = E - 1                                          # one row
+    cnt, off, rows, pos = binding.moe_permute(_up(ids), E)
+    at, rows_h = off.cpu().numpy(), rows.cpu().numpy()
+    q, s = _matrix(E, K, N, 9)
+    b = d.normal_bf16((E, N), 0.5, 9, 1, E, N)
+    W = [torch.from_numpy(orc.mxfp4_dequantize(q[e], s[e]).T.copy()).cuda() for e in range(E)]
+    bias = torch.from_numpy(orc.widen(b)).cuda()
+    hq, sh = binding.moe_quantize_rows_mxfp4(torch.randn((T * k, K), device="cuda").bfloat16() * 3)
+    o = binding.moe_down_w4a4(hq, sh, _up(q), _up(s), dev(b), cnt, off, T, k, path="gemm").double()
+    h = torch.from_numpy(orc.mxfp4_dequantize_rows(hq.cpu().numpy(), sh.cpu().numpy())).cuda()
+    for e in range(E):
+        part = slice(int(at[e]), int(at[e + 1]))
+        tol = (K / 64 + 9) * ULP * (h[part].abs() @ W[e].abs() + bias[e].abs())
+        assert bool(((o[part] - (h[part] @ W[e] + bias[e])).abs() <= tol).all()), f"o of expert {e}"
+    xq, sx = binding.moe_quantize_rows_mxfp4(torch.randn((T, K), device="cuda").bfloat16() * float(60.0 / np.sqrt(K)))
+    gq, gs = binding.moe_gate_up_w4a4(xq, sx, _up(q), _up(s), dev(b), cnt, off, rows, k=k, path="gemm")
+    gq, gs = gq.cpu().numpy(), gs.cpu().numpy()
+    x = torch.from_numpy(orc.mxfp4_dequantize_rows(xq.cpu().numpy(), sx.cpu().numpy())).cuda()
+    for e in list(range(0, E, 5)) + [E - 1]:
+        part = slice(int(at[e]), int(at[e + 1]))
+        a = x[torch.from_numpy(rows_h[part] // k).cuda().long()]
+        u = ((K / 64 + 9) * ULP * (a.abs() @ W[e].abs() + bias[e].abs())).cpu().numpy()
+        want = orc.clamped_glu((a @ W[e] + bias[e]).cpu().numpy())
+        tol = 8.8 * u[:, 0::2] + 7.0 * u[:, 1::2] + 2.0 ** -20 * np.abs(want)
+        _check_h(gq[part], gs[:, part], want, tol, f"h of expert {e}")
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_outputs_past_four_gib(path):
+    """Rows of o that lie beyond 2^32 bytes."""
+    _need_gpu()
+    S, K, N = 400000, 64, 2880
+    q, s = _matrix(1, K, N, 10)
+    bd = d.normal_bf16((1, N), 0.5, 10, 1, 1, N)
+    hq, sh = binding.moe_quantize_rows_mxfp4(torch.randn((S, K), device="cuda").bfloat16())
+    cnt, off, rows, pos = binding.moe_permute(torch.zeros((S, 1), dtype=torch.int32, device="cuda"), 1)
+    o = binding.moe_down_w4a4(hq, sh, _up(q), _up(s), dev(bd), cnt, off, S, 1, path=path)
+    pick = np.r_[0:3, 372820:372840, S - 70:S]
+    h = orc.mxfp4_dequantize_rows(hq.cpu().numpy()[pick], sh.cpu().numpy()[:, pick])
+    W, b = orc.mxfp4_dequantize(q[0], s[0]).T, orc.widen(bd[0])
+    got = o[torch.from_numpy(pick).cuda()].cpu().numpy().astype(np.float64)
+    _within(got, h @ W + b, (K / 64 + 9) * ULP * (np.abs(h) @ np.abs(W) + np.abs(b)), "o")
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_two_calls_at_once(path):
+    """Two streams, each with its own workspace, in turn without a wait between them."""
+    _need_gpu()
+    E, k, H, I = 8, 4, 352, 224
+    sets = [[_up(a) for a in _block(T, E, k, H, I, 17)] for T in (64, 301)]
+    want = [bf16_bits(binding.moe_forward_w4a4(*g, k=k, path=path)) for g in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    spaces = [binding.alloc_workspace_w4a4(g[0].shape[0], H, E, k, I) for g in sets]
+    torch.cuda.synchronize()
+    ys = [[binding.moe_forward_w4a4(*g, k=k, workspace=w, path=path, stream=s)
+           for g, w, s in zip(sets, spaces, streams)] for _ in range(8)]
+    torch.cuda.synchronize()
+    for pair in ys:
+        for y, bits in zip(pair, want):
+            assert (bf16_bits(y) == bits).all()
+
+
+def test_same_expert_twice_in_a_row():
+    """Stage calls with an expert that a token names twice: two slots, two rows of h and of o."""
+    _need_gpu()
+    T, E, k, H, I = 40, 4, 3, 160, 96
+    ids = _routing(T, E, k, 18)
+    ids[:, 2] = ids[:, 0]
+    cnt, off, rows, pos = binding.moe_permute(_up(ids), E)
+    gq, gs = _matrix(E, H, 2 * I, 19)
+    dq, ds = _matrix(E, I, H, 20)
+    z = torch.zeros((E, 2 * I), dtype=torch.bfloat16, device="cuda"), torch.zeros((E, H), dtype=torch.bfloat16, device="cuda")
+    xq, sx = _rows(T, H, 21)
+    for path in PATHS:
+        hq, sh = binding.moe_gate_up_w4a4(_up(xq), _up(sx), _up(gq), _up(gs), z[0], cnt, off, rows, k=k, path=path)
+        o = binding.moe_down_w4a4(hq, sh, _up(dq), _up(ds), z[1], cnt, off, T, k, path=path)
+        at = pos.view(T, k).long()
+        assert (hq[at[:, 0]] == hq[at[:, 2]]).all() and (o[at[:, 0]] == o[at[:, 2]]).all()
+        assert (at[:, 0] != at[:, 2]).all()
