@@ -48,15 +48,13 @@
 // rest 1.85 ms with the column sums (735), matrix pipes 38 to 43% busy, without the
 // products 376 / 609 / 1714 us (measured before D, GU and DX had the tiles above).  At
 // T = 512, 64 rows, memory: 4.2 GB of weights read and gradients written in 0.95 ms.
-#include "device_common.h"
+#include "backward_device.h"
 #include "launch.h"
 
 #include <type_traits>
 
 namespace moe {
 namespace {
-
-#define LDS3 __attribute__((address_space(3)))
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
@@ -156,7 +154,7 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
   const int m_end = min(M, m0 + height);
   const int ni = m_end - m0 > 64 ? 2 : 1;           // row blocks of 32 a wave
   auto token = [&](int slot) {
-    return p.per_token ? __umulhi((uint32_t)slot, p.per_token) : (uint32_t)slot;
+    return token_of((uint32_t)slot, p.per_token);
   };
 
   // ---- direct-load assignments.  K contiguous: wave w fills the w-th quarter of the
@@ -532,126 +530,47 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
   }
 }
 
-// ---------------------------------------------------------------------------
-// Column sums over an expert's slots, of rows V[..] times a factor of the slot: dbgu
-// sums dgu, dbd w dy, dWr dl x and dbr dl.  One workgroup per expert and 512
-// columns, its four waves take every fourth row, eight
-// columns a lane, eight rows in flight; the sums meet in LDS in a fixed order.
-// ---------------------------------------------------------------------------
-constexpr int kSumWaves = kThreads / kWave;
-constexpr int kSumAhead = 8;
-constexpr int kSumCols = 8 * kWave;
-
-struct Sum {
-  const bf16_t* V;
-  const float* factor;   // of the slot; null: 1, and V has the rows of the permuted order, else the tokens'
-  int C, parts;          // columns, pieces of 512 of them (0: not asked for)
-  bf16_t *out, *out_factor;   // [E][C]; [E], the sum of the factors, or null
-};
-
-template <bool GATHER>
-__device__ __forceinline__ void column_sum(const Sum& p, const Args& a, int e, int piece, LDS3 char* smem) {
-  LDS3 float (*part)[8][kWave] = (LDS3 float (*)[8][kWave])smem;
-  LDS3 float* part_f = (LDS3 float*)(smem + kSumWaves * 8 * kWave * 4);
-  const int lane = threadIdx.x & (kWave - 1);
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int n = a.cnt[e], row0 = a.off[e], C = p.C;
-  const int col = piece * kSumCols + 8 * lane;
-  const int at = min(col, C - 8);   // C % 8 == 0
-  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum_f = 0.f;
-  for (int m0 = wave; m0 < n; m0 += kSumWaves * kSumAhead) {
-    u32x4_t v[kSumAhead];
-    float f[kSumAhead];
-#pragma unroll
-    for (int i = 0; i < kSumAhead; ++i) {
-      const int at_m = row0 + min(m0 + kSumWaves * i, n - 1);
-      const uint32_t slot = GATHER ? (uint32_t)a.rows[at_m] : 0u;
-      const size_t row = GATHER ? (a.per_token ? __umulhi(slot, a.per_token) : slot) : (size_t)at_m;
-      f[i] = GATHER ? p.factor[slot] : 1.f;
-      v[i] = ld16(p.V + row * C + at);
-    }
-#pragma unroll
-    for (int i = 0; i < kSumAhead; ++i) {
-      if (m0 + kSumWaves * i < n) {   // wave-uniform
-        sum_f += f[i];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          sum[2 * q] = fmaf(f[i], bf16lo(v[i][q]), sum[2 * q]);
-          sum[2 * q + 1] = fmaf(f[i], bf16hi(v[i][q]), sum[2 * q + 1]);
-        }
-      }
-    }
-  }
-#pragma unroll
-  for (int q = 0; q < 8; ++q) part[wave][q][lane] = sum[q];
-  if (lane == 0) part_f[wave] = sum_f;
-  __syncthreads();
-  if (wave == 0) {
-    float s[8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      s[q] = part[0][q][lane];
-#pragma unroll
-      for (int w = 1; w < kSumWaves; ++w) s[q] += part[w][q][lane];
-    }
-    if (col < C)
-      *reinterpret_cast<u32x4_t*>(p.out + (size_t)e * C + col) =
-          u32x4_t{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7])};
-    if (p.out_factor && piece == 0 && lane == 0) {
-      float f = part_f[0];
-#pragma unroll
-      for (int w = 1; w < kSumWaves; ++w) f += part_f[w];
-      p.out_factor[e] = (bf16_t)f32_to_bf16(f);
-    }
-  }
-}
-
 template <int KIND>
 __global__ __launch_bounds__(kThreads, 2) void backward_gemm_kernel(const Args p) {
   __shared__ __align__(1024) char smem[kLds];
   product<KIND>(p, blockIdx.x, (LDS3 char*)smem);
 }
 
-// What only needs dgu, wh and dl, in one launch: DX's tiles, which are long, the
-// column sums, then the tiles of the weight gradients, which are short and fill the
-// places that DX's last round leaves (DX and others in turns: no gain; five launches:
+// What needs dgu and wh, in one launch: DX's tiles, which are long, the column sums and
+// dl, then the tiles of the weight gradients, which are short and fill the places
+// that DX's last round leaves (DX and others in turns: no gain; launches of their own:
 // T = 512, E = 32 1155 -> 1080 us, T = 2047, E = 128 4257 -> 4059).  Blocks come in
 // groups of eight, one a XCD.
 struct Tail {
   Args dx, wgu, wd;
-  Sum sum[3];            // dbgu, dbd, dWr
-  int begin[4];          // first group of the sums, WGU, WD, and the end
+  Slots slots;
+  Sum dbgu, dbd;
+  Dl dl;
+  int begin[5];          // first group of the sums, dl, WGU, WD, and the end
 };
 
 __global__ __launch_bounds__(kThreads, 2) void backward_tail_kernel(const Tail p) {
   __shared__ __align__(1024) char smem_g[kLds];
   LDS3 char* smem = (LDS3 char*)smem_g;
+  static_assert(kSumWaves * kWave == kThreads && kSumLds <= kLds, "column sums");
   const int group = blockIdx.x / kXcds;
   if (group < p.begin[0]) {
     product<kDX>(p.dx, blockIdx.x, smem);
   } else if (group < p.begin[1]) {
-    int item = blockIdx.x - p.begin[0] * kXcds;
-    const int parts = p.sum[0].parts + p.sum[1].parts + p.sum[2].parts;
-    const int e = item / parts;
+    const int item = blockIdx.x - p.begin[0] * kXcds, parts = p.dbgu.parts + p.dbd.parts;
+    const int e = item / parts, piece = item - e * parts;
     if (e >= p.dx.E) return;                       // workgroup-uniform
-    item -= e * parts;
-    if (item < p.sum[0].parts) {
-      column_sum<false>(p.sum[0], p.wgu, e, item, smem);
-    } else {
-      item -= p.sum[0].parts;
-      const bool second = item >= p.sum[1].parts;
-      column_sum<true>(p.sum[second ? 2 : 1], p.wgu, e, second ? item - p.sum[1].parts : item, smem);
-    }
+    if (piece < p.dbgu.parts) column_sum<false>(p.dbgu, p.slots, e, piece, smem);
+    else column_sum<true>(p.dbd, p.slots, e, piece - p.dbgu.parts, smem);
   } else if (group < p.begin[2]) {
-    product<kWGU>(p.wgu, blockIdx.x - p.begin[1] * kXcds, smem);
+    const int64_t t = (int64_t)(blockIdx.x - p.begin[1] * kXcds) * (kThreads / kWave) + threadIdx.x / kWave;
+    if (t < p.dl.T) token_dl(p.dl, t, threadIdx.x & (kWave - 1));
+  } else if (group < p.begin[3]) {
+    product<kWGU>(p.wgu, blockIdx.x - p.begin[2] * kXcds, smem);
   } else {
-    product<kWD>(p.wd, blockIdx.x - p.begin[2] * kXcds, smem);
+    product<kWD>(p.wd, blockIdx.x - p.begin[3] * kXcds, smem);
   }
 }
-
-// slot / k for the slots that can be (T H below 2^30 and H >= 8: below 2^30) as the
-// high word of slot times 2^32 / k rounded up: off by less than slot / 2^30 / k
-uint32_t per_token(int k) { return k == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + k - 1) / k); }
 
 // groups of eight blocks of a product; fills in the tile counts
 template <int KIND>
@@ -704,10 +623,11 @@ hipError_t launch_backward_gu(const void* x, const void* Wgu, const void* bgu, c
   return launch<kGU>(a, T * k, stream);
 }
 
-hipError_t launch_backward_tail(const void* dy, const void* x, const void* Wgu, const float* w, const void* dgu,
-                                const void* wh, const float* dl, const int32_t* cnt, const int32_t* off,
-                                const int32_t* rows, int64_t T, int H, int E, int k, int I, float* dxs, void* dWgu,
-                                void* dbgu, void* dWd, void* dbd, void* dWr, void* dbr, hipStream_t stream) {
+hipError_t launch_backward_tail(const void* dy, const void* x, const void* Wgu, const void* bd, const int32_t* ids,
+                                const float* w, const float* dw_part, const void* dgu, const void* wh,
+                                const int32_t* cnt, const int32_t* off, const int32_t* rows, const int32_t* pos,
+                                int64_t T, int H, int E, int k, int I, float* dxs, float* dl, void* dWgu, void* dbgu,
+                                void* dWd, void* dbd, hipStream_t stream) {
   const int64_t S = T * k;
   Tail p{};
   Args a{};
@@ -716,17 +636,17 @@ hipError_t launch_backward_tail(const void* dy, const void* x, const void* Wgu, 
   p.dx.A = (const bf16_t*)dgu, p.dx.B = (const bf16_t*)Wgu, p.dx.N = H, p.dx.K = 2 * I, p.dx.out = dxs;
   p.wgu.A = (const bf16_t*)x, p.wgu.B = (const bf16_t*)dgu, p.wgu.M = H, p.wgu.N = 2 * I, p.wgu.out = dWgu;
   p.wd.A = (const bf16_t*)wh, p.wd.B = (const bf16_t*)dy, p.wd.M = I, p.wd.N = H, p.wd.out = dWd;
-  auto sum = [](const void* V, const float* factor, int C, void* out, void* out_factor) {
-    return Sum{(const bf16_t*)V, factor, C, out ? (C + kSumCols - 1) / kSumCols : 0, (bf16_t*)out, (bf16_t*)out_factor};
-  };
-  p.sum[0] = sum(dgu, nullptr, 2 * I, dbgu, nullptr);
-  p.sum[1] = sum(dy, w, H, dbd, nullptr);
-  p.sum[2] = sum(x, dl, H, dWr, dbr);
-  const int64_t sums = (int64_t)E * (p.sum[0].parts + p.sum[1].parts + p.sum[2].parts);
-  int64_t at = groups<kDX>(p.dx, S);
-  const int64_t after[4] = {0, (sums + kXcds - 1) / kXcds, dWgu ? groups<kWGU>(p.wgu, S) : 0, dWd ? groups<kWD>(p.wd, S) : 0};
-  for (int i = 0; i < 4; ++i) {
-    at += after[i];
+  p.slots = Slots{cnt, off, rows, a.per_token};
+  p.dbgu = sum_of(dgu, nullptr, 2 * I, dbgu, nullptr);
+  p.dbd = sum_of(dy, w, H, dbd, nullptr);
+  p.dl = Dl{(const bf16_t*)dy, (const bf16_t*)bd, ids, pos, w, dw_part, backward_dw_parts(I), H, k, T, dl};
+  auto in_groups = [](int64_t blocks) { return (blocks + kXcds - 1) / kXcds; };
+  const int64_t n[5] = {groups<kDX>(p.dx, S), in_groups((int64_t)E * (p.dbgu.parts + p.dbd.parts)),
+                        in_groups((T + kThreads / kWave - 1) / (kThreads / kWave)), dWgu ? groups<kWGU>(p.wgu, S) : 0,
+                        dWd ? groups<kWD>(p.wd, S) : 0};
+  int64_t at = 0;
+  for (int i = 0; i < 5; ++i) {
+    at += n[i];
     if (at * kXcds > 0x7FFFFFFF) return hipErrorInvalidValue;
     p.begin[i] = (int)at;
   }

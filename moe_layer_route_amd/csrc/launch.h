@@ -147,24 +147,25 @@ hipError_t launch_add_rmsnorm(const void* x, const void* residual, const void* g
                               void* residual_out, void* y, void* codes, float* scales, hipStream_t stream);
 
 // The backward pass (backward_gemm.hip, backward.hip): d [S][I] = dy . Wd^T; then
-// dgu, wh and the parts of dw [backward_dw_parts(I)][S]; dl [T][k]; dxs [S][H] with
-// the gradients of the weights (the experts' four or the router's two may be NULL);
-// and dx.  The weights' gradients read up to 28 bytes behind rows (other parts of
-// the workspace) without using them.
+// dgu, wh and the parts of dw [backward_dw_parts(I)][S]; dxs [S][H] and dl [T][k]
+// with the gradients of the experts' weights (or NULL); and dx with the router's (or
+// NULL).  The weights' gradients read up to 28 bytes behind rows (other parts of the
+// workspace) without using them.
 hipError_t launch_backward_d(const void* dy, const void* Wd, const int32_t* cnt, const int32_t* off, const int32_t* rows,
                              int64_t T, int H, int E, int k, int I, float* d, hipStream_t stream);
 int backward_dw_parts(int I);
 hipError_t launch_backward_gu(const void* x, const void* Wgu, const void* bgu, const float* w, const float* d,
                               const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T, int H, int E,
                               int k, int I, void* dgu, void* wh, float* dw_part, hipStream_t stream);
-hipError_t launch_backward_dl(const void* dy, const void* bd, const int32_t* ids, const int32_t* pos, const float* w,
-                              const float* dw_part, int parts, int64_t T, int H, int k, float* dl, hipStream_t stream);
-hipError_t launch_backward_tail(const void* dy, const void* x, const void* Wgu, const float* w, const void* dgu,
-                                const void* wh, const float* dl, const int32_t* cnt, const int32_t* off,
-                                const int32_t* rows, int64_t T, int H, int E, int k, int I, float* dxs, void* dWgu,
-                                void* dbgu, void* dWd, void* dbd, void* dWr, void* dbr, hipStream_t stream);
-hipError_t launch_backward_dx_sum(const float* dxs, const int32_t* ids, const int32_t* pos, const float* dl,
-                                  const void* Wr, int64_t T, int H, int k, void* dx, hipStream_t stream);
+hipError_t launch_backward_tail(const void* dy, const void* x, const void* Wgu, const void* bd, const int32_t* ids,
+                                const float* w, const float* dw_part, const void* dgu, const void* wh,
+                                const int32_t* cnt, const int32_t* off, const int32_t* rows, const int32_t* pos,
+                                int64_t T, int H, int E, int k, int I, float* dxs, float* dl, void* dWgu, void* dbgu,
+                                void* dWd, void* dbd, hipStream_t stream);
+hipError_t launch_backward_dx_sum(const float* dxs, const void* x, const int32_t* ids, const int32_t* cnt,
+                                  const int32_t* off, const int32_t* rows, const int32_t* pos, const float* dl,
+                                  const void* Wr, int64_t T, int H, int E, int k, void* dx, void* dWr, void* dbr,
+                                  hipStream_t stream);
 
 // measurement probes (probe.hip)
 hipError_t launch_probe_mfma(int iters, int workgroups, float* out, hipStream_t stream);

@@ -1643,13 +1643,12 @@ int moe_backward(const void* dy, const void* x, const void* Wr, const void* Wgu,
   if (int st = hip_status(fn, moe::launch_backward_gu(x, Wgu, bgu, topk_w, wide, cnt, off, rows, T, H, E, k, I, dgu, wh,
                                                       dw_part, s)))
     return st;
-  if (int st = hip_status(fn, moe::launch_backward_dl(dy, bd, topk_ids, pos, topk_w, dw_part,
-                                                      moe::backward_dw_parts(I), T, H, k, dl, s)))
+  if (int st = hip_status(fn, moe::launch_backward_tail(dy, x, Wgu, bd, topk_ids, topk_w, dw_part, dgu, wh, cnt, off,
+                                                        rows, pos, T, H, E, k, I, wide, dl, dWgu, dbgu, dWd, dbd, s)))
     return st;
-  if (int st = hip_status(fn, moe::launch_backward_tail(dy, x, Wgu, topk_w, dgu, wh, dl, cnt, off, rows, T, H, E, k, I,
-                                                        wide, dWgu, dbgu, dWd, dbd, dWr, dbr, s)))
+  if (int st = hip_status(fn, moe::launch_backward_dx_sum(wide, x, topk_ids, cnt, off, rows, pos, dl, Wr, T, H, E, k, dx,
+                                                          dWr, dbr, s)))
     return st;
-  if (int st = hip_status(fn, moe::launch_backward_dx_sum(wide, topk_ids, pos, dl, Wr, T, H, k, dx, s))) return st;
   return ok();
 }
 
