@@ -738,15 +738,17 @@ static int run_down_int4(const char* fn, const void* h, const void* Wq, const vo
   return hip_status(fn, moe::launch_int4_down(h, Wq, Ws, Wz, bd, cnt, off, T, H, E, k, I, G, o, s));
 }
 
-// Router, padding and permutation of the int4 blocks and of the FP8 block behind
-// the norm; o is scratch until down writes it.
+// Router, padding and permutation of the int4 and W4A4 blocks and of the FP8 block
+// behind the norm; o is scratch until down writes it.  With xq, x as MXFP4 rows too.
 static int route_and_permute(const char* fn, const void* x, const void* Wr, const void* br, int64_t T, int32_t H,
                              int32_t E, int32_t k, const int32_t* n_valid, int32_t e_begin, int32_t n_local, float* o,
                              int32_t* ids, float* w, int32_t* cnt, int32_t* off, int32_t* rows, int32_t* pos,
-                             hipStream_t s) {
+                             hipStream_t s, void* xq = nullptr, void* sx = nullptr) {
   if (moe::takes_few(T, H, E, k))
     return hip_status(fn, moe::launch_few_route(x, Wr, br, T, H, E, k, n_valid, e_begin, n_local,
-                                                reinterpret_cast<double*>(o), ids, w, cnt, off, rows, pos, s));
+                                                reinterpret_cast<double*>(o), ids, w, cnt, off, rows, pos, s, xq, sx));
+  if (xq)
+    if (int st = hip_status(fn, moe::launch_mxfp4_rows(x, T, H, xq, sx, s))) return st;
   if (int st = hip_status(fn, moe::launch_route(x, Wr, br, T, H, E, k, ids, w, route_method(T), s))) return st;
   if (n_valid)
     if (int st = hip_status(fn, moe::launch_mask_padding(ids, w, T, k, n_valid, s))) return st;
@@ -1448,9 +1450,9 @@ static int forward_w4a4(const char* fn, const void* x, const void* Wr, const voi
   void *xq = ws + F.xq, *sx = ws + F.sx, *hq = ws + F.hq, *sh = ws + F.sh;
   hipStream_t s = (hipStream_t)stream;
 
-  if (int st = route_and_permute(fn, x, Wr, br, T, H, E, k, n_valid, e_begin, n_local, o, ids, w, cnt, off, rows, pos, s))
+  if (int st = route_and_permute(fn, x, Wr, br, T, H, E, k, n_valid, e_begin, n_local, o, ids, w, cnt, off, rows, pos, s,
+                                 xq, sx))
     return st;
-  if (int st = hip_status(fn, moe::launch_mxfp4_rows(x, T, H, xq, sx, s))) return st;
   if (int st = run_gate_up_w4a4(fn, xq, sx, Wgu_q, Wgu_s, bgu, cnt, off, rows, T, H, n_local, k, I, hq, sh, path, s))
     return st;
   if (int st = run_down_w4a4(fn, hq, sh, Wd_q, Wd_s, bd, cnt, off, T, H, n_local, k, I, o, path, s)) return st;

@@ -52,6 +52,34 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
   return max(v, moved<kMirror>(v));
 }
 
+// MXFP4 codes and scales of values 128 group .. of row r of a [R][K], by a row of 16
+// lanes (this one is l): a quad of lanes has one block, the row one scale word.
+// Whole rows of lanes call it.
+__device__ __forceinline__ void quantize_128(const bf16_t* __restrict__ a, int64_t r, int64_t R, int K, int group,
+                                             int l, uint32_t* __restrict__ codes, uint32_t* __restrict__ scales) {
+  constexpr int kRowRor4 = 0x124, kRowRor8 = 0x128;   // rotations within a row of 16 lanes
+  const int k = 128 * group + 8 * l;
+  const bool in = r < R && k < K;
+  u32x4_t v = u32x4_t{0u, 0u, 0u, 0u};
+  if (in) v = ld16(a + r * K + k);
+  uint32_t m = max(max(abs_max2(v.x), abs_max2(v.y)), max(abs_max2(v.z), abs_max2(v.w)));
+  m = max(m, moved<kXor1>(m));
+  m = max(m, moved<kXor2>(m));
+  const uint32_t s = mx_scale_byte(m);
+  const float scale = ue8m0_to_f32(s);
+  uint32_t c = encode2<0>(0u, v.x, scale);
+  c = encode2<1>(c, v.y, scale);
+  c = encode2<2>(c, v.z, scale);
+  c = encode2<3>(c, v.w, scale);
+  if (s == 255) c = 0;
+  if (in) codes[(r * K + k) / 8] = c;
+  // the quads' scales, blocks past K 0, as one word
+  uint32_t w = in ? s << (8 * (l / 4)) : 0u;
+  w |= moved<kRowRor4>(w);
+  w |= moved<kRowRor8>(w);
+  if (l == 0 && r < R) scales[(int64_t)group * R + r] = w;
+}
+
 __device__ __forceinline__ i32x8_t fp4_operand(u32x4_t v) {
   return i32x8_t{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
 }

@@ -21,33 +21,11 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRowsPerWg = kThreads / 16;
 
-constexpr int kRowRor4 = 0x124, kRowRor8 = 0x128;   // rotations within a row of 16 lanes
-
 __global__ __launch_bounds__(kThreads) void mxfp4_rows_kernel(const bf16_t* __restrict__ a, int64_t r_begin,
                                                              int64_t R, int K, uint32_t* __restrict__ codes,
                                                              uint32_t* __restrict__ scales) {
   const int64_t r = r_begin + (int64_t)blockIdx.x * kRowsPerWg + threadIdx.x / 16;
-  const int l = threadIdx.x % 16, group = blockIdx.y;
-  const int k = 128 * group + 8 * l;
-  const bool in = r < R && k < K;
-  u32x4_t v = u32x4_t{0u, 0u, 0u, 0u};
-  if (in) v = ld16(a + r * K + k);
-  uint32_t m = max(max(abs_max2(v.x), abs_max2(v.y)), max(abs_max2(v.z), abs_max2(v.w)));
-  m = max(m, moved<kXor1>(m));
-  m = max(m, moved<kXor2>(m));
-  const uint32_t s = mx_scale_byte(m);
-  const float scale = ue8m0_to_f32(s);
-  uint32_t c = encode2<0>(0u, v.x, scale);
-  c = encode2<1>(c, v.y, scale);
-  c = encode2<2>(c, v.z, scale);
-  c = encode2<3>(c, v.w, scale);
-  if (s == 255) c = 0;
-  if (in) codes[(r * K + k) / 8] = c;
-  // the quads' scales, blocks past K 0, as one word
-  uint32_t w = in ? s << (8 * (l / 4)) : 0u;
-  w |= moved<kRowRor4>(w);
-  w |= moved<kRowRor8>(w);
-  if (l == 0 && r < R) scales[(int64_t)group * R + r] = w;
+  quantize_128(a, r, R, K, blockIdx.y, threadIdx.x % 16, codes, scales);
 }
 
 __global__ __launch_bounds__(kThreads) void mxfp4_rows_back_kernel(const uint32_t* __restrict__ codes,

@@ -10,6 +10,7 @@
 // one workgroup then picks and permutes.
 #include "device_common.h"
 #include "launch.h"
+#include "mxfp4_device.h"
 #include "route_key.h"
 #include "wave_reduce.h"
 
@@ -81,6 +82,9 @@ __global__ __launch_bounds__(kLogitThreads) void few_logits_kernel(const bf16_t*
 // slots than threads), as in the permutation's own kernel: equal ids of a wave by
 // ballots over the id's bits, counts per wave and expert, and their sums in the
 // order of the waves.
+//   The workgroups behind the first quantise x to MXFP4 rows where the experts take
+// those (a launch of its own beside an idle card: one token 27.5 -> 25.7 us for the
+// W4A4 block, 64 tokens 97.7 -> 96.2).
 constexpr int kMaxTokens = 64;
 constexpr int kMaxThreads = 16 * kMaxTokens;
 constexpr int kSlotWaves = kMaxTokens * MOE_MAX_K_DEV / kWave;
@@ -89,7 +93,13 @@ template <int KEYS>
 __global__ __launch_bounds__(kMaxThreads) void few_decide_kernel(
     const double* __restrict__ logits, int T, int E, int k, const int32_t* __restrict__ n_valid, int e_begin,
     int n_local, int32_t* __restrict__ ids, float* __restrict__ w, int32_t* __restrict__ cnt,
-    int32_t* __restrict__ off, int32_t* __restrict__ rows, int32_t* __restrict__ pos) {
+    int32_t* __restrict__ off, int32_t* __restrict__ rows, int32_t* __restrict__ pos, const bf16_t* __restrict__ x,
+    int H, uint32_t* __restrict__ codes, uint32_t* __restrict__ scales) {
+  if (blockIdx.x > 0) {   // workgroup-uniform
+    const int item = ((int)blockIdx.x - 1) * ((int)blockDim.x / 16) + (int)threadIdx.x / 16;
+    quantize_128(x, item % T, item / T < (H + 127) / 128 ? T : 0, H, item / T, threadIdx.x & 15, codes, scales);
+    return;
+  }
   __shared__ int count[kSlotWaves][MOE_MAX_E_DEV];   // per wave and expert, then what precedes it
   __shared__ int first[MOE_MAX_E_DEV];               // an expert's count, then its first row
   __shared__ int slot_id[kMaxThreads];
@@ -200,13 +210,16 @@ bool takes_few(int64_t T, int H, int E, int k) { return T <= kMaxTokens && (int6
 
 hipError_t launch_few_route(const void* x, const void* Wr, const void* br, int64_t T, int H, int E, int k,
                             const int32_t* n_valid, int e_begin, int n_local, double* logits, int32_t* ids, float* w,
-                            int32_t* cnt, int32_t* off, int32_t* rows, int32_t* pos, hipStream_t stream) {
+                            int32_t* cnt, int32_t* off, int32_t* rows, int32_t* pos, hipStream_t stream, void* xq,
+                            void* sx) {
   if (T > kMaxTokens) return hipErrorInvalidValue;
   hipError_t err = launch_few_logits(x, Wr, br, T, H, E, logits, stream);
   if (err != hipSuccess) return err;
-  const int waves = (int)(T + 3) / 4;
-  hipLaunchKernelGGL(E <= 64 ? few_decide_kernel<4> : few_decide_kernel<16>, dim3(1), dim3(waves * kWave), 0, stream,
-                     logits, (int)T, E, k, n_valid, e_begin, n_local, ids, w, cnt, off, rows, pos);
+  const int waves = (int)(T + 3) / 4, groups = (H + 127) / 128;
+  const int more = xq ? ((int)T * groups + 4 * waves - 1) / (4 * waves) : 0;
+  hipLaunchKernelGGL(E <= 64 ? few_decide_kernel<4> : few_decide_kernel<16>, dim3((unsigned)(1 + more)),
+                     dim3(waves * kWave), 0, stream, logits, (int)T, E, k, n_valid, e_begin, n_local, ids, w, cnt, off,
+                     rows, pos, (const bf16_t*)x, H, (uint32_t*)xq, (uint32_t*)sx);
   return hipGetLastError();
 }
 
