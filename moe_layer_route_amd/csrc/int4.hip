@@ -18,6 +18,7 @@
 //   scales bf16 [E][ceil(K/G)][N], zeros uint8 of the same shape.
 #include "device_common.h"
 #include "int4_device.h"
+#include "few_slots.h"
 #include "launch.h"
 #include "route_key.h"
 #include "wave_reduce.h"
@@ -178,47 +179,6 @@ __device__ __forceinline__ bool nth_live_expert(const int32_t* __restrict__ cnt,
 //             it.  Two slots of one expert read its weights twice.
 enum Mode { kGrouped, kSlots };
 
-// The decision of a call in slots: logits in; ids, weights and the identity
-// permutation out (gate_up), ids in (down).
-struct Slots {
-  const double* logits;   // [T][E]
-  int32_t* ids;           // [T][k]
-  float* w;               // [T][k]
-  int32_t* pos;           // [T k]
-  int k;
-};
-
-// The picks of one token, best first (float32 logit descending, index
-// ascending), up to and with pick `last`; wl takes their float64 logits.
-__device__ __forceinline__ void pick_experts(const double* __restrict__ logits, int E, int last, int lane,
-                                             int (&sel)[MOE_MAX_K_DEV], double (&wl)[MOE_MAX_K_DEV]) {
-  constexpr int kPer = MOE_MAX_E_DEV / kWave;
-  double l[kPer];
-  uint64_t key[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = lane + kWave * i;
-    l[i] = e < E ? logits[e] : 0.0;
-    key[i] = e < E ? make_key((float)l[i], e) : 0;
-  }
-#pragma unroll
-  for (int j = 0; j < MOE_MAX_K_DEV; ++j) {
-    if (j > last) break;
-    uint64_t best = key[0];
-#pragma unroll
-    for (int i = 1; i < kPer; ++i) best = key[i] > best ? key[i] : best;
-    sel[j] = key_expert(wave_max(best));
-    double mine = 0.0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (lane + kWave * i == sel[j]) {
-        key[i] = 0;
-        mine = l[i];
-      }
-    wl[j] = lane_f64(mine, __builtin_amdgcn_readfirstlane(sel[j] % kWave));
-  }
-}
-
 template <bool GATE_UP, int MG, int GS, bool ZERO, int WAVES, int NS, Mode MODE>
 __global__ __launch_bounds__(WAVES * kWave, WAVES == 8 || MG > 1 || NS > GS ? 2 : 3) void int4_stream_kernel(
     const bf16_t* __restrict__ A, const uint8_t* __restrict__ Wq, const uint16_t* __restrict__ Ws,
@@ -238,31 +198,8 @@ __global__ __launch_bounds__(WAVES * kWave, WAVES == 8 || MG > 1 || NS > GS ? 2 
       const int t = (int)blockIdx.y / slots.k, j = (int)blockIdx.y % slots.k;
       const bool decide = (int)blockIdx.x * NS >= strips;   // block-uniform: past the strips
       if (decide && (j != 0 || wave != 0)) return;          // no barrier follows there
-      int sel[MOE_MAX_K_DEV];
-      double wl[MOE_MAX_K_DEV];
-      pick_experts(slots.logits + (size_t)t * E, E, decide ? slots.k - 1 : j, lane, sel, wl);
-      if (decide) {
-        // lane i < k takes pick i; softmax over the picks in float64, summed in order
-        int my = sel[0];
-        double myl = wl[0];
-#pragma unroll
-        for (int i = 1; i < MOE_MAX_K_DEV; ++i)
-          if (i < slots.k && lane == i) my = sel[i], myl = wl[i];
-        const double z = lane < slots.k ? exp(myl - wl[0]) : 0.0;
-        double sum = 0.0;
-#pragma unroll
-        for (int i = 0; i < MOE_MAX_K_DEV; ++i) sum += lane_f64(z, i);
-        if (lane < slots.k) {
-          const int slot = t * slots.k + lane;
-          slots.ids[slot] = my;
-          slots.w[slot] = (float)(z / sum);
-          slots.pos[slot] = slot;
-        }
-        return;
-      }
-#pragma unroll
-      for (int i = 0; i < MOE_MAX_K_DEV; ++i)
-        if (i == j) e = __builtin_amdgcn_readfirstlane(sel[i]);
+      if (decide) return write_decision(slots, t, E, lane);
+      e = slot_expert(slots, t, j, E, lane);
     } else {
       e = slots.ids[blockIdx.y];
     }

@@ -122,7 +122,7 @@ hipError_t launch_int4_down(const void* h, const void* Wq, const void* Ws, const
 // x as MXFP4 rows as well.
 bool takes_few(int64_t T, int H, int E, int k);
 hipError_t launch_few_logits(const void* x, const void* Wr, const void* br, int64_t T, int H, int E, double* logits,
-                             hipStream_t stream);
+                             hipStream_t stream, void* xq = nullptr, void* sx = nullptr);
 hipError_t launch_few_route(const void* x, const void* Wr, const void* br, int64_t T, int H, int E, int k,
                             const int32_t* n_valid, int e_begin, int n_local, double* logits, int32_t* ids, float* w,
                             int32_t* cnt, int32_t* off, int32_t* rows, int32_t* pos, hipStream_t stream,
@@ -131,6 +131,10 @@ hipError_t launch_few_route(const void* x, const void* Wr, const void* br, int64
 // (h, o in slot order; ids, w and the identity pos written for the combine):
 // the streaming kernels' results without a router and a permutation launch.
 // logits: scratch of T E doubles that is neither h nor pos.
+hipError_t launch_w4a4_slots(const void* x, const void* Wr, const void* br, const void* Wgu_q, const void* Wgu_s,
+                             const void* bgu, const void* Wd_q, const void* Wd_s, const void* bd, int64_t T, int H, int E,
+                             int k, int I, double* logits, int32_t* ids, float* w, int32_t* pos, void* xq, void* sx,
+                             void* hq, void* sh, float* o, hipStream_t stream);
 hipError_t launch_int4_slots(const void* x, const void* Wr, const void* br, const void* Wgu_q, const void* Wgu_s,
                              const void* Wgu_z, const void* bgu, const void* Wd_q, const void* Wd_s, const void* Wd_z,
                              const void* bd, int64_t T, int H, int E, int k, int I, int G, double* logits, int32_t* ids,

@@ -24,8 +24,16 @@ template <int EB, int TB>
 __global__ __launch_bounds__(kLogitThreads) void few_logits_kernel(const bf16_t* __restrict__ x,
                                                                    const bf16_t* __restrict__ Wr,
                                                                    const bf16_t* __restrict__ br, int T, int H, int E,
-                                                                   double* __restrict__ logits) {
+                                                                   double* __restrict__ logits,
+                                                                   uint32_t* __restrict__ codes,
+                                                                   uint32_t* __restrict__ scales) {
   constexpr int kWaves = kLogitThreads / kWave;
+  if ((int)blockIdx.y * TB >= T) {   // workgroup-uniform: behind the tokens' rows of workgroups, x as MXFP4 rows
+    const int piece = (((int)blockIdx.y - (T + TB - 1) / TB) * (int)gridDim.x + (int)blockIdx.x) * (kLogitThreads / 16) +
+                      (int)threadIdx.x / 16;
+    quantize_128(x, piece % T, piece / T < (H + 127) / 128 ? T : 0, H, piece / T, threadIdx.x & 15, codes, scales);
+    return;
+  }
   __shared__ double part[kWaves][EB * TB];
   const int e0 = blockIdx.x * EB, t0 = blockIdx.y * TB;
   const u32x4_t *xr[TB], *wr[EB];
@@ -192,12 +200,15 @@ __global__ __launch_bounds__(kMaxThreads) void few_decide_kernel(
 }  // namespace
 
 hipError_t launch_few_logits(const void* x, const void* Wr, const void* br, int64_t T, int H, int E, double* logits,
-                             hipStream_t stream) {
+                             hipStream_t stream, void* xq, void* sx) {
   const bool blocks = T >= 4;
   const int eb = blocks ? 2 : 1, tb = blocks ? 4 : 1;
   auto kern = blocks ? few_logits_kernel<2, 4> : few_logits_kernel<1, 1>;
-  hipLaunchKernelGGL(kern, dim3((unsigned)((E + eb - 1) / eb), (unsigned)((T + tb - 1) / tb)), dim3(kLogitThreads), 0,
-                     stream, (const bf16_t*)x, (const bf16_t*)Wr, (const bf16_t*)br, (int)T, H, E, logits);
+  const int64_t wide = (E + eb - 1) / eb, per_row = wide * (kLogitThreads / 16);
+  const int64_t more = xq ? (T * ((H + 127) / 128) + per_row - 1) / per_row : 0;
+  hipLaunchKernelGGL(kern, dim3((unsigned)wide, (unsigned)((T + tb - 1) / tb + more)), dim3(kLogitThreads), 0, stream,
+                     (const bf16_t*)x, (const bf16_t*)Wr, (const bf16_t*)br, (int)T, H, E, logits, (uint32_t*)xq,
+                     (uint32_t*)sx);
   return hipGetLastError();
 }
 

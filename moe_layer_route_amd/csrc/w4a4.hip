@@ -35,6 +35,7 @@
 // 195 us, 5.8 TB/s (down 106).  With the operand's own shape, 16 columns x 64 bytes
 // straight into registers, these took 69, 32, 262 and 132 us.  One token, four live
 // experts: 9.7 and 8.3 us for 35 and 18 MB, each workgroup's chain of waits.
+#include "few_slots.h"
 #include "launch.h"
 #include "mxfp4_device.h"
 
@@ -81,7 +82,10 @@ __device__ __forceinline__ int live_expert(const int32_t* __restrict__ cnt, int 
   return __builtin_amdgcn_readfirstlane(__shfl(found, __ffsll((unsigned long long)who) - 1, kWave));
 }
 
-template <bool GATE_UP, int MG>
+// SLOTS: a workgroup column per token slot (M = 1, rows in slot order); gate_up picks
+// the slot's expert from the logits, and one more column of workgroups writes the
+// decision for the later launches, from which down reads it.
+template <bool GATE_UP, int MG, bool SLOTS>
 __global__ __launch_bounds__(kWaves * kWave) void w4a4_stream_kernel(
     const uint8_t* __restrict__ A,       // gate_up: x codes [T][K/2]; down: h codes [S][K/2] (permuted order)
     const uint8_t* __restrict__ As,      // [ceil(K/128)][a_rows][4]
@@ -92,20 +96,33 @@ __global__ __launch_bounds__(kWaves * kWave) void w4a4_stream_kernel(
     const int32_t* __restrict__ rows,    // gate_up only: permuted slot ids
     int K, int N, int E, int kslots, int a_rows, int64_t S,
     void* __restrict__ out,              // gate_up: h codes [S][I/2]; down: float32 [S][N]
-    uint8_t* __restrict__ out_s) {       // gate_up: h scales [ceil(I/128)][S][4]
+    uint8_t* __restrict__ out_s,         // gate_up: h scales [ceil(I/128)][S][4]
+    Slots slots) {
   using C = Shape<MG>;
   __shared__ __align__(1024) char smem_g[C::kLds];
   LDS3 char* smem = (LDS3 char*)smem_g;
   const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
 
   const int lane = threadIdx.x & (kWave - 1);
-  const int e = S < E ? live_expert(cnt, E, blockIdx.y, lane) : (int)blockIdx.y;
-  if (e < 0) return;                                       // block-uniform
-  const int M = cnt[e];
-  if (M == 0) return;                                      // block-uniform
-  const int row0 = off[e];
-  const int nblk = K / 32;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  int e, M = 1, row0 = blockIdx.y;
+  if constexpr (SLOTS && GATE_UP) {
+    const int t = (int)blockIdx.y / kslots, j = (int)blockIdx.y % kslots;
+    if ((int)blockIdx.x * kCols >= N) {                    // block-uniform
+      if (j == 0 && wave == 0) write_decision(slots, t, E, lane);
+      return;
+    }
+    e = slot_expert(slots, t, j, E, lane);
+  } else if constexpr (SLOTS) {
+    e = slots.ids[blockIdx.y];
+  } else {
+    e = S < E ? live_expert(cnt, E, blockIdx.y, lane) : (int)blockIdx.y;
+    if (e < 0) return;                                     // block-uniform
+    M = cnt[e];
+    if (M == 0) return;                                    // block-uniform
+    row0 = off[e];
+  }
+  const int nblk = K / 32;
   const int g = lane >> 4, c = lane & 15;
   const int n0 = blockIdx.x * kCols;
   const int ncol = n0 + 4 * c;
@@ -157,7 +174,9 @@ __global__ __launch_bounds__(kWaves * kWave) void w4a4_stream_kernel(
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int m = row0 + min(r0 + 4 * MG * wave + 4 * q + i, M - 1);
-        row[i] = GATE_UP ? (uint32_t)(((const __attribute__((address_space(4))) int32_t*)rows)[m] / kslots) : (uint32_t)m;
+        row[i] = !GATE_UP ? (uint32_t)m
+                 : SLOTS  ? (uint32_t)(m / kslots)
+                          : (uint32_t)(((const __attribute__((address_space(4))) int32_t*)rows)[m] / kslots);
       }
       auto pick = [&](int i) {
         const uint32_t lo = i == 0 ? row[0] : row[1], hi = i == 2 ? row[2] : row[3];
@@ -267,24 +286,26 @@ __global__ __launch_bounds__(kWaves * kWave) void w4a4_stream_kernel(
 template <bool GATE_UP>
 hipError_t launch(const void* A, const void* As, const void* Wq, const void* Ws, const void* bias, const int32_t* cnt,
                   const int32_t* off, const int32_t* rows, int64_t T, int K, int N, int E, int k, void* out,
-                  void* out_s, hipStream_t stream) {
+                  void* out_s, const Slots* slots, hipStream_t stream) {
   const int64_t S = T * k, a_rows = GATE_UP ? T : S;
   // 32-bit buffer offsets: the token codes and one expert's codes below 2 GiB,
   // so an offset at kOutOfRange never comes back into range
   if (a_rows * K / 2 >= ((int64_t)1 << 31) || (int64_t)N * K / 2 >= ((int64_t)1 << 31)) return hipErrorNotSupported;
-  const dim3 grid((unsigned)((N + kCols - 1) / kCols), (unsigned)(S < E ? S : E));
+  const int columns = (N + kCols - 1) / kCols;
+  const dim3 grid((unsigned)(columns + (slots && GATE_UP ? 1 : 0)), (unsigned)(slots || S < E ? S : E));
   // Rows a pass by the mean rows an expert: 16, 32 or 64.  More rows cost LDS (two
   // instead of three workgroups a CU at 64) and reads of rows that are not there;
   // fewer cost another pass over the weights.  gate_up of 2880 x 5760, 16 / 32 / 64:
   // 32 experts, 8 rows each 51 / 54 / 66 us, 12: 58 / 54 / 64, 24: 92 / 63 / 69, 32:
   // 105 / 78 / 72; 128 experts, 8: 196 / 200 / 236, 16: 265 / 219 / 251, 32: 408 /
   // 301 / 278.
-  auto kern = S <= 10 * (int64_t)E   ? w4a4_stream_kernel<GATE_UP, 1>
-              : S <= 27 * (int64_t)E ? w4a4_stream_kernel<GATE_UP, 2>
-                                     : w4a4_stream_kernel<GATE_UP, 4>;
+  auto kern = slots                  ? w4a4_stream_kernel<GATE_UP, 1, true>
+              : S <= 10 * (int64_t)E ? w4a4_stream_kernel<GATE_UP, 1, false>
+              : S <= 27 * (int64_t)E ? w4a4_stream_kernel<GATE_UP, 2, false>
+                                     : w4a4_stream_kernel<GATE_UP, 4, false>;
   hipLaunchKernelGGL(kern, grid, dim3(kWaves * kWave), 0, stream, (const uint8_t*)A, (const uint8_t*)As,
                      (const uint8_t*)Wq, (const uint8_t*)Ws, (const bf16_t*)bias, cnt, off, rows, K, N, E, k,
-                     (int)a_rows, S, out, (uint8_t*)out_s);
+                     (int)a_rows, S, out, (uint8_t*)out_s, slots ? *slots : Slots{});
   return hipGetLastError();
 }
 
@@ -293,13 +314,25 @@ hipError_t launch(const void* A, const void* As, const void* Wq, const void* Ws,
 hipError_t launch_w4a4_gate_up(const void* xq, const void* sx, const void* Wq, const void* Ws, const void* bgu,
                                const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T, int H, int E,
                                int k, int I, void* hq, void* sh, hipStream_t stream) {
-  return launch<true>(xq, sx, Wq, Ws, bgu, cnt, off, rows, T, H, 2 * I, E, k, hq, sh, stream);
+  return launch<true>(xq, sx, Wq, Ws, bgu, cnt, off, rows, T, H, 2 * I, E, k, hq, sh, nullptr, stream);
 }
 
 hipError_t launch_w4a4_down(const void* hq, const void* sh, const void* Wq, const void* Ws, const void* bd,
                             const int32_t* cnt, const int32_t* off, int64_t T, int H, int E, int k, int I, float* o,
                             hipStream_t stream) {
-  return launch<false>(hq, sh, Wq, Ws, bd, cnt, off, nullptr, T, I, H, E, k, o, nullptr, stream);
+  return launch<false>(hq, sh, Wq, Ws, bd, cnt, off, nullptr, T, I, H, E, k, o, nullptr, nullptr, stream);
+}
+
+hipError_t launch_w4a4_slots(const void* x, const void* Wr, const void* br, const void* Wgu_q, const void* Wgu_s,
+                             const void* bgu, const void* Wd_q, const void* Wd_s, const void* bd, int64_t T, int H, int E,
+                             int k, int I, double* logits, int32_t* ids, float* w, int32_t* pos, void* xq, void* sx,
+                             void* hq, void* sh, float* o, hipStream_t stream) {
+  hipError_t e = launch_few_logits(x, Wr, br, T, H, E, logits, stream, xq, sx);
+  if (e != hipSuccess) return e;
+  const Slots slots{logits, ids, w, pos, k};
+  e = launch<true>(xq, sx, Wgu_q, Wgu_s, bgu, nullptr, nullptr, nullptr, T, H, 2 * I, E, k, hq, sh, &slots, stream);
+  if (e != hipSuccess) return e;
+  return launch<false>(hq, sh, Wd_q, Wd_s, bd, nullptr, nullptr, nullptr, T, I, H, E, k, o, nullptr, &slots, stream);
 }
 
 }  // namespace moe

@@ -296,7 +296,8 @@ def _block(T, E, k, H, I, seed):
 
 
 BLOCKS = [(1, 32, 4, 320, 96), (7, 8, 2, 96, 160), (64, 8, 4, 352, 224), (200, 4, 1, 288, 544), (90, 60, 8, 160, 64),
-          (700, 4, 2, 544, 288), (1, 1, 1, 32, 32), (2, 4, 4, 2880, 2880)]
+          (700, 4, 2, 544, 288), (1, 1, 1, 32, 32), (2, 4, 4, 2880, 2880), (5, 100, 4, 288, 96), (3, 64, 5, 160, 64),
+          (8, 256, 8, 96, 32)]
 
 
 @pytest.mark.parametrize("path", ["auto"] + PATHS)
