@@ -33,6 +33,8 @@
 #include "launch.h"
 #include "mxfp4_device.h"
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
@@ -151,8 +153,7 @@ __global__ __launch_bounds__(kThreads, 2) void w4a4_gemm_kernel(
   }
   const uint32_t bs_off = n0 + 4 * lane < N ? (uint32_t)wave * (uint32_t)N + (uint32_t)(n0 + 4 * lane) : kOOR;
 
-  // eight loads a wave and stage (the waits below count them); a stage past the
-  // last is out of range
+  // eight loads a wave and stage (the waits below count them)
   auto dma = [&](int st, int buf, int i) {   // 0, 1: A; 2 .. 5: B; 6, 7: scales
     const int k0 = st * kRowBytes;
     if (i < 2)
@@ -212,7 +213,8 @@ __global__ __launch_bounds__(kThreads, 2) void w4a4_gemm_kernel(
   };
   // fragments in the order they are read (a0 b0 a1 b1 b2 b3), two products behind
   // each, in three slots
-#define MX_MFMA(J, I, Q) acc[I][Q] = mfma_fp4_32<J, Q>(fa[I], fb[Q], acc[I][Q], s4.a[I], s4.b[J])
+#define MX_MFMA(J, I, Q) \
+  if constexpr (I < NI) acc[I][Q] = mfma_fp4_32<J, Q>(fa[I], fb[Q], acc[I][Q], s4.a[I], s4.b[J])
 #define MX_SLOT(J)                                          \
   if (u == 0) {                                             \
     MX_MFMA(J, 0, 0);                                       \
@@ -222,14 +224,6 @@ __global__ __launch_bounds__(kThreads, 2) void w4a4_gemm_kernel(
   } else {                                                  \
     MX_MFMA(J, 1, 2); MX_MFMA(J, 0, 3); MX_MFMA(J, 1, 3);   \
   }
-  auto slot = [&](int j, int u, const u32x4_t (&fa)[2], const u32x4_t (&fb)[4], const Scales& s4) {
-    if (j == 0) {
-      MX_SLOT(0)
-    } else {
-      MX_SLOT(1)
-    }
-  };
-
   // prologue: stages 0 .. kRing - 2
 #pragma unroll
   for (int st = 0; st < kRing - 1; ++st)
@@ -238,46 +232,67 @@ __global__ __launch_bounds__(kThreads, 2) void w4a4_gemm_kernel(
   asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
   __builtin_amdgcn_s_barrier();
 
-  u32x4_t fa0[2], fb0[4], fa1[2], fb1[4];
-  // Step j of stage s in three slots: slot u reads two fragments for step j,
-  // issues loads of stage s + kRing - 1 into the buffer that stage s - 1 left at
-  // the last barrier, and products of the step before.
-  auto step = [&](int s, int buf, int nbuf, int j, u32x4_t (&fa_rd)[2], u32x4_t (&fb_rd)[4], const u32x4_t (&fa_mm)[2],
-                  const u32x4_t (&fb_mm)[4], const Scales& s4, bool do_mfma) {
-#pragma unroll
-    for (int u = 0; u < 3; ++u) {
-      dma(s + kRing - 1, nbuf, 4 * j + u);
-      if (u == 2) dma(s + kRing - 1, nbuf, 4 * j + 3);
-      __builtin_amdgcn_sched_barrier(0);
-      if (u == 0) {
-        fa_rd[0] = read_a(buf, j, 0);
-        fb_rd[0] = read_b(buf, j, 0);
-      } else if (u == 1) {
-        fa_rd[1] = read_a(buf, j, 1);
-        fb_rd[1] = read_b(buf, j, 1);
+  // The loop for the NI row blocks of 32 that the wave has rows in: the products of the
+  // others are left out.
+  auto loop = [&](auto ni_c) {
+    constexpr int NI = decltype(ni_c)::value;
+    auto slot = [&](int j, int u, const u32x4_t (&fa)[2], const u32x4_t (&fb)[4], const Scales& s4) {
+      if (j == 0) {
+        MX_SLOT(0)
       } else {
-        fb_rd[2] = read_b(buf, j, 2);
-        fb_rd[3] = read_b(buf, j, 3);
+        MX_SLOT(1)
       }
-      if (do_mfma) slot(j ^ 1, u, fa_mm, fb_mm, s4);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  };
-  int buf = 0, nbuf = kRing - 1;
-  for (int s = 0; s < ns; ++s) {
-    last = sc;
-    read_scales(s, buf);
-    step(s, buf, nbuf, 0, fa0, fb0, fa1, fb1, last, s > 0);
-    step(s, buf, nbuf, 1, fa1, fb1, fa0, fb0, sc, true);
-    // stage s + 1 has landed when only the loads of the stage behind it are out
-    asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    nbuf = buf;
-    buf = buf == kRing - 1 ? 0 : buf + 1;
-  }
+    };
+
+    u32x4_t fa0[2], fb0[4], fa1[2], fb1[4];
+    // Step j of stage s in three slots: slot u reads two fragments for step j,
+    // issues loads of stage s + kRing - 1 into the buffer that stage s - 1 left at
+    // the last barrier, and products of the step before.
+    auto step = [&](int s, int buf, int nbuf, int j, u32x4_t (&fa_rd)[2], u32x4_t (&fb_rd)[4], const u32x4_t (&fa_mm)[2],
+                    const u32x4_t (&fb_mm)[4], const Scales& s4, bool do_mfma) {
 #pragma unroll
-  for (int u = 0; u < 3; ++u) slot(1, u, fa1, fb1, sc);
-  // the loads past the last stage wrote zeros into LDS that nothing reads; they end before the wave does
+      for (int u = 0; u < 3; ++u) {
+        if (s + kRing - 1 < ns) {
+          dma(s + kRing - 1, nbuf, 4 * j + u);
+          if (u == 2) dma(s + kRing - 1, nbuf, 4 * j + 3);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (NI == 0) {
+        } else if (u == 0) {
+          fa_rd[0] = read_a(buf, j, 0);
+          fb_rd[0] = read_b(buf, j, 0);
+        } else if (u == 1) {
+          if (NI > 1) fa_rd[1] = read_a(buf, j, 1);
+          fb_rd[1] = read_b(buf, j, 1);
+        } else {
+          fb_rd[2] = read_b(buf, j, 2);
+          fb_rd[3] = read_b(buf, j, 3);
+        }
+        if (do_mfma) slot(j ^ 1, u, fa_mm, fb_mm, s4);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    int buf = 0, nbuf = kRing - 1;
+    for (int s = 0; s < ns; ++s) {
+      last = sc;
+      if (NI > 0) read_scales(s, buf);
+      step(s, buf, nbuf, 0, fa0, fb0, fa1, fb1, last, s > 0);
+      step(s, buf, nbuf, 1, fa1, fb1, fa0, fb0, sc, true);
+      // stage s + 1 has landed when only the loads of the stage behind it, if any, are out
+      if (s + kRing - 1 < ns) asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)" ::: "memory");
+      else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      nbuf = buf;
+      buf = buf == kRing - 1 ? 0 : buf + 1;
+    }
+#pragma unroll
+    for (int u = 0; u < 3; ++u) slot(1, u, fa1, fb1, sc);
+  };
+  const int ni = min(2, max(0, (M - m0 - 64 * wm + 31) / 32));   // wave-uniform
+  if (ni == 2) loop(std::integral_constant<int, 2>{});
+  else if (ni == 1) loop(std::integral_constant<int, 1>{});
+  else loop(std::integral_constant<int, 0>{});
+  // (with one stage, the second's loads wrote zeros; they end before the wave does)
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
   // ---- epilogue.  Lane l, element v of block (i, q): row 32i + 8 (v / 4) + 4 (l
@@ -291,7 +306,8 @@ __global__ __launch_bounds__(kThreads, 2) void w4a4_gemm_kernel(
   }
   if (GATE_UP) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i) {
+      if (i >= ni) break;
 #pragma unroll
       for (int v4 = 0; v4 < 4; ++v4) {
         f32x4_t quad[4];
@@ -302,6 +318,7 @@ __global__ __launch_bounds__(kThreads, 2) void w4a4_gemm_kernel(
         store_glu_quad(quad, bb, m0 + 64 * wm + 32 * i + 8 * v4 + 4 * fg, M, row0, ncol, N, lane,
                        reinterpret_cast<uint8_t*>(out), out_s, S);
       }
+    }
   } else {
     if (ncol >= N) return;                                   // N % 32 == 0: four columns are all in or all out
 #pragma unroll
