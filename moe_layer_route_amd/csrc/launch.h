@@ -69,20 +69,22 @@ hipError_t launch_mxfp4_rows(const void* a, int64_t R, int K, void* codes, void*
 hipError_t launch_mxfp4_rows_back(const void* codes, const void* scales, int64_t R, int K, void* out,
                                   hipStream_t stream);
 // W4A4: MXFP4 rows times MXFP4 weights; gate_up leaves h as MXFP4 rows
+// (near: the slots to expect on these experts, by which the variant is chosen; T k of
+// them is what there can be)
 hipError_t launch_w4a4_gate_up(const void* xq, const void* sx, const void* Wq, const void* Ws, const void* bgu,
                                const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T, int H, int E,
-                               int k, int I, void* hq, void* sh, hipStream_t stream);
+                               int k, int I, int64_t near, void* hq, void* sh, hipStream_t stream);
 hipError_t launch_w4a4_down(const void* hq, const void* sh, const void* Wq, const void* Ws, const void* bd,
-                            const int32_t* cnt, const int32_t* off, int64_t T, int H, int E, int k, int I, float* o,
-                            hipStream_t stream);
+                            const int32_t* cnt, const int32_t* off, int64_t T, int H, int E, int k, int I, int64_t near,
+                            float* o, hipStream_t stream);
 
 // the LDS-tiled grouped GEMMs (w4a4_gemm.hip)
 hipError_t launch_gemm_w4a4_gate_up(const void* xq, const void* sx, const void* Wq, const void* Ws, const void* bgu,
                                     const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T, int H, int E,
-                                    int k, int I, void* hq, void* sh, hipStream_t stream);
+                                    int k, int I, int64_t near, void* hq, void* sh, hipStream_t stream);
 hipError_t launch_gemm_w4a4_down(const void* hq, const void* sh, const void* Wq, const void* Ws, const void* bd,
-                                 const int32_t* cnt, const int32_t* off, int64_t T, int H, int E, int k, int I, float* o,
-                                 hipStream_t stream);
+                                 const int32_t* cnt, const int32_t* off, int64_t T, int H, int E, int k, int I,
+                                 int64_t near, float* o, hipStream_t stream);
 
 // FP8 W8A8 (OCP E4M3): weight codes [E][N][K] with one float32 scale per
 // expert; activation codes [R][K] with one scale per row (K % 16 == 0)

@@ -1381,19 +1381,20 @@ static int w4a4_path(int32_t path, int64_t S, int32_t E, int32_t N) {
 
 static int run_gate_up_w4a4(const char* fn, const void* xq, const void* sx, const void* Wgu_q, const void* Wgu_s,
                             const void* bgu, const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T,
-                            int32_t H, int32_t E, int32_t k, int32_t I, void* hq, void* sh, int32_t path,
+                            int32_t H, int32_t E, int32_t k, int32_t I, int64_t near, void* hq, void* sh, int32_t path,
                             hipStream_t s) {
-  if (w4a4_path(path, T * k, E, 2 * I) == MOE_PATH_GEMM)
-    return hip_status(fn, moe::launch_gemm_w4a4_gate_up(xq, sx, Wgu_q, Wgu_s, bgu, cnt, off, rows, T, H, E, k, I, hq, sh, s));
-  return hip_status(fn, moe::launch_w4a4_gate_up(xq, sx, Wgu_q, Wgu_s, bgu, cnt, off, rows, T, H, E, k, I, hq, sh, s));
+  if (w4a4_path(path, near, E, 2 * I) == MOE_PATH_GEMM)
+    return hip_status(fn, moe::launch_gemm_w4a4_gate_up(xq, sx, Wgu_q, Wgu_s, bgu, cnt, off, rows, T, H, E, k, I, near,
+                                                        hq, sh, s));
+  return hip_status(fn, moe::launch_w4a4_gate_up(xq, sx, Wgu_q, Wgu_s, bgu, cnt, off, rows, T, H, E, k, I, near, hq, sh, s));
 }
 
 static int run_down_w4a4(const char* fn, const void* hq, const void* sh, const void* Wd_q, const void* Wd_s,
                          const void* bd, const int32_t* cnt, const int32_t* off, int64_t T, int32_t H, int32_t E,
-                         int32_t k, int32_t I, float* o, int32_t path, hipStream_t s) {
-  if (w4a4_path(path, T * k, E, H) == MOE_PATH_GEMM)
-    return hip_status(fn, moe::launch_gemm_w4a4_down(hq, sh, Wd_q, Wd_s, bd, cnt, off, T, H, E, k, I, o, s));
-  return hip_status(fn, moe::launch_w4a4_down(hq, sh, Wd_q, Wd_s, bd, cnt, off, T, H, E, k, I, o, s));
+                         int32_t k, int32_t I, int64_t near, float* o, int32_t path, hipStream_t s) {
+  if (w4a4_path(path, near, E, H) == MOE_PATH_GEMM)
+    return hip_status(fn, moe::launch_gemm_w4a4_down(hq, sh, Wd_q, Wd_s, bd, cnt, off, T, H, E, k, I, near, o, s));
+  return hip_status(fn, moe::launch_w4a4_down(hq, sh, Wd_q, Wd_s, bd, cnt, off, T, H, E, k, I, near, o, s));
 }
 
 // The forward with MXFP4 on both sides: the experts [e_begin, e_begin + n_local)
@@ -1465,9 +1466,10 @@ static int forward_w4a4(const char* fn, const void* x, const void* Wr, const voi
   if (int st = route_and_permute(fn, x, Wr, br, T, H, E, k, n_valid, e_begin, n_local, o, ids, w, cnt, off, rows, pos, s,
                                  xq, sx))
     return st;
-  if (int st = run_gate_up_w4a4(fn, xq, sx, Wgu_q, Wgu_s, bgu, cnt, off, rows, T, H, n_local, k, I, hq, sh, path, s))
+  const int64_t near = (T * k * n_local + E - 1) / E;   // of a rank's share, with evenly chosen experts
+  if (int st = run_gate_up_w4a4(fn, xq, sx, Wgu_q, Wgu_s, bgu, cnt, off, rows, T, H, n_local, k, I, near, hq, sh, path, s))
     return st;
-  if (int st = run_down_w4a4(fn, hq, sh, Wd_q, Wd_s, bd, cnt, off, T, H, n_local, k, I, o, path, s)) return st;
+  if (int st = run_down_w4a4(fn, hq, sh, Wd_q, Wd_s, bd, cnt, off, T, H, n_local, k, I, near, o, path, s)) return st;
   if (int st = hip_status(fn, moe::launch_combine(o, pos, w, T, H, k, y, s, partial))) return st;
   return ok();
 }
@@ -1521,7 +1523,7 @@ int moe_gate_up_w4a4(const void* xq, const void* sx, const void* Wgu_q, const vo
   if (int st = check_w4a4_rows(fn, "x", T, H)) return st;
   if (int st = check_w4a4_rows(fn, "h", T * k, I)) return st;
   if (T == 0) return ok();
-  if (int st = run_gate_up_w4a4(fn, xq, sx, Wgu_q, Wgu_s, bgu, cnt, off, rows, T, H, E, k, I, hq, sh, path,
+  if (int st = run_gate_up_w4a4(fn, xq, sx, Wgu_q, Wgu_s, bgu, cnt, off, rows, T, H, E, k, I, T * k, hq, sh, path,
                                 (hipStream_t)stream))
     return st;
   return ok();
@@ -1545,7 +1547,7 @@ int moe_down_w4a4(const void* hq, const void* sh, const void* Wd_q, const void* 
     return fail(MOE_ERR_INVALID_ARG, "%s: unknown path %d", fn, path);
   if (int st = check_w4a4_rows(fn, "h", T * k, I)) return st;
   if (T == 0) return ok();
-  if (int st = run_down_w4a4(fn, hq, sh, Wd_q, Wd_s, bd, cnt, off, T, H, E, k, I, o, path, (hipStream_t)stream))
+  if (int st = run_down_w4a4(fn, hq, sh, Wd_q, Wd_s, bd, cnt, off, T, H, E, k, I, T * k, o, path, (hipStream_t)stream))
     return st;
   return ok();
 }

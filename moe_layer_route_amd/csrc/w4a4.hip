@@ -285,8 +285,8 @@ __global__ __launch_bounds__(kWaves * kWave) void w4a4_stream_kernel(
 
 template <bool GATE_UP>
 hipError_t launch(const void* A, const void* As, const void* Wq, const void* Ws, const void* bias, const int32_t* cnt,
-                  const int32_t* off, const int32_t* rows, int64_t T, int K, int N, int E, int k, void* out,
-                  void* out_s, const Slots* slots, hipStream_t stream) {
+                  const int32_t* off, const int32_t* rows, int64_t T, int K, int N, int E, int k, int64_t near,
+                  void* out, void* out_s, const Slots* slots, hipStream_t stream) {
   const int64_t S = T * k, a_rows = GATE_UP ? T : S;
   // 32-bit buffer offsets: the token codes and one expert's codes below 2 GiB,
   // so an offset at kOutOfRange never comes back into range
@@ -300,8 +300,8 @@ hipError_t launch(const void* A, const void* As, const void* Wq, const void* Ws,
   // 105 / 78 / 72; 128 experts, 8: 196 / 200 / 236, 16: 265 / 219 / 251, 32: 408 /
   // 301 / 278.
   auto kern = slots                  ? w4a4_stream_kernel<GATE_UP, 1, true>
-              : S <= 10 * (int64_t)E ? w4a4_stream_kernel<GATE_UP, 1, false>
-              : S <= 27 * (int64_t)E ? w4a4_stream_kernel<GATE_UP, 2, false>
+              : near <= 10 * (int64_t)E ? w4a4_stream_kernel<GATE_UP, 1, false>
+              : near <= 27 * (int64_t)E ? w4a4_stream_kernel<GATE_UP, 2, false>
                                      : w4a4_stream_kernel<GATE_UP, 4, false>;
   hipLaunchKernelGGL(kern, grid, dim3(kWaves * kWave), 0, stream, (const uint8_t*)A, (const uint8_t*)As,
                      (const uint8_t*)Wq, (const uint8_t*)Ws, (const bf16_t*)bias, cnt, off, rows, K, N, E, k,
@@ -313,14 +313,14 @@ hipError_t launch(const void* A, const void* As, const void* Wq, const void* Ws,
 
 hipError_t launch_w4a4_gate_up(const void* xq, const void* sx, const void* Wq, const void* Ws, const void* bgu,
                                const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T, int H, int E,
-                               int k, int I, void* hq, void* sh, hipStream_t stream) {
-  return launch<true>(xq, sx, Wq, Ws, bgu, cnt, off, rows, T, H, 2 * I, E, k, hq, sh, nullptr, stream);
+                               int k, int I, int64_t near, void* hq, void* sh, hipStream_t stream) {
+  return launch<true>(xq, sx, Wq, Ws, bgu, cnt, off, rows, T, H, 2 * I, E, k, near, hq, sh, nullptr, stream);
 }
 
 hipError_t launch_w4a4_down(const void* hq, const void* sh, const void* Wq, const void* Ws, const void* bd,
-                            const int32_t* cnt, const int32_t* off, int64_t T, int H, int E, int k, int I, float* o,
-                            hipStream_t stream) {
-  return launch<false>(hq, sh, Wq, Ws, bd, cnt, off, nullptr, T, I, H, E, k, o, nullptr, nullptr, stream);
+                            const int32_t* cnt, const int32_t* off, int64_t T, int H, int E, int k, int I,
+                            int64_t near, float* o, hipStream_t stream) {
+  return launch<false>(hq, sh, Wq, Ws, bd, cnt, off, nullptr, T, I, H, E, k, near, o, nullptr, nullptr, stream);
 }
 
 hipError_t launch_w4a4_slots(const void* x, const void* Wr, const void* br, const void* Wgu_q, const void* Wgu_s,
@@ -330,9 +330,9 @@ hipError_t launch_w4a4_slots(const void* x, const void* Wr, const void* br, cons
   hipError_t e = launch_few_logits(x, Wr, br, T, H, E, logits, stream, xq, sx);
   if (e != hipSuccess) return e;
   const Slots slots{logits, ids, w, pos, k};
-  e = launch<true>(xq, sx, Wgu_q, Wgu_s, bgu, nullptr, nullptr, nullptr, T, H, 2 * I, E, k, hq, sh, &slots, stream);
+  e = launch<true>(xq, sx, Wgu_q, Wgu_s, bgu, nullptr, nullptr, nullptr, T, H, 2 * I, E, k, T * k, hq, sh, &slots, stream);
   if (e != hipSuccess) return e;
-  return launch<false>(hq, sh, Wd_q, Wd_s, bd, nullptr, nullptr, nullptr, T, I, H, E, k, o, nullptr, &slots, stream);
+  return launch<false>(hq, sh, Wd_q, Wd_s, bd, nullptr, nullptr, nullptr, T, I, H, E, k, T * k, o, nullptr, &slots, stream);
 }
 
 }  // namespace moe

@@ -495,8 +495,8 @@ __global__ __launch_bounds__(kThreads, 2) void w4a4_mid_kernel(
 
 template <bool GATE_UP>
 hipError_t launch(const void* A, const void* As, const void* Wq, const void* Ws, const void* bias, const int32_t* cnt,
-                  const int32_t* off, const int32_t* rows, int64_t T, int K, int N, int E, int k, void* out, void* out_s,
-                  hipStream_t stream) {
+                  const int32_t* off, const int32_t* rows, int64_t T, int K, int N, int E, int k, int64_t near,
+                  void* out, void* out_s, hipStream_t stream) {
   const int64_t S = T * k, a_rows = GATE_UP ? T : S;
   // 32-bit buffer offsets: the token codes and one expert's codes below 2 GiB
   if (a_rows * K / 2 >= ((int64_t)1 << 31) || (int64_t)N * K / 2 >= ((int64_t)1 << 31)) return hipErrorNotSupported;
@@ -505,7 +505,7 @@ hipError_t launch(const void* A, const void* As, const void* Wq, const void* Ws,
   // against 128 x 256: 64 rows each 84 and 48 us against 96 and 51, 128 rows 113 and
   // 60 against 117 and 75, 192 rows 144 and 72 against 131 and 80, 512 rows 284 and
   // 166 against 253 and 174; 128 experts, 32 rows 299 and 150 against 287 and 152.
-  const int64_t big = (S / kBM + (S < E ? S : E)) * ((N + kBN - 1) / kBN);
+  const int64_t big = (near / kBM + (near < E ? near : E)) * ((N + kBN - 1) / kBN);
   const bool mid = big < 1792;
   const int n_tiles = (N + (mid ? kMidBN : kBN) - 1) / (mid ? kMidBN : kBN);
   // at most sum_e ceil(cnt_e / 128) <= S / 128 + min(E, S) M tiles
@@ -523,14 +523,14 @@ hipError_t launch(const void* A, const void* As, const void* Wq, const void* Ws,
 
 hipError_t launch_gemm_w4a4_gate_up(const void* xq, const void* sx, const void* Wq, const void* Ws, const void* bgu,
                                     const int32_t* cnt, const int32_t* off, const int32_t* rows, int64_t T, int H, int E,
-                                    int k, int I, void* hq, void* sh, hipStream_t stream) {
-  return launch<true>(xq, sx, Wq, Ws, bgu, cnt, off, rows, T, H, 2 * I, E, k, hq, sh, stream);
+                                    int k, int I, int64_t near, void* hq, void* sh, hipStream_t stream) {
+  return launch<true>(xq, sx, Wq, Ws, bgu, cnt, off, rows, T, H, 2 * I, E, k, near, hq, sh, stream);
 }
 
 hipError_t launch_gemm_w4a4_down(const void* hq, const void* sh, const void* Wq, const void* Ws, const void* bd,
-                                 const int32_t* cnt, const int32_t* off, int64_t T, int H, int E, int k, int I, float* o,
-                                 hipStream_t stream) {
-  return launch<false>(hq, sh, Wq, Ws, bd, cnt, off, nullptr, T, I, H, E, k, o, nullptr, stream);
+                                 const int32_t* cnt, const int32_t* off, int64_t T, int H, int E, int k, int I,
+                                 int64_t near, float* o, hipStream_t stream) {
+  return launch<false>(hq, sh, Wq, Ws, bd, cnt, off, nullptr, T, I, H, E, k, near, o, nullptr, stream);
 }
 
 }  // namespace moe

@@ -513,3 +513,41 @@ def test_same_expert_twice_in_a_row():
         at = pos.view(T, k).long()
         assert (hq[at[:, 0]] == hq[at[:, 2]]).all() and (o[at[:, 0]] == o[at[:, 2]]).all()
         assert (at[:, 0] != at[:, 2]).all()
+
+
+def test_graph_replays_of_few_tokens():
+    """One workgroup column a slot: captured, and replayed over other bytes in the workspace."""
+    _need_gpu()
+    T, E, k, H, I = 2, 40, 4, 288, 96
+    g = [_up(a) for a in _block(T, E, k, H, I, 22)]
+    ws, y = binding.alloc_workspace_w4a4(T, H, E, k, I), torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+    binding.moe_forward_w4a4(*g, k=k, y=y, workspace=ws)
+    eager = bf16_bits(y).copy()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        binding.moe_forward_w4a4(*g, k=k, y=y, workspace=ws)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        binding.moe_forward_w4a4(*g, k=k, y=y, workspace=ws)
+    for i in range(4):
+        y.view(torch.int16).fill_(-1)
+        ws.fill_(0xAB if i % 2 else 0x11)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert (bf16_bits(y) == eager).all()
+
+
+@pytest.mark.parametrize("T", [1, 40, 600])
+def test_ep_rank_of_many(T):
+    """One rank of eight by itself, at sizes that take different variants, against the oracle."""
+    _need_gpu()
+    E, k, H, I = 32, 4, 160, 96
+    args = _block(T, E, k, H, I, 23)
+    g = [_up(a) for a in args]
+    for lo in (0, 28):
+        part = binding.moe_forward_ep_w4a4(*g[:3], *(t[lo:lo + 4].contiguous() for t in g[3:]), e_begin=lo, k=k)
+        ref = orc.moe_forward_w4a4(*args[:3], *(a[lo:lo + 4] for a in args[3:]), k, experts=range(lo, lo + 4))
+        assert_y_close(host_f64(part), ref["y"], f"the share of experts from {lo}")
