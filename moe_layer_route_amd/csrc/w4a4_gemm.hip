@@ -8,7 +8,7 @@
 // Tile: 128 rows x 256 columns, K stages of 128 codes (64 bytes of every row and
 // column), four waves in a 2 x 2 grid, each 64 x 128 = 2 x 4 blocks of
 // v_mfma_scale_f32_32x32x64_f8f6f4 (128 float32 accumulators a lane).  A second
-// kernel below has tiles of 128 x 128 for launches of few tiles.
+// kernel below has tiles of 256 x 256 and of 128 x 128; the launch says which is taken.
 //   Staging: codes and scales HBM/L2 -> LDS by direct loads into a ring of three
 //   stage buffers (24 KB of codes, 2 KB of scales each), two stages ahead; 78 KB, so
 //   two workgroups share a CU and one multiplies while the other starts or ends.
@@ -24,12 +24,12 @@
 //   scales' word of block 2 (l / 32) + j: picked by the instruction itself.
 //   Stage s: its loads were issued during stage s - 2; each wave waits for its own
 //   at the end of stage s - 1 and the barrier makes all of them visible.
-// What bounds it: the load path and the products in turn.  2880 x 5760, 512 rows an
-// expert, 32 experts: 253 us, 2.1 PFLOP/s, matrix pipes 26% busy at 2.1 GHz, a wave
-// waiting for 28% of its time and for its turn to issue for 38% (down 170 us, 1.6
-// PFLOP/s).  One expert of 16384 rows: 222 us, without the loads 143, without the
-// products 176, without both 89.  Tiles of 256 x 256 by four waves took 316 us where
-// these take 256, by eight 293.
+// What bounds them: the load path and the products in turn.  2880 x 5760, 512 rows an
+// expert, 32 experts: 255 to 265 us, 2.1 PFLOP/s with either large tile, matrix pipes 26%
+// busy at 2.1 GHz (down 166 and 149 us, 1.6 and 1.8 PFLOP/s).  One expert of 16384 rows
+// by these tiles: 222 us, without the loads 143, without the products 176, without both
+// 89.  With stages of this size, tiles of 256 x 256 by eight waves took 293 us where
+// these took 256; with whole lines and four waves, one a SIMD, 316.
 #include "launch.h"
 #include "mxfp4_device.h"
 
@@ -333,46 +333,63 @@ __global__ __launch_bounds__(kThreads, 2) void w4a4_gemm_kernel(
   }
 }
 
-// ---- the same product by tiles of 128 x 128 with K stages of 256 codes: a whole
-// 128-byte line of every row and column at a time.  Two stage buffers of 34 KB, two
-// workgroups a CU; four waves in a 2 x 2 grid, each 64 x 64 = 4 x 4 blocks of
+// ---- the same product by tiles of 256 x 256 or 128 x 128 with K stages of 256 codes: a
+// whole 128-byte line of every row and column at a time (with 64 bytes every load is a
+// request to L2 of its own).  Two stage buffers of 68 or 34 KB: one workgroup of sixteen
+// waves a CU, or two of four; each wave 64 x 64 = 4 x 4 blocks of
 // v_mfma_scale_f32_16x16x128_f8f6f4, two steps of 128 values a stage.
 //   LDS row 16j + t of a wave's 64 columns is column 4t + j, so a lane's four column
 //   blocks are neighbouring columns, as in the tiles above; chunk c of row r sits at
 //   slot c ^ ((r >> 1) & 7).
 //   Lane (g = lane / 16, c = lane % 16) has block g of a step's four; its scales are
 //   byte g of the row's word and the word of the four columns. ----
-constexpr int kMidBN = 128;
-constexpr int kMidRow = 128;                       // bytes of a row and stage
-constexpr int kMidA = 0, kMidB = kMidA + kBM * kMidRow, kMidAs = kMidB + kMidBN * kMidRow, kMidBs = kMidAs + 1024;
-constexpr int kMidStage = kMidBs + 1024;           // 34 KB
+constexpr int kLine = 128;                         // bytes of a row and stage
+template <int BM_, int BN_>
+struct Lines {
+  static constexpr int BM = BM_, BN = BN_, WN = BN / 64, WAVES = BM / 64 * WN, THREADS = WAVES * kWave;
+  static constexpr int A = 0, B = A + BM * kLine, As = B + BN * kLine, Bs = As + 8 * BM, STAGE = Bs + 8 * BN;
+  static constexpr int ALOADS = BM / 8 / WAVES, BLOADS = BN / 8 / WAVES;   // a wave and stage
+  static constexpr int SA = BM / 32, SB = BN / 32, SLOADS = (SA + SB) / WAVES;   // loads of scales; of a wave
+};
 
-template <bool GATE_UP>
-__global__ __launch_bounds__(kThreads, 2) void w4a4_mid_kernel(
+// one row block by four column blocks
+__device__ __forceinline__ void products(f32x4_t (&acc)[4], u32x4_t a, const u32x4_t (&b)[4], uint32_t sa, uint32_t sb) {
+  acc[0] = mfma_fp4_16<0, 0>(a, b[0], acc[0], sa, sb);
+  acc[1] = mfma_fp4_16<0, 1>(a, b[1], acc[1], sa, sb);
+  acc[2] = mfma_fp4_16<0, 2>(a, b[2], acc[2], sa, sb);
+  acc[3] = mfma_fp4_16<0, 3>(a, b[3], acc[3], sa, sb);
+}
+
+template <bool GATE_UP, class C>
+__global__ __launch_bounds__(C::THREADS, C::WAVES == 16 ? 4 : 2) void w4a4_lines_kernel(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ As, const uint8_t* __restrict__ Wq,
     const uint8_t* __restrict__ Ws, const bf16_t* __restrict__ bias, const int32_t* __restrict__ cnt,
     const int32_t* __restrict__ off, const int32_t* __restrict__ rows, int K, int N, int E, int kslots, int a_rows,
     int64_t S, int n_tiles, void* __restrict__ out, uint8_t* __restrict__ out_s) {
-  __shared__ __align__(1024) char smem_g[2 * kMidStage];
+  __shared__ __align__(1024) char smem_g[2 * C::STAGE];
   LDS3 char* smem = (LDS3 char*)smem_g;
   const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
 
   const int tid = threadIdx.x;
   const int lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int wm = wave >> 1, wn = wave & 1;
+  const int wm = wave / C::WN, wn = wave % C::WN;
   const int g = lane >> 4, c = lane & 15;
 
   int e, m0, nt;
-  if (!grouped_gemm_tile(cnt, E, kBM, n_tiles, kMBlock, lane, e, m0, nt)) return;   // workgroup-uniform
-  const int n0 = nt * kMidBN;
+  if (!grouped_gemm_tile(cnt, E, C::BM, n_tiles, kMBlock, lane, e, m0, nt)) return;   // workgroup-uniform
+  const int n0 = nt * C::BN;
   const int M = cnt[e];
+  // an expert's rows split evenly over its tiles, in steps of 64
+  const int row_tiles = (M + C::BM - 1) / C::BM, height = (M + 64 * row_tiles - 1) / (64 * row_tiles) * 64;
+  m0 = m0 / C::BM * height;
+  const int m_end = min(M, m0 + height);
   const int row0 = off[e];
   const int Kb = K / 2;
   const int nblk = K / 32;
   const int ns = (nblk + 7) / 8;
 
-  // ---- direct-load assignments: wave w fills rows 32w .. 32w + 31 of A and of B,
+  // ---- direct-load assignments: each wave fills its share of the rows of A and of B,
   // eight an instruction (row 8i + l / 8, chunk (l % 8) ^ ((r >> 1) & 7)) ----
   const u32x4_t a_rs = rsrc_words(A, 0x7FFFFFFFu);
   const u32x4_t b_rs = rsrc_words(Wq + (size_t)e * N * Kb, 0x7FFFFFFFu);
@@ -381,45 +398,58 @@ __global__ __launch_bounds__(kThreads, 2) void w4a4_mid_kernel(
   auto row_of = [&](int m) {
     return GATE_UP ? (uint32_t)(rows[row0 + m] / kslots) : (uint32_t)(row0 + m);
   };
-  uint32_t a_off[4], b_off[4];
-  int chunk[4];
+  uint32_t a_off[C::ALOADS], b_off[C::BLOADS];
+  auto row_a = [&](int i) { return C::BM / C::WAVES * wave + 8 * i + (lane >> 3); };
+  auto row_b = [&](int i) { return C::BN / C::WAVES * wave + 8 * i + (lane >> 3); };
+  auto chunk = [&](int r) { return (lane & 7) ^ ((r >> 1) & 7); };
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 32 * wave + 8 * i + (lane >> 3);
-    chunk[i] = (lane & 7) ^ ((r >> 1) & 7);
-    const int n = n0 + (r & ~63) + 4 * (r & 15) + ((r >> 4) & 3);
-    b_off[i] = n < N ? (uint32_t)n * (uint32_t)Kb + 16u * chunk[i] : kOOR;
+  for (int i = 0; i < C::BLOADS; ++i) {
+    const int r = row_b(i), n = n0 + (r & ~63) + 4 * (r & 15) + ((r >> 4) & 3);
+    b_off[i] = n < N ? (uint32_t)n * (uint32_t)Kb + 16u * chunk(r) : kOOR;
   }
-  // weight scales: blocks 2w and 2w + 1 of the stage, four columns a lane
-  const int bs_n = n0 + 4 * (lane & 31), bs_b = 2 * wave + (lane >> 5);
-  const uint32_t bs_off = bs_n < N ? (uint32_t)bs_b * (uint32_t)N + (uint32_t)bs_n : kOOR;
-  // row scales: rows 32w + l / 2, word l % 2 of the stage's two
-  uint32_t as_off = kOOR;
-
-  auto load_b = [&](int st, int buf) {
-    const uint32_t k0 = (uint32_t)st * kMidRow, at = lds0 + buf * kMidStage;
+  // scales, 256 bytes an instruction: the first SA have 32 rows each (row l / 2, word l
+  // % 2 of the stage's two), the others four columns a lane of one or two blocks
+  uint32_t s_off[C::SLOADS];
+  int s_blk[C::SLOADS];
+  auto rows_scales = [&](int i) { return C::SLOADS == 2 ? i == 0 : wave < C::SA; };   // wave-uniform
+  static_assert(C::SA == C::SB && (C::SLOADS == 1 || C::SLOADS == 2), "a wave has one load of each, or one");
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      dma16(b_rs, 8 * st + chunk[i] < nblk ? b_off[i] : kOOR, k0, at + kMidB + (32 * wave + 8 * i) * kMidRow);
-    dma4(bs_rs, 8 * st + bs_b < nblk ? bs_off : kOOR, (uint32_t)(8 * st) * (uint32_t)N, at + kMidBs + 256 * wave);
+  for (int i = 0; i < C::SLOADS; ++i) {
+    const int at = 64 * (wave + C::WAVES * i - C::SA) + lane, n = n0 + at % (C::BN / 4) * 4;
+    s_blk[i] = rows_scales(i) ? 4 * (lane & 1) : at / (C::BN / 4);
+    s_off[i] = !rows_scales(i) && n < N ? (uint32_t)s_blk[i] * (uint32_t)N + (uint32_t)n : kOOR;
+  }
+  auto load_scales = [&](int i, int st, uint32_t at) {
+    const uint32_t off = 8 * st + s_blk[i] < nblk ? s_off[i] : kOOR;
+    if (rows_scales(i)) dma4(as_rs, off, (uint32_t)(2 * st) * (uint32_t)a_rows * 4u, at + C::As + 256 * (wave + C::WAVES * i));
+    else dma4(bs_rs, off, (uint32_t)(8 * st) * (uint32_t)N, at + C::Bs + 256 * (wave + C::WAVES * i - C::SA));
+  };
+  auto load_b = [&](int st, int buf) {
+    const uint32_t at = lds0 + buf * C::STAGE;
+#pragma unroll
+    for (int i = 0; i < C::BLOADS; ++i)
+      dma16(b_rs, 8 * st + chunk(row_b(i)) < nblk ? b_off[i] : kOOR, (uint32_t)st * kLine,
+            at + C::B + (C::BN / C::WAVES * wave + 8 * i) * kLine);
   };
   auto load_a = [&](int st, int buf) {
-    const uint32_t k0 = (uint32_t)st * kMidRow, at = lds0 + buf * kMidStage;
+    const uint32_t at = lds0 + buf * C::STAGE;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      dma16(a_rs, 8 * st + chunk[i] < nblk ? a_off[i] : kOOR, k0, at + kMidA + (32 * wave + 8 * i) * kMidRow);
-    dma4(as_rs, 8 * st + 4 * (lane & 1) < nblk ? as_off : kOOR, (uint32_t)(2 * st) * (uint32_t)a_rows * 4u,
-         at + kMidAs + 256 * wave);
+    for (int i = 0; i < C::ALOADS; ++i)
+      dma16(a_rs, 8 * st + chunk(row_a(i)) < nblk ? a_off[i] : kOOR, (uint32_t)st * kLine,
+            at + C::A + (C::BM / C::WAVES * wave + 8 * i) * kLine);
+#pragma unroll
+    for (int i = 0; i < C::SLOADS; ++i) load_scales(i, st, at);
   };
   load_b(0, 0);   // ahead of the rows
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int m = m0 + 32 * wave + 8 * i + (lane >> 3);
-    a_off[i] = m < M ? row_of(m) * (uint32_t)Kb + 16u * chunk[i] : kOOR;
+  for (int i = 0; i < C::ALOADS; ++i) {
+    const int m = m0 + row_a(i);
+    a_off[i] = m < m_end ? row_of(m) * (uint32_t)Kb + 16u * chunk(row_a(i)) : kOOR;
   }
-  {
-    const int m = m0 + 32 * wave + (lane >> 1);
-    if (m < M) as_off = ((uint32_t)(lane & 1) * (uint32_t)a_rows + row_of(m)) * 4u;
+#pragma unroll
+  for (int i = 0; i < C::SLOADS; ++i) {
+    const int m = m0 + 32 * (wave + C::WAVES * i) + (lane >> 1);
+    if (rows_scales(i) && m < m_end) s_off[i] = ((uint32_t)(lane & 1) * (uint32_t)a_rows + row_of(m)) * 4u;
   }
   load_a(0, 0);
 
@@ -430,8 +460,8 @@ __global__ __launch_bounds__(kThreads, 2) void w4a4_mid_kernel(
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
   const uint32_t xr = (uint32_t)((c >> 1) & 7);
-  const uint32_t a_rd = kMidA + (64 * wm + c) * kMidRow, b_rd = kMidB + (64 * wn + c) * kMidRow;
-  const bool live = m0 + 64 * wm < M;                      // wave-uniform: some of its rows are there
+  const uint32_t a_rd = C::A + (64 * wm + c) * kLine, b_rd = C::B + (64 * wn + c) * kLine;
+  const bool live = m0 + 64 * wm < m_end;                      // wave-uniform: some of its rows are there
   for (int s = 0; s < ns; ++s) {
     const int buf = s & 1;
     // stage s has landed, and every wave is done with stage s - 1's buffer
@@ -442,28 +472,35 @@ __global__ __launch_bounds__(kThreads, 2) void w4a4_mid_kernel(
       load_a(s + 1, buf ^ 1);
     }
     if (!live) continue;
-    const LDS3 char* at = smem + buf * kMidStage;
+    const LDS3 char* at = smem + buf * C::STAGE;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const bool in = 8 * s + 4 * t + g < nblk;            // no caller's byte past K is used: 255 would be a NaN
       const uint32_t xo = 16u * ((uint32_t)(4 * t + g) ^ xr);
-      u32x4_t b[4], a[4];
-      uint32_t sa[4];
+      u32x4_t b[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = *(const LDS3 u32x4_t*)(at + b_rd + xo + 16 * j * kMidRow);
-      const uint32_t sb = *(const LDS3 uint32_t*)(at + kMidBs + (4 * t + g) * kMidBN + 64 * wn + 4 * c);
+      for (int j = 0; j < 4; ++j) b[j] = *(const LDS3 u32x4_t*)(at + b_rd + xo + 16 * j * kLine);
+      const uint32_t sb = *(const LDS3 uint32_t*)(at + C::Bs + (4 * t + g) * C::BN + 64 * wn + 4 * c);
+      if constexpr (C::WAVES == 4) {
+        // all row blocks ahead of the products
+        u32x4_t a[4];
+        uint32_t sa[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a[i] = *(const LDS3 u32x4_t*)(at + a_rd + xo + 16 * i * kMidRow);
-        sa[i] = *(const LDS3 uint8_t*)(at + kMidAs + 8 * (64 * wm + 16 * i + c) + 4 * t + g);
-      }
+        for (int i = 0; i < 4; ++i) {
+          a[i] = *(const LDS3 u32x4_t*)(at + a_rd + xo + 16 * i * kLine);
+          sa[i] = *(const LDS3 uint8_t*)(at + C::As + 8 * (64 * wm + 16 * i + c) + 4 * t + g);
+        }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t si = in ? sa[i] : 0u;
-        acc[i][0] = mfma_fp4_16<0, 0>(a[i], b[0], acc[i][0], si, sb);
-        acc[i][1] = mfma_fp4_16<0, 1>(a[i], b[1], acc[i][1], si, sb);
-        acc[i][2] = mfma_fp4_16<0, 2>(a[i], b[2], acc[i][2], si, sb);
-        acc[i][3] = mfma_fp4_16<0, 3>(a[i], b[3], acc[i][3], si, sb);
+        for (int i = 0; i < 4; ++i) products(acc[i], a[i], b, in ? sa[i] : 0u, sb);
+      } else {
+        // each before its own: four waves a SIMD have 128 registers each
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const u32x4_t a = *(const LDS3 u32x4_t*)(at + a_rd + xo + 16 * i * kLine);
+          const uint32_t sa = *(const LDS3 uint8_t*)(at + C::As + 8 * (64 * wm + 16 * i + c) + 4 * t + g);
+          products(acc[i], a, b, in ? sa : 0u, sb);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
     }
   }
@@ -482,11 +519,11 @@ __global__ __launch_bounds__(kThreads, 2) void w4a4_mid_kernel(
   for (int i = 0; i < 4; ++i) {
     const int m4 = m0 + 64 * wm + 16 * i + 4 * g;          // rows m4 .. m4 + 3
     if constexpr (GATE_UP) {
-      store_glu_quad(acc[i], bb, m4, M, row0, ncol, N, lane, reinterpret_cast<uint8_t*>(out), out_s, S);
+      store_glu_quad(acc[i], bb, m4, m_end, row0, ncol, N, lane, reinterpret_cast<uint8_t*>(out), out_s, S);
     } else {
 #pragma unroll
       for (int v = 0; v < 4; ++v)
-        if (m4 + v < M && ncol < N)
+        if (m4 + v < m_end && ncol < N)
           *reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(out) + (size_t)(row0 + m4 + v) * N + ncol) =
               f32x4_t{acc[i][0][v] + bb[0], acc[i][1][v] + bb[1], acc[i][2][v] + bb[2], acc[i][3][v] + bb[3]};
     }
@@ -500,23 +537,33 @@ hipError_t launch(const void* A, const void* As, const void* Wq, const void* Ws,
   const int64_t S = T * k, a_rows = GATE_UP ? T : S;
   // 32-bit buffer offsets: the token codes and one expert's codes below 2 GiB
   if (a_rows * K / 2 >= ((int64_t)1 << 31) || (int64_t)N * K / 2 >= ((int64_t)1 << 31)) return hipErrorNotSupported;
-  // Tiles of 128 x 128 where those of 128 x 256 are few: 512 run at a time, and the
-  // last round is seldom full.  2880 x 5760 and 2880 x 2880, 32 experts, 128 x 128
-  // against 128 x 256: 64 rows each 84 and 48 us against 96 and 51, 128 rows 113 and
-  // 60 against 117 and 75, 192 rows 144 and 72 against 131 and 80, 512 rows 284 and
-  // 166 against 253 and 174; 128 experts, 32 rows 299 and 150 against 287 and 152.
-  const int64_t big = (near / kBM + (near < E ? near : E)) * ((N + kBN - 1) / kBN);
-  const bool mid = big < 1792;
-  const int n_tiles = (N + (mid ? kMidBN : kBN) - 1) / (mid ? kMidBN : kBN);
-  // at most sum_e ceil(cnt_e / 128) <= S / 128 + min(E, S) M tiles
-  const int64_t tiles = (S / kBM + (S < E ? S : E)) * n_tiles;
-  const int64_t grid = (tiles + kXcds - 1) / kXcds * kXcds;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-  auto kern = mid ? w4a4_mid_kernel<GATE_UP> : w4a4_gemm_kernel<GATE_UP>;
-  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(kThreads), 0, stream, (const uint8_t*)A,
-                     (const uint8_t*)As, (const uint8_t*)Wq, (const uint8_t*)Ws, (const bf16_t*)bias, cnt, off, rows, K,
-                     N, E, k, (int)a_rows, S, n_tiles, out, (uint8_t*)out_s);
-  return hipGetLastError();
+  // Three tilings.  256 x 256 past 100 rows an expert, where it reads the weights least
+  // often; below, 128 x 128 where tiles of 128 x 256 are few (512 run at a time, and the
+  // last round is seldom full), else those.  gate_up (2880 x 5760) and down (2880 x
+  // 2880) in us, 128 x 256 | 128 x 128 | 256 x 256:
+  //   32 experts, 64 rows each 100, 51 | 93, 50 | 94, 54;  96 rows 103, 56 | 97, 53 | 96,
+  //   57;  128 rows 116, 74 | 120, 66 | 102, 60;  192 rows 128, 81 | 154, 75 | 118, 69;
+  //   512 rows 255, 166 | 314, 176 | 264, 149;
+  //   128 experts, 64 rows 312, 170 | 343, 171 | 355, 178;  94 rows 332, 186 | 368, 186 |
+  //   378, 189;  128 rows 410, 236 | 454, 233 | 406, 205;  188 rows 486, 285 | 597, 297 |
+  //   460, 238.
+  const int64_t wide = (near / kBM + (near < E ? near : E)) * ((N + kBN - 1) / kBN);
+  auto run = [&](auto kern, int bm, int bn, int threads) {
+    const int n_tiles = (N + bn - 1) / bn;
+    // at most sum_e ceil(cnt_e / bm) <= S / bm + min(E, S) M tiles
+    const int64_t tiles = (S / bm + (S < E ? S : E)) * n_tiles;
+    const int64_t grid = (tiles + kXcds - 1) / kXcds * kXcds;
+    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(threads), 0, stream, (const uint8_t*)A, (const uint8_t*)As,
+                       (const uint8_t*)Wq, (const uint8_t*)Ws, (const bf16_t*)bias, cnt, off, rows, K, N, E, k,
+                       (int)a_rows, S, n_tiles, out, (uint8_t*)out_s);
+    return hipGetLastError();
+  };
+  using Large = Lines<256, 256>;
+  using Small = Lines<128, 128>;
+  if (near > 100 * (int64_t)E) return run(w4a4_lines_kernel<GATE_UP, Large>, Large::BM, Large::BN, Large::THREADS);
+  if (wide < 1792) return run(w4a4_lines_kernel<GATE_UP, Small>, Small::BM, Small::BN, Small::THREADS);
+  return run(w4a4_gemm_kernel<GATE_UP>, kBM, kBN, kThreads);
 }
 
 }  // namespace

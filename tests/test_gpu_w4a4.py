@@ -425,7 +425,7 @@ def test_other_stream():
 
 @pytest.mark.parametrize("K", [32, 672])
 def test_products_of_many_tiles(K):
-    """So many tiles that the GEMM takes its wide ones: ragged experts, some of one row, against 64 bits."""
+    """So many tiles and rows that the GEMM takes its large ones: ragged experts, some of one row, against 64 bits."""
     _need_gpu()
     T, E, k, N = 4096, 32, 4, 2880
     rng = np.random.default_rng(K)
@@ -551,3 +551,30 @@ def test_ep_rank_of_many(T):
         part = binding.moe_forward_ep_w4a4(*g[:3], *(t[lo:lo + 4].contiguous() for t in g[3:]), e_begin=lo, k=k)
         ref = orc.moe_forward_w4a4(*args[:3], *(a[lo:lo + 4] for a in args[3:]), k, experts=range(lo, lo + 4))
         assert_y_close(host_f64(part), ref["y"], f"the share of experts from {lo}")
+
+
+@pytest.mark.parametrize("K", [64, 352])
+def test_products_of_many_experts(K):
+    """Many tiles of few rows each (the GEMM's tiles of 128 x 256): against 64 bits."""
+    _need_gpu()
+    T, E, k, N = 900, 150, 4, 2880
+    ids = _routing(T, E, k, 24, 140)
+    cnt, off, rows, pos = binding.moe_permute(_up(ids), E)
+    at, rows_h = off.cpu().numpy(), rows.cpu().numpy()
+    q, s = _matrix(E, K, N, 25)
+    b = d.normal_bf16((E, N), 0.5, 25, 1, E, N)
+    hq, sh = binding.moe_quantize_rows_mxfp4(torch.randn((T * k, K), device="cuda").bfloat16() * 3)
+    o = binding.moe_down_w4a4(hq, sh, _up(q), _up(s), dev(b), cnt, off, T, k, path="gemm").cpu().numpy().astype(np.float64)
+    h = orc.mxfp4_dequantize_rows(hq.cpu().numpy(), sh.cpu().numpy())
+    xq, sx = binding.moe_quantize_rows_mxfp4(torch.randn((T, K), device="cuda").bfloat16() * float(60.0 / np.sqrt(K)))
+    gq, gs = binding.moe_gate_up_w4a4(xq, sx, _up(q), _up(s), dev(b), cnt, off, rows, k=k, path="gemm")
+    gq, gs, x = gq.cpu().numpy(), gs.cpu().numpy(), orc.mxfp4_dequantize_rows(xq.cpu().numpy(), sx.cpu().numpy())
+    for e in range(0, 140, 9):
+        part = slice(at[e], at[e + 1])
+        W, bias = orc.mxfp4_dequantize(q[e], s[e]).T, orc.widen(b[e])
+        tol = (K / 64 + 9) * ULP * (np.abs(h[part]) @ np.abs(W) + np.abs(bias))
+        _within(o[part], h[part] @ W + bias, tol, f"o of expert {e}")
+        a = x[rows_h[part] // k]
+        u = (K / 64 + 9) * ULP * (np.abs(a) @ np.abs(W) + np.abs(bias))
+        want = orc.clamped_glu(a @ W + bias)
+        _check_h(gq[part], gs[:, part], want, 8.8 * u[:, 0::2] + 7.0 * u[:, 1::2] + 2.0 ** -20 * np.abs(want), f"h of expert {e}")
