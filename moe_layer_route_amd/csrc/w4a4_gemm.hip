@@ -538,12 +538,14 @@ hipError_t launch(const void* A, const void* As, const void* Wq, const void* Ws,
   // 32-bit buffer offsets: the token codes and one expert's codes below 2 GiB
   if (a_rows * K / 2 >= ((int64_t)1 << 31) || (int64_t)N * K / 2 >= ((int64_t)1 << 31)) return hipErrorNotSupported;
   // Three tilings.  256 x 256 past 100 rows an expert, where it reads the weights least
-  // often; below, 128 x 128 where tiles of 128 x 256 are few (512 run at a time, and the
-  // last round is seldom full), else those.  gate_up (2880 x 5760) and down (2880 x
-  // 2880) in us, 128 x 256 | 128 x 128 | 256 x 256:
+  // often, for gate_up up to 250: beyond, two workgroups a CU that multiply beside each
+  // other's GLU and codes do as well or better.  Below, 128 x 128 where tiles of 128 x
+  // 256 are few (512 run at a time, and the last round is seldom full), else those.
+  // gate_up (2880 x 5760) and down (2880 x 2880) in us, 128 x 256 | 128 x 128 | 256 x 256:
   //   32 experts, 64 rows each 100, 51 | 93, 50 | 94, 54;  96 rows 103, 56 | 97, 53 | 96,
   //   57;  128 rows 116, 74 | 120, 66 | 102, 60;  192 rows 128, 81 | 154, 75 | 118, 69;
-  //   512 rows 255, 166 | 314, 176 | 264, 149;
+  //   313 rows 176, 110 | 210, 112 | 186, 93;  512 rows 255, 166 | 314, 176 | 270, 149;
+  //   1024 rows 470, 308 | - | 450, 278;
   //   128 experts, 64 rows 312, 170 | 343, 171 | 355, 178;  94 rows 332, 186 | 368, 186 |
   //   378, 189;  128 rows 410, 236 | 454, 233 | 406, 205;  188 rows 486, 285 | 597, 297 |
   //   460, 238.
@@ -561,8 +563,10 @@ hipError_t launch(const void* A, const void* As, const void* Wq, const void* Ws,
   };
   using Large = Lines<256, 256>;
   using Small = Lines<128, 128>;
-  if (near > 100 * (int64_t)E) return run(w4a4_lines_kernel<GATE_UP, Large>, Large::BM, Large::BN, Large::THREADS);
-  if (wide < 1792) return run(w4a4_lines_kernel<GATE_UP, Small>, Small::BM, Small::BN, Small::THREADS);
+  const bool many = near > 100 * (int64_t)E;
+  if (many && (!GATE_UP || near <= 250 * (int64_t)E))
+    return run(w4a4_lines_kernel<GATE_UP, Large>, Large::BM, Large::BN, Large::THREADS);
+  if (!many && wide < 1792) return run(w4a4_lines_kernel<GATE_UP, Small>, Small::BM, Small::BN, Small::THREADS);
   return run(w4a4_gemm_kernel<GATE_UP>, kBM, kBN, kThreads);
 }
 

@@ -423,11 +423,12 @@ def test_other_stream():
     assert (host_f64(back) == orc.mxfp4_dequantize_rows(*orc.mxfp4_quantize_rows(host_f64(g[0])))).all()
 
 
-@pytest.mark.parametrize("K", [32, 672])
-def test_products_of_many_tiles(K):
-    """So many tiles and rows that the GEMM takes its large ones: ragged experts, some of one row, against 64 bits."""
+@pytest.mark.parametrize("T,K", [(4096, 32), (4096, 672), (1500, 352)])
+def test_products_of_many_tiles(T, K):
+    """So many tiles and rows that the GEMM takes its large ones (of gate_up: at the fewer tokens): ragged experts, some
+    of one row, against 64 bits."""
     _need_gpu()
-    T, E, k, N = 4096, 32, 4, 2880
+    E, k, N = 32, 4, 2880
     rng = np.random.default_rng(K)
     # experts of very different size: the first few take most of the tokens
     p = 1.0 / (1.0 + np.arange(E)) ** 1.5
