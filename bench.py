@@ -36,6 +36,7 @@ import argparse
 import hashlib
 import json
 import os
+import re
 import sys
 import time
 
@@ -107,6 +108,15 @@ def _source_digest(files):
     return h.hexdigest()[:16]
 
 
+def _kernel_sources(kernel_file):
+    """The files a counter summary's digest covers: the kernel's source, device_common.h and the headers of device code
+    for its number format that it includes."""
+    csrc = "moe_layer_route_amd/csrc/"
+    with open(os.path.join(ROOT, kernel_file)) as fh:
+        formats = re.findall(r'^#include "(\w+_device\.h)"', fh.read(), re.M)
+    return [kernel_file, csrc + "device_common.h", *(csrc + f for f in formats)]
+
+
 def _traffic(kernel_file, workload, stem=None):
     """HBM bytes per launch from the committed rocprofv3 counter summary, or
     None when there is none or the kernel source changed since it was taken.
@@ -120,7 +130,7 @@ def _traffic(kernel_file, workload, stem=None):
         if "=" in line and not line.startswith("#"):
             a, b = line.split("=", 1)
             kv[a.strip()] = b.strip()
-    if kv.get("source_digest") != _source_digest([kernel_file, "moe_layer_route_amd/csrc/device_common.h"]):
+    if kv.get("source_digest") != _source_digest(_kernel_sources(kernel_file)):
         return None
     try:
         return float(kv["hbm_bytes_per_launch"])

@@ -135,7 +135,8 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
     nt = r / p.tiles_m;
     m0 = (r - nt * p.tiles_m) * kBM;
   } else {
-    if (!grouped_gemm_tile(p.cnt, p.E, kBM, p.tiles_n, kMBlock, block, lane, e, m0, nt)) return;   // workgroup-uniform
+    // (these kinds come first in their launch: block is the workgroup's own number)
+    if (!grouped_gemm_tile(p.cnt, p.E, kBM, p.tiles_n, kMBlock, lane, e, m0, nt)) return;   // workgroup-uniform
   }
   const int n0 = nt * C::BN;
   const int rows_e = p.cnt[e];

@@ -118,7 +118,7 @@ __device__ __forceinline__ int wave_incl_scan(int v, int lane) {
 // gets the same expert, first row and N tile; false for a block past the last
 // tile (the grid is an upper bound).  Experts 4 lane .. 4 lane + 3: E <= 256.
 __device__ __forceinline__ bool grouped_gemm_tile(const int32_t* __restrict__ cnt, int E, int bm, int n_tiles,
-                                                  int mblock, int block, int lane, int& e, int& m0, int& nt) {
+                                                  int mblock, int lane, int& e, int& m0, int& nt) {
   constexpr int kXcdCount = 8;
   int mt[4], tc[4], sum = 0;
 #pragma unroll
@@ -131,8 +131,8 @@ __device__ __forceinline__ bool grouped_gemm_tile(const int32_t* __restrict__ cn
   const int incl = wave_incl_scan(sum, lane);
   const int R = __shfl(incl, kWave - 1, kWave);
   const int Q = (R + kXcdCount - 1) / kXcdCount;
-  const int xi = block / kXcdCount;
-  const int L = block % kXcdCount * Q + xi;
+  const int xi = (int)blockIdx.x / kXcdCount;
+  const int L = (int)(blockIdx.x % kXcdCount) * Q + xi;
   int fe = -1, fm = 0, fn = 0;
   if (xi < Q && L < R) {
     int start = incl - sum;
@@ -157,10 +157,6 @@ __device__ __forceinline__ bool grouped_gemm_tile(const int32_t* __restrict__ cn
   m0 = __builtin_amdgcn_readfirstlane(__shfl(fm, src, kWave));
   nt = __builtin_amdgcn_readfirstlane(__shfl(fn, src, kWave));
   return true;
-}
-__device__ __forceinline__ bool grouped_gemm_tile(const int32_t* __restrict__ cnt, int E, int bm, int n_tiles,
-                                                  int mblock, int lane, int& e, int& m0, int& nt) {
-  return grouped_gemm_tile(cnt, E, bm, n_tiles, mblock, (int)blockIdx.x, lane, e, m0, nt);
 }
 
 // Raw buffer descriptor words (base, byte range, stride 0) for the direct-to-LDS
