@@ -736,9 +736,9 @@ MOE_API int moe_down_w4a4(const void* hq, const void* sh, const void* Wd_q, cons
  *   x, Wr, Wgu, bgu, Wd, bd  as given to moe_forward
  *   topk_ids int32 [T][k], topk_w float [T][k]   as moe_forward (or moe_route,
  *                            moe_forward_padded) returned them.  A slot whose id
- *                            lies outside [0, E) is skipped (a padding token
- *                            gets dx = 0 and adds nothing); an id twice in a
- *                            row is two slots.
+ *                            lies outside [0, E) is skipped, whatever its weight
+ *                            (a padding token gets dx = 0 and adds nothing); an
+ *                            id twice in a row is two slots.
  *   dx   bf16 [T][H]    out  through the experts and through the router
  *   dWr  bf16 [E][H], dbr bf16 [E]   out, both NULL to skip
  *   dWgu bf16 [E][H][2I], dbgu bf16 [E][2I], dWd bf16 [E][I][H], dbd bf16 [E][H]

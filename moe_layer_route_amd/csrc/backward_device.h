@@ -123,10 +123,11 @@ __device__ __forceinline__ float wave_sum(float v) {
 __device__ __forceinline__ void token_dl(const Dl& p, int64_t t, int lane) {
   const int k = p.k, H = p.H;
   const int64_t S = p.T * k;
-  float dw[MOE_MAX_K_DEV];
+  // a skipped slot's weight takes no part, whatever it is
+  float dw[MOE_MAX_K_DEV], w[MOE_MAX_K_DEV];
 #pragma unroll
   for (int j = 0; j < MOE_MAX_K_DEV; ++j) {
-    dw[j] = 0.f;
+    dw[j] = w[j] = 0.f;
     if (j < k) {
       const int64_t s = t * k + j;
       const int at = p.pos[s];
@@ -141,16 +142,17 @@ __device__ __forceinline__ void token_dl(const Dl& p, int64_t t, int lane) {
         }
         for (int q = lane; q < p.parts; q += kWave) sum += p.dw_part[(size_t)q * S + at];
         dw[j] = wave_sum(sum);
+        w[j] = p.w[s];
       }
     }
   }
   float mean = 0.f;
 #pragma unroll
   for (int j = 0; j < MOE_MAX_K_DEV; ++j)
-    if (j < k) mean = fmaf(p.w[t * k + j], dw[j], mean);
+    if (j < k) mean = fmaf(w[j], dw[j], mean);
 #pragma unroll
   for (int j = 0; j < MOE_MAX_K_DEV; ++j)
-    if (j < k && lane == j) p.dl[t * k + j] = p.w[t * k + j] * (dw[j] - mean);
+    if (j < k && lane == j) p.dl[t * k + j] = w[j] * (dw[j] - mean);
 }
 
 }  // namespace

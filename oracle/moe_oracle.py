@@ -609,13 +609,15 @@ def moe_forward_w4a4(x, Wr, br, Wgu_q, Wgu_s, bgu, Wd_q, Wd_s, bd, k: int, exper
 #       beyond (gate above 7; up above 7 or below -7);
 #   B2  the pick of experts has no gradient, the softmax over the picks has;
 #   B3  slots whose id lies outside [0, E) are skipped: they are no term of y,
-#       and their weights' gradients count as 0 in the softmax's.
+#       their weights' gradients count as 0 in the softmax's, and their weights
+#       are not looked at.
 # --------------------------------------------------------------------------
 def moe_backward(dy, x, Wr, Wgu, bgu, Wd, bd, ids, w):
     """Gradients in float64, nothing rounded: a dict of dx, dWr, dbr, dWgu, dbgu, dWd, dbd."""
     dyv, xv, w = widen(dy), widen(x), np.asarray(w, np.float64)
     T, H = xv.shape
     E, I = Wd.shape[:2]
+    w = np.where((ids >= 0) & (ids < E), w, 0.0)
     g = {"dx": np.zeros((T, H)), "dWr": np.zeros((E, H)), "dbr": np.zeros(E), "dWgu": np.zeros((E, H, 2 * I)),
          "dbgu": np.zeros((E, 2 * I)), "dWd": np.zeros((E, I, H)), "dbd": np.zeros((E, H))}
     dw = np.zeros_like(w)
