@@ -743,6 +743,8 @@ MOE_API int moe_down_w4a4(const void* hq, const void* sh, const void* Wd_q, cons
  *   dWr  bf16 [E][H], dbr bf16 [E]   out, both NULL to skip
  *   dWgu bf16 [E][H][2I], dbgu bf16 [E][2I], dWd bf16 [E][I][H], dbd bf16 [E][H]
  *                       out, all four NULL to skip; an expert without slots gets 0
+ * dy, dx, dWr, dWgu and dWd are 16-byte aligned, as x and the weights; dbgu and
+ * dbd 4-byte, as the biases; dbr 2-byte.
  * Formulas (e, w, slot s of token t; z = sigmoid(1.702 g), g and u clamped):
  *   d = dy . Wd[e]^T;  h = (u + 1) g z;  dw = h . d + bd[e] . dy
  *   dgate = w d (u + 1) z (1 + 1.702 g (1 - z)), 0 where gate > 7

@@ -9,6 +9,9 @@ namespace {
 
 #define LDS3 __attribute__((address_space(3)))
 
+// 16 bytes of a bias or of its gradient, which need not begin at more than a word
+typedef u32x4_t u32x4_word_t __attribute__((aligned(4)));
+
 struct Slots {
   const int32_t *cnt, *off, *rows;
   uint32_t per_token;   // slot / k = umulhi(slot, per_token); 0: k = 1
@@ -86,7 +89,7 @@ __device__ __forceinline__ void column_sum(const Sum& p, const Slots& a, int e, 
       for (int w = 1; w < kSumWaves; ++w) s[q] += part[w][q][lane];
     }
     if (col < C)
-      *reinterpret_cast<u32x4_t*>(p.out + (size_t)e * C + col) =
+      *reinterpret_cast<u32x4_word_t*>(p.out + (size_t)e * C + col) =
           u32x4_t{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7])};
     if (p.out_factor && piece == 0 && lane == 0) {
       float f = part_f[0];
@@ -134,7 +137,7 @@ __device__ __forceinline__ void token_dl(const Dl& p, int64_t t, int lane) {
       if (at >= 0) {   // wave-uniform
         float sum = 0.f;
         const u32x4_t* a = reinterpret_cast<const u32x4_t*>(p.dy + t * H);
-        const u32x4_t* b = reinterpret_cast<const u32x4_t*>(p.bd + (size_t)p.ids[s] * H);
+        const u32x4_word_t* b = reinterpret_cast<const u32x4_word_t*>(p.bd + (size_t)p.ids[s] * H);
         for (int c = lane; c < H / 8; c += kWave) {
           const u32x4_t u = a[c], v = b[c];
 #pragma unroll

@@ -1596,7 +1596,7 @@ int moe_backward(const void* dy, const void* x, const void* Wr, const void* Wgu,
   CHECK_PTR(Wgu, 16);
   CHECK_PTR(bgu, 4);
   CHECK_PTR(Wd, 16);
-  CHECK_PTR(bd, 16);
+  CHECK_PTR(bd, 4);
   CHECK_PTR(topk_ids, 4);
   CHECK_PTR(topk_w, 4);
   CHECK_PTR(dx, 16);
@@ -1611,9 +1611,9 @@ int moe_backward(const void* dy, const void* x, const void* Wr, const void* Wgu,
   }
   if (experts) {
     CHECK_PTR(dWgu, 16);
-    CHECK_PTR(dbgu, 16);
+    CHECK_PTR(dbgu, 4);
     CHECK_PTR(dWd, 16);
-    CHECK_PTR(dbd, 16);
+    CHECK_PTR(dbd, 4);
   }
   const size_t row = (size_t)T * H * 2, S = (size_t)T * k, wgu = (size_t)E * H * I * 4;
   const struct { const char* name; const void* p; size_t n; } ins[] = {

@@ -2,10 +2,15 @@
 skipped slots, and refusals of the C ABI (nothing here reaches a launch)."""
 from __future__ import annotations
 
+import ctypes
+import os
+
 import numpy as np
 import pytest
 
-from moe_layer_route_amd import datagen as d
+pytest.importorskip("torch")
+
+from moe_layer_route_amd import binding, datagen as d
 import oracle.moe_oracle as orc
 
 
@@ -26,3 +31,31 @@ def test_oracle_skips_the_weight_of_a_skipped_slot(fill):
     got = orc.moe_backward(*a, ids, np.where(skipped, np.float32(fill), w))
     assert all((got[v] == want[v]).all() for v in want) and np.abs(want["dx"]).max() > 0
     assert (want["dx"][4] == 0).all()
+
+
+# ------------------------------------------------------------------------------------------------ the C ABI
+BASE = 1 << 36     # addresses that are never read, 64 GiB apart
+NAMES = ("dy", "x", "Wr", "Wgu", "bgu", "Wd", "bd", "topk_ids", "topk_w", "dx", "dWr", "dbr", "dWgu", "dbgu", "dWd", "dbd")
+OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(binding.LIB_PATH):
+        pytest.skip("library not built")
+    return binding.library()
+
+
+def _call(lib, T=0, H=64, E=4, k=2, I=32, ws_bytes=0, **add):
+    """moe_backward on addresses 64 GiB apart, each moved by add[name] bytes."""
+    p = [ctypes.c_void_p(BASE * (i + 1) + add.get(n, 0)) for i, n in enumerate(NAMES)]
+    return lib.moe_backward(*p[:9], T, H, E, k, I, *p[9:], ctypes.c_void_p(BASE * 20), ws_bytes, None)
+
+
+@pytest.mark.parametrize("name,step", [(n, 4 if n in ("bgu", "bd", "dbgu", "dbd", "topk_ids", "topk_w") else
+                                        2 if n == "dbr" else 16) for n in NAMES])
+def test_alignment(lib, name, step):
+    """Biases and their gradients from any word on, as the forward call takes them; everything else as it says."""
+    assert _call(lib, **{name: step}) == OK, lib.moe_last_error()
+    assert _call(lib, **{name: step // 2}) == INVALID
+    assert f"{name} is not {step}-byte aligned" in lib.moe_last_error().decode()
