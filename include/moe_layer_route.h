@@ -757,8 +757,10 @@ MOE_API int moe_down_w4a4(const void* hq, const void* sh, const void* Wd_q, cons
  * fixed order, each gradient rounded once to bf16 (not accumulated into).
  * Outputs overlap neither inputs nor each other nor the workspace
  * (MOE_ERR_INVALID_ARG, as far as it is checked: outputs against inputs and each
- * other).  x and dy must take less than 2 GiB each (MOE_ERR_UNSUPPORTED).  T = 0
- * is a valid call that enqueues nothing: the weights' gradients stay as they are.
+ * other).  x and dy must take less than 2 GiB each, and no launch may need 2^32
+ * threads, as some 2^26 tokens of H = 8 do (MOE_ERR_UNSUPPORTED, before anything
+ * is enqueued).  T = 0 is a valid call that enqueues nothing: the weights'
+ * gradients stay as they are.
  */
 MOE_API size_t moe_workspace_bytes_backward(int64_t T, int32_t H, int32_t E, int32_t k, int32_t I);
 MOE_API int moe_backward(const void* dy, const void* x, const void* Wr, const void* Wgu, const void* bgu,

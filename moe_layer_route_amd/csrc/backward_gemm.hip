@@ -51,6 +51,7 @@
 #include "backward_device.h"
 #include "launch.h"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace moe {
@@ -573,6 +574,8 @@ __global__ __launch_bounds__(kThreads, 2) void backward_tail_kernel(const Tail p
   }
 }
 
+constexpr int64_t in_groups(int64_t blocks) { return (blocks + kXcds - 1) / kXcds; }
+
 // groups of eight blocks of a product; fills in the tile counts
 template <int KIND>
 int64_t groups(Args& a, int64_t S) {
@@ -587,14 +590,14 @@ int64_t groups(Args& a, int64_t S) {
     tiles = (S / kBM + (S < a.E ? S : a.E)) * a.tiles_n;
   }
   a.S = S;
-  return (tiles + kXcds - 1) / kXcds;
+  return in_groups(tiles);
 }
+
+int64_t dl_groups(int64_t T) { return in_groups((T + kThreads / kWave - 1) / (kThreads / kWave)); }
 
 template <int KIND>
 hipError_t launch(Args a, int64_t S, hipStream_t stream) {
   const int64_t grid = groups<KIND>(a, S) * kXcds;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-  if (grid == 0) return hipSuccess;
   hipLaunchKernelGGL((backward_gemm_kernel<KIND>), dim3((unsigned)grid), dim3(kThreads), 0, stream, a);
   return hipGetLastError();
 }
@@ -607,6 +610,17 @@ hipError_t launch_backward_d(const void* dy, const void* Wd, const int32_t* cnt,
   a.A = (const bf16_t*)dy, a.B = (const bf16_t*)Wd, a.cnt = cnt, a.off = off, a.rows = rows;
   a.N = I, a.K = H, a.E = E, a.per_token = per_token(k), a.out = d;
   return launch<kD>(a, T * k, stream);
+}
+
+bool backward_fits(int64_t T, int H, int E, int k, int I) {
+  const int64_t S = T * k;
+  Args d{}, gu{}, dx{}, wgu{}, wd{};
+  d.E = gu.E = dx.E = wgu.E = wd.E = E;
+  d.N = I, gu.N = 2 * I, dx.N = H, wgu.M = H, wgu.N = 2 * I, wd.M = I, wd.N = H;
+  const int64_t sums = (int64_t)E * ((2 * I + kSumCols - 1) / kSumCols + (H + kSumCols - 1) / kSumCols);
+  const int64_t tail = groups<kDX>(dx, S) + in_groups(sums) + dl_groups(T) + groups<kWGU>(wgu, S) + groups<kWD>(wd, S);
+  const int64_t most = std::max({groups<kD>(d, S), groups<kGU>(gu, S), tail});
+  return most * kXcds * kThreads < (int64_t)1 << 32;
 }
 
 int backward_dw_parts(int I) {
@@ -641,17 +655,10 @@ hipError_t launch_backward_tail(const void* dy, const void* x, const void* Wgu, 
   p.dbgu = sum_of(dgu, nullptr, 2 * I, dbgu, nullptr);
   p.dbd = sum_of(dy, w, H, dbd, nullptr);
   p.dl = Dl{(const bf16_t*)dy, (const bf16_t*)bd, ids, pos, w, dw_part, backward_dw_parts(I), H, k, T, dl};
-  auto in_groups = [](int64_t blocks) { return (blocks + kXcds - 1) / kXcds; };
-  const int64_t n[5] = {groups<kDX>(p.dx, S), in_groups((int64_t)E * (p.dbgu.parts + p.dbd.parts)),
-                        in_groups((T + kThreads / kWave - 1) / (kThreads / kWave)), dWgu ? groups<kWGU>(p.wgu, S) : 0,
-                        dWd ? groups<kWD>(p.wd, S) : 0};
+  const int64_t n[5] = {groups<kDX>(p.dx, S), in_groups((int64_t)E * (p.dbgu.parts + p.dbd.parts)), dl_groups(T),
+                        dWgu ? groups<kWGU>(p.wgu, S) : 0, dWd ? groups<kWD>(p.wd, S) : 0};
   int64_t at = 0;
-  for (int i = 0; i < 5; ++i) {
-    at += n[i];
-    if (at * kXcds > 0x7FFFFFFF) return hipErrorInvalidValue;
-    p.begin[i] = (int)at;
-  }
-  if (at == 0) return hipSuccess;
+  for (int i = 0; i < 5; ++i) p.begin[i] = (int)(at += n[i]);
   hipLaunchKernelGGL(backward_tail_kernel, dim3((unsigned)(at * kXcds)), dim3(kThreads), 0, stream, p);
   return hipGetLastError();
 }

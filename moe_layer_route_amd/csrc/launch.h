@@ -159,6 +159,8 @@ hipError_t launch_add_rmsnorm(const void* x, const void* residual, const void* g
 // with the gradients of the experts' weights (or NULL); and dx with the router's (or
 // NULL).  The weights' gradients read up to 28 bytes behind rows (other parts of the
 // workspace) without using them.
+// backward_fits: whether every launch stays below the 2^32 threads that a grid can have.
+bool backward_fits(int64_t T, int H, int E, int k, int I);
 hipError_t launch_backward_d(const void* dy, const void* Wd, const int32_t* cnt, const int32_t* off, const int32_t* rows,
                              int64_t T, int H, int E, int k, int I, float* d, hipStream_t stream);
 int backward_dw_parts(int I);

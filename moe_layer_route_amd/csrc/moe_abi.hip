@@ -1635,6 +1635,9 @@ int moe_backward(const void* dy, const void* x, const void* Wr, const void* Wgu,
   if (T * (int64_t)H * 2 >= (int64_t)1 << 31)
     return fail(MOE_ERR_UNSUPPORTED, "%s: x and dy of %lld rows of %d take 2 GiB or more: split the batch", fn,
                 (long long)T, H);
+  if (!moe::backward_fits(T, H, E, k, I))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: T=%lld with k=%d takes a launch of 2^32 threads or more: split the batch", fn,
+                (long long)T, k);
   if (T == 0) return ok();
   const BackwardLayout L = backward_layout(T, H, E, k, I);
   if (workspace == nullptr || workspace_bytes < L.total)

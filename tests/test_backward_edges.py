@@ -59,3 +59,15 @@ def test_alignment(lib, name, step):
     assert _call(lib, **{name: step}) == OK, lib.moe_last_error()
     assert _call(lib, **{name: step // 2}) == INVALID
     assert f"{name} is not {step}-byte aligned" in lib.moe_last_error().decode()
+
+
+def test_sizes_that_no_launch_holds(lib):
+    """Refused before anything is enqueued: rows that 31-bit offsets do not reach, and launches of 2^32 threads (the
+    workspace is too small throughout, which is looked at last)."""
+    for T, H, k, I in ((1 << 24, 64, 1, 64), (1 << 27, 8, 1, 8), (1 << 17, 8192, 4, 8)):
+        assert _call(lib, T=T, H=H, k=k, I=I) == UNSUPPORTED and b"2 GiB" in lib.moe_last_error(), (T, H, k, I)
+    for T, k, I in ((1 << 26, 1, 8), ((1 << 26) + 12345, 2, 8), ((1 << 27) - 1, 4, 96), (1 << 25, 4, 2048)):
+        assert _call(lib, T=T, H=8, k=k, I=I) == UNSUPPORTED, (T, k, I, lib.moe_last_error())
+        assert b"2^32 threads" in lib.moe_last_error()
+    for T, H, k, I in ((1 << 25, 8, 4, 8), ((1 << 26) - (1 << 22), 8, 1, 8), ((1 << 25), 8, 4, 1024), (1 << 18, 2880, 4, 2880)):
+        assert _call(lib, T=T, H=H, k=k, I=I) == WORKSPACE, (T, H, k, I, lib.moe_last_error())
