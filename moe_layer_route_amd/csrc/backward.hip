@@ -16,6 +16,8 @@
 namespace moe {
 namespace {
 
+#define LDS3 __attribute__((address_space(3)))
+
 // ---------------------------------------------------------------------------
 // The first workgroups sum the router's columns (dWr, dbr), the others dx: one
 // thread per four columns of a token.
@@ -26,7 +28,7 @@ template <int KMAX>
 __global__ __launch_bounds__(kDxThreads) void backward_dx_kernel(
     const float* __restrict__ dxs, const int32_t* __restrict__ ids, const int32_t* __restrict__ pos,
     const float* __restrict__ dl, const bf16_t* __restrict__ Wr, int64_t T, int H, int k, bf16_t* __restrict__ dx,
-    const Sum router, const Slots slots, int sums) {
+    const Sum router, const Permuted slots, int sums) {
   __shared__ char smem[kSumLds];
   if ((int)blockIdx.x < sums) {   // workgroup-uniform
     const int e = blockIdx.x / router.parts;
@@ -74,7 +76,7 @@ hipError_t launch_backward_dx_sum(const float* dxs, const void* x, const int32_t
   const int64_t sums = (int64_t)E * router.parts, blocks = sums + (T * (H / 4) + kDxThreads - 1) / kDxThreads;
   auto kern = k <= 4 ? backward_dx_kernel<4> : backward_dx_kernel<MOE_MAX_K_DEV>;
   hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(kDxThreads), 0, stream, dxs, ids, pos, dl, (const bf16_t*)Wr, T,
-                     H, k, (bf16_t*)dx, router, Slots{cnt, off, rows, per_token(k)}, (int)sums);
+                     H, k, (bf16_t*)dx, router, Permuted{cnt, off, rows, per_token(k)}, (int)sums);
   return hipGetLastError();
 }
 

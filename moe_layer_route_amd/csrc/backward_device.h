@@ -12,7 +12,8 @@ namespace {
 // 16 bytes of a bias or of its gradient, which need not begin at more than a word
 typedef u32x4_t u32x4_word_t __attribute__((aligned(4)));
 
-struct Slots {
+// the permutation's arrays, as permute.hip leaves them
+struct Permuted {
   const int32_t *cnt, *off, *rows;
   uint32_t per_token;   // slot / k = umulhi(slot, per_token); 0: k = 1
 };
@@ -44,7 +45,7 @@ struct Sum {
 };
 
 template <bool GATHER>
-__device__ __forceinline__ void column_sum(const Sum& p, const Slots& a, int e, int piece, LDS3 char* smem) {
+__device__ __forceinline__ void column_sum(const Sum& p, const Permuted& a, int e, int piece, LDS3 char* smem) {
   LDS3 float (*part)[8][kWave] = (LDS3 float (*)[8][kWave])smem;
   LDS3 float* part_f = (LDS3 float*)(smem + kSumWaves * 8 * kWave * 4);
   const int lane = threadIdx.x & (kWave - 1);
@@ -160,3 +161,5 @@ __device__ __forceinline__ void token_dl(const Dl& p, int64_t t, int lane) {
 
 }  // namespace
 }  // namespace moe
+
+#undef LDS3

@@ -39,10 +39,10 @@
 //   Measured against both and not kept: 256 x 256 by eight waves, one workgroup a CU,
 //   stages of 64 (ring of two) or 32 (ring of four): the whole pass at T = 4096, E =
 //   32 2.82 and 2.85 ms against 2.84, at T = 512 1.19 and 1.12 against 0.99.
-//   Tile heights: an expert's rows are split evenly over its tiles of at most 128,
-//   in steps of 64, and a tile of 64 ni rows has ni row blocks a wave: the loop is
-//   built for each ni, and once more for the tiles that reach past the last
-//   column, whose waves leave out the column blocks without any.
+//   An expert's last tile has what is left of its rows: with at most 64 a wave has
+//   one row block instead of two.  The loop is built for either, and once more for the
+//   tiles that reach past the last column, whose waves leave out the column blocks
+//   without any.
 // What bounds it (H = I = 2880, E = 32): at T = 4096, 512 rows an expert, the load
 // path and the clock (1.9 to 2.0 GHz of 2.4): D 331 us (820 TFLOP/s), GU 668 (814), the
 // rest 1.85 ms with the column sums (735), matrix pipes 38 to 43% busy, without the
@@ -56,6 +56,8 @@
 
 namespace moe {
 namespace {
+
+#define LDS3 __attribute__((address_space(3)))
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
@@ -146,14 +148,7 @@ __device__ __forceinline__ void product(const Args& p, int block, LDS3 char* sme
   const int K = kWeightGrad ? rows_e : p.K;
   const int N = p.N;
   const int ns = (K + C::BK - 1) / C::BK;
-  // the tile's rows: an expert's split evenly over its tiles, in steps of 64
-  int height = kBM;
-  if (!kWeightGrad) {
-    const int tiles = (M + kBM - 1) / kBM;
-    height = (M + 64 * tiles - 1) / (64 * tiles) * 64;
-    m0 = m0 / kBM * height;
-  }
-  const int m_end = min(M, m0 + height);
+  const int m_end = min(M, m0 + kBM);
   const int ni = m_end - m0 > 64 ? 2 : 1;           // row blocks of 32 a wave
   auto token = [&](int slot) {
     return token_of((uint32_t)slot, p.per_token);
@@ -545,7 +540,7 @@ __global__ __launch_bounds__(kThreads, 2) void backward_gemm_kernel(const Args p
 // groups of eight, one a XCD.
 struct Tail {
   Args dx, wgu, wd;
-  Slots slots;
+  Permuted slots;
   Sum dbgu, dbd;
   Dl dl;
   int begin[5];          // first group of the sums, dl, WGU, WD, and the end
@@ -651,7 +646,7 @@ hipError_t launch_backward_tail(const void* dy, const void* x, const void* Wgu, 
   p.dx.A = (const bf16_t*)dgu, p.dx.B = (const bf16_t*)Wgu, p.dx.N = H, p.dx.K = 2 * I, p.dx.out = dxs;
   p.wgu.A = (const bf16_t*)x, p.wgu.B = (const bf16_t*)dgu, p.wgu.M = H, p.wgu.N = 2 * I, p.wgu.out = dWgu;
   p.wd.A = (const bf16_t*)wh, p.wd.B = (const bf16_t*)dy, p.wd.M = I, p.wd.N = H, p.wd.out = dWd;
-  p.slots = Slots{cnt, off, rows, a.per_token};
+  p.slots = Permuted{cnt, off, rows, a.per_token};
   p.dbgu = sum_of(dgu, nullptr, 2 * I, dbgu, nullptr);
   p.dbd = sum_of(dy, w, H, dbd, nullptr);
   p.dl = Dl{(const bf16_t*)dy, (const bf16_t*)bd, ids, pos, w, dw_part, backward_dw_parts(I), H, k, T, dl};

@@ -380,9 +380,15 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES == 16 ? 4 : 2) void w4a4_lines
   if (!grouped_gemm_tile(cnt, E, C::BM, n_tiles, kMBlock, lane, e, m0, nt)) return;   // workgroup-uniform
   const int n0 = nt * C::BN;
   const int M = cnt[e];
-  // an expert's rows split evenly over its tiles, in steps of 64
-  const int row_tiles = (M + C::BM - 1) / C::BM, height = (M + 64 * row_tiles - 1) / (64 * row_tiles) * 64;
-  m0 = m0 / C::BM * height;
+  // 256 rows: an expert's rows split evenly over its tiles, in steps of 64, which for two
+  // tiles of up to 384 rows (three of up to 576) are tiles of 192; steps of 64 leave tiles
+  // of 128 as they are
+  int height = C::BM;
+  if (C::BM > 128) {
+    const int row_tiles = (M + C::BM - 1) / C::BM;
+    height = (M + 64 * row_tiles - 1) / (64 * row_tiles) * 64;
+    m0 = m0 / C::BM * height;
+  }
   const int m_end = min(M, m0 + height);
   const int row0 = off[e];
   const int Kb = K / 2;
