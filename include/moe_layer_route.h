@@ -690,8 +690,8 @@ MOE_API size_t moe_workspace_bytes_w4a4(int64_t T, int32_t H, int32_t E, int32_t
  * Products are exact and summed in float32.  H % 32 == 0 and I % 32 == 0;
  * moe_workspace_bytes_w4a4 bytes of workspace; path: MOE_PATH_GEMV streams the
  * weights, MOE_PATH_GEMM is the LDS-tiled grouped GEMM, AUTO picks from T*k/E.
- * x, h and one expert's matrix must take fewer than 2^32 values each
- * (MOE_ERR_UNSUPPORTED, before anything is enqueued).
+ * x must take less than 4 GiB - 64 bytes (the router reads it), h fewer than 2^32
+ * values (MOE_ERR_UNSUPPORTED, before anything is enqueued).
  */
 MOE_API int moe_forward_w4a4(const void* x, const void* Wr, const void* br, const void* Wgu_q, const void* Wgu_s,
                              const void* bgu, const void* Wd_q, const void* Wd_s, const void* bd,
@@ -716,7 +716,8 @@ MOE_API int moe_forward_ep_w4a4(const void* x, const void* Wr, const void* br, c
 /* Stage calls of moe_forward_w4a4, permuted order as in moe_gate_up and
  * moe_down: gate_up takes x as MXFP4 rows [T] and leaves h as MXFP4 rows [T*k]
  * (hq uint8 [T*k][I/2], sh uint8 [ceil(I/128)][T*k][4]); down takes those.
- * Rows from off[E] on (slots of no expert) are neither read nor written. */
+ * Rows from off[E] on (slots of no expert) are neither read nor written.  x and h
+ * of fewer than 2^32 values each (MOE_ERR_UNSUPPORTED). */
 MOE_API int moe_gate_up_w4a4(const void* xq, const void* sx, const void* Wgu_q, const void* Wgu_s, const void* bgu,
                              const int32_t* cnt, const int32_t* off, const int32_t* rows,
                              int64_t T, int32_t H, int32_t E, int32_t k, int32_t I, void* hq, void* sh,
@@ -753,6 +754,8 @@ MOE_API int moe_down_w4a4(const void* hq, const void* sh, const void* Wd_q, cons
  *   dx[t] = sum_j [dgate, dup]_j . Wgu[e_j]^T + dl_j Wr[e_j]
  *   dWgu[e] = sum x^T [dgate, dup], dWd[e] = sum (w h)^T dy, dWr[e] = sum dl x,
  *   and the biases' gradients the sums of [dgate, dup], w dy and dl.
+ * sum_i w_i dw_i is over all picks of a token, so the call needs the whole layer's
+ * weights: the gradients of moe_forward_ep are not the sums of calls on shares.
  * bf16 operands ([dgate, dup] and w h are rounded to bf16), float32 sums in a
  * fixed order, each gradient rounded once to bf16 (not accumulated into).
  * Outputs overlap neither inputs nor each other nor the workspace
