@@ -44,10 +44,11 @@
 //   tiles that reach past the last column, whose waves leave out the column blocks
 //   without any.
 // What bounds it (H = I = 2880, E = 32): at T = 4096, 512 rows an expert, the load
-// path and the clock (1.9 to 2.0 GHz of 2.4): D 331 us (820 TFLOP/s), GU 668 (814), the
-// rest 1.85 ms with the column sums (735), matrix pipes 38 to 43% busy, without the
-// products 376 / 609 / 1714 us (measured before D, GU and DX had the tiles above).  At
-// T = 512, 64 rows, memory: 4.2 GB of weights read and gradients written in 0.95 ms.
+// path and the clock (1.9 to 2.0 GHz of 2.4): D 328 us (830 TFLOP/s), GU 673 (808), the
+// rest 1.77 ms with the column sums (767), matrix pipes 38 to 46% busy.  Without the
+// products they take 300, 603 and 1528 us, without the loads 203, 432 and 1123, without
+// both 91, 227 and 618.  At T = 512, 64 rows, memory: D 105 us, GU 218, the rest 643 for
+// 4.2 GB of weights read and gradients written, and without the products 105, 214, 605.
 #include "backward_device.h"
 #include "launch.h"
 

@@ -543,18 +543,26 @@ hipError_t launch(const void* A, const void* As, const void* Wq, const void* Ws,
   const int64_t S = T * k, a_rows = GATE_UP ? T : S;
   // 32-bit buffer offsets: the token codes and one expert's codes below 2 GiB
   if (a_rows * K / 2 >= ((int64_t)1 << 31) || (int64_t)N * K / 2 >= ((int64_t)1 << 31)) return hipErrorNotSupported;
-  // Three tilings.  256 x 256 past 100 rows an expert, where it reads the weights least
-  // often, for gate_up up to 250: beyond, two workgroups a CU that multiply beside each
-  // other's GLU and codes do as well or better.  Below, 128 x 128 where tiles of 128 x
-  // 256 are few (512 run at a time, and the last round is seldom full), else those.
+  // Three tilings by the mean rows an expert.  256 x 256 past 100, where it reads the
+  // weights least often; for gate_up up to 250, since from there to some 800 rows two
+  // workgroups a CU that multiply beside each other's GLU and codes are 2 to 6% ahead
+  // (past 1000 they are 4% behind, with skewed picks of 128 experts 8%: one bound on the
+  // mean does not follow that).  Up to 100, 128 x 128 where tiles of 128 x 256 are fewer
+  // than 3.5 rounds of the 512 that run at a time (the last round is seldom full: 1288
+  // of them are behind, 4416 ahead), else those.
   // gate_up (2880 x 5760) and down (2880 x 2880) in us, 128 x 256 | 128 x 128 | 256 x 256:
   //   32 experts, 64 rows each 100, 51 | 93, 50 | 94, 54;  96 rows 103, 56 | 97, 53 | 96,
-  //   57;  128 rows 116, 74 | 120, 66 | 102, 60;  192 rows 128, 81 | 154, 75 | 118, 69;
-  //   313 rows 176, 110 | 210, 112 | 186, 93;  512 rows 255, 166 | 314, 176 | 270, 149;
-  //   1024 rows 470, 308 | - | 450, 278;
-  //   128 experts, 64 rows 312, 170 | 343, 171 | 355, 178;  94 rows 332, 186 | 368, 186 |
-  //   378, 189;  128 rows 410, 236 | 454, 233 | 406, 205;  188 rows 486, 285 | 597, 297 |
-  //   460, 238.
+  //   57;  128 rows 117, 77 | 126, 68 | 104, 62;  192 rows 131, 82 | 157, 79 | 116, 71;
+  //   256 rows 172, 97 | 195, 105 | 172, 95;  313 rows 175, 112 | 213, 114 | 186, 91;
+  //   512 rows 261, 170 | 319, 179 | 267, 154;  768 rows 355, 238 | 432, 253 | 370, 221;
+  //   1024 rows 468, 309 | 599, 337 | 447, 284;  2048 rows 892, 562 | 1142, 636 | 855, 509;
+  //   128 experts, 64 rows 312, 170 | 343, 171 | 355, 178;  104 rows 341, 207 | 377, 193 |
+  //   385, 193;  128 rows 402, 235 | 467, 239 | 409, 205;  188 rows 484, 285 | 597, 299 |
+  //   461, 237;  512 rows 1001, 619 | 1254, 676 | 1026, 581, skewed 1113, 713 | 1368, 732 |
+  //   1026, 580.
+  // Past 100 rows the number of tiles does not count, though few of them leave CUs idle: 8
+  // experts of H = 1024, I = 512 with 128 or 256 rows, gate_up 15 and 14 us where 128 x
+  // 128 takes 11; 16 experts of H = 4096, I = 1536 with 512 rows 92 where 256 x 256 takes 83.
   const int64_t wide = (near / kBM + (near < E ? near : E)) * ((N + kBN - 1) / kBN);
   auto run = [&](auto kern, int bm, int bn, int threads) {
     const int n_tiles = (N + bn - 1) / bn;
