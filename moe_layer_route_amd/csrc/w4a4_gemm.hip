@@ -545,9 +545,9 @@ hipError_t launch(const void* A, const void* As, const void* Wq, const void* Ws,
   if (a_rows * K / 2 >= ((int64_t)1 << 31) || (int64_t)N * K / 2 >= ((int64_t)1 << 31)) return hipErrorNotSupported;
   // Three tilings by the mean rows an expert.  256 x 256 past 100, where it reads the
   // weights least often; for gate_up up to 250, since from there to some 800 rows two
-  // workgroups a CU that multiply beside each other's GLU and codes are 2 to 6% ahead
-  // (past 1000 they are 4% behind, with skewed picks of 128 experts 8%: one bound on the
-  // mean does not follow that).  Up to 100, 128 x 128 where tiles of 128 x 256 are fewer
+  // workgroups a CU that multiply beside each other's GLU and codes are 2 to 7% ahead
+  // (past 1000 they are 4 to 5% behind, with skewed picks of 128 experts 8%: one bound on
+  // the mean does not follow that).  Up to 100, 128 x 128 where tiles of 128 x 256 are fewer
   // than 3.5 rounds of the 512 that run at a time (the last round is seldom full: 1288
   // of them are behind, 4416 ahead), else those.
   // gate_up (2880 x 5760) and down (2880 x 2880) in us, 128 x 256 | 128 x 128 | 256 x 256:
